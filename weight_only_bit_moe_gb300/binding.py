@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI declared in include/moe_w4a16.h.
+"""ctypes binding of the C ABI declared in include/ (moe_w4a16.h, moe_requant.h,
+moe_products.h).
 
 Argument marshalling only: torch tensors are passed as their data pointers,
 streams as their CUDA handles; every step of the layer runs in the library's
@@ -22,7 +23,10 @@ MOE_ACT_SILU_MUL, MOE_ACT_SIGMOID_ALPHA, MOE_ACT_RELU2 = 0, 1, 2
 EXPORTED = ("moe_repack_size", "moe_repack_weights", "moe_repack_weights_ex", "moe_align_capacity", "moe_align", "moe_choose_block_m",
             "moe_workspace_size", "moe_w4a16_forward", "moe_w4a16_forward_noalloc", "moe_get_status",
             "moe_set_trace_events", "moe_set_test_starve_wait", "moe_status_string", "moe_requant_fp8",
-            "moe_requant_launch_geometry")
+            "moe_requant_launch_geometry", "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw",
+            "moe_quant_fp8_block", "moe_gemm_fp8_block")
+MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
+MOE_PRODUCTS_WORKSPACE_BYTES = 48 << 20  # workspace of the products in moe_products.h
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20  # fixed workspace of moe_w4a16_forward_noalloc
 
 
@@ -81,6 +85,13 @@ def load(path: str = ""):
                 "moe_requant_fp8": (i32, [p, p, i64, i64, i64, p, i32, i32, i32, i32, p, p, i32, p]),
                 "moe_requant_launch_geometry": (i32, [i32, i32, i32, i32, ctypes.POINTER(i32),
                                                       ctypes.POINTER(i32)]),
+                "moe_grouped_mm": (i32, [i32, p, i64, p, i64, i64, p, i32, i32, i32, i32, p, i64, p, i64, p]),
+                "moe_grouped_mm_dx": (i32, [i32, p, i64, p, i64, i64, p, i32, i32, i32, i32, p, i64, p, i64, p]),
+                "moe_grouped_mm_dw": (i32, [i32, p, i64, p, i64, p, i32, i32, i32, i32, i32, i32, p, i64, i64, p,
+                                            i64, p]),
+                "moe_quant_fp8_block": (i32, [i32, p, i64, i32, p, i32, i32, i32, p, i64, p, i64, i64, p]),
+                "moe_gemm_fp8_block": (i32, [p, i64, p, i64, i64, p, i64, i64, p, i64, i64, i64, p, i32, i32, i32,
+                                             i32, i32, p, i64, p, i64, p]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -227,3 +238,41 @@ def moe_requant_launch_geometry(num_experts: int, K: int, expected_rows: int, sm
     _check("moe_requant_launch_geometry", load().moe_requant_launch_geometry(
         num_experts, K, expected_rows, sm_count, ctypes.byref(c), ctypes.byref(t)))
     return c.value, t.value
+
+
+def moe_grouped_mm(dtype, x, x_stride, w, w_stride_e, w_stride_n, offsets, num_experts, rows, N, K, out, out_stride,
+                   workspace, workspace_bytes, stream=None):
+    return _check("moe_grouped_mm", load().moe_grouped_mm(
+        dtype, _p(x), x_stride, _p(w), w_stride_e, w_stride_n, _p(offsets), num_experts, rows, N, K, _p(out),
+        out_stride, _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def moe_grouped_mm_dx(dtype, dy, dy_stride, w, w_stride_e, w_stride_n, offsets, num_experts, rows, N, K, dx,
+                      dx_stride, workspace, workspace_bytes, stream=None):
+    return _check("moe_grouped_mm_dx", load().moe_grouped_mm_dx(
+        dtype, _p(dy), dy_stride, _p(w), w_stride_e, w_stride_n, _p(offsets), num_experts, rows, N, K, _p(dx),
+        dx_stride, _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def moe_grouped_mm_dw(dtype, dy, dy_stride, x, x_stride, offsets, num_experts, rows, N, K, dw_dtype, accumulate, dw,
+                      dw_stride_e, dw_stride_n, workspace, workspace_bytes, stream=None):
+    return _check("moe_grouped_mm_dw", load().moe_grouped_mm_dw(
+        dtype, _p(dy), dy_stride, _p(x), x_stride, _p(offsets), num_experts, rows, N, K, dw_dtype, accumulate,
+        _p(dw), dw_stride_e, dw_stride_n, _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def moe_quant_fp8_block(dtype, x, x_stride, x_rows, row_index, rows, K, gated, q, q_stride, scale, scale_strides,
+                        stream=None):
+    """scale_strides = (m, g) element strides of the fp32 scale buffer."""
+    return _check("moe_quant_fp8_block", load().moe_quant_fp8_block(
+        dtype, _p(x), x_stride, x_rows, _p(row_index), rows, K, gated, _p(q), q_stride, _p(scale),
+        scale_strides[0], scale_strides[1], _stream(stream)))
+
+
+def moe_gemm_fp8_block(x, x_stride, x_scale, xs_strides, w, w_strides, w_scale, ws_strides, offsets, num_experts,
+                       rows, N, K, out_dtype, out, out_stride, workspace, workspace_bytes, stream=None):
+    """xs_strides = (m, g), w_strides = (e, n), ws_strides = (e, n, k)."""
+    return _check("moe_gemm_fp8_block", load().moe_gemm_fp8_block(
+        _p(x), x_stride, _p(x_scale), xs_strides[0], xs_strides[1], _p(w), w_strides[0], w_strides[1], _p(w_scale),
+        ws_strides[0], ws_strides[1], ws_strides[2], _p(offsets), num_experts, rows, N, K, out_dtype, _p(out),
+        out_stride, _p(workspace), workspace_bytes, _stream(stream)))
