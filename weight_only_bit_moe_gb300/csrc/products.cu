@@ -1,5 +1,5 @@
 // Entry points of moe_products.h: argument rules and the choice of the kernel.
-#include "products.cuh"
+#include "products_tc.cuh"
 
 using namespace moe;
 
@@ -8,8 +8,6 @@ namespace moe {
 constexpr int kMaxGroups = 1024;
 // gridDim.y of the plain kernel counts 64-column tiles
 constexpr int kMaxDim = 65535 * 64;
-
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 static int check_products(const ProdArgs& g, const void* workspace, int64_t workspace_bytes) {
   if (g.E < 1 || g.E > kMaxGroups || g.rows < 0 || g.N < 1 || g.K < 1 || g.N > kMaxDim || g.K > kMaxDim)
@@ -23,6 +21,11 @@ static int check_products(const ProdArgs& g, const void* workspace, int64_t work
 static bool on_elements(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 static int run(const ProdArgs& g, int mode, void* stream) {
+  if (g.in_type != kE4m3) {
+    bool done = false;
+    if (launch_grouped_tc(g, mode, (cudaStream_t)stream, &done) != cudaSuccess) return MOE_ERR_CUDA;
+    if (done) return MOE_OK;
+  }
   return launch_products_any(g, mode, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
