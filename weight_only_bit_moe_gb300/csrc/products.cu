@@ -21,11 +21,11 @@ static int check_products(const ProdArgs& g, const void* workspace, int64_t work
 static bool on_elements(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 static int run(const ProdArgs& g, int mode, void* stream) {
-  if (g.in_type != kE4m3) {
-    bool done = false;
-    if (launch_grouped_tc(g, mode, (cudaStream_t)stream, &done) != cudaSuccess) return MOE_ERR_CUDA;
-    if (done) return MOE_OK;
-  }
+  bool done = false;
+  const cudaError_t rc = g.in_type == kE4m3 ? launch_fp8_tc(g, (cudaStream_t)stream, &done)
+                                            : launch_grouped_tc(g, mode, (cudaStream_t)stream, &done);
+  if (rc != cudaSuccess) return MOE_ERR_CUDA;
+  if (done) return MOE_OK;
   return launch_products_any(g, mode, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -45,9 +45,6 @@ constexpr int kGtGran = 32;           // n is a multiple of this for cta_group::
 constexpr int kGtStages = 6;
 constexpr int kGtOperandBytes = 128 * 128;              // 128 rows x 64 terms of 16 bits
 constexpr int kGtStageBytes = 2 * kGtOperandBytes;      // P and Q
-constexpr int kGtTokenChunk = 8;      // row tiles that run next to each other through a group's features
-constexpr int kGtGroups = 1024;
-constexpr int kGtSplitItems = 160;    // items of a split launch, at most (sizes the scratch)
 
 struct GroupedTcArgs {
   CUtensorMap map_p, map_q;    // full boxes
@@ -64,70 +61,32 @@ struct GtSmem {
   static constexpr int kBytes = kMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;
 };
-static_assert(GtSmem::kAlloc + (kGtGroups + 1) * 4 + 64 <= 227 * 1024, "shared memory over the per-CTA limit");
+static_assert(GtSmem::kAlloc + (kProdGroups + 1) * 4 + 64 <= 227 * 1024, "shared memory over the per-CTA limit");
 
-// A work item: slice `split` of the tile of P rows p0.. and Q rows q0.. (dW: x's
-// columns) of expert e.
-struct GtItem {
-  int e, p0, q0, n;   // n: Q rows of the tile
-  int t0, t1;         // stages of the slice
-  int split;
-  int tile;           // the tile's number
+// Item w of dW: a regular grid of tiles, x's columns fastest.
+struct DwPlan {
+  int p_tiles, q_tiles;
 };
-
-template <int MODE>
-struct GtPlan {
-  int tiles, S, stages, p_tiles, q_tiles;  // q_tiles: dW only
-};
-
-template <int MODE>
-__device__ __forceinline__ GtItem gt_item(const GroupedTcArgs& a, const GtPlan<MODE>& pl, const int* start, int w) {
-  const ProdArgs& g = a.g;
-  GtItem it;
-  it.tile = w / pl.S;
-  it.split = w - it.tile * pl.S;
-  if (MODE == kProdDw) {
-    const int per = pl.p_tiles * pl.q_tiles;
-    it.e = it.tile / per;
-    const int l = it.tile - it.e * per;
-    it.p0 = (l / pl.q_tiles) * kGtP;
-    it.q0 = (l % pl.q_tiles) * kGtN;
-    it.n = min(kGtN, g.K - it.q0);
-    int r0, r1;
-    group_rows(g, it.e, r0, r1);
-    const int st = (r1 - r0 + 63) / 64;
-    it.t0 = (int)((int64_t)it.split * st / pl.S);
-    it.t1 = (int)((int64_t)(it.split + 1) * st / pl.S);
-    return it;
-  }
-  // the group: the last e with start[e] <= tile
-  int lo = 0, hi = g.E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (start[mid] <= it.tile) lo = mid;
-    else hi = mid - 1;
-  }
-  it.e = lo;
-  const int l = it.tile - start[lo];
+__device__ __forceinline__ ProdItem dw_item(const ProdArgs& g, const DwPlan& pl, int w) {
+  ProdItem it;
+  const int per = pl.p_tiles * pl.q_tiles;
+  it.tile = w;
+  it.split = 0;
+  it.e = w / per;
+  const int l = w - it.e * per;
+  it.p0 = (l / pl.q_tiles) * kGtP;
+  it.q0 = (l % pl.q_tiles) * kGtN;
+  it.n = min(kGtN, g.K - it.q0);
   int r0, r1;
-  group_rows(g, lo, r0, r1);
-  const int m = r1 - r0, nt = (m + kGtN - 1) / kGtN;
-  // chunks of row tiles; inside one, row tiles fastest, then features
-  const int c = l / (kGtTokenChunk * pl.p_tiles), r = l - c * kGtTokenChunk * pl.p_tiles;
-  const int width = min(kGtTokenChunk, nt - c * kGtTokenChunk);
-  const int t = c * kGtTokenChunk + r % width;
-  it.p0 = (r / width) * kGtP;
-  const int q = ((m + nt - 1) / nt + kGtGran - 1) / kGtGran * kGtGran;  // equal tiles
-  it.q0 = r0 + t * q;
-  it.n = min(q, r1 - it.q0);
-  it.t0 = (int)((int64_t)it.split * pl.stages / pl.S);
-  it.t1 = (int)((int64_t)(it.split + 1) * pl.stages / pl.S);
+  group_rows(g, it.e, r0, r1);
+  it.t0 = 0;
+  it.t1 = (r1 - r0 + 63) / 64;
   return it;
 }
 
 // One CTA's share of a stage into `slot` (P at +0, Q at +kGtOperandBytes).
 template <int MODE>
-__device__ __forceinline__ void gt_load_stage(const GroupedTcArgs& a, const GtItem& it, int t, uint32_t rank,
+__device__ __forceinline__ void gt_load_stage(const GroupedTcArgs& a, const ProdItem& it, int t, uint32_t rank,
                                               int half, int boxes, int r0, int r1, uint32_t slot, uint32_t bar) {
   const int p = it.p0 + (int)rank * 128;
   const uint32_t qs = slot + kGtOperandBytes;
@@ -185,7 +144,7 @@ template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     grouped_tc_kernel(const __grid_constant__ GroupedTcArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ int start[kGtGroups + 1];  // first tile of each group
+  __shared__ int start[kProdGroups + 1];  // first tile of each group
   __shared__ int warp_tot[kGtThreads / 32];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smem_s = smem_u32(smem);
@@ -215,67 +174,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
   }
 
   // --- the plan: tiles per group (rows), or a regular grid of tiles (dW)
-  GtPlan<MODE> pl;
+  RowPlan pl;
+  DwPlan dw;
   const int j_dim = MODE == kProdDx ? g.K : g.N;
   pl.p_tiles = (j_dim + kGtP - 1) / kGtP;
-  pl.q_tiles = (g.K + kGtN - 1) / kGtN;
+  pl.stages = ((MODE == kProdDx ? g.N : g.K) + 63) / 64;
+  dw.p_tiles = pl.p_tiles;
+  dw.q_tiles = (g.K + kGtN - 1) / kGtN;
   if (MODE == kProdDw) {
-    pl.tiles = g.E * pl.p_tiles * pl.q_tiles;
-    pl.stages = 0;
-    for (int e = tid; e < g.E; e += kGtThreads)
-      if (blockIdx.x == 0 && group_bad(g, e)) atomicOr(g.status, kStatusRouting);
+    if (blockIdx.x == 0)
+      for (int e = tid; e < g.E; e += kGtThreads)
+        if (group_bad(g, e)) atomicOr(g.status, kStatusRouting);
   } else {
-    pl.stages = ((MODE == kProdDx ? g.N : g.K) + 63) / 64;
-    constexpr int kPer = (kGtGroups + kGtThreads - 1) / kGtThreads;
-    int cnt[kPer], run = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid * kPer + i;
-      cnt[i] = 0;
-      if (e < g.E) {
-        int r0, r1;
-        group_rows(g, e, r0, r1);
-        cnt[i] = (r1 - r0 + kGtN - 1) / kGtN * pl.p_tiles;
-        if (blockIdx.x == 0 && group_bad(g, e)) atomicOr(g.status, kStatusRouting);
-      }
-      run += cnt[i];
-    }
-    int incl = run;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += u;
-    }
-    if (lane == 31) warp_tot[warp] = incl;
-    __syncthreads();
-    int pos = incl - run;
-    for (int w = 0; w < warp; ++w) pos += warp_tot[w];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid * kPer + i;
-      if (e < g.E) start[e] = pos;
-      pos += cnt[i];
-      if (e == g.E - 1) start[g.E] = pos;
-    }
+    plan_groups<kGtN, kGtThreads>(g, pl.p_tiles, start, warp_tot);
   }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers exist before either signals them
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  if (MODE != kProdDw) pl.tiles = start[g.E];
-  pl.S = 1;
-  if (MODE != kProdDw && pl.tiles < a.pairs && pl.tiles > 0) {
-    // slices of the sum: time in stages of the longest pair, six stages for what an item costs
-    // besides its stages and one for each partial that the last pair adds
-    int best = pl.stages + 6;
-    const int smax = min(min(pl.stages, 32), kGtSplitItems / pl.tiles);
-    for (int s = 2; s <= smax; ++s) {
-      const int waves = (pl.tiles * s + a.pairs - 1) / a.pairs;
-      const int cost = waves * ((pl.stages + s - 1) / s + 6) + s;
-      if (cost < best) { best = cost; pl.S = s; }
-    }
-  }
+  pl.tiles = MODE == kProdDw ? g.E * dw.p_tiles * dw.q_tiles : start[g.E];
+  pl.S = MODE == kProdDw ? 1 : plan_slices(pl.tiles, pl.stages, a.pairs);
+  auto item = [&](int w) { return MODE == kProdDw ? dw_item(g, dw, w) : row_item<kGtN, kGtGran>(g, pl, start, w); };
   const int items = pl.tiles * pl.S;
 
   if (warp == 0) {
@@ -283,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     if (lane == 0) {
       uint32_t k = 0;
       for (int w = pair; w < items; w += a.pairs) {
-        const GtItem it = gt_item<MODE>(a, pl, start, w);
+        const ProdItem it = item(w);
         const int half = gt_half<MODE>(it.n);
         int r0 = 0, r1 = 0;
         if (MODE == kProdDw) group_rows(g, it.e, r0, r1);
@@ -313,7 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
       const uint32_t bf = g.in_type == kBf16 ? 1u : 0u;
       uint32_t k = 0, ic = 0;
       for (int w = pair; w < items; w += a.pairs) {
-        const GtItem it = gt_item<MODE>(a, pl, start, w);
+        const ProdItem it = item(w);
         if (it.t0 >= it.t1) continue;  // (dW: a group without rows; the epilogue writes zeros)
         int r0 = 0, r1 = 0;
         if (MODE == kProdDw) group_rows(g, it.e, r0, r1);
@@ -351,10 +271,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     const int et = tid - kGtEpiWarp0 * 32;
     const uint32_t acc_empty_s = map_to_rank(smem_u32(acc_empty), 0);
     int32_t* counters = reinterpret_cast<int32_t*>(g.scratch);
-    float* partial = reinterpret_cast<float*>(g.scratch + 4096);
+    float* partial = reinterpret_cast<float*>(g.scratch + kProdCounterBytes);
     uint32_t ic = 0;
     for (int w = pair; w < items; w += a.pairs) {
-      const GtItem it = gt_item<MODE>(a, pl, start, w);
+      const ProdItem it = item(w);
       const int p = it.p0 + (int)rank * 128 + quarter * 32;  // this warp's first P row
       const bool none = it.t0 >= it.t1;
       const int acc = ic & 1;
@@ -474,6 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
                 stg128(static_cast<uint16_t*>(g.out) + (int64_t)(it.q0 + row) * g.out_ld + j, o);
             }
           }
+          __syncwarp();  // whole warps read tensor memory
         }
       }
       if (!none) {

@@ -75,6 +75,16 @@ __device__ __forceinline__ void umma2_f16_elect(uint32_t d, uint64_t a, uint64_t
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// The same of 32 E4M3 terms.
+__device__ __forceinline__ void umma2_f8_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
 // Arrive on the barrier at this offset in both CTAs once the MMAs issued so far are done.
 __device__ __forceinline__ void umma2_commit_elect(uint64_t* bar) {
   asm volatile(
@@ -97,6 +107,30 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+
+// 32 TMEM lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Two fp32 sums in a 64-bit register pair.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, uint32_t& lo, uint32_t& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+}
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
 }
 
 // Operand whose rows run along the sum's other dimension (contiguous along rows
@@ -127,13 +161,119 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return v;
 }
 
+// ---------------------------------------------------------------- work items
+// The tiles of a product by rows: a group of m rows has ceil(m / ROWS) row tiles,
+// each times the tiles of output features; with few tiles the sum is cut into S
+// slices.
+constexpr int kProdGroups = 1024;       // groups, at most
+constexpr int kProdFeatures = 256;      // output features of a tile
+constexpr int kProdTokenChunk = 8;      // row tiles that run next to each other through a group's features
+constexpr int kProdSplitItems = 160;    // items of a launch that splits sums, at most (sizes the scratch)
+constexpr int kProdCounterBytes = 4096; // scratch: arrival counters, then partial tiles
+
+struct RowPlan {
+  int tiles, S, stages, p_tiles;
+};
+struct ProdItem {
+  int e, p0, q0, n;  // expert, first feature (dW: column of dy), first row (dW: column of x), rows
+  int t0, t1;        // stages of the slice
+  int split, tile;
+};
+
+// First tile of each group into start[0 .. E]; all THREADS threads of the CTA.
+template <int ROWS, int THREADS>
+__device__ __forceinline__ void plan_groups(const ProdArgs& g, int p_tiles, int* start, int* warp_tot) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kPer = (kProdGroups + THREADS - 1) / THREADS;
+  int cnt[kPer], run = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = tid * kPer + i;
+    cnt[i] = 0;
+    if (e < g.E) {
+      int r0, r1;
+      group_rows(g, e, r0, r1);
+      cnt[i] = (r1 - r0 + ROWS - 1) / ROWS * p_tiles;
+      if (blockIdx.x == 0 && group_bad(g, e)) atomicOr(g.status, kStatusRouting);
+    }
+    run += cnt[i];
+  }
+  int incl = run;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) warp_tot[warp] = incl;
+  __syncthreads();
+  int pos = incl - run;
+  for (int w = 0; w < warp; ++w) pos += warp_tot[w];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = tid * kPer + i;
+    if (e < g.E) start[e] = pos;
+    pos += cnt[i];
+    if (e == g.E - 1) start[g.E] = pos;
+  }
+}
+
+// Slices of the sum, when there are fewer tiles than CTA pairs: time in stages of
+// the busiest pair, plus six stages for what an item costs besides its stages and
+// one for each partial that the last pair adds.
+__device__ __forceinline__ int plan_slices(int tiles, int stages, int pairs) {
+  int S = 1;
+  if (tiles < pairs && tiles > 0) {
+    int best = stages + 6;
+    const int smax = min(min(stages, 32), kProdSplitItems / tiles);
+    for (int s = 2; s <= smax; ++s) {
+      const int waves = (tiles * s + pairs - 1) / pairs;
+      const int cost = waves * ((stages + s - 1) / s + 6) + s;
+      if (cost < best) { best = cost; S = s; }
+    }
+  }
+  return S;
+}
+
+// Item w: its slice, then row tiles in chunks of kProdTokenChunk -- inside a chunk
+// row tiles fastest, then features, so that the tiles which run at one time share
+// rows and weights in L2.  A group's rows are cut into equal tiles, rounded to GRAN.
+template <int ROWS, int GRAN>
+__device__ __forceinline__ ProdItem row_item(const ProdArgs& g, const RowPlan& pl, const int* start, int w) {
+  ProdItem it;
+  it.tile = w / pl.S;
+  it.split = w - it.tile * pl.S;
+  // the group: the last e with start[e] <= tile
+  int lo = 0, hi = g.E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= it.tile) lo = mid;
+    else hi = mid - 1;
+  }
+  it.e = lo;
+  const int l = it.tile - start[lo];
+  int r0, r1;
+  group_rows(g, lo, r0, r1);
+  const int m = r1 - r0, nt = (m + ROWS - 1) / ROWS;
+  const int c = l / (kProdTokenChunk * pl.p_tiles), r = l - c * kProdTokenChunk * pl.p_tiles;
+  const int width = min(kProdTokenChunk, nt - c * kProdTokenChunk);
+  const int t = c * kProdTokenChunk + r % width;
+  it.p0 = (r / width) * kProdFeatures;
+  const int q = ((m + nt - 1) / nt + GRAN - 1) / GRAN * GRAN;
+  it.q0 = r0 + t * q;
+  it.n = min(q, r1 - it.q0);
+  it.t0 = (int)((int64_t)it.split * pl.stages / pl.S);
+  it.t1 = (int)((int64_t)(it.split + 1) * pl.stages / pl.S);
+  return it;
+}
+
 // ---------------------------------------------------------------- host
 // A tensor map of 2 or 3 dimensions (innermost first), 128-byte swizzle; strides in bytes of the outer ones.
 bool make_prod_map(CUtensorMap* m, int elem_type, const void* base, int nd, const uint64_t* dims,
                    const uint64_t* strides, const uint32_t* box);
 int prod_sm_count();  // of the current device; 0 on an error
 
-// Whether the tensor-core kernels can address these operands (16-byte rules).
+// The tensor-core kernels; *done stays false for operands that they cannot address (16-byte rules).
+cudaError_t launch_fp8_tc(const ProdArgs& g, cudaStream_t st, bool* done);
 cudaError_t launch_grouped_tc(const ProdArgs& g, int mode, cudaStream_t st, bool* done);
 
 }  // namespace moe
