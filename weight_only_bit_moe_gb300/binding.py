@@ -57,6 +57,8 @@ def load(path: str = ""):
     """Load the CUDA library (once).  Raises if it is missing: there is no fallback.
     MOE_W4A16_LIB overrides the library path (e.g. an alternative build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     path = path or os.environ.get("MOE_W4A16_LIB", LIB_PATH)
     with _lock:
         if _lib is None:
