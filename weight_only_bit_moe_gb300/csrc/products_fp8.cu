@@ -108,40 +108,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
 
   if (warp == kF8Producer) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      uint32_t k = 0;
-      for (int w = pair; w < items; w += a.pairs) {
-        const ProdItem it = row_item<C::kRows, C::kGran>(g, pl, start, w);
-        // boxes of 16 rows of x per CTA, and their rows' first
-        const int half = (it.n + 31) / 32 * 16;  // rows on N: rows per CTA
-        const int boxes = ROWS_M ? (f8_rows(it.n, rank) + 15) / 16 : half / 16;
-        const int both = ROWS_M ? (f8_rows(it.n, 0) + 15) / 16 + (f8_rows(it.n, 1) + 15) / 16 : 2 * boxes;
-        const int x0 = it.q0 + rank * (ROWS_M ? 128 : half);
-        const int w0 = it.p0 + rank * 128;
-        for (int t = it.t0; t < it.t1; ++t, ++k) {
-          const int s = k % C::kStages;
-          mbar_wait(&empty[s], ((k / C::kStages) + 1) & 1, abort_flag, g.status);
-          if (*abort_flag) break;
-          const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * 128 * 128 + both * 2048);
-          const uint32_t ps = smem_s + s * C::kSlot, qs = ps + C::kPBytes;
-          tma2_3d(ROWS_M ? qs : ps, &a.map_w, 128 * t, w0, it.e, bar);
-          const uint32_t xd = ROWS_M ? ps : qs;
-          if (ROWS_M && boxes == 8) {
-            tma2_2d(xd, &a.map_x, 128 * t, x0, bar);
-          } else {
-            for (int b = 0; b < boxes; ++b) tma2_2d(xd + 2048 * b, &a.map_xs, 128 * t, x0 + 16 * b, bar);
-          }
-        }
+    const uint32_t full_s = map_to_rank(smem_u32(full), 0);
+    uint32_t k = 0;
+    for (int w = pair; w < items; w += a.pairs) {
+      const ProdItem it = row_item<C::kRows, C::kGran>(g, pl, start, w);
+      // boxes of 16 rows of x per CTA, and their rows' first
+      const int half = (it.n + 31) / 32 * 16;  // rows on N: rows per CTA
+      const int boxes = ROWS_M ? (f8_rows(it.n, rank) + 15) / 16 : half / 16;
+      const int both = ROWS_M ? (f8_rows(it.n, 0) + 15) / 16 + (f8_rows(it.n, 1) + 15) / 16 : 2 * boxes;
+      const int x0 = it.q0 + rank * (ROWS_M ? 128 : half);
+      const int w0 = it.p0 + rank * 128;
+      for (int t = it.t0; t < it.t1; ++t, ++k) {
+        const int s = k % C::kStages;
+        mbar_wait(&empty[s], ((k / C::kStages) + 1) & 1, abort_flag, g.status);
         if (*abort_flag) break;
-      }
-      // leave no copy in flight (the leader's barriers count the peer's copies too)
-      if (rank == 0)
-        for (uint32_t i = 0; i < (uint32_t)C::kStages && i < k; ++i) {
-          const uint32_t u = k - 1 - i;
-          mbar_drain(&full[u % C::kStages], (u / C::kStages) & 1, g.status);
+        __syncwarp();
+        const uint32_t bar = full_s + 8 * s;
+        if (rank == 0) expect_tx_elect(&full[s], 2 * 128 * 128 + both * 2048);
+        const uint32_t ps = smem_s + s * C::kSlot, qs = ps + C::kPBytes;
+        tma2_3d(ROWS_M ? qs : ps, &a.map_w, 128 * t, w0, it.e, bar);
+        const uint32_t xd = ROWS_M ? ps : qs;
+        if (ROWS_M && boxes == 8) {
+          tma2_2d(xd, &a.map_x, 128 * t, x0, bar);
+        } else {
+          for (int b = 0; b < boxes; ++b) tma2_2d(xd + 2048 * b, &a.map_xs, 128 * t, x0 + 16 * b, bar);
         }
+      }
+      if (*abort_flag) break;
     }
+    // leave no copy in flight (the leader's barriers count the peer's copies too)
+    if (rank == 0)
+      for (uint32_t i = 0; i < (uint32_t)C::kStages && i < k; ++i) {
+        const uint32_t u = k - 1 - i;
+        mbar_drain(&full[u % C::kStages], (u / C::kStages) & 1, g.status);
+      }
   } else if (warp == kF8Mma) {
     // ------------------------------------------------------------ MMA issuer (leader)
     if (rank == 0) {

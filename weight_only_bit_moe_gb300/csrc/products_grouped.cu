@@ -20,8 +20,8 @@
 // CTA, six in flight.  Roles: one producer thread per CTA issues TMA, counted
 // by the leader's barrier; the leader's MMA warp issues; eight epilogue warps
 // per CTA drain one of two TMEM accumulators while the MMAs fill the other.
-// Row tiles are fetched in boxes of 16 rows when they are short, so a decode
-// step moves the weights and little else.  dW's last stage of a group fetches
+// Row tiles are fetched in boxes as large as they are, so a decode step moves the
+// weights and little else.  dW's last stage of a group fetches
 // its rows by index (gather), rows past the group's end as zeros.
 //
 // When there are fewer tiles than CTA pairs the sum is cut into S slices, each a
@@ -47,10 +47,12 @@ constexpr int kGtOperandBytes = 128 * 128;              // 128 rows x 64 terms o
 constexpr int kGtStageBytes = 2 * kGtOperandBytes;      // P and Q
 
 struct GroupedTcArgs {
-  CUtensorMap map_p, map_q;    // full boxes
-  CUtensorMap map_ps, map_qs;  // rows: 16-row boxes of Q; dW: single rows of both, for gathers
+  CUtensorMap map_p;
+  CUtensorMap map_q[4];  // by row: boxes of 128, 64, 32 and 16 rows of Q; dW: [0] boxes of both, and
+                         // single rows for gathers, [1] of P and [2] of Q
   ProdArgs g;
-  int pairs;                   // CTA pairs of the launch
+  int pairs;             // CTA pairs of the launch
+  int blocked;           // operands stored MN-major have whole blocks of 64 columns: one box brings two
   int wide_store;              // 32-byte stores are aligned
 };
 
@@ -84,45 +86,63 @@ __device__ __forceinline__ ProdItem dw_item(const ProdArgs& g, const DwPlan& pl,
   return it;
 }
 
-// One CTA's share of a stage into `slot` (P at +0, Q at +kGtOperandBytes).
-template <int MODE>
-__device__ __forceinline__ void gt_load_stage(const GroupedTcArgs& a, const ProdItem& it, int t, uint32_t rank,
-                                              int half, int boxes, int r0, int r1, uint32_t slot, uint32_t bar) {
-  const int p = it.p0 + (int)rank * 128;
-  const uint32_t qs = slot + kGtOperandBytes;
-  if (MODE == kProdDw) {
-    const int row = r0 + 64 * t, v = min(64, r1 - row);
-    const int q = it.q0 + (int)rank * half;
-    if (v == 64) {
-      tma2_2d(slot, &a.map_p, p, row, bar);
-      tma2_2d(slot + 8192, &a.map_p, p + 64, row, bar);
-      tma2_2d(qs, &a.map_q, q, row, bar);
-      if (half > 64) tma2_2d(qs + 8192, &a.map_q, q + 64, row, bar);
-    } else {
-      const int fours = (v + 15) / 16 * 4;
-      for (int i = 0; i < fours; ++i) {
-        const int b = row + 4 * i, none = a.g.rows;  // one past the last row: outside the tensor
-        const int4 r = make_int4(b < r1 ? b : none, b + 1 < r1 ? b + 1 : none, b + 2 < r1 ? b + 2 : none,
-                                 b + 3 < r1 ? b + 3 : none);
-        tma2_gather4(slot + 512 * i, &a.map_ps, p, r, bar);
-        tma2_gather4(slot + 8192 + 512 * i, &a.map_ps, p + 64, r, bar);
-        tma2_gather4(qs + 512 * i, &a.map_qs, q, r, bar);
-        if (half > 64) tma2_gather4(qs + 8192 + 512 * i, &a.map_qs, q + 64, r, bar);
-      }
-    }
-    return;
+// The last rows [row, r1) of a group, fewer than 64, of `blocks` blocks of 64
+// columns: rows up to a multiple of 16 are fetched, those at or past r1 as zeros
+// (row `none` lies outside the tensor).
+__device__ __forceinline__ void gt_gather(const CUtensorMap* map, int col, int blocks, int row, int r1, int none,
+                                          uint32_t slot, uint32_t bar) {
+  const int fours = (r1 - row + 15) / 16 * 4;
+  for (int i = 0; i < fours; ++i) {
+    const int b = row + 4 * i;
+    const int4 r = make_int4(b < r1 ? b : none, b + 1 < r1 ? b + 1 : none, b + 2 < r1 ? b + 2 : none,
+                             b + 3 < r1 ? b + 3 : none);
+    for (int c = 0; c < blocks; ++c) tma2_gather4(slot + 8192 * c + 512 * i, map, col + 64 * c, r, bar);
   }
+}
+
+// One CTA's share of a stage of P and of Q.
+template <int MODE>
+__device__ __forceinline__ void gt_load_p(const GroupedTcArgs& a, const ProdItem& it, int t, int p, int row, int r1,
+                                          uint32_t slot, uint32_t bar) {
   if (MODE == kProdFwd) {
     tma2_3d(slot, &a.map_p, 64 * t, p, it.e, bar);
+  } else if (MODE == kProdDx) {
+    if (a.blocked) {
+      tma2_4d(slot, &a.map_p, 0, 64 * t, p / 64, it.e, bar);
+    } else {
+      tma2_3d(slot, &a.map_p, p, 64 * t, it.e, bar);
+      tma2_3d(slot + 8192, &a.map_p, p + 64, 64 * t, it.e, bar);
+    }
+  } else if (r1 - row < 64) {
+    gt_gather(&a.map_q[1], p, 2, row, r1, a.g.rows, slot, bar);
+  } else if (a.blocked) {
+    tma2_3d(slot, &a.map_p, 0, row, p / 64, bar);
   } else {
-    tma2_3d(slot, &a.map_p, p, 64 * t, it.e, bar);
-    tma2_3d(slot + 8192, &a.map_p, p + 64, 64 * t, it.e, bar);
+    tma2_2d(slot, &a.map_p, p, row, bar);
+    tma2_2d(slot + 8192, &a.map_p, p + 64, row, bar);
   }
-  const int q = it.q0 + (int)rank * half;
-  if (boxes == 8) {
-    tma2_2d(qs, &a.map_q, 64 * t, q, bar);
+}
+template <int MODE>
+__device__ __forceinline__ void gt_load_q(const GroupedTcArgs& a, int t, int q, int half, int row, int r1,
+                                          uint32_t slot, uint32_t bar) {
+  if (MODE != kProdDw) {
+    // rows in boxes of 128, or of 64, 32 and 16
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int box = 128 >> i;
+      if (half & box) {
+        tma2_2d(slot + 128 * at, &a.map_q[i], 64 * t, q + at, bar);
+        at += box;
+      }
+    }
+  } else if (r1 - row < 64) {
+    gt_gather(&a.map_q[2], q, 2, row, r1, a.g.rows, slot, bar);
+  } else if (a.blocked) {
+    tma2_3d(slot, &a.map_q[0], 0, row, q / 64, bar);
   } else {
-    for (int b = 0; b < boxes; ++b) tma2_2d(qs + 2048 * b, &a.map_qs, 64 * t, q + 16 * b, bar);
+    tma2_2d(slot, &a.map_q[0], q, row, bar);
+    tma2_2d(slot + 8192, &a.map_q[0], q + 64, row, bar);
   }
 }
 
@@ -136,7 +156,7 @@ __device__ __forceinline__ int gt_half(int n) {
 // Bytes that both CTAs' loads of stage t bring.
 template <int MODE>
 __device__ __forceinline__ uint32_t gt_stage_bytes(int half, int v) {
-  if (MODE == kProdDw) return 2u * (uint32_t)(v == 64 ? 64 : (v + 15) / 16 * 16) * 128u * (half > 64 ? 4u : 3u);
+  if (MODE == kProdDw) return 2u * (uint32_t)(v == 64 ? 64 : (v + 15) / 16 * 16) * 128u * 4u;
   return 2u * (uint32_t)(kGtOperandBytes + half * 128);
 }
 
@@ -158,7 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&misc[1]);
   const ProdArgs& g = a.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_rank();
+  const int rank = (int)cluster_rank();
   const int pair = blockIdx.x >> 1;
 
   if (tid == 0) {
@@ -197,34 +217,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
   pl.S = MODE == kProdDw ? 1 : plan_slices(pl.tiles, pl.stages, a.pairs);
   auto item = [&](int w) { return MODE == kProdDw ? dw_item(g, dw, w) : row_item<kGtN, kGtGran>(g, pl, start, w); };
   const int items = pl.tiles * pl.S;
+  const uint32_t full_s = map_to_rank(smem_u32(full), 0);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      uint32_t k = 0;
-      for (int w = pair; w < items; w += a.pairs) {
-        const ProdItem it = item(w);
-        const int half = gt_half<MODE>(it.n);
-        int r0 = 0, r1 = 0;
-        if (MODE == kProdDw) group_rows(g, it.e, r0, r1);
-        for (int t = it.t0; t < it.t1; ++t, ++k) {
-          const int s = k % kGtStages;
-          mbar_wait(&empty[s], ((k / kGtStages) + 1) & 1, abort_flag, g.status);
-          if (*abort_flag) break;
-          if (rank == 0)
-            mbar_arrive_expect_tx(&full[s], gt_stage_bytes<MODE>(half, min(64, r1 - (r0 + 64 * t))));
-          gt_load_stage<MODE>(a, it, t, rank, half, half / 16, r0, r1, smem_s + s * kGtStageBytes,
-                              map_to_rank(smem_u32(&full[s]), 0));
-        }
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ producers of P (warp 0) and Q (warp 2)
+    uint32_t k = 0;
+    for (int w = pair; w < items; w += a.pairs) {
+      const ProdItem it = item(w);
+      const int half = gt_half<MODE>(it.n);
+      int r0 = 0, r1 = 0;
+      if (MODE == kProdDw) group_rows(g, it.e, r0, r1);
+      const int p = it.p0 + rank * 128, q = it.q0 + rank * half;
+      for (int t = it.t0; t < it.t1; ++t, ++k) {
+        const int s = k % kGtStages, row = r0 + 64 * t;
+        mbar_wait(&empty[s], ((k / kGtStages) + 1) & 1, abort_flag, g.status);
         if (*abort_flag) break;
-      }
-      // leave no copy in flight (the leader's barriers count the peer's copies too)
-      if (rank == 0)
-        for (uint32_t i = 0; i < (uint32_t)kGtStages && i < k; ++i) {
-          const uint32_t u = k - 1 - i;
-          mbar_drain(&full[u % kGtStages], (u / kGtStages) & 1, g.status);
+        __syncwarp();
+        const uint32_t slot = smem_s + s * kGtStageBytes, bar = full_s + 8 * s;
+        if (warp == 0) {
+          if (rank == 0) expect_tx_elect(&full[s], gt_stage_bytes<MODE>(half, min(64, r1 - row)));
+          gt_load_p<MODE>(a, it, t, p, row, r1, slot, bar);
+        } else {
+          gt_load_q<MODE>(a, t, q, half, row, r1, slot + kGtOperandBytes, bar);
         }
+      }
+      if (*abort_flag) break;
     }
+    // leave no copy in flight (the leader's barriers count the peer's copies too)
+    if (rank == 0 && warp == 0)
+      for (uint32_t i = 0; i < (uint32_t)kGtStages && i < k; ++i) {
+        const uint32_t u = k - 1 - i;
+        mbar_drain(&full[u % kGtStages], (u / kGtStages) & 1, g.status);
+      }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
     if (rank == 0) {
@@ -275,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     uint32_t ic = 0;
     for (int w = pair; w < items; w += a.pairs) {
       const ProdItem it = item(w);
-      const int p = it.p0 + (int)rank * 128 + quarter * 32;  // this warp's first P row
+      const int p = it.p0 + rank * 128 + quarter * 32;  // this warp's first P row
       const bool none = it.t0 >= it.t1;
       const int acc = ic & 1;
       if (!none) {
@@ -373,8 +397,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
                   h[u] = g.out_type == kBf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
                 }
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                  if (8 * b < cols) stg128(dst + 8 * b, make_uint4(h[4 * b], h[4 * b + 1], h[4 * b + 2], h[4 * b + 3]));
+                for (int b = 0; b < 2; ++b) {
+                  const uint32_t o[8] = {h[8 * b], h[8 * b + 1], h[8 * b + 2], h[8 * b + 3],
+                                         h[8 * b + 4], h[8 * b + 5], h[8 * b + 6], h[8 * b + 7]};
+                  if (a.wide_store && 16 * b + 16 <= cols) {
+                    stg256(dst + 16 * b, o);
+                  } else {
+                    if (16 * b < cols) stg128(dst + 16 * b, make_uint4(o[0], o[1], o[2], o[3]));
+                    if (16 * b + 8 < cols) stg128(dst + 16 * b + 8, make_uint4(o[4], o[5], o[6], o[7]));
+                  }
+                }
               }
             }
           } else {
@@ -432,8 +464,8 @@ bool make_prod_map(CUtensorMap* m, int elem_type, const void* base, int nd, cons
                    const uint64_t* strides, const uint32_t* box) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = prod_map_encoder();
   if (!enc) return false;
-  cuuint64_t d[3], s[2];
-  cuuint32_t b[3], es[3] = {1u, 1u, 1u};
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4], es[4] = {1u, 1u, 1u, 1u};
   for (int i = 0; i < nd; ++i) d[i] = dims[i], b[i] = box[i];
   for (int i = 0; i + 1 < nd; ++i) s[i] = strides[i];
   const CUtensorMapDataType t = elem_type == kBf16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -489,27 +521,46 @@ cudaError_t launch_grouped_tc(const ProdArgs& g, int mode, cudaStream_t st, bool
   GroupedTcArgs a;
   a.g = g;
   const uint64_t ald = (uint64_t)g.a_ld * 2, wld = (uint64_t)g.w_ld * 2;
+  const uint64_t N = (uint64_t)g.N, K = (uint64_t)g.K, rows = (uint64_t)g.rows, E = (uint64_t)g.E;
+  const int ty = g.in_type;
   bool ok;
   if (mode == kProdDw) {
-    const uint64_t dp[2] = {(uint64_t)g.N, (uint64_t)g.rows}, dq[2] = {(uint64_t)g.K, (uint64_t)g.rows};
+    a.blocked = g.N % 64 == 0 && g.K % 64 == 0;
+    const uint64_t dp[2] = {N, rows}, dq[2] = {K, rows};
     const uint32_t box[2] = {64, 64}, one[2] = {64, 1};
-    ok = make_prod_map(&a.map_p, g.in_type, g.a, 2, dp, &ald, box) && make_prod_map(&a.map_q, g.in_type, g.w, 2, dq, &wld, box) &&
-         make_prod_map(&a.map_ps, g.in_type, g.a, 2, dp, &ald, one) && make_prod_map(&a.map_qs, g.in_type, g.w, 2, dq, &wld, one);
+    ok = make_prod_map(&a.map_q[1], ty, g.a, 2, dp, &ald, one) && make_prod_map(&a.map_q[2], ty, g.w, 2, dq, &wld, one);
+    if (a.blocked) {
+      const uint64_t bp[3] = {64, rows, N / 64}, bq[3] = {64, rows, K / 64}, sp[2] = {ald, 128}, sq[2] = {wld, 128};
+      const uint32_t two[3] = {64, 64, 2};
+      ok = ok && make_prod_map(&a.map_p, ty, g.a, 3, bp, sp, two) && make_prod_map(&a.map_q[0], ty, g.w, 3, bq, sq, two);
+    } else {
+      ok = ok && make_prod_map(&a.map_p, ty, g.a, 2, dp, &ald, box) && make_prod_map(&a.map_q[0], ty, g.w, 2, dq, &wld, box);
+    }
+    a.map_q[3] = a.map_q[2];
   } else {
-    const uint64_t dw[3] = {(uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.E};
-    const uint64_t sw[2] = {wld, g.E > 1 ? (uint64_t)g.w_se * 2 : wld};
-    const uint32_t boxw[3] = {64, mode == kProdFwd ? 128u : 64u, 1};
-    const uint64_t da[2] = {(uint64_t)(mode == kProdFwd ? g.K : g.N), (uint64_t)g.rows};
-    const uint32_t box[2] = {64, 128}, small[2] = {64, 16};
-    ok = make_prod_map(&a.map_p, g.in_type, g.w, 3, dw, sw, boxw) && make_prod_map(&a.map_q, g.in_type, g.a, 2, da, &ald, box) &&
-         make_prod_map(&a.map_qs, g.in_type, g.a, 2, da, &ald, small);
-    a.map_ps = a.map_qs;
+    a.blocked = mode == kProdDx && g.K % 64 == 0;
+    const uint64_t we = g.E > 1 ? (uint64_t)g.w_se * 2 : wld;
+    if (a.blocked) {
+      const uint64_t d[4] = {64, N, K / 64, E}, st4[3] = {wld, 128, we};
+      const uint32_t two[4] = {64, 64, 2, 1};
+      ok = make_prod_map(&a.map_p, ty, g.w, 4, d, st4, two);
+    } else {
+      const uint64_t d[3] = {K, N, E}, st3[2] = {wld, we};
+      const uint32_t box[3] = {64, mode == kProdFwd ? 128u : 64u, 1};
+      ok = make_prod_map(&a.map_p, ty, g.w, 3, d, st3, box);
+    }
+    const uint64_t da[2] = {mode == kProdFwd ? K : N, rows};
+    for (int i = 0; i < 4 && ok; ++i) {
+      const uint32_t box[2] = {64, 128u >> i};
+      ok = make_prod_map(&a.map_q[i], ty, g.a, 2, da, &ald, box);
+    }
   }
   if (!ok) return cudaSuccess;  // (the plain kernel takes what a tensor map cannot describe)
   const int sms = prod_sm_count();
   if (sms < 2) return cudaErrorInvalidDevice;
   a.pairs = sms / 2;
-  a.wide_store = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0 && g.out_ld % 8 == 0 && g.out_se % 8 == 0;
+  const int per32 = g.out_type == kFp32 ? 8 : 16;  // elements of 32 bytes
+  a.wide_store = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0 && g.out_ld % per32 == 0 && g.out_se % per32 == 0;
   *done = true;
   if (mode == kProdFwd) return launch_mode<kProdFwd>(a, st);
   if (mode == kProdDx) return launch_mode<kProdDx>(a, st);
