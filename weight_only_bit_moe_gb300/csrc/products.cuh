@@ -70,6 +70,8 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, int type, float v
   else static_cast<float*>(p)[i] = v;
 }
 
+int prod_sm_count();  // of the current device; 0 on an error
+
 cudaError_t launch_products_any(const ProdArgs& g, int mode, cudaStream_t st);
 
 }  // namespace moe

@@ -291,7 +291,6 @@ __device__ __forceinline__ ProdItem row_item(const ProdArgs& g, const RowPlan& p
 // A tensor map of 2 to 4 dimensions (innermost first), 128-byte swizzle; strides in bytes of the outer ones.
 bool make_prod_map(CUtensorMap* m, int elem_type, const void* base, int nd, const uint64_t* dims,
                    const uint64_t* strides, const uint32_t* box);
-int prod_sm_count();  // of the current device; 0 on an error
 
 // The tensor-core kernels; *done stays false for operands that they cannot address (16-byte rules).
 cudaError_t launch_fp8_tc(const ProdArgs& g, cudaStream_t st, bool* done);

@@ -1,13 +1,19 @@
 // FP8 quantisation of activation rows in blocks of 1 x 128 (moe_products.h):
 //   v = x[row]  or  silu(gate) * up,   s = max(max |v| / 448, 2^-126),
 //   q = e4m3_rn(v * (1 / s)).
-// One warp per block of 128 columns, four columns per lane, one pass: the
-// values stay in registers between the maximum and the rounding.
+// A stream: two bytes in (four when gated), one out, a scale per 128.  Sixteen
+// lanes hold a block, eight values each, so every load is 16 bytes and every
+// store 8; a warp takes up to 1024 columns of a row at a time with all their
+// loads in flight before the first maximum.  The values stay in registers
+// between the maximum and the rounding.  Operands off the 16-byte grid run a
+// form of the same with single elements.
 #include "products.cuh"
 
 namespace moe {
 
 constexpr int kQuThreads = 256;
+constexpr int kQuWarps = kQuThreads / 32;
+constexpr int kQuCtas = 5;  // resident on an SM
 
 struct QuantArgs {
   const void* x;
@@ -21,13 +27,156 @@ struct QuantArgs {
   int64_t s_m, s_g;
 };
 
+// silu(g) * u in fp32.  exp(-g) = 2^(t + l), t = fp32(-g log2 e) and l what that
+// rounding left out: 2^t on the special-function unit, times 1 + l ln 2.  The
+// quotient is within 2 ulp, and 0 where exp(-g) passes 2^126.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+  const float t = g * -kLog2e, l = fmaf(g, -kLog2e, -t);
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmin_nan(t, 127.5f)));
+  return __fdividef(g, 1.0f + fmaf(e, l * kLn2, e)) * u;
+}
+
+// Scale of a block whose largest magnitude is `top`.
+__device__ __forceinline__ float block_scale(float top) { return fmax_nan(__fdiv_rn(top, 448.0f), 1.17549435e-38f); }
+
+__device__ __forceinline__ void widen8(const uint4& u, int type, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (type == kBf16) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
+// The largest magnitude of each block, for a warp whose lanes 0-15 and 16-31 hold
+// eight values of a block of each chunk.  Lanes trade chunks as they reduce, so a
+// lane ends up with the maximum of chunk mine(lane) of its half: half the
+// exchanges, and one division per lane for all chunks.
+//
+// Plain rows: the magnitudes' bits order like the values (NaN above infinity), so
+// 16-bit integer maxima do, two chunks in one register.  Four chunks: lanes with
+// bit 3 take chunks 2 and 3; bit 2 tells which of the two the lane answers for.
+__device__ __forceinline__ int mine4(int lane) { return ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1); }
+__device__ __forceinline__ float block_max4(const uint4 (&in)[4], int lane, int type) {
+  uint32_t m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    const uint32_t p = max_u16x2(max_u16x2(in[i].x & kAbs, in[i].y & kAbs), max_u16x2(in[i].z & kAbs, in[i].w & kAbs));
+    m[i] = max(p & 0xFFFFu, p >> 16);
+  }
+  const uint32_t lo = m[0] | (m[1] << 16), hi = m[2] | (m[3] << 16);
+  const bool up = lane & 8;
+  uint32_t v = max_u16x2(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, 8));
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v = max_u16x2(v, __shfl_xor_sync(0xffffffffu, v, o));
+  v = lane & 4 ? v >> 16 : v & 0xFFFFu;
+  return type == kBf16 ? __uint_as_float(v << 16) : __half2float(__ushort_as_half((uint16_t)v));
+}
+// Gated rows: fp32 values, two chunks; lanes with bit 3 answer for chunk 1.
+__device__ __forceinline__ int mine2(int lane) { return (lane >> 3) & 1; }
+__device__ __forceinline__ float block_max2(const float (&v)[2][8], int lane) {
+  float m[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    m[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m[i] = fmax_nan(m[i], fabsf(v[i][j]));
+  }
+  const bool up = lane & 8;
+  float t = fmax_nan(up ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, up ? m[0] : m[1], 8));
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) t = fmax_nan(t, __shfl_xor_sync(0xffffffffu, t, o));
+  return t;
+}
+
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float r) {
+  uint32_t o[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float2 lo = make_float2(__fmul_rn(v[4 * h], r), __fmul_rn(v[4 * h + 1], r));
+    const float2 hi = make_float2(__fmul_rn(v[4 * h + 2], r), __fmul_rn(v[4 * h + 3], r));
+    o[h] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
+           ((uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16);
+  }
+  return make_uint2(o[0], o[1]);
+}
+
+// A warp takes kChunks chunks of 256 columns of one row at a time: enough 16-byte
+// loads in flight to stream, few enough registers for five CTAs on an SM.
 template <bool GATED>
-__global__ void __launch_bounds__(kQuThreads) quant_block_kernel(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(kQuThreads, kQuCtas) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
+  constexpr int kChunks = GATED ? 2 : 4;
+  const int lane = threadIdx.x & 31;
+  const uint32_t per_row = (a.K + 256 * kChunks - 1) / (256 * kChunks);
+  const uint32_t units = a.rows * per_row;  // (fits: checked by the caller)
+  for (uint32_t u = blockIdx.x * kQuWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kQuWarps) {
+    const int row = u / per_row, c0 = (u - row * per_row) * 256 * kChunks;
+    const int src = a.row_index ? __ldg(a.row_index + row) : row;
+    const bool live = (unsigned)src < (unsigned)a.x_rows;
+    const uint16_t* x = static_cast<const uint16_t*>(a.x) + (int64_t)(live ? src : 0) * a.x_ld + c0 + 8 * lane;
+    const int left = a.K - c0 - 8 * lane;  // columns from this lane's first on
+    uint4 in[kChunks], up[GATED ? kChunks : 1];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      in[i] = make_uint4(0, 0, 0, 0);
+      if (GATED) up[i] = make_uint4(0, 0, 0, 0);
+      if (live && left > 256 * i) {
+        in[i] = __ldg(reinterpret_cast<const uint4*>(x + 256 * i));
+        if (GATED) up[i] = __ldg(reinterpret_cast<const uint4*>(x + a.K + 256 * i));
+      }
+    }
+    float v[GATED ? 2 : 1][8], top;
+    int mine;
+    if constexpr (GATED) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float w[8];
+        widen8(in[i], a.type, v[i]);
+        widen8(up[i], a.type, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = silu_mul(v[i][j], w[j]);
+      }
+      top = block_max2(v, lane);
+      mine = mine2(lane);
+    } else {
+      top = block_max4(in, lane, a.type);
+      mine = mine4(lane);
+    }
+    const float s = block_scale(top), r = __frcp_rn(s);
+    // one lane of those that hold the block's scale stores it
+    const int block = (c0 >> 7) + 2 * mine + (lane >> 4);
+    if ((lane & (GATED ? 7 : 3)) == 0 && 128 * block < a.K) a.scale[row * a.s_m + block * a.s_g] = s;
+    uint8_t* q = a.q + (int64_t)row * a.q_ld + c0 + 8 * lane;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      // chunk i's reciprocal from the first lane of this half that holds it
+      const int from = (lane & 16) + (GATED ? 8 * i : 8 * (i >> 1) + 4 * (i & 1));
+      const float ri = __shfl_sync(0xffffffffu, r, from);
+      if constexpr (!GATED) widen8(in[i], a.type, v[0]);
+      if (left > 256 * i) *reinterpret_cast<uint2*>(q + 256 * i) = codes8(v[GATED ? i : 0], ri);
+    }
+  }
+}
+
+// Any alignment: a warp per block, four columns per lane.
+template <bool GATED>
+__global__ void __launch_bounds__(kQuThreads) quant_any_kernel(const __grid_constant__ QuantArgs a) {
   const int lane = threadIdx.x & 31;
   const int blocks = (a.K + 127) / 128;
   const int64_t total = (int64_t)a.rows * blocks;
-  const int64_t step = (int64_t)gridDim.x * (kQuThreads / 32);
-  for (int64_t u = (int64_t)blockIdx.x * (kQuThreads / 32) + (threadIdx.x >> 5); u < total; u += step) {
+  const int64_t step = (int64_t)gridDim.x * kQuWarps;
+  for (int64_t u = (int64_t)blockIdx.x * kQuWarps + (threadIdx.x >> 5); u < total; u += step) {
     const int row = (int)(u / blocks), b = (int)(u % blocks);
     const int src = a.row_index ? a.row_index[row] : row;
     const bool live = (unsigned)src < (unsigned)a.x_rows;
@@ -39,13 +188,13 @@ __global__ void __launch_bounds__(kQuThreads) quant_block_kernel(const __grid_co
       if (live && c < a.K) {
         const int64_t at = (int64_t)src * a.x_ld + c;
         v[i] = load_elem(a.x, at, a.type);
-        if (GATED) v[i] = __fmul_rn(__fdiv_rn(v[i], __fadd_rn(1.0f, expf(-v[i]))), load_elem(a.x, at + a.K, a.type));
+        if (GATED) v[i] = silu_mul(v[i], load_elem(a.x, at + a.K, a.type));
       }
       top = fmax_nan(top, fabsf(v[i]));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float s = fmax_nan(__fdiv_rn(top, 448.0f), 1.17549435e-38f), r = __frcp_rn(s);
+    const float s = block_scale(top), r = __frcp_rn(s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = b * 128 + 4 * lane + i;
@@ -54,6 +203,19 @@ __global__ void __launch_bounds__(kQuThreads) quant_block_kernel(const __grid_co
     }
     if (lane == 0) a.scale[row * a.s_m + b * a.s_g] = s;
   }
+}
+
+template <bool GATED>
+static void launch_quant(const QuantArgs& a, int sms, cudaStream_t st) {
+  const int cols = GATED ? 512 : 1024;  // columns a warp takes at a time
+  const int64_t units = (int64_t)a.rows * ((a.K + cols - 1) / cols);
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.x) & 15) | (reinterpret_cast<uintptr_t>(a.q) & 7)) == 0 &&
+                    a.x_ld % 8 == 0 && a.q_ld % 8 == 0 && a.K % 8 == 0 && units < ((int64_t)1 << 31);
+  const int64_t work = wide ? units : (int64_t)a.rows * ((a.K + 127) / 128);
+  const int64_t ctas = (work + kQuWarps - 1) / kQuWarps, most = (int64_t)sms * (wide ? kQuCtas : 8);
+  const int grid = (int)(ctas < most ? ctas : most);
+  if (wide) quant_rows_kernel<GATED><<<grid, kQuThreads, 0, st>>>(a);
+  else quant_any_kernel<GATED><<<grid, kQuThreads, 0, st>>>(a);
 }
 
 }  // namespace moe
@@ -68,15 +230,11 @@ extern "C" int moe_quant_fp8_block(int dtype, const void* x, int64_t x_stride, i
   if (x_stride < (int64_t)K * (gated ? 2 : 1) || q_stride < K || (!row_index && rows != x_rows)) return MOE_ERR_INVALID;
   if (rows == 0) return MOE_OK;
   if ((!x && x_rows > 0) || !q || !scale || (reinterpret_cast<uintptr_t>(x) & 1)) return MOE_ERR_INVALID;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MOE_ERR_CUDA;
-  QuantArgs a{x, x_stride, x_rows, row_index, rows, K, dtype, static_cast<uint8_t*>(q), q_stride, scale,
-              scale_stride_m, scale_stride_g};
-  const int64_t blocks = (int64_t)rows * ((K + 127) / 128);
-  const int64_t want = (blocks + kQuThreads / 32 - 1) / (kQuThreads / 32);
-  const int ctas = (int)(want < sms * 8 ? want : sms * 8);
-  if (gated) quant_block_kernel<true><<<ctas, kQuThreads, 0, (cudaStream_t)stream>>>(a);
-  else quant_block_kernel<false><<<ctas, kQuThreads, 0, (cudaStream_t)stream>>>(a);
+  const int sms = prod_sm_count();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  const QuantArgs a{x, x_stride, x_rows, row_index, rows, K, dtype, static_cast<uint8_t*>(q), q_stride, scale,
+                    scale_stride_m, scale_stride_g};
+  if (gated) launch_quant<true>(a, sms, (cudaStream_t)stream);
+  else launch_quant<false>(a, sms, (cudaStream_t)stream);
   return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

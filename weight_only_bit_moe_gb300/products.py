@@ -202,7 +202,7 @@ def quant_fp8_block(x: torch.Tensor, rows: Optional[torch.Tensor] = None, gated:
                     out: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None, stream=None):
     """(q, scale): rows of x (those that the int32 index `rows` names, in its order) as E4M3 with one fp32
     scale per 128 columns; gated: of silu(x[:, :K]) * x[:, K:] with K half of x's columns.  scale has shape
-    [rows, ceil(K / 128)] and, made here, the blocks outermost in memory."""
+    [rows, ceil(K / 128)], in any strides."""
     dev = x.device
     _on(dev, rows=rows, out=out, scale=scale)
     dt = _half("quant_fp8_block", x)
@@ -223,7 +223,7 @@ def quant_fp8_block(x: torch.Tensor, rows: Optional[torch.Tensor] = None, gated:
     elif out.dtype != torch.float8_e4m3fn:
         raise ValueError(f"out: {out.dtype}, expected float8_e4m3fn")
     if scale is None:
-        scale = torch.empty((G, R), dtype=torch.float32, device=dev).t()
+        scale = torch.empty((R, G), dtype=torch.float32, device=dev)
     elif scale.dtype != torch.float32 or tuple(scale.shape) != (R, G):
         raise ValueError(f"scale: {scale.dtype} {tuple(scale.shape)}, expected float32 [{R}, {G}]")
     out_ld = _matrix(out, "out", K, R)
