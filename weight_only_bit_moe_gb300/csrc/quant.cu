@@ -7,7 +7,7 @@
 // loads in flight before the first maximum.  The values stay in registers
 // between the maximum and the rounding.  Operands off the 16-byte grid run a
 // form of the same with single elements.
-#include "products.cuh"
+#include "products_tc.cuh"
 
 namespace moe {
 
@@ -27,25 +27,51 @@ struct QuantArgs {
   int64_t s_m, s_g;
 };
 
-// silu(g) * u in fp32.  exp(-g) = 2^(t + l), t = fp32(-g log2 e) and l what that
-// rounding left out: 2^t on the special-function unit, times 1 + l ln 2.  The
-// quotient is within 2 ulp, and 0 where exp(-g) passes 2^126.
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
-  const float t = g * -kLog2e, l = fmaf(g, -kLog2e, -t);
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmin_nan(t, 127.5f)));
-  return __fdividef(g, 1.0f + fmaf(e, l * kLn2, e)) * u;
+// silu(g) * u in fp32, two values at a time.  exp(-g) = 2^(t + l), t = fp32(-g log2 e)
+// and l what that rounding left out: 2^t on the special-function unit, times 1 + l ln 2.
+// The reciprocal of 1 + exp(-g) is within an ulp, and 0 where that passes 2^126.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t both(float v) { return pack2(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ void silu_mul2(float& g0, float& g1, float u0, float u1) {
+  const uint64_t g = pack2(__float_as_uint(g0), __float_as_uint(g1));
+  const uint64_t t = mul2(g, both(-1.44269504f));
+  uint64_t l = t;  // minus what t left out
+  fma2(l, g, both(1.44269504f));
+  l = mul2(l, both(-0.693147181f));
+  uint32_t t0, t1;
+  unpack2(t, t0, t1);
+  float e0, e1;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fmin_nan(__uint_as_float(t0), 127.5f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fmin_nan(__uint_as_float(t1), 127.5f)));
+  uint64_t e = pack2(__float_as_uint(e0), __float_as_uint(e1)), d = e;
+  fma2(d, e, l);
+  fma2(d, both(1.0f), both(1.0f));
+  uint32_t d0, d1;
+  unpack2(d, d0, d1);
+  float r0, r1;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(__uint_as_float(d0)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(__uint_as_float(d1)));
+  const uint64_t v = mul2(mul2(g, pack2(__float_as_uint(r0), __float_as_uint(r1))),
+                          pack2(__float_as_uint(u0), __float_as_uint(u1)));
+  uint32_t v0, v1;
+  unpack2(v, v0, v1);
+  g0 = __uint_as_float(v0);
+  g1 = __uint_as_float(v1);
 }
 
 // Scale of a block whose largest magnitude is `top`.
 __device__ __forceinline__ float block_scale(float top) { return fmax_nan(__fdiv_rn(top, 448.0f), 1.17549435e-38f); }
 
-__device__ __forceinline__ void widen8(const uint4& u, int type, float (&v)[8]) {
+template <int TYPE>
+__device__ __forceinline__ void widen8(const uint4& u, float (&v)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (type == kBf16) {
+    if (TYPE == kBf16) {
       v[2 * i] = __uint_as_float(w[i] << 16);
       v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     } else {
@@ -56,7 +82,11 @@ __device__ __forceinline__ void widen8(const uint4& u, int type, float (&v)[8]) 
   }
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 
 // The largest magnitude of each block, for a warp whose lanes 0-15 and 16-31 hold
 // eight values of a block of each chunk.  Lanes trade chunks as they reduce, so a
@@ -67,7 +97,8 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return _
 // 16-bit integer maxima do, two chunks in one register.  Four chunks: lanes with
 // bit 3 take chunks 2 and 3; bit 2 tells which of the two the lane answers for.
 __device__ __forceinline__ int mine4(int lane) { return ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1); }
-__device__ __forceinline__ float block_max4(const uint4 (&in)[4], int lane, int type) {
+template <int TYPE>
+__device__ __forceinline__ float block_max4(const uint4 (&in)[4], int lane) {
   uint32_t m[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -81,7 +112,7 @@ __device__ __forceinline__ float block_max4(const uint4 (&in)[4], int lane, int 
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) v = max_u16x2(v, __shfl_xor_sync(0xffffffffu, v, o));
   v = lane & 4 ? v >> 16 : v & 0xFFFFu;
-  return type == kBf16 ? __uint_as_float(v << 16) : __half2float(__ushort_as_half((uint16_t)v));
+  return TYPE == kBf16 ? __uint_as_float(v << 16) : __half2float(__ushort_as_half((uint16_t)v));
 }
 // Gated rows: fp32 values, two chunks; lanes with bit 3 answer for chunk 1.
 __device__ __forceinline__ int mine2(int lane) { return (lane >> 3) & 1; }
@@ -100,72 +131,86 @@ __device__ __forceinline__ float block_max2(const float (&v)[2][8], int lane) {
   return t;
 }
 
+__device__ __forceinline__ uint32_t codes4(const float (&v)[8], int i, uint64_t rr) {
+  uint32_t a, b, c, d, o;
+  unpack2(mul2(pack2(__float_as_uint(v[i]), __float_as_uint(v[i + 1])), rr), a, b);
+  unpack2(mul2(pack2(__float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])), rr), c, d);
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(o)
+      : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)), "f"(__uint_as_float(d)));
+  return o;
+}
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float r) {
-  uint32_t o[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float2 lo = make_float2(__fmul_rn(v[4 * h], r), __fmul_rn(v[4 * h + 1], r));
-    const float2 hi = make_float2(__fmul_rn(v[4 * h + 2], r), __fmul_rn(v[4 * h + 3], r));
-    o[h] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
-           ((uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16);
-  }
-  return make_uint2(o[0], o[1]);
+  const uint64_t rr = both(r);
+  return make_uint2(codes4(v, 0, rr), codes4(v, 4, rr));
 }
 
-// A warp takes kChunks chunks of 256 columns of one row at a time: enough 16-byte
-// loads in flight to stream, few enough registers for five CTAs on an SM.
-template <bool GATED>
-__global__ void __launch_bounds__(kQuThreads, kQuCtas) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
+// One warp, kChunks chunks of 256 columns of one row from column c0 on: enough
+// 16-byte loads in flight to stream, few enough registers for five CTAs on an SM.
+// WHOLE: every lane's columns lie inside the row and the row exists.
+template <bool GATED, int TYPE, bool WHOLE>
+__device__ __forceinline__ void quant_unit(const QuantArgs& a, int row, int src, int c0, int lane) {
   constexpr int kChunks = GATED ? 2 : 4;
-  const int lane = threadIdx.x & 31;
-  const uint32_t per_row = (a.K + 256 * kChunks - 1) / (256 * kChunks);
-  const uint32_t units = a.rows * per_row;  // (fits: checked by the caller)
-  for (uint32_t u = blockIdx.x * kQuWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kQuWarps) {
-    const int row = u / per_row, c0 = (u - row * per_row) * 256 * kChunks;
-    const int src = a.row_index ? __ldg(a.row_index + row) : row;
-    const bool live = (unsigned)src < (unsigned)a.x_rows;
-    const uint16_t* x = static_cast<const uint16_t*>(a.x) + (int64_t)(live ? src : 0) * a.x_ld + c0 + 8 * lane;
-    const int left = a.K - c0 - 8 * lane;  // columns from this lane's first on
-    uint4 in[kChunks], up[GATED ? kChunks : 1];
+  const bool live = WHOLE || (unsigned)src < (unsigned)a.x_rows;
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + (int64_t)(live ? src : 0) * a.x_ld + c0 + 8 * lane;
+  const int left = WHOLE ? 256 * kChunks : a.K - c0 - 8 * lane;  // columns from this lane's first on
+  uint4 in[kChunks], up[GATED ? kChunks : 1];
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
+  for (int i = 0; i < kChunks; ++i) {
+    if (WHOLE || (live && left > 256 * i)) {
+      in[i] = __ldg(reinterpret_cast<const uint4*>(x + 256 * i));
+      if (GATED) up[i] = __ldg(reinterpret_cast<const uint4*>(x + a.K + 256 * i));
+    } else {
       in[i] = make_uint4(0, 0, 0, 0);
       if (GATED) up[i] = make_uint4(0, 0, 0, 0);
-      if (live && left > 256 * i) {
-        in[i] = __ldg(reinterpret_cast<const uint4*>(x + 256 * i));
-        if (GATED) up[i] = __ldg(reinterpret_cast<const uint4*>(x + a.K + 256 * i));
-      }
     }
-    float v[GATED ? 2 : 1][8], top;
-    int mine;
-    if constexpr (GATED) {
+  }
+  float v[GATED ? 2 : 1][8], top;
+  int mine;
+  if constexpr (GATED) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float w[8];
-        widen8(in[i], a.type, v[i]);
-        widen8(up[i], a.type, w);
+    for (int i = 0; i < 2; ++i) {
+      float w[8];
+      widen8<TYPE>(in[i], v[i]);
+      widen8<TYPE>(up[i], w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = silu_mul(v[i][j], w[j]);
-      }
-      top = block_max2(v, lane);
-      mine = mine2(lane);
-    } else {
-      top = block_max4(in, lane, a.type);
-      mine = mine4(lane);
+      for (int j = 0; j < 8; j += 2) silu_mul2(v[i][j], v[i][j + 1], w[j], w[j + 1]);
     }
-    const float s = block_scale(top), r = __frcp_rn(s);
-    // one lane of those that hold the block's scale stores it
-    const int block = (c0 >> 7) + 2 * mine + (lane >> 4);
-    if ((lane & (GATED ? 7 : 3)) == 0 && 128 * block < a.K) a.scale[row * a.s_m + block * a.s_g] = s;
-    uint8_t* q = a.q + (int64_t)row * a.q_ld + c0 + 8 * lane;
+    top = block_max2(v, lane);
+    mine = mine2(lane);
+  } else {
+    top = block_max4<TYPE>(in, lane);
+    mine = mine4(lane);
+  }
+  const float s = block_scale(top), r = __frcp_rn(s);
+  // one lane of those that hold the block's scale stores it
+  const int block = (c0 >> 7) + 2 * mine + (lane >> 4);
+  if ((lane & (GATED ? 7 : 3)) == 0 && (WHOLE || 128 * block < a.K)) a.scale[row * a.s_m + block * a.s_g] = s;
+  uint8_t* q = a.q + (int64_t)row * a.q_ld + c0 + 8 * lane;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      // chunk i's reciprocal from the first lane of this half that holds it
-      const int from = (lane & 16) + (GATED ? 8 * i : 8 * (i >> 1) + 4 * (i & 1));
-      const float ri = __shfl_sync(0xffffffffu, r, from);
-      if constexpr (!GATED) widen8(in[i], a.type, v[0]);
-      if (left > 256 * i) *reinterpret_cast<uint2*>(q + 256 * i) = codes8(v[GATED ? i : 0], ri);
-    }
+  for (int i = 0; i < kChunks; ++i) {
+    // chunk i's reciprocal from the first lane of this half that holds it
+    const int from = (lane & 16) + (GATED ? 8 * i : 8 * (i >> 1) + 4 * (i & 1));
+    const float ri = __shfl_sync(0xffffffffu, r, from);
+    if constexpr (!GATED) widen8<TYPE>(in[i], v[0]);
+    if (WHOLE || left > 256 * i) *reinterpret_cast<uint2*>(q + 256 * i) = codes8(v[GATED ? i : 0], ri);
+  }
+}
+
+template <bool GATED, int TYPE>
+__global__ void __launch_bounds__(kQuThreads, kQuCtas) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
+  constexpr int kCols = GATED ? 512 : 1024;
+  const int lane = threadIdx.x & 31;
+  const uint32_t per_row = (a.K + kCols - 1) / kCols;
+  const uint32_t units = a.rows * per_row;  // (fits: checked by the caller)
+  for (uint32_t u = blockIdx.x * kQuWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kQuWarps) {
+    const int row = u / per_row, c0 = (u - row * per_row) * kCols;
+    const int src = a.row_index ? __ldg(a.row_index + row) : row;
+    if (c0 + kCols <= a.K && (unsigned)src < (unsigned)a.x_rows) quant_unit<GATED, TYPE, true>(a, row, src, c0, lane);
+    else quant_unit<GATED, TYPE, false>(a, row, src, c0, lane);
   }
 }
 
@@ -188,7 +233,10 @@ __global__ void __launch_bounds__(kQuThreads) quant_any_kernel(const __grid_cons
       if (live && c < a.K) {
         const int64_t at = (int64_t)src * a.x_ld + c;
         v[i] = load_elem(a.x, at, a.type);
-        if (GATED) v[i] = silu_mul(v[i], load_elem(a.x, at + a.K, a.type));
+        if (GATED) {
+          float unused = 0.0f;
+          silu_mul2(v[i], unused, load_elem(a.x, at + a.K, a.type), 0.0f);
+        }
       }
       top = fmax_nan(top, fabsf(v[i]));
     }
@@ -212,9 +260,11 @@ static void launch_quant(const QuantArgs& a, int sms, cudaStream_t st) {
   const bool wide = ((reinterpret_cast<uintptr_t>(a.x) & 15) | (reinterpret_cast<uintptr_t>(a.q) & 7)) == 0 &&
                     a.x_ld % 8 == 0 && a.q_ld % 8 == 0 && a.K % 8 == 0 && units < ((int64_t)1 << 31);
   const int64_t work = wide ? units : (int64_t)a.rows * ((a.K + 127) / 128);
-  const int64_t ctas = (work + kQuWarps - 1) / kQuWarps, most = (int64_t)sms * (wide ? kQuCtas : 8);
+  // up to sixteen rounds of CTAs are left to the hardware's balance
+  const int64_t ctas = (work + kQuWarps - 1) / kQuWarps, most = (int64_t)sms * (wide ? kQuCtas : 8) * 16;
   const int grid = (int)(ctas < most ? ctas : most);
-  if (wide) quant_rows_kernel<GATED><<<grid, kQuThreads, 0, st>>>(a);
+  if (wide && a.type == kBf16) quant_rows_kernel<GATED, kBf16><<<grid, kQuThreads, 0, st>>>(a);
+  else if (wide) quant_rows_kernel<GATED, kFp16><<<grid, kQuThreads, 0, st>>>(a);
   else quant_any_kernel<GATED><<<grid, kQuThreads, 0, st>>>(a);
 }
 
