@@ -22,81 +22,118 @@ from . import binding as B
 
 BLOCK = 128  # columns per FP8 scale; also rows of a weight block
 _DTYPE = {torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_FP16, torch.float32: B.MOE_FP32}
-_HALF = (torch.bfloat16, torch.float16)
 
 # One workspace per device and stream, as the kernels of one stream run one after another.
 _workspaces = {}
 
 
 def _handle(device: torch.device, stream) -> int:
+    """CUDA handle of the stream (default: the device's current one)."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _workspace(device: torch.device, handle: int) -> torch.Tensor:
+def _workspace(device: torch.device, handle: int) -> int:
+    """Address of the workspace of this device and stream."""
     ws = _workspaces.get((device.index, handle))
     if ws is None:
         ws = torch.zeros(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
         # the zeros are written on the current stream, the kernels run on `handle`
         torch.cuda.current_stream(device).synchronize()
         _workspaces[(device.index, handle)] = ws
-    return ws
+    return ws.data_ptr()
+
+
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """An output of a kernel that runs on `stream`, from that stream's memory."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def products_status(device="cuda", stream=None) -> int:
     """Synchronises the stream and returns (and clears) the device status of its products:
     MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_INVALID (offsets that decrease or leave the rows)."""
-    device = torch.device("cuda", torch.cuda.current_device()) if str(device) == "cuda" else torch.device(device)
+    device = torch.device(device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
     handle = _handle(device, stream)
     return B.moe_get_status(_workspace(device, handle), handle)
 
 
-def _matrix(t: torch.Tensor, name: str, width: Optional[int] = None, rows: Optional[int] = None) -> int:
-    """Row stride of a 2-D row-major matrix of `width` columns."""
-    if t.dim() != 2 or (width is not None and t.shape[1] != width) or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{'rows' if rows is None else rows}, "
-                         f"{'columns' if width is None else width}]")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+# The checks below read each attribute of a tensor once: for a decode step they are most of a call's host time.
+
+def _rows(t: torch.Tensor, name: str, width: int, rows: int) -> int:
+    """Row stride of a row-major matrix of that shape."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != width:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [{rows}, {width}]")
+    s0, s1 = t.stride()
+    if s1 != 1 and width > 1:
         raise ValueError(f"{name}: the columns of a row must be contiguous (strides {t.stride()})")
-    if t.shape[0] <= 1:
-        return max(t.stride(0), t.shape[1])
-    if t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
-    return t.stride(0)
+    if s0 < width:
+        if rows > 1:
+            raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+        return width
+    return s0
 
 
-def _bank(t: torch.Tensor, name: str) -> Tuple[int, int]:
+def _bank(t: torch.Tensor, name: str, shape) -> Tuple[int, int]:
     """(expert, row) strides of a bank [E, N, K]."""
-    if t.dim() != 3:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [experts, N, K]")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and shape[2] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous (strides {t.stride()})")
-    row = t.stride(1) if t.shape[1] > 1 else max(t.stride(1), t.shape[2])
-    if row < t.shape[2]:
-        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
-    return t.stride(0), row
+    if s1 < shape[2]:
+        if shape[1] > 1:
+            raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+        return s0, shape[2]
+    return s0, s1
 
 
-def _on(device: torch.device, **tensors) -> None:
+def _dims(t: torch.Tensor, name: str, dims: int):
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected {dims} dimensions")
+    return shape
+
+
+def _on(device: torch.device, *tensors: Optional[torch.Tensor]) -> None:
     if device.type != "cuda":
         raise ValueError(f"the products run on a GPU, not on {device}")
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+            raise ValueError(f"tensors on {device} and {t.device}")
 
 
 def _check_offsets(offsets: torch.Tensor, E: int) -> None:
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != E + 1 or not offsets.is_contiguous():
+    if offsets.dtype is not torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
         raise ValueError(f"offsets: expected contiguous int32 [{E + 1}], got {offsets.dtype} {tuple(offsets.shape)}")
 
 
-def _half(name: str, *tensors: torch.Tensor) -> int:
-    dtype = tensors[0].dtype
-    if dtype not in _HALF or any(t.dtype != dtype for t in tensors):
+def _half(name: str, dtype: torch.dtype, *others: torch.dtype) -> int:
+    if dtype is torch.bfloat16:
+        code = B.MOE_BF16
+    elif dtype is torch.float16:
+        code = B.MOE_FP16
+    else:
+        code = None
+    for o in others:
+        if o is not dtype:
+            code = None
+    if code is None:
         raise ValueError(f"{name}: operands of one type, bfloat16 or float16, expected; got "
-                         f"{', '.join(str(t.dtype) for t in tensors)}")
-    return _DTYPE[dtype]
+                         f"{', '.join(str(d) for d in (dtype, *others))}")
+    return code
+
+
+def _call(name: str, *args) -> None:
+    rc = getattr(B.load(), name)(*args)
+    if rc != B.MOE_OK:
+        raise B.MoeError(name, rc)
 
 
 def expert_order(topk_ids: torch.Tensor, num_experts: int, expert_base: int = 0):
@@ -113,42 +150,41 @@ def expert_order(topk_ids: torch.Tensor, num_experts: int, expert_base: int = 0)
     return order, offsets
 
 
+def _by_row(fn: str, name: str, a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+            out: Optional[torch.Tensor], stream, forward: bool) -> torch.Tensor:
+    dev = a.device
+    _on(dev, w, offsets, out)
+    shape = _dims(w, "w", 3)
+    E, N, K = shape
+    rows = _dims(a, name, 2)[0]
+    width, out_width = (K, N) if forward else (N, K)
+    w_e, w_n = _bank(w, "w", shape)
+    ld = _rows(a, name, width, rows)
+    _check_offsets(offsets, E)
+    dtype = a.dtype
+    if out is None:
+        code = _half(fn, dtype, w.dtype)
+        out = _empty((rows, out_width), dtype, dev, stream)
+        out_ld = out_width
+    else:
+        code = _half(fn, dtype, w.dtype, out.dtype)
+        out_ld = _rows(out, "out", out_width, rows)
+    h = _handle(dev, stream)
+    _call(fn, code, a.data_ptr(), ld, w.data_ptr(), w_e, w_n, offsets.data_ptr(), E, rows, N, K, out.data_ptr(),
+          out_ld, _workspace(dev, h), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    return out
+
+
 def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
     """y[r] = w[e] x[r] for the rows r of expert e: x [rows, K], w [E, N, K] -> [rows, N]."""
-    dev = x.device
-    _on(dev, w=w, offsets=offsets, out=out)
-    w_e, w_n = _bank(w, "w")
-    E, N, K = w.shape
-    ld = _matrix(x, "x", K)
-    _check_offsets(offsets, E)
-    if out is None:
-        out = torch.empty((x.shape[0], N), dtype=x.dtype, device=dev)
-    dt = _half("grouped_mm", x, w, out)
-    out_ld = _matrix(out, "out", N, x.shape[0])
-    h = _handle(dev, stream)
-    B.moe_grouped_mm(dt, x, ld, w, w_e, w_n, offsets, E, x.shape[0], N, K, out, out_ld, _workspace(dev, h),
-                     B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
-    return out
+    return _by_row("moe_grouped_mm", "x", x, w, offsets, out, stream, True)
 
 
 def grouped_mm_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     """Gradient of grouped_mm by x: dx[r] = w[e]^T dy[r]; dy [rows, N], w [E, N, K] -> [rows, K]."""
-    dev = dy.device
-    _on(dev, w=w, offsets=offsets, out=out)
-    w_e, w_n = _bank(w, "w")
-    E, N, K = w.shape
-    ld = _matrix(dy, "dy", N)
-    _check_offsets(offsets, E)
-    if out is None:
-        out = torch.empty((dy.shape[0], K), dtype=dy.dtype, device=dev)
-    dt = _half("grouped_mm_dx", dy, w, out)
-    out_ld = _matrix(out, "out", K, dy.shape[0])
-    h = _handle(dev, stream)
-    B.moe_grouped_mm_dx(dt, dy, ld, w, w_e, w_n, offsets, E, dy.shape[0], N, K, out, out_ld, _workspace(dev, h),
-                        B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
-    return out
+    return _by_row("moe_grouped_mm_dx", "dy", dy, w, offsets, out, stream, False)
 
 
 def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -156,23 +192,32 @@ def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out:
     """Gradient of grouped_mm by w: dw[e] = sum over the rows of e of dy[r] x[r]^T; dy [rows, N], x [rows, K]
     -> [E, N, K], in out_dtype (the operands' type or float32).  accumulate adds to a float32 out."""
     dev = dy.device
-    _on(dev, x=x, offsets=offsets, out=out)
-    N, K, E = dy.shape[-1], x.shape[-1], offsets.shape[0] - 1
-    ld = _matrix(dy, "dy")
-    x_ld = _matrix(x, "x", None, dy.shape[0])
+    _on(dev, x, offsets, out)
+    rows, N = _dims(dy, "dy", 2)
+    K = _dims(x, "x", 2)[1]
+    E = _dims(offsets, "offsets", 1)[0] - 1
+    ld = _rows(dy, "dy", N, rows)
+    x_ld = _rows(x, "x", K, rows)
     _check_offsets(offsets, E)
-    dt = _half("grouped_mm_dw", dy, x)
-    if accumulate and (out is None or out.dtype != torch.float32):
+    dtype = dy.dtype
+    code = _half("grouped_mm_dw", dtype, x.dtype)
+    if out_dtype is None:
+        out_dtype = dtype if out is None else out.dtype
+    if out_dtype is not dtype and out_dtype is not torch.float32:
+        raise ValueError(f"grouped_mm_dw: {out_dtype} gradients, expected {dtype} or float32")
+    if accumulate and (out is None or out_dtype is not torch.float32):
         raise ValueError("grouped_mm_dw: accumulate needs a float32 out")
     if out is None:
-        out = torch.empty((E, N, K), dtype=out_dtype or dy.dtype, device=dev)
-    if tuple(out.shape) != (E, N, K) or out.dtype not in (dy.dtype, torch.float32) or (
-            out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError(f"out: {out.dtype} {tuple(out.shape)}, expected [{E}, {N}, {K}] of {out_dtype or dy.dtype}")
-    o_e, o_n = _bank(out, "out")
+        out = _empty((E, N, K), out_dtype, dev, stream)
+        o_e, o_n = N * K, K
+    else:
+        if tuple(out.shape) != (E, N, K) or out.dtype is not out_dtype:
+            raise ValueError(f"out: {out.dtype} {tuple(out.shape)}, expected {out_dtype} [{E}, {N}, {K}]")
+        o_e, o_n = _bank(out, "out", out.shape)
     h = _handle(dev, stream)
-    B.moe_grouped_mm_dw(dt, dy, ld, x, x_ld, offsets, E, dy.shape[0], N, K, _DTYPE[out.dtype], int(accumulate), out,
-                        o_e, o_n, _workspace(dev, h), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    _call("moe_grouped_mm_dw", code, dy.data_ptr(), ld, x.data_ptr(), x_ld, offsets.data_ptr(), E, rows, N, K,
+          code if out_dtype is dtype else B.MOE_FP32, int(accumulate), out.data_ptr(), o_e, o_n, _workspace(dev, h),
+          B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
     return out
 
 
@@ -204,64 +249,85 @@ def quant_fp8_block(x: torch.Tensor, rows: Optional[torch.Tensor] = None, gated:
     scale per 128 columns; gated: of silu(x[:, :K]) * x[:, K:] with K half of x's columns.  scale has shape
     [rows, ceil(K / 128)], in any strides."""
     dev = x.device
-    _on(dev, rows=rows, out=out, scale=scale)
-    dt = _half("quant_fp8_block", x)
-    ld = _matrix(x, "x")
-    K = x.shape[1]
+    _on(dev, rows, out, scale)
+    code = _half("quant_fp8_block", x.dtype)
+    x_rows, K = _dims(x, "x", 2)
+    ld = _rows(x, "x", K, x_rows)
     if gated:
         if K % 2:
             raise ValueError(f"x: {K} columns do not split into gate and up halves")
         K //= 2
-    R = x.shape[0]
+    R, index = x_rows, None
     if rows is not None:
-        if rows.dtype != torch.int32 or rows.dim() != 1 or not rows.is_contiguous():
+        if rows.dtype is not torch.int32 or rows.dim() != 1 or not rows.is_contiguous():
             raise ValueError(f"rows: expected a contiguous int32 vector, got {rows.dtype} {tuple(rows.shape)}")
-        R = rows.shape[0]
+        R, index = rows.shape[0], rows.data_ptr()
     G = -(-K // BLOCK)
     if out is None:
-        out = torch.empty((R, K), dtype=torch.float8_e4m3fn, device=dev)
-    elif out.dtype != torch.float8_e4m3fn:
-        raise ValueError(f"out: {out.dtype}, expected float8_e4m3fn")
+        out = _empty((R, K), torch.float8_e4m3fn, dev, stream)
+        out_ld = K
+    else:
+        if out.dtype is not torch.float8_e4m3fn:
+            raise ValueError(f"out: {out.dtype}, expected float8_e4m3fn")
+        out_ld = _rows(out, "out", K, R)
     if scale is None:
-        scale = torch.empty((R, G), dtype=torch.float32, device=dev)
-    elif scale.dtype != torch.float32 or tuple(scale.shape) != (R, G):
-        raise ValueError(f"scale: {scale.dtype} {tuple(scale.shape)}, expected float32 [{R}, {G}]")
-    out_ld = _matrix(out, "out", K, R)
-    B.moe_quant_fp8_block(dt, x, ld, x.shape[0], rows, R, K, int(gated), out, out_ld, scale,
-                          (scale.stride(0), scale.stride(1)), _handle(dev, stream))
+        scale = _empty((R, G), torch.float32, dev, stream)
+        s_m, s_g = G, 1
+    else:
+        if scale.dtype is not torch.float32 or tuple(scale.shape) != (R, G):
+            raise ValueError(f"scale: {scale.dtype} {tuple(scale.shape)}, expected float32 [{R}, {G}]")
+        s_m, s_g = scale.stride()
+    _call("moe_quant_fp8_block", code, x.data_ptr(), ld, x_rows, index, R, K, 1 if gated else 0, out.data_ptr(), out_ld,
+          scale.data_ptr(), s_m, s_g, _handle(dev, stream))
     return out, scale
 
 
 def gemm_fp8_block(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
                    offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-                   out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+                   out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """Block-scaled FP8 product: x [rows, K] with x_scale [rows, ceil(K / 128)], w [N, K] with w_scale
-    [ceil(N / 128), ceil(K / 128)] -> [rows, N]; with offsets, w and w_scale have a leading expert dimension
-    and the rows of expert e take w[e]."""
+    [ceil(N / 128), ceil(K / 128)] -> [rows, N] in out_dtype (bfloat16, float16 or float32; bfloat16 unless
+    out is given); with offsets, w and w_scale have a leading expert dimension and the rows of expert e take
+    w[e].  Scales may have any strides."""
     dev = x.device
-    _on(dev, x_scale=x_scale, w=w, w_scale=w_scale, offsets=offsets, out=out)
-    if offsets is None:
-        w, w_scale = w.unsqueeze(0), w_scale.unsqueeze(0)
-    if x.dtype != torch.float8_e4m3fn or w.dtype != torch.float8_e4m3fn:
+    _on(dev, x_scale, w, w_scale, offsets, out)
+    if x.dtype is not torch.float8_e4m3fn or w.dtype is not torch.float8_e4m3fn:
         raise ValueError(f"gemm_fp8_block: float8_e4m3fn operands expected, got {x.dtype} and {w.dtype}")
-    w_e, w_n = _bank(w, "w")
-    E, N, K = w.shape
-    ld = _matrix(x, "x", K)
-    R, G = x.shape[0], -(-K // BLOCK)
-    if x_scale.dtype != torch.float32 or tuple(x_scale.shape) != (R, G):
-        raise ValueError(f"x_scale: {x_scale.dtype} {tuple(x_scale.shape)}, expected float32 [{R}, {G}]")
-    if w_scale.dtype != torch.float32 or tuple(w_scale.shape) != (E, -(-N // BLOCK), G):
-        raise ValueError(f"w_scale: {w_scale.dtype} {tuple(w_scale.shape)}, expected float32 "
-                         f"[{E}, {-(-N // BLOCK)}, {G}]")
-    if offsets is not None:
+    if x_scale.dtype is not torch.float32 or w_scale.dtype is not torch.float32:
+        raise ValueError(f"gemm_fp8_block: float32 scales expected, got {x_scale.dtype} and {w_scale.dtype}")
+    if offsets is None:
+        N, K = _dims(w, "w", 2)
+        E, w_e, w_n = 1, 0, _rows(w, "w", K, N)
+        at = None
+    else:
+        shape = _dims(w, "w", 3)
+        E, N, K = shape
+        w_e, w_n = _bank(w, "w", shape)
         _check_offsets(offsets, E)
+        at = offsets.data_ptr()
+    R, G, GN = _dims(x, "x", 2)[0], -(-K // BLOCK), -(-N // BLOCK)
+    ld = _rows(x, "x", K, R)
+    if tuple(x_scale.shape) != (R, G):
+        raise ValueError(f"x_scale: {tuple(x_scale.shape)}, expected [{R}, {G}]")
+    if tuple(w_scale.shape) != ((GN, G) if offsets is None else (E, GN, G)):
+        raise ValueError(f"w_scale: {tuple(w_scale.shape)}, expected [{'' if offsets is None else f'{E}, '}{GN}, {G}]")
+    ws = w_scale.stride()
     if out is None:
-        out = torch.empty((R, N), dtype=out_dtype, device=dev)
-    if out.dtype not in _DTYPE:
-        raise ValueError(f"out: {out.dtype}, expected bfloat16, float16 or float32")
-    out_ld = _matrix(out, "out", N, R)
+        out_dtype = out_dtype or torch.bfloat16
+        code = _DTYPE.get(out_dtype)
+    else:
+        code = _DTYPE.get(out.dtype) if out_dtype is None or out_dtype is out.dtype else None
+    if code is None:
+        raise ValueError(f"gemm_fp8_block: out of {out_dtype if out is None else out.dtype}, expected bfloat16, "
+                         "float16 or float32 and, with out_dtype, that type")
+    if out is None:
+        out = _empty((R, N), out_dtype, dev, stream)
+        out_ld = N
+    else:
+        out_ld = _rows(out, "out", N, R)
+    s_m, s_g = x_scale.stride()
     h = _handle(dev, stream)
-    B.moe_gemm_fp8_block(x, ld, x_scale, (x_scale.stride(0), x_scale.stride(1)), w, (w_e, w_n), w_scale,
-                         w_scale.stride(), offsets, E, R, N, K, _DTYPE[out.dtype], out, out_ld, _workspace(dev, h),
-                         B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    _call("moe_gemm_fp8_block", x.data_ptr(), ld, x_scale.data_ptr(), s_m, s_g, w.data_ptr(), w_e, w_n,
+          w_scale.data_ptr(), 0 if offsets is None else ws[0], ws[-2], ws[-1], at, E, R, N, K, code, out.data_ptr(),
+          out_ld, _workspace(dev, h), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
     return out
