@@ -2,24 +2,28 @@
 //
 //   y[r, n] = sum_b xs[r, b] ws[n / 128, b] D_b[r, n],   D_b[r, n] = sum_{k in b} x[r, k] w[n, k]
 //
-// over blocks b of 128 terms, dense or grouped by expert.  A pair of CTAs
-// (cta_group::2) computes each D_b of its tile into tensor memory -- a stage of
-// the pipeline is one block, 128 bytes of every row -- and eight epilogue warps
-// per CTA add it, times its scale, to fp32 sums in registers while the MMAs fill
-// the next buffer.  Scales are arbitrary fp32, so D_b cannot stay in the tensor
-// core's accumulator over blocks; reading it back once per block is what bounds
-// the product where it is not memory.
+// over blocks b of 128 terms, dense or grouped by expert.  A CTA computes each D_b
+// of its tile into tensor memory -- a stage of the pipeline is one block, 128
+// bytes of every row -- and eight epilogue warps add it, times its scale, to fp32
+// sums in registers while the MMAs fill another buffer.  Scales are arbitrary
+// fp32, so D_b cannot stay in the tensor core's accumulator over blocks; the
+// hand-over of a buffer and the multiply-adds, 128 x 256 a block, are what bounds
+// the product where memory does not.
 //
 // Two orientations:
-//   rows on M (prompts): 256 rows x 256 features, a thread owns one row and the
+//   rows on M (prompts): 128 rows x 256 features, a thread owns one row and the
 //     128 features of one weight block: one scale per thread and block, taken as
 //     a scalar into packed fp32 multiply-adds.
-//   rows on N (decode): 256 features x up to 64 rows, a thread owns one feature
+//   rows on N (decode): 128 features x up to 64 rows, a thread owns one feature
 //     and 32 rows, whose scales it reads from shared memory.  The tile moves the
-//     weights once and costs the MMA round_up(rows, 32) / 256 of a full one.
+//     weights once.
 // With rows on N a 256-row tile would read 32 scales from shared memory for 128
 // sums, more than the shared memory delivers in the time of the block's MMAs;
 // with rows on M a tile of few rows would run the MMA nearly empty.
+//
+// Single CTAs, not the pairs of the 16-bit products: a buffer passes from the MMA
+// to the epilogue and back once a block, and across two CTAs that round trip took
+// longer than the block's MMAs.
 #include <atomic>
 
 #include "gemm.cuh"
@@ -33,14 +37,15 @@ constexpr int kF8FactorStages = 64;  // blocks whose scales are staged at a time
 
 template <bool ROWS_M>
 struct Fp8Cfg {
-  static constexpr int kRows = ROWS_M ? 256 : 64;  // rows of a tile
-  static constexpr int kGran = ROWS_M ? 16 : 32;
+  static constexpr int kRows = ROWS_M ? 128 : 64;       // rows of a tile
+  static constexpr int kFeatures = ROWS_M ? 256 : 128;  // features of a tile
+  static constexpr int kGran = 16;
   static constexpr int kAcc = ROWS_M ? 128 : 32;   // sums per thread
   static constexpr int kBufCols = ROWS_M ? 256 : 64, kBufs = ROWS_M ? 2 : 4;
   static constexpr int kPBytes = 128 * 128;
-  static constexpr int kQBytes = ROWS_M ? 128 * 128 : 32 * 128;
+  static constexpr int kQBytes = ROWS_M ? 256 * 128 : 64 * 128;
   static constexpr int kSlot = kPBytes + kQBytes;
-  static constexpr int kStages = ROWS_M ? 6 : 9;
+  static constexpr int kStages = ROWS_M ? 4 : 8;
   static constexpr int kBar = kStages * kSlot;
   static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 1;
   static constexpr int kMisc = kBar + kNumBars * 8;
@@ -51,175 +56,168 @@ struct Fp8Cfg {
 };
 
 struct Fp8TcArgs {
-  CUtensorMap map_x, map_xs;  // 128- and 16-row boxes of x
-  CUtensorMap map_w;          // 128-row boxes of a bank's expert
+  CUtensorMap map_x[4];  // boxes of 128, 64, 32 and 16 rows of x
+  CUtensorMap map_w;     // boxes of a tile's features
   ProdArgs g;
-  int pairs;
-  int wide_store;
+  int wide_store;        // 32-byte stores are aligned
 };
 
-// Rows of CTA `rank` of a tile with rows on M: valid ones, and those copied (whole boxes of 16).
-__device__ __forceinline__ int f8_rows(int n, int rank) { return min(max(n - rank * 128, 0), 128); }
-
 template <bool ROWS_M>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
-    fp8_tc_kernel(const __grid_constant__ Fp8TcArgs a) {
+__global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_constant__ Fp8TcArgs a) {
   using C = Fp8Cfg<ROWS_M>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ int start[kProdGroups + 1];
   __shared__ int warp_tot[kF8Threads / 32];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smem_s = smem_u32(smem);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBar);  // the leader's count both CTAs' copies
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBar);
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
-  uint64_t* acc_empty = acc_full + C::kBufs;  // the leader's
+  uint64_t* acc_empty = acc_full + C::kBufs;
   uint64_t* drain_bar = acc_empty + C::kBufs;
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kMisc);  // [0] tmem base, [1] abort, [2] last
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&misc[1]);
   const ProdArgs& g = a.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)cluster_rank();
-  const int pair = blockIdx.x >> 1;
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-    for (int i = 0; i < C::kBufs; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 2 * kF8EpiWarps); }
+    for (int i = 0; i < C::kBufs; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], kF8EpiWarps); }
     mbar_init(drain_bar, 1);
     misc[1] = 0;
     fence_mbar_init();
   }
   if (warp == kF8Mma) {
-    tmem_alloc2(&misc[0], 512);
-    tmem_relinquish2();
+    tmem_alloc(&misc[0], 512);
+    tmem_relinquish();
   }
   RowPlan pl;
-  pl.p_tiles = (g.N + kProdFeatures - 1) / kProdFeatures;
+  pl.p_tiles = (g.N + C::kFeatures - 1) / C::kFeatures;
   pl.stages = (g.K + 127) / 128;
   plan_groups<C::kRows, kF8Threads>(g, pl.p_tiles, start, warp_tot);
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // both CTAs' barriers exist before either signals them
   tc_fence_after();
   const uint32_t tmem = misc[0];
   pl.tiles = start[g.E];
-  pl.S = plan_slices(pl.tiles, pl.stages, a.pairs);
+  pl.S = plan_slices(pl.tiles, pl.stages, gridDim.x, 1);
   const int items = pl.tiles * pl.S;
 
   if (warp == kF8Producer) {
     // ------------------------------------------------------------ producer
-    const uint32_t full_s = map_to_rank(smem_u32(full), 0);
     uint32_t k = 0;
-    for (int w = pair; w < items; w += a.pairs) {
-      const ProdItem it = row_item<C::kRows, C::kGran>(g, pl, start, w);
-      // boxes of 16 rows of x per CTA, and their rows' first
-      const int half = (it.n + 31) / 32 * 16;  // rows on N: rows per CTA
-      const int boxes = ROWS_M ? (f8_rows(it.n, rank) + 15) / 16 : half / 16;
-      const int both = ROWS_M ? (f8_rows(it.n, 0) + 15) / 16 + (f8_rows(it.n, 1) + 15) / 16 : 2 * boxes;
-      const int x0 = it.q0 + rank * (ROWS_M ? 128 : half);
-      const int w0 = it.p0 + rank * 128;
+    for (int w = blockIdx.x; w < items; w += gridDim.x) {
+      const ProdItem it = row_item<C::kRows, C::kGran, C::kFeatures>(g, pl, start, w);
+      const int rows = (it.n + 15) / 16 * 16;  // copied
       for (int t = it.t0; t < it.t1; ++t, ++k) {
         const int s = k % C::kStages;
         mbar_wait(&empty[s], ((k / C::kStages) + 1) & 1, abort_flag, g.status);
         if (*abort_flag) break;
         __syncwarp();
-        const uint32_t bar = full_s + 8 * s;
-        if (rank == 0) expect_tx_elect(&full[s], 2 * 128 * 128 + both * 2048);
-        const uint32_t ps = smem_s + s * C::kSlot, qs = ps + C::kPBytes;
-        tma2_3d(ROWS_M ? qs : ps, &a.map_w, 128 * t, w0, it.e, bar);
+        const uint32_t bar = smem_u32(&full[s]), ps = smem_s + s * C::kSlot, qs = ps + C::kPBytes;
+        expect_tx_elect(&full[s], (C::kFeatures + rows) * 128);
+        tma1_3d(ROWS_M ? qs : ps, &a.map_w, 128 * t, it.p0, it.e, bar);
         const uint32_t xd = ROWS_M ? ps : qs;
-        if (ROWS_M && boxes == 8) {
-          tma2_2d(xd, &a.map_x, 128 * t, x0, bar);
-        } else {
-          for (int b = 0; b < boxes; ++b) tma2_2d(xd + 2048 * b, &a.map_xs, 128 * t, x0 + 16 * b, bar);
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int box = 128 >> i;
+          if (rows & box) {
+            tma1_2d(xd + 128 * at, &a.map_x[i], 128 * t, it.q0 + at, bar);
+            at += box;
+          }
         }
       }
       if (*abort_flag) break;
     }
-    // leave no copy in flight (the leader's barriers count the peer's copies too)
-    if (rank == 0)
-      for (uint32_t i = 0; i < (uint32_t)C::kStages && i < k; ++i) {
-        const uint32_t u = k - 1 - i;
-        mbar_drain(&full[u % C::kStages], (u / C::kStages) & 1, g.status);
-      }
-  } else if (warp == kF8Mma) {
-    // ------------------------------------------------------------ MMA issuer (leader)
-    if (rank == 0) {
-      uint32_t k = 0;
-      for (int w = pair; w < items; w += a.pairs) {
-        const ProdItem it = row_item<C::kRows, C::kGran>(g, pl, start, w);
-        // E4M3 operands and fp32 sums have the fields of fp16 operands and fp32 sums
-        const uint32_t idesc = idesc_f16_f32(256, ROWS_M ? 256 : (it.n + 31) / 32 * 32, 0u);
-        for (int t = it.t0; t < it.t1; ++t, ++k) {
-          const int s = k % C::kStages, b = k % C::kBufs;
-          mbar_wait(&acc_empty[b], ((k / C::kBufs) + 1) & 1, abort_flag, g.status);
-          mbar_wait(&full[s], (k / C::kStages) & 1, abort_flag, g.status);
-          __syncwarp();
-          tc_fence_after();
-          const uint64_t pd = smem_desc_sw128(smem_s + s * C::kSlot);
-          const uint64_t qd = smem_desc_sw128(smem_s + s * C::kSlot + C::kPBytes);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) umma2_f8_elect(tmem + b * C::kBufCols, pd + 2 * i, qd + 2 * i, idesc, i > 0);
-          umma2_commit_elect(&empty[s]);
-          umma2_commit_elect(&acc_full[b]);
-        }
-      }
-      umma2_commit_elect(drain_bar);
-      mbar_drain(drain_bar, 0, g.status);
-      __syncwarp();
+    // leave no copy in flight
+    for (uint32_t i = 0; i < (uint32_t)C::kStages && i < k; ++i) {
+      const uint32_t u = k - 1 - i;
+      mbar_drain(&full[u % C::kStages], (u / C::kStages) & 1, g.status);
     }
+  } else if (warp == kF8Mma) {
+    // ------------------------------------------------------------ MMA issuer
+    uint32_t k = 0;
+    for (int w = blockIdx.x; w < items; w += gridDim.x) {
+      const ProdItem it = row_item<C::kRows, C::kGran, C::kFeatures>(g, pl, start, w);
+      // E4M3 operands and fp32 sums have the fields of fp16 operands and fp32 sums
+      const uint32_t idesc = idesc_f16_f32(128, ROWS_M ? 256 : (it.n + 15) / 16 * 16, 0u);
+      for (int t = it.t0; t < it.t1; ++t, ++k) {
+        const int s = k % C::kStages, b = k % C::kBufs;
+        mbar_wait(&full[s], (k / C::kStages) & 1, abort_flag, g.status);
+        mbar_wait(&acc_empty[b], ((k / C::kBufs) + 1) & 1, abort_flag, g.status);
+        __syncwarp();
+        tc_fence_after();
+        umma1_f8_block_elect(tmem + b * C::kBufCols, smem_desc_sw128(smem_s + s * C::kSlot),
+                             smem_desc_sw128(smem_s + s * C::kSlot + C::kPBytes), idesc);
+        umma_commit_elect(&acc_full[b]);
+        umma_commit_elect(&empty[s]);
+      }
+    }
+    umma_commit_elect(drain_bar);
+    mbar_drain(drain_bar, 0, g.status);
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, sub = warp >> 2;  // TMEM lanes; half of the tile's columns
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t acc_empty_s = map_to_rank(smem_u32(acc_empty), 0);
     float* factors = reinterpret_cast<float*>(smem + C::kFactors);
     int32_t* counters = reinterpret_cast<int32_t*>(g.scratch);
     float4* partial = reinterpret_cast<float4*>(g.scratch + kProdCounterBytes);
     const int n_blocks = (g.N + 127) / 128;
     uint32_t k = 0;
-    for (int w = pair; w < items; w += a.pairs) {
-      const ProdItem it = row_item<C::kRows, C::kGran>(g, pl, start, w);
-      uint64_t sum[C::kAcc / 2];
+    for (int w = blockIdx.x; w < items; w += gridDim.x) {
+      const ProdItem it = row_item<C::kRows, C::kGran, C::kFeatures>(g, pl, start, w);
+      float sum[C::kAcc];
 #pragma unroll
-      for (int i = 0; i < C::kAcc / 2; ++i) sum[i] = 0;
+      for (int i = 0; i < C::kAcc; ++i) sum[i] = 0.0f;
       if (ROWS_M) {
-        // one row, the 128 features of one weight block: one scale a block, fetched two blocks ahead
-        const int r = rank * 128 + quarter * 32 + lane;
+        // one row, the 128 features of one weight block: one scale a block.  Its two factors are
+        // fetched two blocks ahead, two blocks at a time, and first touched when they are due.
+        const int r = quarter * 32 + lane;
         const int nb = min(it.p0 / 128 + sub, n_blocks - 1);
-        const float* xs = g.xs + (int64_t)(it.q0 + min(r, it.n - 1)) * g.xs_m;
-        const float* ws = g.ws + it.e * g.ws_e + nb * g.ws_n;
-        auto scale = [&](int t) { return t < it.t1 ? __ldg(xs + t * g.xs_g) * __ldg(ws + t * g.ws_k) : 0.0f; };
-        float s0 = scale(it.t0), s1 = scale(it.t0 + 1);
-        for (int t = it.t0; t < it.t1; ++t, ++k) {
-          const int b = k % C::kBufs;
-          const float s2 = scale(t + 2);
-          const uint64_t ss = pack2(__float_as_uint(s0), __float_as_uint(s0));
-          mbar_wait(&acc_full[b], (k / C::kBufs) & 1, abort_flag, g.status);
-          tc_fence_after();
-          const uint32_t tb = lanes + b * C::kBufCols + sub * 128;
-          uint32_t v[2][16];
-          tmem_ld16(tb, v[0]);
+        const float* xs = g.xs + (int64_t)(it.q0 + min(r, it.n - 1)) * g.xs_m + it.t0 * g.xs_g;
+        const float* ws = g.ws + it.e * g.ws_e + nb * g.ws_n + it.t0 * g.ws_k;
+        float x[2], y[2];
+        int ahead = it.t0;
+        auto fetch = [&](int i) {
+          x[i] = __ldg(xs), y[i] = __ldg(ws);
+          if (++ahead < it.t1) xs += g.xs_g, ws += g.ws_k;
+        };
+        fetch(0);
+        fetch(1);
+        for (int t = it.t0; t < it.t1; t += 2) {
+          const float s0 = x[0] * y[0], s1 = x[1] * y[1];
+          fetch(0);
+          fetch(1);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            tmem_ld_wait();
-            if (c < 7) {
-              tmem_ld16(tb + 16 * (c + 1), v[(c + 1) & 1]);  // arrives while this chunk is added
-            } else {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(acc_empty_s + 8 * b);
+          for (int h = 0; h < 2; ++h) {
+            if (t + h < it.t1) {
+              const int b = k % C::kBufs;
+              const float sc = h ? s1 : s0;
+              mbar_wait(&acc_full[b], (k / C::kBufs) & 1, abort_flag, g.status);
+              tc_fence_after();
+              const uint32_t tb = lanes + b * C::kBufCols + sub * 128;
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                uint32_t v[16];
+                tmem_ld16(tb + 16 * c, v);
+                tmem_ld_wait();
+                if (c == 7) {
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&acc_empty[b]);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[16 * c + i] = fmaf(__uint_as_float(v[i]), sc, sum[16 * c + i]);
+              }
+              ++k;
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) fma2(sum[8 * c + i], pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), ss);
           }
-          s0 = s1;
-          s1 = s2;
         }
       } else {
         // one feature, 32 rows
-        const int half = (it.n + 31) / 32 * 16;
-        const int nb = min((it.p0 + rank * 128) / 128, n_blocks - 1);
+        const int nb = it.p0 / 128;
         for (int t = it.t0; t < it.t1; ++t, ++k) {
           const int in = (t - it.t0) % kF8FactorStages;
           if (in == 0) {
@@ -237,21 +235,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
           mbar_wait(&acc_full[b], (k / C::kBufs) & 1, abort_flag, g.status);
           tc_fence_after();
           uint32_t v[32];
-          const bool live = 32 * sub < 2 * half;
+          const bool live = 32 * sub < it.n;
           if (live) {
             tmem_ld32(lanes + b * C::kBufCols + 32 * sub, v);
             tmem_ld_wait();
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(acc_empty_s + 8 * b);
+          if (lane == 0) mbar_arrive(&acc_empty[b]);
           if (live) {
             const uint32_t fs = smem_u32(factors) + (in * 64 + 32 * sub) * 4;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const uint4 f = lds128(fs + 16 * i);
-              fma2(sum[2 * i], pack2(v[4 * i], v[4 * i + 1]), pack2(f.x, f.y));
-              fma2(sum[2 * i + 1], pack2(v[4 * i + 2], v[4 * i + 3]), pack2(f.z, f.w));
+              sum[4 * i] = fmaf(__uint_as_float(v[4 * i]), __uint_as_float(f.x), sum[4 * i]);
+              sum[4 * i + 1] = fmaf(__uint_as_float(v[4 * i + 1]), __uint_as_float(f.y), sum[4 * i + 1]);
+              sum[4 * i + 2] = fmaf(__uint_as_float(v[4 * i + 2]), __uint_as_float(f.z), sum[4 * i + 2]);
+              sum[4 * i + 3] = fmaf(__uint_as_float(v[4 * i + 3]), __uint_as_float(f.w), sum[4 * i + 3]);
             }
           }
         }
@@ -259,18 +259,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
       bool finish = true;
       if (pl.S > 1) {
         // this thread's sums of the slice, in its own order
-        float4* mine = partial + (int64_t)((it.tile * pl.S + it.split) * 2 + rank) * (128 * 256 / 4) + tid;
+        float4* mine = partial + (int64_t)(it.tile * pl.S + it.split) * (128 * 256 / 4) + tid;
 #pragma unroll
         for (int i = 0; i < C::kAcc / 4; ++i) {
-          uint4 u;
-          unpack2(sum[2 * i], u.x, u.y);
-          unpack2(sum[2 * i + 1], u.z, u.w);
-          __stcg(reinterpret_cast<uint4*>(mine) + i * kF8EpiThreads, u);
+          __stcg(mine + i * kF8EpiThreads, make_float4(sum[4 * i], sum[4 * i + 1], sum[4 * i + 2], sum[4 * i + 3]));
         }
         named_bar_sync(1, kF8EpiThreads);
         if (tid == 0) {
           __threadfence();
-          const unsigned old = atomicInc(reinterpret_cast<unsigned*>(&counters[it.tile * 2 + rank]), (unsigned)(pl.S - 1));
+          const unsigned old = atomicInc(reinterpret_cast<unsigned*>(&counters[it.tile]), (unsigned)(pl.S - 1));
           misc[2] = old == (unsigned)(pl.S - 1) ? 1u : 0u;
           __threadfence();
         }
@@ -278,37 +275,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
         finish = misc[2] != 0;
         if (finish) {
 #pragma unroll
-          for (int i = 0; i < C::kAcc / 2; ++i) sum[i] = 0;
-          const uint64_t one = pack2(0x3F800000u, 0x3F800000u);
+          for (int i = 0; i < C::kAcc; ++i) sum[i] = 0.0f;
           for (int s = 0; s < pl.S; ++s) {
-            const float4* src = partial + (int64_t)((it.tile * pl.S + s) * 2 + rank) * (128 * 256 / 4) + tid;
+            const float4* src = partial + (int64_t)(it.tile * pl.S + s) * (128 * 256 / 4) + tid;
 #pragma unroll
             for (int i = 0; i < C::kAcc / 4; ++i) {
-              const uint4 u = __ldcg(reinterpret_cast<const uint4*>(src) + i * kF8EpiThreads);
-              fma2(sum[2 * i], pack2(u.x, u.y), one);
-              fma2(sum[2 * i + 1], pack2(u.z, u.w), one);
+              const float4 u = __ldcg(src + i * kF8EpiThreads);
+              sum[4 * i] += u.x, sum[4 * i + 1] += u.y, sum[4 * i + 2] += u.z, sum[4 * i + 3] += u.w;
             }
           }
         }
       }
       if (!finish) continue;
       if (ROWS_M) {
-        const int r = rank * 128 + quarter * 32 + lane;
+        const int r = quarter * 32 + lane;
         const int j0 = it.p0 + sub * 128;
         const int64_t at = (int64_t)(it.q0 + r) * g.out_ld + j0;
 #pragma unroll
         for (int c = 0; c < C::kAcc / 16; ++c) {  // sixteen features at a time
           const int left = r < it.n ? g.N - j0 - 16 * c : 0;
-          uint32_t v[16];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) unpack2(sum[8 * c + i], v[2 * i], v[2 * i + 1]);
+          const float* v = &sum[16 * c];
           if (left >= 16) {
             if (g.out_type == kFp32) {
               float* dst = static_cast<float*>(g.out) + at + 16 * c;
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t o[8] = {v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3],
-                                       v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]};
+                uint32_t o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(v[8 * h + i]);
                 if (a.wide_store) {
                   stg256(dst + 8 * h, o);
                 } else {
@@ -321,8 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
               uint32_t o[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float lo = __uint_as_float(v[2 * i]), hi = __uint_as_float(v[2 * i + 1]);
-                o[i] = g.out_type == kBf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+                o[i] = g.out_type == kBf16 ? pack_bf16x2(v[2 * i], v[2 * i + 1]) : pack_f16x2(v[2 * i], v[2 * i + 1]);
               }
               if (a.wide_store) {
                 stg256(dst, o);
@@ -334,20 +327,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              if (i < left) store_elem(g.out, at + 16 * c + i, g.out_type, __uint_as_float(v[i]));
+              if (i < left) store_elem(g.out, at + 16 * c + i, g.out_type, v[i]);
           }
         }
       } else {
         // 32 consecutive features of a row per store
-        const int j = it.p0 + rank * 128 + quarter * 32 + lane;
+        const int j = it.p0 + quarter * 32 + lane;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          uint32_t lo, hi;
-          unpack2(sum[i], lo, hi);
-          const int r = 32 * sub + 2 * i;
-          if (j < g.N && r < it.n) store_elem(g.out, (int64_t)(it.q0 + r) * g.out_ld + j, g.out_type, __uint_as_float(lo));
-          if (j < g.N && r + 1 < it.n)
-            store_elem(g.out, (int64_t)(it.q0 + r + 1) * g.out_ld + j, g.out_type, __uint_as_float(hi));
+        for (int i = 0; i < 32; ++i) {
+          const int r = 32 * sub + i;
+          if (j < g.N && r < it.n) store_elem(g.out, (int64_t)(it.q0 + r) * g.out_ld + j, g.out_type, sum[i]);
         }
       }
       __syncwarp();  // whole warps read tensor memory
@@ -355,13 +344,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // neither CTA leaves while the other may signal or read it
   tc_fence_after();
-  if (warp == kF8Mma) tmem_dealloc2(tmem, 512);
+  if (warp == kF8Mma) tmem_dealloc(tmem, 512);
 }
 
 template <bool ROWS_M>
-static cudaError_t launch_orientation(const Fp8TcArgs& a, cudaStream_t st) {
+static cudaError_t launch_orientation(const Fp8TcArgs& a, int sms, cudaStream_t st) {
   static std::atomic<bool> ready[64] = {};
   int dev = 0;
   cudaError_t rc = cudaGetDevice(&dev);
@@ -373,7 +361,7 @@ static cudaError_t launch_orientation(const Fp8TcArgs& a, cudaStream_t st) {
     if (rc != cudaSuccess) return rc;
     ready[dev].store(true, std::memory_order_release);
   }
-  fp8_tc_kernel<ROWS_M><<<2 * a.pairs, kF8Threads, bytes, st>>>(a);
+  fp8_tc_kernel<ROWS_M><<<sms, kF8Threads, bytes, st>>>(a);
   return cudaPeekAtLastError();
 }
 
@@ -386,24 +374,27 @@ cudaError_t launch_fp8_tc(const ProdArgs& g, cudaStream_t st, bool* done) {
   const int out_bytes = g.out_type == kFp32 ? 4 : 2;
   if (!grid16b(g.a, g.a_ld) || !grid16b(g.w, g.w_ld) || !grid16b(g.out, g.out_ld * out_bytes)) return cudaSuccess;
   if (g.E > 1 && (g.w_se % 16 != 0 || g.w_se <= 0)) return cudaSuccess;
-  if (((double)g.rows / 64 + g.E) * ((g.N + 255) / 256) > 1e9) return cudaSuccess;  // tile numbers are 32-bit
+  if (((double)g.rows / 64 + g.E) * ((g.N + 127) / 128) > 1e9) return cudaSuccess;  // tile numbers are 32-bit
+  // 64 rows an expert on average: up to there one or two tiles of 64 rows stream the weights at the
+  // memory's rate, above it the row tiles of the other orientation do not run emptier than the memory
+  const bool rows_m = g.rows > (int64_t)64 * g.E;
   Fp8TcArgs a;
   a.g = g;
   const uint64_t xd[2] = {(uint64_t)g.K, (uint64_t)g.rows}, xl = (uint64_t)g.a_ld;
   const uint64_t wd[3] = {(uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.E};
   const uint64_t wl[2] = {(uint64_t)g.w_ld, g.E > 1 ? (uint64_t)g.w_se : (uint64_t)g.w_ld};
-  const uint32_t box[2] = {128, 128}, small[2] = {128, 16}, wbox[3] = {128, 128, 1};
-  if (!make_prod_map(&a.map_x, kE4m3, g.a, 2, xd, &xl, box) || !make_prod_map(&a.map_xs, kE4m3, g.a, 2, xd, &xl, small) ||
-      !make_prod_map(&a.map_w, kE4m3, g.w, 3, wd, wl, wbox))
-    return cudaSuccess;  // (the plain kernel takes what a tensor map cannot describe)
+  const uint32_t wbox[3] = {128, rows_m ? 256u : 128u, 1};
+  bool ok = make_prod_map(&a.map_w, kE4m3, g.w, 3, wd, wl, wbox);
+  for (int i = 0; i < 4 && ok; ++i) {
+    const uint32_t box[2] = {128, 128u >> i};
+    ok = make_prod_map(&a.map_x[i], kE4m3, g.a, 2, xd, &xl, box);
+  }
+  if (!ok) return cudaSuccess;  // (the plain kernel takes what a tensor map cannot describe)
   const int sms = prod_sm_count();
-  if (sms < 2) return cudaErrorInvalidDevice;
-  a.pairs = sms / 2;
+  if (sms <= 0) return cudaErrorInvalidDevice;
   a.wide_store = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0 && g.out_ld * out_bytes % 32 == 0;
   *done = true;
-  // 64 rows an expert on average: up to there one or two tiles of 64 rows stream the weights at the
-  // memory's rate, above it the row tiles of the other orientation do not run emptier than the memory
-  return g.rows <= (int64_t)64 * g.E ? launch_orientation<false>(a, st) : launch_orientation<true>(a, st);
+  return rows_m ? launch_orientation<true>(a, sms, st) : launch_orientation<false>(a, sms, st);
 }
 
 }  // namespace moe

@@ -214,8 +214,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
   tc_fence_after();
   const uint32_t tmem = misc[0];
   pl.tiles = MODE == kProdDw ? g.E * dw.p_tiles * dw.q_tiles : start[g.E];
-  pl.S = MODE == kProdDw ? 1 : plan_slices(pl.tiles, pl.stages, a.pairs);
-  auto item = [&](int w) { return MODE == kProdDw ? dw_item(g, dw, w) : row_item<kGtN, kGtGran>(g, pl, start, w); };
+  pl.S = MODE == kProdDw ? 1 : plan_slices(pl.tiles, pl.stages, a.pairs, 2);
+  auto item = [&](int w) { return MODE == kProdDw ? dw_item(g, dw, w) : row_item<kGtN, kGtGran, kGtP>(g, pl, start, w); };
   const int items = pl.tiles * pl.S;
   const uint32_t full_s = map_to_rank(smem_u32(full), 0);
 

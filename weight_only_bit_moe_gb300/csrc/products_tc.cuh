@@ -74,6 +74,24 @@ __device__ __forceinline__ void tma2_gather4(uint32_t dst, const CUtensorMap* ma
       : "memory");
 }
 
+// The same within one CTA.
+__device__ __forceinline__ void tma1_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma1_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05 over the CTA pair
 __device__ __forceinline__ void tmem_alloc2(uint32_t* smem_dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_dst)),
@@ -96,16 +114,6 @@ __device__ __forceinline__ void umma2_f16_elect(uint32_t d, uint64_t a, uint64_t
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// The same of 32 E4M3 terms.
-__device__ __forceinline__ void umma2_f8_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
 // Arrive on the barrier at this offset in both CTAs once the MMAs issued so far are done.
 __device__ __forceinline__ void umma2_commit_elect(uint64_t* bar) {
   asm volatile(
@@ -114,6 +122,21 @@ __device__ __forceinline__ void umma2_commit_elect(uint64_t* bar) {
       "mov.b16 m, 3;\n\t"
       "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
           smem_u32(bar))
+      : "memory");
+}
+// One CTA, 128 E4M3 terms (four MMAs of 32) of operands stored with the terms
+// innermost: D = A B, nothing accumulated from before.
+__device__ __forceinline__ void umma1_f8_block_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
+      "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc)
       : "memory");
 }
 // 32 TMEM lanes x 32 consecutive 32-bit columns.
@@ -187,9 +210,8 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // each times the tiles of output features; with few tiles the sum is cut into S
 // slices.
 constexpr int kProdGroups = 1024;       // groups, at most
-constexpr int kProdFeatures = 256;      // output features of a tile
 constexpr int kProdTokenChunk = 8;      // row tiles that run next to each other through a group's features
-constexpr int kProdSplitItems = 160;    // items of a launch that splits sums, at most (sizes the scratch)
+constexpr int kProdPartials = 320;      // partial tiles of 128 x 256 sums that the scratch holds
 constexpr int kProdCounterBytes = 4096; // scratch: arrival counters, then partial tiles
 
 struct RowPlan {
@@ -238,16 +260,17 @@ __device__ __forceinline__ void plan_groups(const ProdArgs& g, int p_tiles, int*
   }
 }
 
-// Slices of the sum, when there are fewer tiles than CTA pairs: time in stages of
-// the busiest pair, plus six stages for what an item costs besides its stages and
-// one for each partial that the last pair adds.
-__device__ __forceinline__ int plan_slices(int tiles, int stages, int pairs) {
+// Slices of the sum, when there are fewer tiles than workers (CTAs or pairs, each
+// with `partials` partial tiles to an item): time in stages of the busiest worker,
+// plus six stages for what an item costs besides its stages and one for each
+// partial that the last worker adds.
+__device__ __forceinline__ int plan_slices(int tiles, int stages, int workers, int partials) {
   int S = 1;
-  if (tiles < pairs && tiles > 0) {
+  if (tiles < workers && tiles > 0) {
     int best = stages + 6;
-    const int smax = min(min(stages, 32), kProdSplitItems / tiles);
+    const int smax = min(min(stages, 32), kProdPartials / partials / tiles);
     for (int s = 2; s <= smax; ++s) {
-      const int waves = (tiles * s + pairs - 1) / pairs;
+      const int waves = (tiles * s + workers - 1) / workers;
       const int cost = waves * ((stages + s - 1) / s + 6) + s;
       if (cost < best) { best = cost; S = s; }
     }
@@ -258,7 +281,7 @@ __device__ __forceinline__ int plan_slices(int tiles, int stages, int pairs) {
 // Item w: its slice, then row tiles in chunks of kProdTokenChunk -- inside a chunk
 // row tiles fastest, then features, so that the tiles which run at one time share
 // rows and weights in L2.  A group's rows are cut into equal tiles, rounded to GRAN.
-template <int ROWS, int GRAN>
+template <int ROWS, int GRAN, int FEATURES>
 __device__ __forceinline__ ProdItem row_item(const ProdArgs& g, const RowPlan& pl, const int* start, int w) {
   ProdItem it;
   it.tile = w / pl.S;
@@ -278,7 +301,7 @@ __device__ __forceinline__ ProdItem row_item(const ProdArgs& g, const RowPlan& p
   const int c = l / (kProdTokenChunk * pl.p_tiles), r = l - c * kProdTokenChunk * pl.p_tiles;
   const int width = min(kProdTokenChunk, nt - c * kProdTokenChunk);
   const int t = c * kProdTokenChunk + r % width;
-  it.p0 = (r / width) * kProdFeatures;
+  it.p0 = (r / width) * FEATURES;
   const int q = ((m + nt - 1) / nt + GRAN - 1) / GRAN * GRAN;
   it.q0 = r0 + t * q;
   it.n = min(q, r1 - it.q0);
