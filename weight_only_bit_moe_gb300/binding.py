@@ -102,6 +102,17 @@ def load(path: str = ""):
     return _lib
 
 
+_functions = {}
+
+
+def function(name: str):
+    """The library's function of that name, looked up once."""
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(load(), name)
+    return fn
+
+
 def _p(t):
     """Device/host pointer of a tensor (or an int address, or None)."""
     if t is None:

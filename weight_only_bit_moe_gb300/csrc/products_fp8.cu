@@ -62,6 +62,18 @@ struct Fp8TcArgs {
   int wide_store;        // 32-byte stores are aligned
 };
 
+// Position in a ring of N slots and the parity of the pass through it.
+template <int N>
+struct Ring {
+  uint32_t i = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 template <bool ROWS_M>
 __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_constant__ Fp8TcArgs a) {
   using C = Fp8Cfg<ROWS_M>;
@@ -91,6 +103,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
     tmem_alloc(&misc[0], 512);
     tmem_relinquish();
   }
+  if (warp == kF8Producer && lane < 5) prefetch_map(lane < 4 ? &a.map_x[lane] : &a.map_w);
   RowPlan pl;
   pl.p_tiles = (g.N + C::kFeatures - 1) / C::kFeatures;
   pl.stages = (g.K + 127) / 128;
@@ -100,58 +113,68 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
   tc_fence_after();
   const uint32_t tmem = misc[0];
   pl.tiles = start[g.E];
-  pl.S = plan_slices(pl.tiles, pl.stages, gridDim.x, 1);
+  pl.S = plan_slices(pl, gridDim.x, 1, ROWS_M ? 1 << 30 : 0, 256);
   const int items = pl.tiles * pl.S;
 
   if (warp == kF8Producer) {
     // ------------------------------------------------------------ producer
-    uint32_t k = 0;
+    Ring<C::kStages> at_slot;
+    uint32_t filled = 0;
     for (int w = blockIdx.x; w < items; w += gridDim.x) {
       const ProdItem it = row_item<C::kRows, C::kGran, C::kFeatures>(g, pl, start, w);
       const int rows = (it.n + 15) / 16 * 16;  // copied
-      for (int t = it.t0; t < it.t1; ++t, ++k) {
-        const int s = k % C::kStages;
-        mbar_wait(&empty[s], ((k / C::kStages) + 1) & 1, abort_flag, g.status);
-        if (*abort_flag) break;
+      for (int t = it.t0; t < it.t1; ++t) {
+        const int s = at_slot.i;
+        mbar_wait(&empty[s], at_slot.phase ^ 1, abort_flag, g.status);
         __syncwarp();
         const uint32_t bar = smem_u32(&full[s]), ps = smem_s + s * C::kSlot, qs = ps + C::kPBytes;
         expect_tx_elect(&full[s], (C::kFeatures + rows) * 128);
         tma1_3d(ROWS_M ? qs : ps, &a.map_w, 128 * t, it.p0, it.e, bar);
         const uint32_t xd = ROWS_M ? ps : qs;
-        int at = 0;
+        if (rows == C::kRows) {
+          tma1_2d(xd, &a.map_x[ROWS_M ? 0 : 1], 128 * t, it.q0, bar);
+        } else {
+          int at = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int box = 128 >> i;
-          if (rows & box) {
-            tma1_2d(xd + 128 * at, &a.map_x[i], 128 * t, it.q0 + at, bar);
-            at += box;
+          for (int i = ROWS_M ? 1 : 2; i < 4; ++i) {
+            const int box = 128 >> i;
+            if (rows & box) {
+              tma1_2d(xd + 128 * at, &a.map_x[i], 128 * t, it.q0 + at, bar);
+              at += box;
+            }
           }
         }
+        at_slot.next();
+        ++filled;
       }
       if (*abort_flag) break;
     }
     // leave no copy in flight
-    for (uint32_t i = 0; i < (uint32_t)C::kStages && i < k; ++i) {
-      const uint32_t u = k - 1 - i;
+    for (uint32_t i = 0; i < (uint32_t)C::kStages && i < filled; ++i) {
+      const uint32_t u = filled - 1 - i;
       mbar_drain(&full[u % C::kStages], (u / C::kStages) & 1, g.status);
     }
   } else if (warp == kF8Mma) {
     // ------------------------------------------------------------ MMA issuer
-    uint32_t k = 0;
+    Ring<C::kStages> at_slot;
+    Ring<C::kBufs> at_buf;
+    const uint64_t pd = smem_desc_sw128(smem_s), qd = smem_desc_sw128(smem_s + C::kPBytes);
     for (int w = blockIdx.x; w < items; w += gridDim.x) {
       const ProdItem it = row_item<C::kRows, C::kGran, C::kFeatures>(g, pl, start, w);
       // E4M3 operands and fp32 sums have the fields of fp16 operands and fp32 sums
       const uint32_t idesc = idesc_f16_f32(128, ROWS_M ? 256 : (it.n + 15) / 16 * 16, 0u);
-      for (int t = it.t0; t < it.t1; ++t, ++k) {
-        const int s = k % C::kStages, b = k % C::kBufs;
-        mbar_wait(&full[s], (k / C::kStages) & 1, abort_flag, g.status);
-        mbar_wait(&acc_empty[b], ((k / C::kBufs) + 1) & 1, abort_flag, g.status);
+      for (int t = it.t0; t < it.t1; ++t) {
+        const uint32_t s = at_slot.i, b = at_buf.i;
+        mbar_wait(&full[s], at_slot.phase, abort_flag, g.status);
+        mbar_wait(&acc_empty[b], at_buf.phase ^ 1, abort_flag, g.status);
         __syncwarp();
         tc_fence_after();
-        umma1_f8_block_elect(tmem + b * C::kBufCols, smem_desc_sw128(smem_s + s * C::kSlot),
-                             smem_desc_sw128(smem_s + s * C::kSlot + C::kPBytes), idesc);
+        const uint32_t slot = s * (C::kSlot >> 4);  // (descriptor addresses count 16 bytes and do not carry)
+        umma1_f8_block_elect(tmem + b * C::kBufCols, pd + slot, qd + slot, idesc);
         umma_commit_elect(&acc_full[b]);
         umma_commit_elect(&empty[s]);
+        at_slot.next();
+        at_buf.next();
       }
     }
     umma_commit_elect(drain_bar);
@@ -165,7 +188,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
     int32_t* counters = reinterpret_cast<int32_t*>(g.scratch);
     float4* partial = reinterpret_cast<float4*>(g.scratch + kProdCounterBytes);
     const int n_blocks = (g.N + 127) / 128;
-    uint32_t k = 0;
+    Ring<C::kBufs> at_buf;
     for (int w = blockIdx.x; w < items; w += gridDim.x) {
       const ProdItem it = row_item<C::kRows, C::kGran, C::kFeatures>(g, pl, start, w);
       float sum[C::kAcc];
@@ -193,9 +216,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (t + h < it.t1) {
-              const int b = k % C::kBufs;
+              const uint32_t b = at_buf.i;
               const float sc = h ? s1 : s0;
-              mbar_wait(&acc_full[b], (k / C::kBufs) & 1, abort_flag, g.status);
+              mbar_wait(&acc_full[b], at_buf.phase, abort_flag, g.status);
               tc_fence_after();
               const uint32_t tb = lanes + b * C::kBufCols + sub * 128;
 #pragma unroll
@@ -211,14 +234,14 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
 #pragma unroll
                 for (int i = 0; i < 16; ++i) sum[16 * c + i] = fmaf(__uint_as_float(v[i]), sc, sum[16 * c + i]);
               }
-              ++k;
+              at_buf.next();
             }
           }
         }
       } else {
         // one feature, 32 rows
         const int nb = it.p0 / 128;
-        for (int t = it.t0; t < it.t1; ++t, ++k) {
+        for (int t = it.t0; t < it.t1; ++t, at_buf.next()) {
           const int in = (t - it.t0) % kF8FactorStages;
           if (in == 0) {
             named_bar_sync(2, kF8EpiThreads);  // the readers of the last scales are done
@@ -231,8 +254,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
             }
             named_bar_sync(2, kF8EpiThreads);
           }
-          const int b = k % C::kBufs;
-          mbar_wait(&acc_full[b], (k / C::kBufs) & 1, abort_flag, g.status);
+          const uint32_t b = at_buf.i;
+          mbar_wait(&acc_full[b], at_buf.phase, abort_flag, g.status);
           tc_fence_after();
           uint32_t v[32];
           const bool live = 32 * sub < it.n;
@@ -266,18 +289,17 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
         }
         named_bar_sync(1, kF8EpiThreads);
         if (tid == 0) {
-          __threadfence();
-          const unsigned old = atomicInc(reinterpret_cast<unsigned*>(&counters[it.tile]), (unsigned)(pl.S - 1));
-          misc[2] = old == (unsigned)(pl.S - 1) ? 1u : 0u;
-          __threadfence();
+          misc[2] = slice_arrive_last(&counters[it.tile], pl.S) ? 1u : 0u;
         }
         named_bar_sync(1, kF8EpiThreads);
         finish = misc[2] != 0;
         if (finish) {
 #pragma unroll
           for (int i = 0; i < C::kAcc; ++i) sum[i] = 0.0f;
-          for (int s = 0; s < pl.S; ++s) {
-            const float4* src = partial + (int64_t)(it.tile * pl.S + s) * (128 * 256 / 4) + tid;
+          // (rows on N: four slices' loads in flight)
+          const float4* src = partial + (int64_t)it.tile * pl.S * (128 * 256 / 4) + tid;
+#pragma unroll(ROWS_M ? 1 : 4)
+          for (int s = 0; s < pl.S; ++s, src += 128 * 256 / 4) {
 #pragma unroll
             for (int i = 0; i < C::kAcc / 4; ++i) {
               const float4 u = __ldcg(src + i * kF8EpiThreads);

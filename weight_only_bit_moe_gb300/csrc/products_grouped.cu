@@ -193,6 +193,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     tmem_relinquish2();
   }
 
+  if (warp == 0 && lane < 5) prefetch_map(lane < 4 ? &a.map_q[lane] : &a.map_p);
   // --- the plan: tiles per group (rows), or a regular grid of tiles (dW)
   RowPlan pl;
   DwPlan dw;
@@ -214,7 +215,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
   tc_fence_after();
   const uint32_t tmem = misc[0];
   pl.tiles = MODE == kProdDw ? g.E * dw.p_tiles * dw.q_tiles : start[g.E];
-  pl.S = MODE == kProdDw ? 1 : plan_slices(pl.tiles, pl.stages, a.pairs, 2);
+  pl.S = MODE == kProdDw ? 1 : plan_slices(pl, a.pairs, 2, g.rows, kGtN);
   auto item = [&](int w) { return MODE == kProdDw ? dw_item(g, dw, w) : row_item<kGtN, kGtGran, kGtP>(g, pl, start, w); };
   const int items = pl.tiles * pl.S;
   const uint32_t full_s = map_to_rank(smem_u32(full), 0);
@@ -323,10 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
         }
         named_bar_sync(1, kGtEpiThreads);
         if (et == 0) {
-          __threadfence();
-          const unsigned old = atomicInc(reinterpret_cast<unsigned*>(&counters[it.tile * 2 + rank]), (unsigned)(pl.S - 1));
-          misc[2] = old == (unsigned)(pl.S - 1) ? 1u : 0u;
-          __threadfence();
+          misc[2] = slice_arrive_last(&counters[it.tile * 2 + rank], pl.S) ? 1u : 0u;
         }
         named_bar_sync(1, kGtEpiThreads);
         finish = misc[2] != 0;
@@ -338,11 +336,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
             float f[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) f[i] = 0.0f;
-            for (int s = 0; s < pl.S; ++s) {
-              const float* src = partial + ((int64_t)((it.tile * pl.S + s) * 2 + rank) * 128) * kGtN;
+            const float4* src = reinterpret_cast<const float4*>(partial + ((int64_t)it.tile * pl.S * 2 + rank) * 128 * kGtN) +
+                                c * 8 * 128 + quarter * 32 + lane;
+#pragma unroll 4
+            for (int s = 0; s < pl.S; ++s, src += 2 * 128 * kGtN / 4) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float4 u = __ldcg(reinterpret_cast<const float4*>(src) + (c * 8 + i) * 128 + quarter * 32 + lane);
+                const float4 u = __ldcg(src + i * 128);
                 f[4 * i] += u.x, f[4 * i + 1] += u.y, f[4 * i + 2] += u.z, f[4 * i + 3] += u.w;
               }
             }

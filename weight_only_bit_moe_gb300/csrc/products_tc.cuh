@@ -9,6 +9,10 @@
 
 namespace moe {
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // ---------------------------------------------------------------- cluster of two
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -261,21 +265,25 @@ __device__ __forceinline__ void plan_groups(const ProdArgs& g, int p_tiles, int*
 }
 
 // Slices of the sum, when there are fewer tiles than workers (CTAs or pairs, each
-// with `partials` partial tiles to an item): time in stages of the busiest worker,
-// plus six stages for what an item costs besides its stages and one for each
-// partial that the last worker adds.
-__device__ __forceinline__ int plan_slices(int tiles, int stages, int workers, int partials) {
-  int S = 1;
-  if (tiles < workers && tiles > 0) {
-    int best = stages + 6;
-    const int smax = min(min(stages, 32), kProdPartials / partials / tiles);
-    for (int s = 2; s <= smax; ++s) {
-      const int waves = (tiles * s + workers - 1) / workers;
-      const int cost = waves * ((stages + s - 1) / s + 6) + s;
-      if (cost < best) { best = cost; S = s; }
-    }
+// with `partials` partial tiles to an item): the S that minimises, in stages,
+//   rounds * (stages / S + 6) + (S > 1 ? 4 + S * (0.5 + 3.5 cols / 256) : 0),
+// six stages for what an item costs besides its stages, and the second term for
+// storing, signalling and adding partial tiles of `cols` columns (fitted to S = 1 ..
+// 12 at sums of 8 to 64 stages: 1 x 256 x 7168 in FP8 takes 20.5, 14.8, 11.6 and 10.7 us
+// at S = 1, 2, 4 and 8; 300 x 512 x 4096 takes 23.0, 20.8 and 23.7 at 1, 4 and 8).
+// Up to ten stages a second slice cannot save what it costs.  The columns
+// are those of an average tile, at most `most`.  A lane per S;
+// called by whole warps.
+__device__ __forceinline__ int plan_slices(const RowPlan& pl, int workers, int partials, int rows, int most) {
+  if (pl.tiles >= workers || pl.tiles == 0 || pl.stages <= 10) return 1;
+  const int cols = min(most, (int)__fdividef((float)rows * pl.p_tiles, (float)pl.tiles));
+  const int s = (threadIdx.x & 31) + 1;
+  uint32_t cost = 0xFFFFFFu;
+  if (s <= pl.stages && s * pl.tiles <= kProdPartials / partials) {
+    const int rounds = (pl.tiles * s + workers - 1) / workers;
+    cost = 4 * rounds * ((pl.stages + s - 1) / s + 6) + (s > 1 ? 16 + s * (2 + 14 * cols / 256) : 0);
   }
-  return S;
+  return (int)(__reduce_min_sync(0xffffffffu, min(cost, 0xFFFFFFu) * 64 + s) & 63);
 }
 
 // Item w: its slice, then row tiles in chunks of kProdTokenChunk -- inside a chunk
@@ -308,6 +316,16 @@ __device__ __forceinline__ ProdItem row_item(const ProdArgs& g, const RowPlan& p
   it.t0 = (int)((int64_t)it.split * pl.stages / pl.S);
   it.t1 = (int)((int64_t)(it.split + 1) * pl.stages / pl.S);
   return it;
+}
+
+// Arrival of one slice of a tile whose partial sums the CTA's threads have stored,
+// called by one of them after a barrier of all: true for the last of `S` arrivals,
+// whose CTA may then (after another barrier) read every slice's.  The counter
+// starts at 0 and is back at 0 after the last.
+__device__ __forceinline__ bool slice_arrive_last(int32_t* counter, int S) {
+  uint32_t old;
+  asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(S - 1) : "memory");
+  return old == (uint32_t)(S - 1);
 }
 
 // ---------------------------------------------------------------- host

@@ -27,25 +27,25 @@ _DTYPE = {torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_FP16, torch.float32: 
 _workspaces = {}
 
 
-def _handle(device: torch.device, stream) -> int:
+def _handle(device: int, stream) -> int:
     """CUDA handle of the stream (default: the device's current one)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _workspace(device: torch.device, handle: int) -> int:
+def _workspace(device: int, handle: int) -> int:
     """Address of the workspace of this device and stream."""
-    ws = _workspaces.get((device.index, handle))
+    ws = _workspaces.get((device, handle))
     if ws is None:
-        ws = torch.zeros(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+        t = torch.zeros(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
         # the zeros are written on the current stream, the kernels run on `handle`
         torch.cuda.current_stream(device).synchronize()
-        _workspaces[(device.index, handle)] = ws
-    return ws.data_ptr()
+        ws = _workspaces[(device, handle)] = (t.data_ptr(), t)
+    return ws[0]
 
 
-def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+def _empty(shape, dtype: torch.dtype, device: int, stream) -> torch.Tensor:
     """An output of a kernel that runs on `stream`, from that stream's memory."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
@@ -58,11 +58,10 @@ def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Ten
 def products_status(device="cuda", stream=None) -> int:
     """Synchronises the stream and returns (and clears) the device status of its products:
     MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_INVALID (offsets that decrease or leave the rows)."""
-    device = torch.device(device)
-    if device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
-    handle = _handle(device, stream)
-    return B.moe_get_status(_workspace(device, handle), handle)
+    index = torch.device(device).index
+    index = torch.cuda.current_device() if index is None else index
+    handle = _handle(index, stream)
+    return B.moe_get_status(_workspace(index, handle), handle)
 
 
 # The checks below read each attribute of a tensor once: for a decode step they are most of a call's host time.
@@ -101,16 +100,19 @@ def _dims(t: torch.Tensor, name: str, dims: int):
     return shape
 
 
-def _on(device: torch.device, *tensors: Optional[torch.Tensor]) -> None:
-    if device.type != "cuda":
-        raise ValueError(f"the products run on a GPU, not on {device}")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
+def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """Index of the GPU that holds every tensor (tensors that are None are skipped)."""
+    device = first.get_device()
+    if device < 0:
+        raise ValueError(f"the products run on a GPU, not on {first.device}")
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    return device
 
 
 def _check_offsets(offsets: torch.Tensor, E: int) -> None:
-    if offsets.dtype is not torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
+    if offsets.dtype is not torch.int32 or offsets.numel() != E + 1 or offsets.dim() != 1 or not offsets.is_contiguous():
         raise ValueError(f"offsets: expected contiguous int32 [{E + 1}], got {offsets.dtype} {tuple(offsets.shape)}")
 
 
@@ -131,7 +133,7 @@ def _half(name: str, dtype: torch.dtype, *others: torch.dtype) -> int:
 
 
 def _call(name: str, *args) -> None:
-    rc = getattr(B.load(), name)(*args)
+    rc = B.function(name)(*args)
     if rc != B.MOE_OK:
         raise B.MoeError(name, rc)
 
@@ -152,8 +154,7 @@ def expert_order(topk_ids: torch.Tensor, num_experts: int, expert_base: int = 0)
 
 def _by_row(fn: str, name: str, a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
             out: Optional[torch.Tensor], stream, forward: bool) -> torch.Tensor:
-    dev = a.device
-    _on(dev, w, offsets, out)
+    dev = _device(a, w, offsets, out)
     shape = _dims(w, "w", 3)
     E, N, K = shape
     rows = _dims(a, name, 2)[0]
@@ -191,8 +192,7 @@ def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out:
                   out_dtype: Optional[torch.dtype] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
     """Gradient of grouped_mm by w: dw[e] = sum over the rows of e of dy[r] x[r]^T; dy [rows, N], x [rows, K]
     -> [E, N, K], in out_dtype (the operands' type or float32).  accumulate adds to a float32 out."""
-    dev = dy.device
-    _on(dev, x, offsets, out)
+    dev = _device(dy, x, offsets, out)
     rows, N = _dims(dy, "dy", 2)
     K = _dims(x, "x", 2)[1]
     E = _dims(offsets, "offsets", 1)[0] - 1
@@ -248,8 +248,7 @@ def quant_fp8_block(x: torch.Tensor, rows: Optional[torch.Tensor] = None, gated:
     """(q, scale): rows of x (those that the int32 index `rows` names, in its order) as E4M3 with one fp32
     scale per 128 columns; gated: of silu(x[:, :K]) * x[:, K:] with K half of x's columns.  scale has shape
     [rows, ceil(K / 128)], in any strides."""
-    dev = x.device
-    _on(dev, rows, out, scale)
+    dev = _device(x, rows, out, scale)
     code = _half("quant_fp8_block", x.dtype)
     x_rows, K = _dims(x, "x", 2)
     ld = _rows(x, "x", K, x_rows)
@@ -289,8 +288,7 @@ def gemm_fp8_block(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_sc
     [ceil(N / 128), ceil(K / 128)] -> [rows, N] in out_dtype (bfloat16, float16 or float32; bfloat16 unless
     out is given); with offsets, w and w_scale have a leading expert dimension and the rows of expert e take
     w[e].  Scales may have any strides."""
-    dev = x.device
-    _on(dev, x_scale, w, w_scale, offsets, out)
+    dev = _device(x, x_scale, w, w_scale, offsets, out)
     if x.dtype is not torch.float8_e4m3fn or w.dtype is not torch.float8_e4m3fn:
         raise ValueError(f"gemm_fp8_block: float8_e4m3fn operands expected, got {x.dtype} and {w.dtype}")
     if x_scale.dtype is not torch.float32 or w_scale.dtype is not torch.float32:
