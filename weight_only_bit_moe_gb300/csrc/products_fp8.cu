@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
     // ------------------------------------------------------------ producer
     Ring<C::kStages> at_slot;
     uint32_t filled = 0;
-    for (int w = blockIdx.x; w < items; w += gridDim.x) {
-      const ProdItem it = row_item<C::kRows, C::kGran, C::kFeatures>(g, pl, start, w);
+    for (int w = blockIdx.x, e = 0; w < items; w += gridDim.x) {
+      const ProdItem it = row_item<C::kRows, C::kGran, C::kFeatures>(g, pl, start, w, e);
       const int rows = (it.n + 15) / 16 * 16;  // copied
       for (int t = it.t0; t < it.t1; ++t) {
         const int s = at_slot.i;
@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
     Ring<C::kStages> at_slot;
     Ring<C::kBufs> at_buf;
     const uint64_t pd = smem_desc_sw128(smem_s), qd = smem_desc_sw128(smem_s + C::kPBytes);
-    for (int w = blockIdx.x; w < items; w += gridDim.x) {
-      const ProdItem it = row_item<C::kRows, C::kGran, C::kFeatures>(g, pl, start, w);
+    for (int w = blockIdx.x, e = 0; w < items; w += gridDim.x) {
+      const ProdItem it = row_item<C::kRows, C::kGran, C::kFeatures>(g, pl, start, w, e);
       // E4M3 operands and fp32 sums have the fields of fp16 operands and fp32 sums
       const uint32_t idesc = idesc_f16_f32(128, ROWS_M ? 256 : (it.n + 15) / 16 * 16, 0u);
       for (int t = it.t0; t < it.t1; ++t) {
@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
     float4* partial = reinterpret_cast<float4*>(g.scratch + kProdCounterBytes);
     const int n_blocks = (g.N + 127) / 128;
     Ring<C::kBufs> at_buf;
-    for (int w = blockIdx.x; w < items; w += gridDim.x) {
-      const ProdItem it = row_item<C::kRows, C::kGran, C::kFeatures>(g, pl, start, w);
+    for (int w = blockIdx.x, e = 0; w < items; w += gridDim.x) {
+      const ProdItem it = row_item<C::kRows, C::kGran, C::kFeatures>(g, pl, start, w, e);
       float sum[C::kAcc];
 #pragma unroll
       for (int i = 0; i < C::kAcc; ++i) sum[i] = 0.0f;
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
               uint32_t o[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                o[i] = g.out_type == kBf16 ? pack_bf16x2(v[2 * i], v[2 * i + 1]) : pack_f16x2(v[2 * i], v[2 * i + 1]);
+                o[i] = g.out_type == kBf16 ? pack_bf16x2(v[2 * i], v[2 * i + 1]) : pack_half2(v[2 * i], v[2 * i + 1]);
               }
               if (a.wide_store) {
                 stg256(dst, o);

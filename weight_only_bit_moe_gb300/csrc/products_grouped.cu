@@ -14,7 +14,8 @@
 //   dW: P = dy's columns, Q = x's columns; the ragged dimension is the sum.
 // The operand order is the bank's own: forward reads both operands with the sum
 // innermost, dx reads W with j innermost and dW both operands so, through the
-// MN-major descriptors -- nothing is transposed in memory.
+// MN-major descriptors -- nothing is transposed in memory.  dW leaves through shared
+// memory by TMA, added to what is there when it accumulates.
 //
 // A stage is 64 terms of the sum (128-byte lines, 128-byte swizzle), 32 KB per
 // CTA, six in flight.  Roles: one producer thread per CTA issues TMA, counted
@@ -42,61 +43,116 @@ constexpr int kGtEpiWarp0 = 4, kGtEpiWarps = 8, kGtEpiThreads = 256;
 constexpr int kGtP = 256;             // P rows per pair
 constexpr int kGtN = 256;             // Q rows per pair, at most
 constexpr int kGtGran = 32;           // n is a multiple of this for cta_group::2, M = 256
-constexpr int kGtStages = 6;
 constexpr int kGtOperandBytes = 128 * 128;              // 128 rows x 64 terms of 16 bits
 constexpr int kGtStageBytes = 2 * kGtOperandBytes;      // P and Q
 
 struct GroupedTcArgs {
   CUtensorMap map_p;
-  CUtensorMap map_q[4];  // by row: boxes of 128, 64, 32 and 16 rows of Q; dW: [0] boxes of both, and
-                         // single rows for gathers, [1] of P and [2] of Q
+  CUtensorMap map_out;   // dW: boxes of 32 rows x 128 bytes of the output
+  union {
+    CUtensorMap map_q[4];     // by row: boxes of 128, 64, 32 and 16 rows of Q
+    CUtensorMap map_tail[4];  // dW: boxes of 16 rows and of one, of P and of Q
+  };
+  CUtensorMap map_dw_q;       // dW: boxes of Q
   ProdArgs g;
   int pairs;             // CTA pairs of the launch
   int blocked;           // operands stored MN-major have whole blocks of 64 columns: one box brings two
-  int wide_store;              // 32-byte stores are aligned
 };
 
+template <int MODE>
 struct GtSmem {
-  static constexpr int kBar = kGtStages * kGtStageBytes;
-  static constexpr int kNumBars = 2 * kGtStages + 4 + 1;
+  static constexpr int kStages = MODE == kProdDw ? 5 : 6;
+  static constexpr int kOut = kStages * kGtStageBytes;  // dW: two 4 KB boxes per epilogue warp
+  static constexpr int kOutBytes = MODE == kProdDw ? kGtEpiWarps * 2 * 4096 : 0;
+  static constexpr int kBar = kOut + kOutBytes;
+  static constexpr int kNumBars = 2 * kStages + 4 + 1;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;
+  static constexpr int kStatic = (MODE == kProdDw ? 0 : (kProdGroups + 1) * 4) + 64;
+  static_assert(kAlloc + kStatic <= 227 * 1024, "shared memory over the per-CTA limit");
 };
-static_assert(GtSmem::kAlloc + (kProdGroups + 1) * 4 + 64 <= 227 * 1024, "shared memory over the per-CTA limit");
 
-// Item w of dW: a regular grid of tiles, x's columns fastest.
-struct DwPlan {
-  int p_tiles, q_tiles;
+// Items of dW: a regular grid of tiles, x's columns fastest, each cut into S
+// slices.  A role steps from item to item with carries instead of divisions.
+struct DwWalk {
+  int p_tiles, q_tiles, S;
+  int e, p, q, s;          // the item's expert, tile and slice
+  int de, dp, dq, ds;      // the step
+  __device__ __forceinline__ void split(int w, int& e, int& p, int& q, int& s) const {
+    s = w % S;
+    w /= S;
+    q = w % q_tiles;
+    w /= q_tiles;
+    p = w % p_tiles;
+    e = w / p_tiles;
+  }
+  __device__ __forceinline__ void init(int p_tiles_, int q_tiles_, int S_, int first, int step) {
+    p_tiles = p_tiles_, q_tiles = q_tiles_, S = S_;
+    split(first, e, p, q, s);
+    split(step, de, dp, dq, ds);
+  }
+  __device__ __forceinline__ void next() {
+    s += ds, q += dq, p += dp, e += de;
+    if (s >= S) s -= S, ++q;
+    if (q >= q_tiles) q -= q_tiles, ++p;
+    if (p >= p_tiles) p -= p_tiles, ++e;
+  }
+  __device__ __forceinline__ ProdItem item(const ProdArgs& g) const {
+    ProdItem it;
+    it.tile = (e * p_tiles + p) * q_tiles + q;
+    it.split = s;
+    it.e = e;
+    it.p0 = p * kGtP;
+    it.q0 = q * kGtN;
+    it.n = min(kGtN, g.K - it.q0);
+    int r0, r1;
+    group_rows(g, e, r0, r1);
+    const int stages = (r1 - r0 + 63) / 64;
+    it.t0 = 0;
+    it.t1 = stages;
+    if (S > 1) {
+      it.t0 = (int)((int64_t)s * stages / S);
+      it.t1 = (int)((int64_t)(s + 1) * stages / S);
+    }
+    return it;
+  }
 };
-__device__ __forceinline__ ProdItem dw_item(const ProdArgs& g, const DwPlan& pl, int w) {
-  ProdItem it;
-  const int per = pl.p_tiles * pl.q_tiles;
-  it.tile = w;
-  it.split = 0;
-  it.e = w / per;
-  const int l = w - it.e * per;
-  it.p0 = (l / pl.q_tiles) * kGtP;
-  it.q0 = (l % pl.q_tiles) * kGtN;
-  it.n = min(kGtN, g.K - it.q0);
-  int r0, r1;
-  group_rows(g, it.e, r0, r1);
-  it.t0 = 0;
-  it.t1 = (r1 - r0 + 63) / 64;
-  return it;
-}
 
-// The last rows [row, r1) of a group, fewer than 64, of `blocks` blocks of 64
-// columns: rows up to a multiple of 16 are fetched, those at or past r1 as zeros
+// A role's position among the items of a launch.
+template <int MODE>
+struct GtWalk {
+  DwWalk dw;
+  int w, e, step;
+  __device__ __forceinline__ GtWalk(const RowPlan& pl, int q_tiles, int pair, int pairs) : w(pair), e(0), step(pairs) {
+    if (MODE == kProdDw) dw.init(pl.p_tiles, q_tiles, pl.S, pair, pairs);
+  }
+  __device__ __forceinline__ ProdItem item(const ProdArgs& g, const RowPlan& pl, const int* start) {
+    return MODE == kProdDw ? dw.item(g) : row_item<kGtN, kGtGran, kGtP>(g, pl, start, w, e);
+  }
+  __device__ __forceinline__ void next() {
+    w += step;
+    if (MODE == kProdDw) dw.next();
+  }
+};
+
+// The last rows [row, r1) of a group, fewer than 64, of two blocks of 64 columns:
+// whole sixteens as boxes, the rest by index in fours, rows at or past r1 as zeros
 // (row `none` lies outside the tensor).
-__device__ __forceinline__ void gt_gather(const CUtensorMap* map, int col, int blocks, int row, int r1, int none,
-                                          uint32_t slot, uint32_t bar) {
-  const int fours = (r1 - row + 15) / 16 * 4;
-  for (int i = 0; i < fours; ++i) {
-    const int b = row + 4 * i;
+__device__ __forceinline__ void gt_tail(const CUtensorMap* sixteen, const CUtensorMap* single, int col, int row, int r1,
+                                        int none, uint32_t slot, uint32_t bar) {
+  int b = row;
+  for (; b + 16 <= r1; b += 16, slot += 2048) {
+    tma2_2d(slot, sixteen, col, b, bar);
+    tma2_2d(slot + 8192, sixteen, col + 64, b, bar);
+  }
+  if (b == r1) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i, b += 4, slot += 512) {
     const int4 r = make_int4(b < r1 ? b : none, b + 1 < r1 ? b + 1 : none, b + 2 < r1 ? b + 2 : none,
                              b + 3 < r1 ? b + 3 : none);
-    for (int c = 0; c < blocks; ++c) tma2_gather4(slot + 8192 * c + 512 * i, map, col + 64 * c, r, bar);
+    tma2_gather4(slot, single, col, r, bar);
+    tma2_gather4(slot + 8192, single, col + 64, r, bar);
   }
 }
 
@@ -114,7 +170,7 @@ __device__ __forceinline__ void gt_load_p(const GroupedTcArgs& a, const ProdItem
       tma2_3d(slot + 8192, &a.map_p, p + 64, 64 * t, it.e, bar);
     }
   } else if (r1 - row < 64) {
-    gt_gather(&a.map_q[1], p, 2, row, r1, a.g.rows, slot, bar);
+    gt_tail(&a.map_tail[0], &a.map_tail[1], p, row, r1, a.g.rows, slot, bar);
   } else if (a.blocked) {
     tma2_3d(slot, &a.map_p, 0, row, p / 64, bar);
   } else {
@@ -137,12 +193,12 @@ __device__ __forceinline__ void gt_load_q(const GroupedTcArgs& a, int t, int q, 
       }
     }
   } else if (r1 - row < 64) {
-    gt_gather(&a.map_q[2], q, 2, row, r1, a.g.rows, slot, bar);
+    gt_tail(&a.map_tail[2], &a.map_tail[3], q, row, r1, a.g.rows, slot, bar);
   } else if (a.blocked) {
-    tma2_3d(slot, &a.map_q[0], 0, row, q / 64, bar);
+    tma2_3d(slot, &a.map_dw_q, 0, row, q / 64, bar);
   } else {
-    tma2_2d(slot, &a.map_q[0], q, row, bar);
-    tma2_2d(slot + 8192, &a.map_q[0], q + 64, row, bar);
+    tma2_2d(slot, &a.map_dw_q, q, row, bar);
+    tma2_2d(slot + 8192, &a.map_dw_q, q + 64, row, bar);
   }
 }
 
@@ -163,18 +219,20 @@ __device__ __forceinline__ uint32_t gt_stage_bytes(int half, int v) {
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     grouped_tc_kernel(const __grid_constant__ GroupedTcArgs a) {
+  using SM = GtSmem<MODE>;
+  constexpr int kStages = SM::kStages;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ int start[kProdGroups + 1];  // first tile of each group
   __shared__ int warp_tot[kGtThreads / 32];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smem_s = smem_u32(smem);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + GtSmem::kBar);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBar);
   uint64_t* full = bars;                    // the leader's count both CTAs' copies
-  uint64_t* empty = full + kGtStages;
-  uint64_t* acc_full = empty + kGtStages;
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + 2;       // the leader's
   uint64_t* drain_bar = acc_empty + 2;
-  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + GtSmem::kMisc);  // [0] tmem base, [1] abort, [2] last
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + SM::kMisc);  // [0] tmem base, [1] abort, [2] last
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&misc[1]);
   const ProdArgs& g = a.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -182,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
   const int pair = blockIdx.x >> 1;
 
   if (tid == 0) {
-    for (int i = 0; i < kGtStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 2 * kGtEpiWarps); }
     mbar_init(drain_bar, 1);
     misc[1] = 0;
@@ -193,15 +251,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     tmem_relinquish2();
   }
 
-  if (warp == 0 && lane < 5) prefetch_map(lane < 4 ? &a.map_q[lane] : &a.map_p);
+  if (warp == 0 && lane < 6) prefetch_map(lane < 4 ? &a.map_q[lane] : lane == 4 ? &a.map_p : &a.map_out);
   // --- the plan: tiles per group (rows), or a regular grid of tiles (dW)
   RowPlan pl;
-  DwPlan dw;
   const int j_dim = MODE == kProdDx ? g.K : g.N;
   pl.p_tiles = (j_dim + kGtP - 1) / kGtP;
-  pl.stages = ((MODE == kProdDx ? g.N : g.K) + 63) / 64;
-  dw.p_tiles = pl.p_tiles;
-  dw.q_tiles = (g.K + kGtN - 1) / kGtN;
+  pl.stages = MODE == kProdDw ? g.rows / g.E / 64 : ((MODE == kProdDx ? g.N : g.K) + 63) / 64;  // (dW: on average)
+  const int q_tiles = (g.K + kGtN - 1) / kGtN;  // dW
   if (MODE == kProdDw) {
     if (blockIdx.x == 0)
       for (int e = tid; e < g.E; e += kGtThreads)
@@ -214,24 +270,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
   cluster_sync_all();  // both CTAs' barriers exist before either signals them
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  pl.tiles = MODE == kProdDw ? g.E * dw.p_tiles * dw.q_tiles : start[g.E];
-  pl.S = MODE == kProdDw ? 1 : plan_slices(pl, a.pairs, 2, g.rows, kGtN);
-  auto item = [&](int w) { return MODE == kProdDw ? dw_item(g, dw, w) : row_item<kGtN, kGtGran, kGtP>(g, pl, start, w); };
+  pl.tiles = MODE == kProdDw ? g.E * pl.p_tiles * q_tiles : start[g.E];
+  pl.S = plan_slices(pl, a.pairs, 2, MODE == kProdDw ? 1 << 30 : g.rows, kGtN);
   const int items = pl.tiles * pl.S;
   const uint32_t full_s = map_to_rank(smem_u32(full), 0);
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ producers of P (warp 0) and Q (warp 2)
     uint32_t k = 0;
-    for (int w = pair; w < items; w += a.pairs) {
-      const ProdItem it = item(w);
+    for (GtWalk<MODE> at(pl, q_tiles, pair, a.pairs); at.w < items; at.next()) {
+      const ProdItem it = at.item(g, pl, start);
       const int half = gt_half<MODE>(it.n);
       int r0 = 0, r1 = 0;
       if (MODE == kProdDw) group_rows(g, it.e, r0, r1);
       const int p = it.p0 + rank * 128, q = it.q0 + rank * half;
       for (int t = it.t0; t < it.t1; ++t, ++k) {
-        const int s = k % kGtStages, row = r0 + 64 * t;
-        mbar_wait(&empty[s], ((k / kGtStages) + 1) & 1, abort_flag, g.status);
+        const int s = k % kStages, row = r0 + 64 * t;
+        mbar_wait(&empty[s], ((k / kStages) + 1) & 1, abort_flag, g.status);
         if (*abort_flag) break;
         __syncwarp();
         const uint32_t slot = smem_s + s * kGtStageBytes, bar = full_s + 8 * s;
@@ -246,9 +301,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     }
     // leave no copy in flight (the leader's barriers count the peer's copies too)
     if (rank == 0 && warp == 0)
-      for (uint32_t i = 0; i < (uint32_t)kGtStages && i < k; ++i) {
+      for (uint32_t i = 0; i < (uint32_t)kStages && i < k; ++i) {
         const uint32_t u = k - 1 - i;
-        mbar_drain(&full[u % kGtStages], (u / kGtStages) & 1, g.status);
+        mbar_drain(&full[u % kStages], (u / kStages) & 1, g.status);
       }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
@@ -257,9 +312,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
       constexpr uint32_t kStepA = MODE == kProdFwd ? 2 : 128, kStepB = MODE == kProdDw ? 128 : 2;  // 16 terms, 16-byte units
       const uint32_t bf = g.in_type == kBf16 ? 1u : 0u;
       uint32_t k = 0, ic = 0;
-      for (int w = pair; w < items; w += a.pairs) {
-        const ProdItem it = item(w);
-        if (it.t0 >= it.t1) continue;  // (dW: a group without rows; the epilogue writes zeros)
+      for (GtWalk<MODE> at(pl, q_tiles, pair, a.pairs); at.w < items; at.next()) {
+        const ProdItem it = at.item(g, pl, start);
+        if (it.t0 >= it.t1) continue;  // (dW: no rows; the epilogue takes zeros)
         int r0 = 0, r1 = 0;
         if (MODE == kProdDw) group_rows(g, it.e, r0, r1);
         const uint32_t idesc = idesc_f16_f32(256, 2 * gt_half<MODE>(it.n), bf) | kMajors;
@@ -269,8 +324,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem + acc * kGtN;
         for (int t = it.t0; t < it.t1; ++t, ++k) {
-          const int s = k % kGtStages;
-          mbar_wait(&full[s], (k / kGtStages) & 1, abort_flag, g.status);
+          const int s = k % kStages;
+          mbar_wait(&full[s], (k / kStages) & 1, abort_flag, g.status);
           __syncwarp();
           tc_fence_after();
           const uint32_t slot = smem_s + s * kGtStageBytes;
@@ -295,136 +350,133 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     const int quarter = warp & 3, sub = (warp - kGtEpiWarp0) >> 2;  // TMEM lanes; which 32-column chunks
     const int et = tid - kGtEpiWarp0 * 32;
     const uint32_t acc_empty_s = map_to_rank(smem_u32(acc_empty), 0);
+    const uint32_t boxes = smem_s + SM::kOut + (warp - kGtEpiWarp0) * 8192;  // dW: this warp's output boxes
     int32_t* counters = reinterpret_cast<int32_t*>(g.scratch);
-    float* partial = reinterpret_cast<float*>(g.scratch + kProdCounterBytes);
-    uint32_t ic = 0;
-    for (int w = pair; w < items; w += a.pairs) {
-      const ProdItem it = item(w);
+    uint4* partial = reinterpret_cast<uint4*>(g.scratch + kProdCounterBytes);
+    uint32_t ic = 0, box = 0;
+    for (GtWalk<MODE> at(pl, q_tiles, pair, a.pairs); at.w < items; at.next()) {
+      const ProdItem it = at.item(g, pl, start);
       const int p = it.p0 + rank * 128 + quarter * 32;  // this warp's first P row
-      const bool none = it.t0 >= it.t1;
+      const bool none = it.t0 >= it.t1;                 // no terms: the sums are zeros
       const int acc = ic & 1;
       if (!none) {
         mbar_wait(&acc_full[acc], (ic >> 1) & 1, abort_flag, g.status);
         tc_fence_after();
       }
       const uint32_t tb = tmem + ((uint32_t)(quarter * 32) << 16) + acc * kGtN;
-      bool finish = true;
       const int chunks = (it.n + 31) / 32;
-      if (MODE != kProdDw && pl.S > 1) {
-        // this thread's values of the slice, 16 bytes per thread and step, in its own order
-        float* mine = partial + ((int64_t)((it.tile * pl.S + it.split) * 2 + rank) * 128) * kGtN;
+      // A thread's sums of a partial tile, 16 bytes per thread and step, in its own order.
+      const int64_t slice = 128 * kGtN / 4;
+      uint4* mine = partial + ((int64_t)it.tile * pl.S * 2 + rank) * slice + quarter * 32 + lane;
+      bool finish = true;
+      if (pl.S > 1) {
         for (int c = sub; c < chunks; c += 2) {
           uint32_t v[32];
-          tmem_ld32(tb + 32 * c, v);
-          tmem_ld_wait();
+          if (none) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+          } else {
+            tmem_ld32(tb + 32 * c, v);
+            tmem_ld_wait();
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            __stcg(reinterpret_cast<uint4*>(mine) + (c * 8 + i) * 128 + quarter * 32 + lane,
-                   make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+            __stcg(mine + it.split * 2 * slice + (c * 8 + i) * 128, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
         }
         named_bar_sync(1, kGtEpiThreads);
-        if (et == 0) {
-          misc[2] = slice_arrive_last(&counters[it.tile * 2 + rank], pl.S) ? 1u : 0u;
-        }
+        if (et == 0) misc[2] = slice_arrive_last(&counters[it.tile * 2 + rank], pl.S) ? 1u : 0u;
         named_bar_sync(1, kGtEpiThreads);
         finish = misc[2] != 0;
       }
-      if (finish) {
+      // 32 columns of the tile: from the slices, from tensor memory, or zeros
+      auto columns = [&](int c, uint32_t (&v)[32]) {
+        if (pl.S > 1) {
+          float f[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) f[i] = 0.0f;
+          const uint4* src = mine + c * 8 * 128;
+#pragma unroll 4
+          for (int s = 0; s < pl.S; ++s, src += 2 * slice) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 u = __ldcg(reinterpret_cast<const float4*>(src) + i * 128);
+              f[4 * i] += u.x, f[4 * i + 1] += u.y, f[4 * i + 2] += u.z, f[4 * i + 3] += u.w;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(f[i]);
+        } else if (!none) {
+          tmem_ld32(tb + 32 * c, v);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
+      };
+      if (finish && MODE == kProdDw) {
+        // lane = row of dW[e], registers = 32 consecutive columns, 128 bytes of the row (two halves of
+        // them when the output has 16 bits): into the warp's box, swizzled, and on by TMA, which writes
+        // whole lines and cuts the box at the matrix's edges
+        const bool wide = g.out_type == kFp32;
+        const int per_warp = kGtN / 2 / (wide ? 32 : 64);
+        for (int i = 0; i < per_warp; ++i) {
+          const int c = sub * 4 + (wide ? i : 2 * i);  // first 32-column chunk of the box
+          if (32 * c >= it.n || p >= g.N) continue;
+          const uint32_t dst = boxes + (box & 1) * 4096;
+          if (lane == 0) tma_store_wait_read<1>();  // the box before last has been read
+          __syncwarp();
+          const uint32_t row = dst + lane * 128;
+          uint32_t v[32];
+          columns(c, v);
+          if (wide) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              sts128(row + ((j ^ (lane & 7)) << 4), make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h == 1) {
+                if (32 * (c + 1) >= it.n) break;  // (columns past the edge are cut)
+                columns(c + 1, v);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t o[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const float lo = __uint_as_float(v[8 * j + 2 * u]), hi = __uint_as_float(v[8 * j + 2 * u + 1]);
+                  o[u] = g.out_type == kBf16 ? pack_bf16x2(lo, hi) : pack_half2(lo, hi);
+                }
+                sts128(row + (((4 * h + j) ^ (lane & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+              }
+            }
+          }
+          fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) {
+            if (g.accumulate) tma_store_3d<true>(&a.map_out, it.q0 + 32 * c, p, it.e, dst);
+            else tma_store_3d<false>(&a.map_out, it.q0 + 32 * c, p, it.e, dst);
+          }
+          ++box;
+        }
+      } else if (finish) {
         for (int c = sub; c < chunks; c += 2) {
           uint32_t v[32];
-          if (MODE != kProdDw && pl.S > 1) {
-            float f[32];
+          columns(c, v);
+          // lane = feature, registers = 32 rows: eight rows at a time, transposed
+          // inside groups of eight lanes, so that a lane stores 16 bytes of one row
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = 0.0f;
-            const float4* src = reinterpret_cast<const float4*>(partial + ((int64_t)it.tile * pl.S * 2 + rank) * 128 * kGtN) +
-                                c * 8 * 128 + quarter * 32 + lane;
-#pragma unroll 4
-            for (int s = 0; s < pl.S; ++s, src += 2 * 128 * kGtN / 4) {
+          for (int b = 0; b < 4; ++b) {
+            uint32_t wd[4];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 u = __ldcg(src + i * 128);
-                f[4 * i] += u.x, f[4 * i + 1] += u.y, f[4 * i + 2] += u.z, f[4 * i + 3] += u.w;
-              }
+            for (int u = 0; u < 4; ++u) {
+              const float lo = __uint_as_float(v[8 * b + 2 * u]), hi = __uint_as_float(v[8 * b + 2 * u + 1]);
+              wd[u] = g.out_type == kBf16 ? pack_bf16x2(lo, hi) : pack_half2(lo, hi);
             }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(f[i]);
-          } else if (!none) {
-            tmem_ld32(tb + 32 * c, v);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
-          }
-          if (MODE == kProdDw) {
-            // lane = row i of dW[e], registers = 32 consecutive columns
-            const int i = p + lane, j = it.q0 + 32 * c;
-            if (i < g.N) {
-              const int64_t at = it.e * g.out_se + (int64_t)i * g.out_ld + j;
-              const int cols = min(32, g.K - j);  // a multiple of 8
-              if (g.out_type == kFp32) {
-                float* dst = static_cast<float*>(g.out) + at;
-                if (g.accumulate) {
-                  for (int b = 0; b < cols; b += 4) {
-#pragma unroll
-                    for (int u = 0; u < 32; u += 4)
-                      if (u == b) {
-                        const float4 o = *reinterpret_cast<const float4*>(dst + u);
-                        v[u] = __float_as_uint(__uint_as_float(v[u]) + o.x);
-                        v[u + 1] = __float_as_uint(__uint_as_float(v[u + 1]) + o.y);
-                        v[u + 2] = __float_as_uint(__uint_as_float(v[u + 2]) + o.z);
-                        v[u + 3] = __float_as_uint(__uint_as_float(v[u + 3]) + o.w);
-                      }
-                  }
-                }
-#pragma unroll
-                for (int b = 0; b < 32; b += 8) {
-                  if (b < cols) {
-                    const uint32_t o[8] = {v[b], v[b + 1], v[b + 2], v[b + 3], v[b + 4], v[b + 5], v[b + 6], v[b + 7]};
-                    if (a.wide_store) {
-                      stg256(dst + b, o);
-                    } else {
-                      stg128(dst + b, make_uint4(o[0], o[1], o[2], o[3]));
-                      stg128(dst + b + 4, make_uint4(o[4], o[5], o[6], o[7]));
-                    }
-                  }
-                }
-              } else {
-                uint16_t* dst = static_cast<uint16_t*>(g.out) + at;
-                uint32_t h[16];
-#pragma unroll
-                for (int u = 0; u < 16; ++u) {
-                  const float lo = __uint_as_float(v[2 * u]), hi = __uint_as_float(v[2 * u + 1]);
-                  h[u] = g.out_type == kBf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
-                }
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                  const uint32_t o[8] = {h[8 * b], h[8 * b + 1], h[8 * b + 2], h[8 * b + 3],
-                                         h[8 * b + 4], h[8 * b + 5], h[8 * b + 6], h[8 * b + 7]};
-                  if (a.wide_store && 16 * b + 16 <= cols) {
-                    stg256(dst + 16 * b, o);
-                  } else {
-                    if (16 * b < cols) stg128(dst + 16 * b, make_uint4(o[0], o[1], o[2], o[3]));
-                    if (16 * b + 8 < cols) stg128(dst + 16 * b + 8, make_uint4(o[4], o[5], o[6], o[7]));
-                  }
-                }
-              }
-            }
-          } else {
-            // lane = feature, registers = 32 rows: eight rows at a time, transposed
-            // inside groups of eight lanes, so that a lane stores 16 bytes of one row
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              uint32_t wd[4];
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const float lo = __uint_as_float(v[8 * b + 2 * u]), hi = __uint_as_float(v[8 * b + 2 * u + 1]);
-                wd[u] = g.out_type == kBf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
-              }
-              const uint4 o = transpose8x8_u16(wd, lane);
-              const int row = 32 * c + 8 * b + (lane & 7), j = p + (lane & 24);
-              if (row < it.n && j < j_dim)
-                stg128(static_cast<uint16_t*>(g.out) + (int64_t)(it.q0 + row) * g.out_ld + j, o);
-            }
+            const uint4 o = transpose8x8_u16(wd, lane);
+            const int row = 32 * c + 8 * b + (lane & 7), j = p + (lane & 24);
+            if (row < it.n && j < j_dim)
+              stg128(static_cast<uint16_t*>(g.out) + (int64_t)(it.q0 + row) * g.out_ld + j, o);
           }
           __syncwarp();  // whole warps read tensor memory
         }
@@ -436,6 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
         ++ic;
       }
     }
+    if (MODE == kProdDw && lane == 0) tma_store_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -470,6 +523,7 @@ bool make_prod_map(CUtensorMap* m, int elem_type, const void* base, int nd, cons
   for (int i = 0; i + 1 < nd; ++i) s[i] = strides[i];
   const CUtensorMapDataType t = elem_type == kBf16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                 : elem_type == kFp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                : elem_type == kFp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   return enc(m, t, (cuuint32_t)nd, const_cast<void*>(base), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -496,11 +550,11 @@ static cudaError_t launch_mode(GroupedTcArgs& a, cudaStream_t st) {
   if (rc != cudaSuccess) return rc;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    rc = cudaFuncSetAttribute(grouped_tc_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, GtSmem::kAlloc);
+    rc = cudaFuncSetAttribute(grouped_tc_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, GtSmem<MODE>::kAlloc);
     if (rc != cudaSuccess) return rc;
     ready[dev].store(true, std::memory_order_release);
   }
-  grouped_tc_kernel<MODE><<<2 * a.pairs, kGtThreads, GtSmem::kAlloc, st>>>(a);
+  grouped_tc_kernel<MODE><<<2 * a.pairs, kGtThreads, GtSmem<MODE>::kAlloc, st>>>(a);
   return cudaPeekAtLastError();
 }
 
@@ -527,16 +581,20 @@ cudaError_t launch_grouped_tc(const ProdArgs& g, int mode, cudaStream_t st, bool
   if (mode == kProdDw) {
     a.blocked = g.N % 64 == 0 && g.K % 64 == 0;
     const uint64_t dp[2] = {N, rows}, dq[2] = {K, rows};
-    const uint32_t box[2] = {64, 64}, one[2] = {64, 1};
-    ok = make_prod_map(&a.map_q[1], ty, g.a, 2, dp, &ald, one) && make_prod_map(&a.map_q[2], ty, g.w, 2, dq, &wld, one);
+    const uint32_t box[2] = {64, 64}, sixteen[2] = {64, 16}, one[2] = {64, 1};
+    ok = make_prod_map(&a.map_tail[0], ty, g.a, 2, dp, &ald, sixteen) && make_prod_map(&a.map_tail[1], ty, g.a, 2, dp, &ald, one) &&
+         make_prod_map(&a.map_tail[2], ty, g.w, 2, dq, &wld, sixteen) && make_prod_map(&a.map_tail[3], ty, g.w, 2, dq, &wld, one);
     if (a.blocked) {
       const uint64_t bp[3] = {64, rows, N / 64}, bq[3] = {64, rows, K / 64}, sp[2] = {ald, 128}, sq[2] = {wld, 128};
       const uint32_t two[3] = {64, 64, 2};
-      ok = ok && make_prod_map(&a.map_p, ty, g.a, 3, bp, sp, two) && make_prod_map(&a.map_q[0], ty, g.w, 3, bq, sq, two);
+      ok = ok && make_prod_map(&a.map_p, ty, g.a, 3, bp, sp, two) && make_prod_map(&a.map_dw_q, ty, g.w, 3, bq, sq, two);
     } else {
-      ok = ok && make_prod_map(&a.map_p, ty, g.a, 2, dp, &ald, box) && make_prod_map(&a.map_q[0], ty, g.w, 2, dq, &wld, box);
+      ok = ok && make_prod_map(&a.map_p, ty, g.a, 2, dp, &ald, box) && make_prod_map(&a.map_dw_q, ty, g.w, 2, dq, &wld, box);
     }
-    a.map_q[3] = a.map_q[2];
+    const uint64_t each = g.out_type == kFp32 ? 4 : 2, od[3] = {K, N, E};
+    const uint64_t os[2] = {(uint64_t)g.out_ld * each, (uint64_t)(g.E > 1 ? g.out_se : g.out_ld) * each};
+    const uint32_t obox[3] = {128 / (uint32_t)each, 32, 1};
+    ok = ok && make_prod_map(&a.map_out, g.out_type, g.out, 3, od, os, obox);
   } else {
     a.blocked = mode == kProdDx && g.K % 64 == 0;
     const uint64_t we = g.E > 1 ? (uint64_t)g.w_se * 2 : wld;
@@ -555,12 +613,11 @@ cudaError_t launch_grouped_tc(const ProdArgs& g, int mode, cudaStream_t st, bool
       ok = make_prod_map(&a.map_q[i], ty, g.a, 2, da, &ald, box);
     }
   }
+  if (mode != kProdDw) a.map_out = a.map_dw_q = a.map_p;
   if (!ok) return cudaSuccess;  // (the plain kernel takes what a tensor map cannot describe)
   const int sms = prod_sm_count();
   if (sms < 2) return cudaErrorInvalidDevice;
   a.pairs = sms / 2;
-  const int per32 = g.out_type == kFp32 ? 8 : 16;  // elements of 32 bytes
-  a.wide_store = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0 && g.out_ld % per32 == 0 && g.out_se % per32 == 0;
   *done = true;
   if (mode == kProdFwd) return launch_mode<kProdFwd>(a, st);
   if (mode == kProdDx) return launch_mode<kProdDx>(a, st);

@@ -198,6 +198,32 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t 
 constexpr uint32_t kIdescMajorA = 1u << 15, kIdescMajorB = 1u << 16;  // operand stored MN-major
 
 // ---------------------------------------------------------------- stores
+// A box from shared memory, by one thread after fence_async_proxy and a warp
+// barrier; ADD: added to what is there (fp32).
+template <bool ADD>
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int c0, int c1, int c2, uint32_t src) {
+  if (ADD)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(src)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(src)
+                 : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the newest `N` boxes of this thread have been read from shared memory.
+template <int N>
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 __device__ __forceinline__ void stg256(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -206,6 +232,11 @@ __device__ __forceinline__ void stg256(void* p, const uint32_t (&v)[8]) {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t v;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+  return v;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t v;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
   return v;
 }
 
@@ -289,32 +320,44 @@ __device__ __forceinline__ int plan_slices(const RowPlan& pl, int workers, int p
 // Item w: its slice, then row tiles in chunks of kProdTokenChunk -- inside a chunk
 // row tiles fastest, then features, so that the tiles which run at one time share
 // rows and weights in L2.  A group's rows are cut into equal tiles, rounded to GRAN.
+// A role walks its items in ascending order, so the search for the group goes on
+// from the last one's (`e`, 0 at first), and the divisions are skipped where the
+// quotient is known: every item costs each role this code before its first copy.
 template <int ROWS, int GRAN, int FEATURES>
-__device__ __forceinline__ ProdItem row_item(const ProdArgs& g, const RowPlan& pl, const int* start, int w) {
+__device__ __forceinline__ ProdItem row_item(const ProdArgs& g, const RowPlan& pl, const int* start, int w, int& e) {
   ProdItem it;
-  it.tile = w / pl.S;
-  it.split = w - it.tile * pl.S;
-  // the group: the last e with start[e] <= tile
-  int lo = 0, hi = g.E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (start[mid] <= it.tile) lo = mid;
-    else hi = mid - 1;
+  it.tile = w;
+  it.split = 0;
+  it.t0 = 0;
+  it.t1 = pl.stages;
+  if (pl.S > 1) {
+    it.tile = w / pl.S;
+    it.split = w - it.tile * pl.S;
+    it.t0 = it.split * pl.stages / pl.S;
+    it.t1 = (it.split + 1) * pl.stages / pl.S;
   }
-  it.e = lo;
-  const int l = it.tile - start[lo];
+  while (start[e + 1] <= it.tile) ++e;  // (ends: tile < start[E], and the last such group is not empty)
+  it.e = e;
+  int l = it.tile - start[e];
   int r0, r1;
-  group_rows(g, lo, r0, r1);
+  group_rows(g, e, r0, r1);
   const int m = r1 - r0, nt = (m + ROWS - 1) / ROWS;
-  const int c = l / (kProdTokenChunk * pl.p_tiles), r = l - c * kProdTokenChunk * pl.p_tiles;
-  const int width = min(kProdTokenChunk, nt - c * kProdTokenChunk);
-  const int t = c * kProdTokenChunk + r % width;
-  it.p0 = (r / width) * FEATURES;
+  if (nt == 1) {
+    it.p0 = l * FEATURES;
+    it.q0 = r0;
+    it.n = m;
+    return it;
+  }
+  int c = 0;
+  if (nt > kProdTokenChunk) {
+    c = l / (kProdTokenChunk * pl.p_tiles);
+    l -= c * kProdTokenChunk * pl.p_tiles;
+  }
+  const int width = min(kProdTokenChunk, nt - c * kProdTokenChunk), f = l / width;
+  it.p0 = f * FEATURES;
   const int q = ((m + nt - 1) / nt + GRAN - 1) / GRAN * GRAN;
-  it.q0 = r0 + t * q;
+  it.q0 = r0 + (c * kProdTokenChunk + l - f * width) * q;
   it.n = min(q, r1 - it.q0);
-  it.t0 = (int)((int64_t)it.split * pl.stages / pl.S);
-  it.t1 = (int)((int64_t)(it.split + 1) * pl.stages / pl.S);
   return it;
 }
 
