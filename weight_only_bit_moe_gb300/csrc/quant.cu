@@ -200,18 +200,17 @@ __device__ __forceinline__ void quant_unit(const QuantArgs& a, int row, int src,
   }
 }
 
+// A warp per unit: rows along x, the units of a row along y (no division, and the
+// hardware balances the CTAs).
 template <bool GATED, int TYPE>
 __global__ void __launch_bounds__(kQuThreads, kQuCtas) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
   constexpr int kCols = GATED ? 512 : 1024;
   const int lane = threadIdx.x & 31;
-  const uint32_t per_row = (a.K + kCols - 1) / kCols;
-  const uint32_t units = a.rows * per_row;  // (fits: checked by the caller)
-  for (uint32_t u = blockIdx.x * kQuWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kQuWarps) {
-    const int row = u / per_row, c0 = (u - row * per_row) * kCols;
-    const int src = a.row_index ? __ldg(a.row_index + row) : row;
-    if (c0 + kCols <= a.K && (unsigned)src < (unsigned)a.x_rows) quant_unit<GATED, TYPE, true>(a, row, src, c0, lane);
-    else quant_unit<GATED, TYPE, false>(a, row, src, c0, lane);
-  }
+  const int row = blockIdx.x * kQuWarps + (threadIdx.x >> 5), c0 = blockIdx.y * kCols;
+  if (row >= a.rows) return;
+  const int src = a.row_index ? __ldg(a.row_index + row) : row;
+  if (c0 + kCols <= a.K && (unsigned)src < (unsigned)a.x_rows) quant_unit<GATED, TYPE, true>(a, row, src, c0, lane);
+  else quant_unit<GATED, TYPE, false>(a, row, src, c0, lane);
 }
 
 // Any alignment: a warp per block, four columns per lane.
@@ -255,17 +254,18 @@ __global__ void __launch_bounds__(kQuThreads) quant_any_kernel(const __grid_cons
 
 template <bool GATED>
 static void launch_quant(const QuantArgs& a, int sms, cudaStream_t st) {
-  const int cols = GATED ? 512 : 1024;  // columns a warp takes at a time
-  const int64_t units = (int64_t)a.rows * ((a.K + cols - 1) / cols);
+  const int cols = GATED ? 512 : 1024;  // columns a warp takes
+  const int per_row = (a.K + cols - 1) / cols;
   const bool wide = ((reinterpret_cast<uintptr_t>(a.x) & 15) | (reinterpret_cast<uintptr_t>(a.q) & 7)) == 0 &&
-                    a.x_ld % 8 == 0 && a.q_ld % 8 == 0 && a.K % 8 == 0 && units < ((int64_t)1 << 31);
-  const int64_t work = wide ? units : (int64_t)a.rows * ((a.K + 127) / 128);
-  // up to sixteen rounds of CTAs are left to the hardware's balance
-  const int64_t ctas = (work + kQuWarps - 1) / kQuWarps, most = (int64_t)sms * (wide ? kQuCtas : 8) * 16;
-  const int grid = (int)(ctas < most ? ctas : most);
-  if (wide && a.type == kBf16) quant_rows_kernel<GATED, kBf16><<<grid, kQuThreads, 0, st>>>(a);
-  else if (wide) quant_rows_kernel<GATED, kFp16><<<grid, kQuThreads, 0, st>>>(a);
-  else quant_any_kernel<GATED><<<grid, kQuThreads, 0, st>>>(a);
+                    a.x_ld % 8 == 0 && a.q_ld % 8 == 0 && a.K % 8 == 0 && per_row <= 65535;
+  if (wide) {
+    const dim3 grid((unsigned)(((int64_t)a.rows + kQuWarps - 1) / kQuWarps), (unsigned)per_row);
+    if (a.type == kBf16) quant_rows_kernel<GATED, kBf16><<<grid, kQuThreads, 0, st>>>(a);
+    else quant_rows_kernel<GATED, kFp16><<<grid, kQuThreads, 0, st>>>(a);
+    return;
+  }
+  const int64_t ctas = ((int64_t)a.rows * ((a.K + 127) / 128) + kQuWarps - 1) / kQuWarps;
+  quant_any_kernel<GATED><<<(int)(ctas < sms * 8 ? ctas : sms * 8), kQuThreads, 0, st>>>(a);
 }
 
 }  // namespace moe
