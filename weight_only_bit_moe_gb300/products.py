@@ -21,6 +21,7 @@ import torch
 from . import binding as B
 
 BLOCK = 128  # columns per FP8 scale; also rows of a weight block
+_HALF = {torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_FP16}
 _DTYPE = {torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_FP16, torch.float32: B.MOE_FP32}
 
 # One workspace per device and stream, as the kernels of one stream run one after another.
@@ -116,26 +117,9 @@ def _check_offsets(offsets: torch.Tensor, E: int) -> None:
         raise ValueError(f"offsets: expected contiguous int32 [{E + 1}], got {offsets.dtype} {tuple(offsets.shape)}")
 
 
-def _half(name: str, dtype: torch.dtype, *others: torch.dtype) -> int:
-    if dtype is torch.bfloat16:
-        code = B.MOE_BF16
-    elif dtype is torch.float16:
-        code = B.MOE_FP16
-    else:
-        code = None
-    for o in others:
-        if o is not dtype:
-            code = None
-    if code is None:
-        raise ValueError(f"{name}: operands of one type, bfloat16 or float16, expected; got "
-                         f"{', '.join(str(d) for d in (dtype, *others))}")
-    return code
-
-
-def _call(name: str, *args) -> None:
-    rc = B.function(name)(*args)
-    if rc != B.MOE_OK:
-        raise B.MoeError(name, rc)
+def _types(name: str, *tensors: torch.Tensor) -> ValueError:
+    return ValueError(f"{name}: operands of one type, bfloat16 or float16, expected; got "
+                      f"{', '.join(str(t.dtype) for t in tensors)}")
 
 
 def expert_order(topk_ids: torch.Tensor, num_experts: int, expert_base: int = 0):
@@ -155,24 +139,32 @@ def expert_order(topk_ids: torch.Tensor, num_experts: int, expert_base: int = 0)
 def _by_row(fn: str, name: str, a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
             out: Optional[torch.Tensor], stream, forward: bool) -> torch.Tensor:
     dev = _device(a, w, offsets, out)
-    shape = _dims(w, "w", 3)
-    E, N, K = shape
-    rows = _dims(a, name, 2)[0]
+    rows, a_width = _dims(a, name, 2)
+    E, N, K = shape = _dims(w, "w", 3)
     width, out_width = (K, N) if forward else (N, K)
-    w_e, w_n = _bank(w, "w", shape)
-    ld = _rows(a, name, width, rows)
-    _check_offsets(offsets, E)
     dtype = a.dtype
+    code = _HALF.get(dtype)
+    if code is None or w.dtype is not dtype:
+        raise _types(fn, a, w)
+    w_e, w_n, step = w.stride()
+    if step != 1 or w_n < K:
+        w_e, w_n = _bank(w, "w", shape)
+    ld, step = a.stride()
+    if a_width != width or step != 1 or ld < width:
+        ld = _rows(a, name, width, rows)
+    _check_offsets(offsets, E)
     if out is None:
-        code = _half(fn, dtype, w.dtype)
         out = _empty((rows, out_width), dtype, dev, stream)
         out_ld = out_width
     else:
-        code = _half(fn, dtype, w.dtype, out.dtype)
+        if out.dtype is not dtype:
+            raise _types(fn, a, out)
         out_ld = _rows(out, "out", out_width, rows)
     h = _handle(dev, stream)
-    _call(fn, code, a.data_ptr(), ld, w.data_ptr(), w_e, w_n, offsets.data_ptr(), E, rows, N, K, out.data_ptr(),
-          out_ld, _workspace(dev, h), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    rc = B.function(fn)(code, a.data_ptr(), ld, w.data_ptr(), w_e, w_n, offsets.data_ptr(), E, rows, N, K,
+                        out.data_ptr(), out_ld, _workspace(dev, h), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    if rc:
+        raise B.MoeError(fn, rc)
     return out
 
 
@@ -200,7 +192,9 @@ def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out:
     x_ld = _rows(x, "x", K, rows)
     _check_offsets(offsets, E)
     dtype = dy.dtype
-    code = _half("grouped_mm_dw", dtype, x.dtype)
+    code = _HALF.get(dtype)
+    if code is None or x.dtype is not dtype:
+        raise _types("grouped_mm_dw", dy, x)
     if out_dtype is None:
         out_dtype = dtype if out is None else out.dtype
     if out_dtype is not dtype and out_dtype is not torch.float32:
@@ -215,9 +209,12 @@ def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out:
             raise ValueError(f"out: {out.dtype} {tuple(out.shape)}, expected {out_dtype} [{E}, {N}, {K}]")
         o_e, o_n = _bank(out, "out", out.shape)
     h = _handle(dev, stream)
-    _call("moe_grouped_mm_dw", code, dy.data_ptr(), ld, x.data_ptr(), x_ld, offsets.data_ptr(), E, rows, N, K,
-          code if out_dtype is dtype else B.MOE_FP32, int(accumulate), out.data_ptr(), o_e, o_n, _workspace(dev, h),
-          B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    rc = B.function("moe_grouped_mm_dw")(
+        code, dy.data_ptr(), ld, x.data_ptr(), x_ld, offsets.data_ptr(), E, rows, N, K,
+        code if out_dtype is dtype else B.MOE_FP32, 1 if accumulate else 0, out.data_ptr(), o_e, o_n,
+        _workspace(dev, h), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    if rc:
+        raise B.MoeError("moe_grouped_mm_dw", rc)
     return out
 
 
@@ -249,7 +246,9 @@ def quant_fp8_block(x: torch.Tensor, rows: Optional[torch.Tensor] = None, gated:
     scale per 128 columns; gated: of silu(x[:, :K]) * x[:, K:] with K half of x's columns.  scale has shape
     [rows, ceil(K / 128)], in any strides."""
     dev = _device(x, rows, out, scale)
-    code = _half("quant_fp8_block", x.dtype)
+    code = _HALF.get(x.dtype)
+    if code is None:
+        raise _types("quant_fp8_block", x)
     x_rows, K = _dims(x, "x", 2)
     ld = _rows(x, "x", K, x_rows)
     if gated:
@@ -276,8 +275,11 @@ def quant_fp8_block(x: torch.Tensor, rows: Optional[torch.Tensor] = None, gated:
         if scale.dtype is not torch.float32 or tuple(scale.shape) != (R, G):
             raise ValueError(f"scale: {scale.dtype} {tuple(scale.shape)}, expected float32 [{R}, {G}]")
         s_m, s_g = scale.stride()
-    _call("moe_quant_fp8_block", code, x.data_ptr(), ld, x_rows, index, R, K, 1 if gated else 0, out.data_ptr(), out_ld,
-          scale.data_ptr(), s_m, s_g, _handle(dev, stream))
+    rc = B.function("moe_quant_fp8_block")(
+        code, x.data_ptr(), ld, x_rows, index, R, K, 1 if gated else 0, out.data_ptr(), out_ld, scale.data_ptr(), s_m,
+        s_g, _handle(dev, stream))
+    if rc:
+        raise B.MoeError("moe_quant_fp8_block", rc)
     return out, scale
 
 
@@ -305,9 +307,9 @@ def gemm_fp8_block(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_sc
         at = offsets.data_ptr()
     R, G, GN = _dims(x, "x", 2)[0], -(-K // BLOCK), -(-N // BLOCK)
     ld = _rows(x, "x", K, R)
-    if tuple(x_scale.shape) != (R, G):
+    if x_scale.shape != (R, G):
         raise ValueError(f"x_scale: {tuple(x_scale.shape)}, expected [{R}, {G}]")
-    if tuple(w_scale.shape) != ((GN, G) if offsets is None else (E, GN, G)):
+    if w_scale.shape != ((GN, G) if offsets is None else (E, GN, G)):
         raise ValueError(f"w_scale: {tuple(w_scale.shape)}, expected [{'' if offsets is None else f'{E}, '}{GN}, {G}]")
     ws = w_scale.stride()
     if out is None:
@@ -325,7 +327,10 @@ def gemm_fp8_block(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_sc
         out_ld = _rows(out, "out", N, R)
     s_m, s_g = x_scale.stride()
     h = _handle(dev, stream)
-    _call("moe_gemm_fp8_block", x.data_ptr(), ld, x_scale.data_ptr(), s_m, s_g, w.data_ptr(), w_e, w_n,
-          w_scale.data_ptr(), 0 if offsets is None else ws[0], ws[-2], ws[-1], at, E, R, N, K, code, out.data_ptr(),
-          out_ld, _workspace(dev, h), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    rc = B.function("moe_gemm_fp8_block")(
+        x.data_ptr(), ld, x_scale.data_ptr(), s_m, s_g, w.data_ptr(), w_e, w_n, w_scale.data_ptr(),
+        0 if offsets is None else ws[0], ws[-2], ws[-1], at, E, R, N, K, code, out.data_ptr(), out_ld,
+        _workspace(dev, h), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    if rc:
+        raise B.MoeError("moe_gemm_fp8_block", rc)
     return out
