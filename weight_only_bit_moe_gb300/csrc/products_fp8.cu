@@ -62,18 +62,6 @@ struct Fp8TcArgs {
   int wide_store;        // 32-byte stores are aligned
 };
 
-// Position in a ring of N slots and the parity of the pass through it.
-template <int N>
-struct Ring {
-  uint32_t i = 0, phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++i == N) {
-      i = 0;
-      phase ^= 1;
-    }
-  }
-};
-
 template <bool ROWS_M>
 __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_constant__ Fp8TcArgs a) {
   using C = Fp8Cfg<ROWS_M>;
@@ -125,8 +113,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
       const int rows = (it.n + 15) / 16 * 16;  // copied
       for (int t = it.t0; t < it.t1; ++t) {
         const int s = at_slot.i;
-        mbar_wait(&empty[s], at_slot.phase ^ 1, abort_flag, g.status);
-        __syncwarp();
+        if (!warp_wait(&empty[s], at_slot.phase ^ 1, abort_flag, g.status)) break;
         const uint32_t bar = smem_u32(&full[s]), ps = smem_s + s * C::kSlot, qs = ps + C::kPBytes;
         expect_tx_elect(&full[s], (C::kFeatures + rows) * 128);
         tma1_3d(ROWS_M ? qs : ps, &a.map_w, 128 * t, it.p0, it.e, bar);
@@ -165,9 +152,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
       const uint32_t idesc = idesc_f16_f32(128, ROWS_M ? 256 : (it.n + 15) / 16 * 16, 0u);
       for (int t = it.t0; t < it.t1; ++t) {
         const uint32_t s = at_slot.i, b = at_buf.i;
-        mbar_wait(&full[s], at_slot.phase, abort_flag, g.status);
-        mbar_wait(&acc_empty[b], at_buf.phase ^ 1, abort_flag, g.status);
-        __syncwarp();
+        if (!warp_wait(&full[s], at_slot.phase, abort_flag, g.status) ||
+            !warp_wait(&acc_empty[b], at_buf.phase ^ 1, abort_flag, g.status))
+          break;
         tc_fence_after();
         const uint32_t slot = s * (C::kSlot >> 4);  // (descriptor addresses count 16 bytes and do not carry)
         umma1_f8_block_elect(tmem + b * C::kBufCols, pd + slot, qd + slot, idesc);
@@ -218,7 +205,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
             if (t + h < it.t1) {
               const uint32_t b = at_buf.i;
               const float sc = h ? s1 : s0;
-              mbar_wait(&acc_full[b], at_buf.phase, abort_flag, g.status);
+              warp_wait(&acc_full[b], at_buf.phase, abort_flag, g.status);
               tc_fence_after();
               const uint32_t tb = lanes + b * C::kBufCols + sub * 128;
 #pragma unroll
@@ -255,7 +242,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
             named_bar_sync(2, kF8EpiThreads);
           }
           const uint32_t b = at_buf.i;
-          mbar_wait(&acc_full[b], at_buf.phase, abort_flag, g.status);
+          warp_wait(&acc_full[b], at_buf.phase, abort_flag, g.status);
           tc_fence_after();
           uint32_t v[32];
           const bool live = 32 * sub < it.n;

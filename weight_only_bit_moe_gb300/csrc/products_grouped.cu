@@ -277,69 +277,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ producers of P (warp 0) and Q (warp 2)
-    uint32_t k = 0;
+    Ring<kStages> slot;
+    uint32_t filled = 0;
     for (GtWalk<MODE> at(pl, q_tiles, pair, a.pairs); at.w < items; at.next()) {
       const ProdItem it = at.item(g, pl, start);
       const int half = gt_half<MODE>(it.n);
       int r0 = 0, r1 = 0;
       if (MODE == kProdDw) group_rows(g, it.e, r0, r1);
       const int p = it.p0 + rank * 128, q = it.q0 + rank * half;
-      for (int t = it.t0; t < it.t1; ++t, ++k) {
-        const int s = k % kStages, row = r0 + 64 * t;
-        mbar_wait(&empty[s], ((k / kStages) + 1) & 1, abort_flag, g.status);
-        if (*abort_flag) break;
-        __syncwarp();
-        const uint32_t slot = smem_s + s * kGtStageBytes, bar = full_s + 8 * s;
+      for (int t = it.t0; t < it.t1; ++t) {
+        const int row = r0 + 64 * t;
+        if (!warp_wait(&empty[slot.i], slot.phase ^ 1, abort_flag, g.status)) break;
+        const uint32_t dst = smem_s + slot.i * kGtStageBytes, bar = full_s + 8 * slot.i;
         if (warp == 0) {
-          if (rank == 0) expect_tx_elect(&full[s], gt_stage_bytes<MODE>(half, min(64, r1 - row)));
-          gt_load_p<MODE>(a, it, t, p, row, r1, slot, bar);
+          if (rank == 0) expect_tx_elect(&full[slot.i], gt_stage_bytes<MODE>(half, min(64, r1 - row)));
+          gt_load_p<MODE>(a, it, t, p, row, r1, dst, bar);
         } else {
-          gt_load_q<MODE>(a, t, q, half, row, r1, slot + kGtOperandBytes, bar);
+          gt_load_q<MODE>(a, t, q, half, row, r1, dst + kGtOperandBytes, bar);
         }
+        slot.next();
+        ++filled;
       }
       if (*abort_flag) break;
     }
     // leave no copy in flight (the leader's barriers count the peer's copies too)
     if (rank == 0 && warp == 0)
-      for (uint32_t i = 0; i < (uint32_t)kStages && i < k; ++i) {
-        const uint32_t u = k - 1 - i;
+      for (uint32_t i = 0; i < (uint32_t)kStages && i < filled; ++i) {
+        const uint32_t u = filled - 1 - i;
         mbar_drain(&full[u % kStages], (u / kStages) & 1, g.status);
       }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
     if (rank == 0) {
       constexpr uint32_t kMajors = MODE == kProdFwd ? 0u : (MODE == kProdDx ? kIdescMajorA : (kIdescMajorA | kIdescMajorB));
-      constexpr uint32_t kStepA = MODE == kProdFwd ? 2 : 128, kStepB = MODE == kProdDw ? 128 : 2;  // 16 terms, 16-byte units
+      constexpr int kStepA = MODE == kProdFwd ? 2 : 128, kStepB = MODE == kProdDw ? 128 : 2;  // 16 terms, 16-byte units
       const uint32_t bf = g.in_type == kBf16 ? 1u : 0u;
-      uint32_t k = 0, ic = 0;
+      const uint64_t pd0 = MODE == kProdFwd ? smem_desc_sw128(smem_s) : smem_desc_sw128_mn(smem_s, 8192);
+      const uint64_t qd0 = MODE == kProdDw ? smem_desc_sw128_mn(smem_s + kGtOperandBytes, 8192)
+                                           : smem_desc_sw128(smem_s + kGtOperandBytes);
+      Ring<kStages> slot;
+      Ring<2> acc;
       for (GtWalk<MODE> at(pl, q_tiles, pair, a.pairs); at.w < items; at.next()) {
         const ProdItem it = at.item(g, pl, start);
         if (it.t0 >= it.t1) continue;  // (dW: no rows; the epilogue takes zeros)
         int r0 = 0, r1 = 0;
         if (MODE == kProdDw) group_rows(g, it.e, r0, r1);
         const uint32_t idesc = idesc_f16_f32(256, 2 * gt_half<MODE>(it.n), bf) | kMajors;
-        const int acc = ic & 1;
-        mbar_wait(&acc_empty[acc], ((ic >> 1) + 1) & 1, abort_flag, g.status);
-        __syncwarp();
-        tc_fence_after();
-        const uint32_t d = tmem + acc * kGtN;
-        for (int t = it.t0; t < it.t1; ++t, ++k) {
-          const int s = k % kStages;
-          mbar_wait(&full[s], (k / kStages) & 1, abort_flag, g.status);
-          __syncwarp();
+        warp_wait(&acc_empty[acc.i], acc.phase ^ 1, abort_flag, g.status);
+        const uint32_t d = tmem + acc.i * kGtN;
+        for (int t = it.t0; t < it.t1; ++t) {
+          if (!warp_wait(&full[slot.i], slot.phase, abort_flag, g.status)) break;
           tc_fence_after();
-          const uint32_t slot = smem_s + s * kGtStageBytes;
-          const uint64_t pd = MODE == kProdFwd ? smem_desc_sw128(slot) : smem_desc_sw128_mn(slot, 8192);
-          const uint64_t qd = MODE == kProdDw ? smem_desc_sw128_mn(slot + kGtOperandBytes, 8192)
-                                              : smem_desc_sw128(slot + kGtOperandBytes);
-          const int steps = MODE == kProdDw ? (min(64, r1 - (r0 + 64 * t)) + 15) / 16 : 4;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < steps) umma2_f16_elect(d, pd + i * kStepA, qd + i * kStepB, idesc, (t > it.t0 || i > 0) ? 1u : 0u);
-          umma2_commit_elect(&empty[s]);
+          const uint32_t at_slot = slot.i * (kGtStageBytes >> 4);  // (descriptor addresses count 16 bytes and do not carry)
+          const uint64_t pd = pd0 + at_slot, qd = qd0 + at_slot;
+          const int rows = MODE == kProdDw ? r1 - (r0 + 64 * t) : 64;
+          if (rows > 48) {
+            umma2_f16_stage_elect<kStepA, kStepB>(d, pd, qd, idesc, t > it.t0 ? 1u : 0u);
+          } else {
+            for (int i = 0; 16 * i < rows; ++i)
+              umma2_f16_elect(d, pd + i * kStepA, qd + i * kStepB, idesc, (t > it.t0 || i > 0) ? 1u : 0u);
+          }
+          umma2_commit_elect(&empty[slot.i]);
+          slot.next();
         }
-        umma2_commit_elect(&acc_full[acc]);
-        ++ic;
+        umma2_commit_elect(&acc_full[acc.i]);
+        acc.next();
       }
       umma2_commit_elect(drain_bar);
       mbar_drain(drain_bar, 0, g.status);
@@ -360,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
       const bool none = it.t0 >= it.t1;                 // no terms: the sums are zeros
       const int acc = ic & 1;
       if (!none) {
-        mbar_wait(&acc_full[acc], (ic >> 1) & 1, abort_flag, g.status);
+        warp_wait(&acc_full[acc], (ic >> 1) & 1, abort_flag, g.status);
         tc_fence_after();
       }
       const uint32_t tb = tmem + ((uint32_t)(quarter * 32) << 16) + acc * kGtN;

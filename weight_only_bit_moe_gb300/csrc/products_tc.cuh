@@ -118,6 +118,24 @@ __device__ __forceinline__ void umma2_f16_elect(uint32_t d, uint64_t a, uint64_t
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// Four such MMAs, 64 terms; the descriptors advance by DA and DB (16-byte units)
+// a step.  One election for the four: the issuing warp's time per stage bounds
+// narrow tiles.
+template <int DA, int DB>
+__device__ __forceinline__ void umma2_f16_stage_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "add.u64 a1, %1, %3;\n\tadd.u64 a2, a1, %3;\n\tadd.u64 a3, a2, %3;\n\t"
+      "add.u64 b1, %2, %4;\n\tadd.u64 b2, b1, %4;\n\tadd.u64 b3, b2, %4;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %5, p;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %5, 1;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "n"(DA), "n"(DB), "r"(idesc), "r"(acc)
+      : "memory");
+}
 // Arrive on the barrier at this offset in both CTAs once the MMAs issued so far are done.
 __device__ __forceinline__ void umma2_commit_elect(uint64_t* bar) {
   asm volatile(
@@ -238,6 +256,24 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t v;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
   return v;
+}
+
+// Position in a ring of N slots and the parity of the pass through it.
+template <int N>
+struct Ring {
+  uint32_t i = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// mbar_wait by a whole warp, with one answer for all its lanes: false once the CTA
+// has given up, and the role then leaves its loop.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
 }
 
 // ---------------------------------------------------------------- work items
