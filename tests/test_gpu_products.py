@@ -121,6 +121,26 @@ def test_dw_accumulate(sizes, N, K):
         U.assert_within(out[e], ref + s, mag + s.abs(), m + 1, f"accumulated dw expert {e}")
 
 
+@pytest.mark.parametrize("sizes", [[2500], [0, 1900, 0], [1500, 40, 1]])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_dw_long_sums_over_few_tiles(sizes, accumulate):
+    # the rows of an expert are cut into slices, of which a short or empty expert fills few or none
+    P = products()
+    off = U.offsets_of(sizes)
+    N, K = 264, 200
+    dy = normal(sum(sizes), N, dtype=torch.bfloat16, seed=40)
+    x = normal(sum(sizes), K, dtype=torch.bfloat16, seed=41)
+    start = normal(len(sizes), N, K, dtype=torch.float32, seed=42) if accumulate else None
+    out = P.grouped_mm_dw(dy, x, off, out=None if start is None else start.clone(), out_dtype=torch.float32,
+                          accumulate=accumulate)
+    half = P.grouped_mm_dw(dy, x, off)
+    for e, (m, ref, mag) in enumerate(U.ref_dw(dy, x, off)):
+        U.assert_within(half[e], ref, mag, m, f"bf16 dw expert {e}")
+        if accumulate:
+            ref, mag = ref + start[e].double(), mag + start[e].double().abs()
+        U.assert_within(out[e], ref, mag, m + 1, f"dw expert {e}")
+
+
 def test_a_row_of_another_expert_does_not_reach_a_gradient():
     # expert 1's rows, next to expert 0's and 2's last and first, hold NaN and infinities
     P = products()
