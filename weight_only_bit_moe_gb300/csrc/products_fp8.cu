@@ -92,6 +92,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
     tmem_relinquish();
   }
   if (warp == kF8Producer && lane < 5) prefetch_map(lane < 4 ? &a.map_x[lane] : &a.map_w);
+  // (launched early: everything before this line touches nothing that an earlier kernel writes)
+  grid_dependents_launch();
+  grid_dependency_wait();
   RowPlan pl;
   pl.p_tiles = (g.N + C::kFeatures - 1) / C::kFeatures;
   pl.stages = (g.K + 127) / 128;
@@ -370,8 +373,7 @@ static cudaError_t launch_orientation(const Fp8TcArgs& a, int sms, cudaStream_t 
     if (rc != cudaSuccess) return rc;
     ready[dev].store(true, std::memory_order_release);
   }
-  fp8_tc_kernel<ROWS_M><<<sms, kF8Threads, bytes, st>>>(a);
-  return cudaPeekAtLastError();
+  return launch_dependent(fp8_tc_kernel<ROWS_M>, dim3(sms), dim3(kF8Threads), bytes, st, a);
 }
 
 static bool grid16b(const void* p, int64_t stride) {

@@ -252,6 +252,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
   }
 
   if (warp == 0 && lane < 6) prefetch_map(lane < 4 ? &a.map_q[lane] : lane == 4 ? &a.map_p : &a.map_out);
+  // (launched early: everything before this line touches nothing that an earlier kernel writes)
+  grid_dependents_launch();
+  grid_dependency_wait();
   // --- the plan: tiles per group (rows), or a regular grid of tiles (dW)
   RowPlan pl;
   const int j_dim = MODE == kProdDx ? g.K : g.N;
@@ -556,8 +559,7 @@ static cudaError_t launch_mode(GroupedTcArgs& a, cudaStream_t st) {
     if (rc != cudaSuccess) return rc;
     ready[dev].store(true, std::memory_order_release);
   }
-  grouped_tc_kernel<MODE><<<2 * a.pairs, kGtThreads, GtSmem<MODE>::kAlloc, st>>>(a);
-  return cudaPeekAtLastError();
+  return launch_dependent(grouped_tc_kernel<MODE>, dim3(2 * a.pairs), dim3(kGtThreads), GtSmem<MODE>::kAlloc, st, a);
 }
 
 static bool grid16(const void* p, int64_t stride) {

@@ -184,6 +184,8 @@ __global__ void __launch_bounds__(kQuThreads, kQuCtas) quant_rows_kernel(const _
   constexpr int kCols = GATED ? 512 : 1024;
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * kQuWarps + (threadIdx.x >> 5), c0 = blockIdx.y * kCols;
+  grid_dependents_launch();
+  grid_dependency_wait();
   if (row >= a.rows) return;
   const int src = a.row_index ? __ldg(a.row_index + row) : row;
   if (c0 + kCols <= a.K && (unsigned)src < (unsigned)a.x_rows) quant_unit<GATED, TYPE, true>(a, row, src, c0, lane);
@@ -227,19 +229,19 @@ __global__ void __launch_bounds__(kQuThreads) quant_any_kernel(const __grid_cons
 }
 
 template <bool GATED>
-static void launch_quant(const QuantArgs& a, int sms, cudaStream_t st) {
+static cudaError_t launch_quant(const QuantArgs& a, int sms, cudaStream_t st) {
   const int cols = GATED ? 512 : 1024;  // columns a warp takes
   const int per_row = (a.K + cols - 1) / cols;
   const bool wide = ((reinterpret_cast<uintptr_t>(a.x) & 15) | (reinterpret_cast<uintptr_t>(a.q) & 7)) == 0 &&
                     a.x_ld % 8 == 0 && a.q_ld % 8 == 0 && a.K % 8 == 0 && per_row <= 65535;
   if (wide) {
     const dim3 grid((unsigned)(((int64_t)a.rows + kQuWarps - 1) / kQuWarps), (unsigned)per_row);
-    if (a.type == kBf16) quant_rows_kernel<GATED, kBf16><<<grid, kQuThreads, 0, st>>>(a);
-    else quant_rows_kernel<GATED, kFp16><<<grid, kQuThreads, 0, st>>>(a);
-    return;
+    return launch_dependent(a.type == kBf16 ? quant_rows_kernel<GATED, kBf16> : quant_rows_kernel<GATED, kFp16>, grid,
+                            dim3(kQuThreads), 0, st, a);
   }
   const int64_t ctas = ((int64_t)a.rows * ((a.K + 127) / 128) + kQuWarps - 1) / kQuWarps;
   quant_any_kernel<GATED><<<(int)(ctas < sms * 8 ? ctas : sms * 8), kQuThreads, 0, st>>>(a);
+  return cudaPeekAtLastError();
 }
 
 }  // namespace moe
@@ -258,7 +260,7 @@ extern "C" int moe_quant_fp8_block(int dtype, const void* x, int64_t x_stride, i
   if (sms <= 0) return MOE_ERR_CUDA;
   const QuantArgs a{x, x_stride, x_rows, row_index, rows, K, dtype, static_cast<uint8_t*>(q), q_stride, scale,
                     scale_stride_m, scale_stride_g};
-  if (gated) launch_quant<true>(a, sms, (cudaStream_t)stream);
-  else launch_quant<false>(a, sms, (cudaStream_t)stream);
-  return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const cudaError_t rc = gated ? launch_quant<true>(a, sms, (cudaStream_t)stream)
+                               : launch_quant<false>(a, sms, (cudaStream_t)stream);
+  return rc == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
