@@ -38,7 +38,7 @@
 
 namespace moe {
 
-constexpr int kGtThreads = 384;       // producer, MMA, two idle warps, eight epilogue warps
+constexpr int kGtThreads = 384;       // three producer warps, MMA, eight epilogue warps
 constexpr int kGtEpiWarp0 = 4, kGtEpiWarps = 8, kGtEpiThreads = 256;
 constexpr int kGtP = 256;             // P rows per pair
 constexpr int kGtN = 256;             // Q rows per pair, at most
@@ -136,23 +136,19 @@ struct GtWalk {
   }
 };
 
-// The last rows [row, r1) of a group, fewer than 64, of two blocks of 64 columns:
-// whole sixteens as boxes, the rest by index in fours, rows at or past r1 as zeros
-// (row `none` lies outside the tensor).
+// The last rows [row, r1) of a group, fewer than 64, of a block of 64 columns: whole
+// sixteens as boxes, the rest by index in fours, rows at or past r1 as zeros (row
+// `none` lies outside the tensor).
 __device__ __forceinline__ void gt_tail(const CUtensorMap* sixteen, const CUtensorMap* single, int col, int row, int r1,
                                         int none, uint32_t slot, uint32_t bar) {
   int b = row;
-  for (; b + 16 <= r1; b += 16, slot += 2048) {
-    tma2_2d(slot, sixteen, col, b, bar);
-    tma2_2d(slot + 8192, sixteen, col + 64, b, bar);
-  }
+  for (; b + 16 <= r1; b += 16, slot += 2048) tma2_2d(slot, sixteen, col, b, bar);
   if (b == r1) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i, b += 4, slot += 512) {
     const int4 r = make_int4(b < r1 ? b : none, b + 1 < r1 ? b + 1 : none, b + 2 < r1 ? b + 2 : none,
                              b + 3 < r1 ? b + 3 : none);
     tma2_gather4(slot, single, col, r, bar);
-    tma2_gather4(slot + 8192, single, col + 64, r, bar);
   }
 }
 
@@ -171,6 +167,7 @@ __device__ __forceinline__ void gt_load_p(const GroupedTcArgs& a, const ProdItem
     }
   } else if (r1 - row < 64) {
     gt_tail(&a.map_tail[0], &a.map_tail[1], p, row, r1, a.g.rows, slot, bar);
+    gt_tail(&a.map_tail[0], &a.map_tail[1], p + 64, row, r1, a.g.rows, slot + 8192, bar);
   } else if (a.blocked) {
     tma2_3d(slot, &a.map_p, 0, row, p / 64, bar);
   } else {
@@ -178,27 +175,28 @@ __device__ __forceinline__ void gt_load_p(const GroupedTcArgs& a, const ProdItem
     tma2_2d(slot + 8192, &a.map_p, p + 64, row, bar);
   }
 }
+// Q has two producers: by row the boxes of 128 and 64 rows and those of 32 and 16
+// (a stage with three boxes took longer than its MMAs from one warp); dW's tail by
+// column block.
 template <int MODE>
-__device__ __forceinline__ void gt_load_q(const GroupedTcArgs& a, int t, int q, int half, int row, int r1,
+__device__ __forceinline__ void gt_load_q(const GroupedTcArgs& a, int which, int t, int q, int half, int row, int r1,
                                           uint32_t slot, uint32_t bar) {
   if (MODE != kProdDw) {
-    // rows in boxes of 128, or of 64, 32 and 16
-    int at = 0;
+    int at = which == 0 ? 0 : half & ~63;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int box = 128 >> i;
+    for (int i = 0; i < 2; ++i) {
+      const int box = (which == 0 ? 128 : 32) >> i;
       if (half & box) {
-        tma2_2d(slot + 128 * at, &a.map_q[i], 64 * t, q + at, bar);
+        tma2_2d(slot + 128 * at, &a.map_q[2 * which + i], 64 * t, q + at, bar);
         at += box;
       }
     }
   } else if (r1 - row < 64) {
-    gt_tail(&a.map_tail[2], &a.map_tail[3], q, row, r1, a.g.rows, slot, bar);
+    gt_tail(&a.map_tail[2], &a.map_tail[3], q + 64 * which, row, r1, a.g.rows, slot + 8192 * which, bar);
   } else if (a.blocked) {
-    tma2_3d(slot, &a.map_dw_q, 0, row, q / 64, bar);
+    if (which == 0) tma2_3d(slot, &a.map_dw_q, 0, row, q / 64, bar);
   } else {
-    tma2_2d(slot, &a.map_dw_q, q, row, bar);
-    tma2_2d(slot + 8192, &a.map_dw_q, q + 64, row, bar);
+    tma2_2d(slot + 8192 * which, &a.map_dw_q, q + 64 * which, row, bar);
   }
 }
 
@@ -278,8 +276,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
   const int items = pl.tiles * pl.S;
   const uint32_t full_s = map_to_rank(smem_u32(full), 0);
 
-  if (warp == 0 || warp == 2) {
-    // ------------------------------------------------------------ producers of P (warp 0) and Q (warp 2)
+  if (warp == 0 || (warp >= 2 && warp < kGtEpiWarp0)) {
+    // ------------------------------------------------------------ producers of P (warp 0) and Q (warps 2, 3)
     Ring<kStages> slot;
     uint32_t filled = 0;
     for (GtWalk<MODE> at(pl, q_tiles, pair, a.pairs); at.w < items; at.next()) {
@@ -296,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
           if (rank == 0) expect_tx_elect(&full[slot.i], gt_stage_bytes<MODE>(half, min(64, r1 - row)));
           gt_load_p<MODE>(a, it, t, p, row, r1, dst, bar);
         } else {
-          gt_load_q<MODE>(a, t, q, half, row, r1, dst + kGtOperandBytes, bar);
+          gt_load_q<MODE>(a, warp - 2, t, q, half, row, r1, dst + kGtOperandBytes, bar);
         }
         slot.next();
         ++filled;
