@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kMisc);  // [0] tmem base, [1] abort, [2] last
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&misc[1]);
   const ProdArgs& g = a.g;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
