@@ -34,11 +34,31 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t both(float v) { return pack2(__float_as_uint(v), __float_as_uint(v)); }
 
-// silu(g) * u, each operation rounded to fp32.  A cheaper exponential and quotient
-// (the special-function units with a correction, within 2^-21) took 11.4 instead of
-// 17.2 us for 4093 rows of 2880, but moved more values across the boundary between
-// two codes: 2.5e-4 relative error of the codes against 64 bits instead of 4e-6.
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), u); }
+// silu(g) * u = g / (1 + exp(-g)) * u of two values, each operation rounded to
+// fp32.  The quotient is one Newton step in the form that Markstein gives for
+// division: r = 1 / d to within an ulp, q = g r, q + (g - q d) r with the residual
+// exact in a fused multiply-add, which rounds like the quotient itself.  Where d
+// passes 2^126 (g below -87.3) r is flushed to 0, and so is the result.
+//
+// A cheaper exponential as well (2^t on the special-function unit with a
+// correction) took 11.4 instead of 12.6 us for 4093 rows of 2880, but moved more
+// values across the boundary between two codes: 2.5e-4 relative error of the codes
+// against 64 bits instead of at most 7e-5.
+__device__ __forceinline__ void silu_mul2(float& g0, float& g1, float u0, float u1) {
+  const float d0 = fmin_nan(1.0f + expf(-g0), 1.7014118e38f), d1 = fmin_nan(1.0f + expf(-g1), 1.7014118e38f);
+  float r0, r1;  // -1 / d
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(-d0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(-d1));
+  const uint64_t n = mul2(pack2(__float_as_uint(g0), __float_as_uint(g1)), both(-1.0f));
+  const uint64_t d = pack2(__float_as_uint(d0), __float_as_uint(d1)), r = pack2(__float_as_uint(r0), __float_as_uint(r1));
+  uint64_t q = mul2(n, r), m = n;
+  fma2(m, q, d);  // q d - g
+  fma2(q, m, r);
+  uint32_t v0, v1;
+  unpack2(mul2(q, pack2(__float_as_uint(u0), __float_as_uint(u1))), v0, v1);
+  g0 = __uint_as_float(v0);
+  g1 = __uint_as_float(v1);
+}
 
 // Scale of a block whose largest magnitude is `top`.
 __device__ __forceinline__ float block_scale(float top) { return fmax_nan(__fdiv_rn(top, 448.0f), 1.17549435e-38f); }
@@ -154,7 +174,7 @@ __device__ __forceinline__ void quant_unit(const QuantArgs& a, int row, int src,
       widen8<TYPE>(in[i], v[i]);
       widen8<TYPE>(up[i], w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = silu_mul(v[i][j], w[j]);
+      for (int j = 0; j < 8; j += 2) silu_mul2(v[i][j], v[i][j + 1], w[j], w[j + 1]);
     }
     top = block_max2(v, lane);
     mine = mine2(lane);
@@ -211,7 +231,10 @@ __global__ void __launch_bounds__(kQuThreads) quant_any_kernel(const __grid_cons
       if (live && c < a.K) {
         const int64_t at = (int64_t)src * a.x_ld + c;
         v[i] = load_elem(a.x, at, a.type);
-        if (GATED) v[i] = silu_mul(v[i], load_elem(a.x, at + a.K, a.type));
+        if (GATED) {
+          float unused = 0.0f;
+          silu_mul2(v[i], unused, load_elem(a.x, at + a.K, a.type), 0.0f);
+        }
       }
       top = fmax_nan(top, fabsf(v[i]));
     }

@@ -46,8 +46,9 @@ def _workspace(device: int, handle: int) -> int:
     return ws[0]
 
 
-def _empty(shape, dtype: torch.dtype, device: int, stream) -> torch.Tensor:
-    """An output of a kernel that runs on `stream`, from that stream's memory."""
+def _empty(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """An output on `like`'s device of a kernel that runs on `stream`, from that stream's memory."""
+    device = like.device  # (a device object: torch takes 2 us longer to make a tensor for a device number)
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if isinstance(stream, int):
@@ -154,7 +155,7 @@ def _by_row(fn: str, name: str, a: torch.Tensor, w: torch.Tensor, offsets: torch
         ld = _rows(a, name, width, rows)
     _check_offsets(offsets, E)
     if out is None:
-        out = _empty((rows, out_width), dtype, dev, stream)
+        out = _empty((rows, out_width), dtype, a, stream)
         out_ld = out_width
     else:
         if out.dtype is not dtype:
@@ -202,7 +203,7 @@ def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out:
     if accumulate and (out is None or out_dtype is not torch.float32):
         raise ValueError("grouped_mm_dw: accumulate needs a float32 out")
     if out is None:
-        out = _empty((E, N, K), out_dtype, dev, stream)
+        out = _empty((E, N, K), out_dtype, dy, stream)
         o_e, o_n = N * K, K
     else:
         if tuple(out.shape) != (E, N, K) or out.dtype is not out_dtype:
@@ -262,14 +263,14 @@ def quant_fp8_block(x: torch.Tensor, rows: Optional[torch.Tensor] = None, gated:
         R, index = rows.shape[0], rows.data_ptr()
     G = -(-K // BLOCK)
     if out is None:
-        out = _empty((R, K), torch.float8_e4m3fn, dev, stream)
+        out = _empty((R, K), torch.float8_e4m3fn, x, stream)
         out_ld = K
     else:
         if out.dtype is not torch.float8_e4m3fn:
             raise ValueError(f"out: {out.dtype}, expected float8_e4m3fn")
         out_ld = _rows(out, "out", K, R)
     if scale is None:
-        scale = _empty((R, G), torch.float32, dev, stream)
+        scale = _empty((R, G), torch.float32, x, stream)
         s_m, s_g = G, 1
     else:
         if scale.dtype is not torch.float32 or tuple(scale.shape) != (R, G):
@@ -321,7 +322,7 @@ def gemm_fp8_block(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_sc
         raise ValueError(f"gemm_fp8_block: out of {out_dtype if out is None else out.dtype}, expected bfloat16, "
                          "float16 or float32 and, with out_dtype, that type")
     if out is None:
-        out = _empty((R, N), out_dtype, dev, stream)
+        out = _empty((R, N), out_dtype, x, stream)
         out_ld = N
     else:
         out_ld = _rows(out, "out", N, R)
