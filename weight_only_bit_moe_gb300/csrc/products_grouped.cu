@@ -56,6 +56,7 @@ struct GroupedTcArgs {
   CUtensorMap map_dw_q;       // dW: boxes of Q
   ProdArgs g;
   int pairs;             // CTA pairs of the launch
+  int wide_store;        // fp32 dW: 32-byte stores are aligned
   int blocked;           // operands stored MN-major have whole blocks of 64 columns: one box brings two
 };
 
@@ -419,12 +420,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
       if (finish && MODE == kProdDw) {
         // lane = row of dW[e], registers = 32 consecutive columns, 128 bytes of the row (two halves of
         // them when the output has 16 bits): into the warp's box, swizzled, and on by TMA, which writes
-        // whole lines and cuts the box at the matrix's edges
+        // whole lines and cuts the box at the matrix's edges.  Of fp32 output half the warps store their
+        // rows' columns themselves, 32 bytes a lane: boxes alone load the shared memory that the MMAs
+        // read from (171 us for 32 empty experts of 2880 x 2880, but 223 to 232 with 230 or 250 rows
+        // each), stores alone the L1's line rate (191, and 223 to 226); halved, 171 and 205 to 207.
         const bool wide = g.out_type == kFp32;
         const int per_warp = kGtN / 2 / (wide ? 32 : 64);
         for (int i = 0; i < per_warp; ++i) {
           const int c = sub * 4 + (wide ? i : 2 * i);  // first 32-column chunk of the box
           if (32 * c >= it.n || p >= g.N) continue;
+          if (a.wide_store && !g.accumulate && wide && sub == 1) {
+            uint32_t v[32];
+            columns(c, v);
+            const int row = p + lane, col = it.q0 + 32 * c;
+            if (row < g.N) {
+              float* dst = static_cast<float*>(g.out) + it.e * g.out_se + (int64_t)row * g.out_ld + col;
+#pragma unroll
+              for (int b = 0; b < 32; b += 8) {
+                const uint32_t o[8] = {v[b], v[b + 1], v[b + 2], v[b + 3], v[b + 4], v[b + 5], v[b + 6], v[b + 7]};
+                if (col + b < g.K) stg256(dst + b, o);  // (K is a multiple of 8)
+              }
+            }
+            __syncwarp();  // whole warps read tensor memory
+            continue;
+          }
           const uint32_t dst = boxes + (box & 1) * 4096;
           if (lane == 0) tma_store_wait_read<1>();  // the box before last has been read
           __syncwarp();
@@ -620,6 +639,7 @@ cudaError_t launch_grouped_tc(const ProdArgs& g, int mode, cudaStream_t st, bool
   const int sms = prod_sm_count();
   if (sms < 2) return cudaErrorInvalidDevice;
   a.pairs = sms / 2;
+  a.wide_store = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0 && g.out_ld % 8 == 0 && g.out_se % 8 == 0;
   *done = true;
   if (mode == kProdFwd) return launch_mode<kProdFwd>(a, st);
   if (mode == kProdDx) return launch_mode<kProdDx>(a, st);
