@@ -48,7 +48,7 @@ typedef enum moe_dtype { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
  *   w       [num_experts, N, K], strides w_stride_e, w_stride_n >= K
  *   out     [rows, N], row stride out_stride >= N
  * Sums are fp32, rounded once to dtype.  num_experts 1..1024, N, K >= 1,
- * rows >= 0 (0 is a no-op).  Tensor cores: x, w and out on 16-byte
+ * 0 <= rows < 2^31 - 1024 (0 is a no-op).  Tensor cores: x, w and out on 16-byte
  * boundaries, every stride a multiple of 8. */
 int moe_grouped_mm(int dtype, const void* x, int64_t x_stride, const void* w, int64_t w_stride_e,
                    int64_t w_stride_n, const int32_t* offsets, int num_experts, int rows, int N, int K,

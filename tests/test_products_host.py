@@ -22,7 +22,7 @@ def mm(lib, fn="moe_grouped_mm", **kw):
 
 
 MM_BAD = [dict(dtype=2), dict(dtype=-1), dict(x_stride=31), dict(w_stride_n=63), dict(out_stride=31),
-          dict(w_stride_e=-1), dict(num_experts=0), dict(num_experts=1025), dict(rows=-1), dict(N=0), dict(K=0),
+          dict(w_stride_e=-1), dict(num_experts=0), dict(num_experts=1025), dict(rows=-1), dict(rows=2 ** 31 - 1), dict(N=0), dict(K=0),
           dict(x=0), dict(w=0), dict(offsets=0), dict(out=0), dict(workspace=0), dict(workspace=BUF + 128),
           dict(x=BUF + 1), dict(w=BUF + 1), dict(out=BUF + 1), dict(N=1 << 23)]
 

@@ -6,11 +6,12 @@ using namespace moe;
 namespace moe {
 
 constexpr int kMaxGroups = 1024;
+constexpr int kMaxRows = 0x7FFFFFFF - 1024;  // row numbers may run past the last one by a tile
 // gridDim.y of the plain kernel counts 64-column tiles
 constexpr int kMaxDim = 65535 * 64;
 
 static int check_products(const ProdArgs& g, const void* workspace, int64_t workspace_bytes) {
-  if (g.E < 1 || g.E > kMaxGroups || g.rows < 0 || g.N < 1 || g.K < 1 || g.N > kMaxDim || g.K > kMaxDim)
+  if (g.E < 1 || g.E > kMaxGroups || g.rows < 0 || g.rows > kMaxRows || g.N < 1 || g.K < 1 || g.N > kMaxDim || g.K > kMaxDim)
     return MOE_ERR_INVALID;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return MOE_ERR_INVALID;
   if (workspace_bytes < MOE_PRODUCTS_WORKSPACE_BYTES) return MOE_ERR_WORKSPACE;

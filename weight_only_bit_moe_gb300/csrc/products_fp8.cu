@@ -33,6 +33,7 @@ namespace moe {
 
 constexpr int kF8Threads = 320;  // eight epilogue warps, producer, MMA
 constexpr int kF8EpiWarps = 8, kF8EpiThreads = 256, kF8Producer = 8, kF8Mma = 9;
+static_assert(kF8Threads == (kF8EpiWarps + 2) * 32, "every other warp would run the epilogue");
 constexpr int kF8FactorStages = 64;  // blocks whose scales are staged at a time (rows on N)
 
 template <bool ROWS_M>
