@@ -17,8 +17,9 @@
  * the arguments; the workspace's status then holds MOE_ERR_INVALID and the
  * outputs of the experts concerned are unspecified.
  *
- * Workspace.  MOE_PRODUCTS_WORKSPACE_BYTES, 256-byte aligned, zeroed by the
- * caller once before its first use and left alone after that; one workspace
+ * Workspace.  MOE_PRODUCTS_WORKSPACE_BYTES, 256-byte aligned, its first
+ * MOE_PRODUCTS_WORKSPACE_HEAD_BYTES zeroed by the caller once before its first
+ * use and left alone after that; one workspace
  * serves any sequence of calls on one stream (calls that may run at the same
  * time need one each).  Its first word is the device status that
  * moe_get_status reads and clears.
@@ -41,6 +42,7 @@ extern "C" {
 typedef enum moe_dtype { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
 
 #define MOE_PRODUCTS_WORKSPACE_BYTES ((int64_t)48 << 20)
+#define MOE_PRODUCTS_WORKSPACE_HEAD_BYTES 8192
 
 /* y[r] = W[e] x[r] for every row r of expert e.
  *   dtype   MOE_BF16 or MOE_FP16: the type of x, w and out

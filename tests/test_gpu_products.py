@@ -342,6 +342,28 @@ def test_graph_capture():
         U.assert_within(out[a:b], ref, mag, 512)
 
 
+def test_graph_capture_on_a_stream_of_its_own():
+    # a capture on a stream without a workspace takes the graph's memory; long sums use its counters twice
+    P = products()
+    off = U.offsets_of([5])
+    w = normal(1, 1024, 4096, dtype=torch.bfloat16, seed=43)
+    x = normal(5, 4096, dtype=torch.bfloat16, seed=44)
+    P.grouped_mm(x, w, off)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first = P.grouped_mm(x, w, off)
+        second = P.grouped_mm(x, w, off)
+    for seed in (45, 46):
+        x.copy_(normal(5, 4096, dtype=torch.bfloat16, seed=seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        (_, ref, mag), = U.ref_fwd(x, w, off)
+        U.assert_within(first, ref, mag, 4096)
+        assert torch.equal(first, second)
+    assert torch.equal(P.grouped_mm(x, w, off), first)  # and outside the graph as before
+
+
 @pytest.mark.parametrize("bad", [[0, 50, 40, 64], [-3, 10, 20, 64], [0, 10, 20, 70]])
 def test_broken_offsets_are_reported(bad):
     # they decrease, start below zero or end past the rows: nothing outside the tensors is touched

@@ -27,6 +27,7 @@ EXPORTED = ("moe_repack_size", "moe_repack_weights", "moe_repack_weights_ex", "m
             "moe_quant_fp8_block", "moe_gemm_fp8_block")
 MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
 MOE_PRODUCTS_WORKSPACE_BYTES = 48 << 20  # workspace of the products in moe_products.h
+MOE_PRODUCTS_WORKSPACE_HEAD_BYTES = 8192  # of which these are zeroed before the first use
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20  # fixed workspace of moe_w4a16_forward_noalloc
 
 

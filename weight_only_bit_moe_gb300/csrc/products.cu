@@ -30,7 +30,11 @@ static int run(const ProdArgs& g, int mode, void* stream) {
   return launch_products_any(g, mode, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// 256 bytes of status, the scratch's counters, its partial tiles.
 static void set_workspace(ProdArgs& g, void* workspace) {
+  static_assert(256 + kProdCounterBytes <= MOE_PRODUCTS_WORKSPACE_HEAD_BYTES, "counters outside the zeroed part");
+  static_assert(256 + kProdCounterBytes + (int64_t)kProdPartials * 128 * 256 * 4 <= MOE_PRODUCTS_WORKSPACE_BYTES,
+                "partial tiles outside the workspace");
   g.status = static_cast<unsigned*>(workspace);
   g.scratch = static_cast<uint8_t*>(workspace) + 256;
 }

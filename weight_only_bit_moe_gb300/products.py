@@ -14,6 +14,7 @@ says where each expert's rows start.  ``expert_order`` makes both from routing i
 """
 from __future__ import annotations
 
+import threading
 from typing import Optional, Tuple
 
 import torch
@@ -24,8 +25,9 @@ BLOCK = 128  # columns per FP8 scale; also rows of a weight block
 _HALF = {torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_FP16}
 _DTYPE = {torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_FP16, torch.float32: B.MOE_FP32}
 
-# One workspace per device and stream, as the kernels of one stream run one after another.
+# One workspace per device and stream, as the kernels of one stream run one after another: (address, tensor).
 _workspaces = {}
+_workspace_lock = threading.Lock()
 
 
 def _handle(device: int, stream) -> int:
@@ -38,12 +40,24 @@ def _handle(device: int, stream) -> int:
 def _workspace(device: int, handle: int) -> int:
     """Address of the workspace of this device and stream."""
     ws = _workspaces.get((device, handle))
-    if ws is None:
-        t = torch.zeros(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
-        # the zeros are written on the current stream, the kernels run on `handle`
-        torch.cuda.current_stream(device).synchronize()
-        ws = _workspaces[(device, handle)] = (t.data_ptr(), t)
-    return ws[0]
+    return ws[0] if ws is not None else _new_workspace(device, handle)
+
+
+def _new_workspace(device: int, handle: int) -> int:
+    if torch.cuda.is_current_stream_capturing():
+        # the graph's own memory, zeroed by the graph: not kept for calls outside it.  The tensor lives until the
+        # next one is made, which is after the call's launch.
+        ws = torch.empty(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=torch.device("cuda", device))
+        ws[:B.MOE_PRODUCTS_WORKSPACE_HEAD_BYTES].zero_()
+        _workspaces["capture"] = (ws.data_ptr(), ws)
+        return ws.data_ptr()
+    with _workspace_lock:
+        if (device, handle) not in _workspaces:
+            ws = torch.zeros(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=torch.device("cuda", device))
+            # the zeros are written on the current stream, the kernels run on `handle`
+            torch.cuda.current_stream(device).synchronize()
+            _workspaces[(device, handle)] = (ws.data_ptr(), ws)
+        return _workspaces[(device, handle)][0]
 
 
 def _empty(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
