@@ -24,7 +24,7 @@
  * time need one each).  Its first word is the device status that
  * moe_get_status reads and clears.
  *
- * Layouts.  Any sizes and strides are computed.  The tensor-core kernels take
+ * Layouts.  Any sizes and strides are computed; outputs must not overlap inputs.  The tensor-core kernels take
  * operands whose base addresses and strides are multiples of 16 bytes (see each
  * function); others run a plain kernel at a small fraction of the speed.
  */
@@ -67,6 +67,7 @@ int moe_grouped_mm_dx(int dtype, const void* dy, int64_t dy_stride, const void* 
  *   dw          [num_experts, N, K], strides dw_stride_e, dw_stride_n >= K, of
  *               type dw_dtype: dtype or MOE_FP32
  *   accumulate  0: dw is written; 1 (MOE_FP32 only): the gradient is added to it
+ *               (values below 2^-126 may count as zeros there)
  * The same inputs give the same bits. */
 int moe_grouped_mm_dw(int dtype, const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
                       const int32_t* offsets, int num_experts, int rows, int N, int K, int dw_dtype,

@@ -304,6 +304,22 @@ def test_autograd():
         assert torch.equal(x.grad[a:b].double(), ref)
 
 
+def test_autograd_with_rows_of_no_expert():
+    # experts held elsewhere: their rows come after the last offset
+    P = products()
+    off = U.offsets_of([7, 20])
+    x = integers(40, 16, top=1, seed=47).requires_grad_()
+    w = integers(2, 24, 16, top=1, seed=48).requires_grad_()
+    y = P.grouped_linear(x, w, off, partial=True)
+    assert (y[27:] == 0).all()
+    y.square().sum().backward()
+    assert (x.grad[27:] == 0).all()
+    for (a, b), ref, _ in U.ref_dx(2 * y.detach(), w.detach(), off):
+        assert torch.equal(x.grad[a:b].double(), ref)
+    for e, (m, ref, _) in enumerate(U.ref_dw(2 * y.detach(), x.detach(), off)):
+        assert torch.equal(w.grad[e].double(), ref)
+
+
 def test_another_stream():
     P = products()
     off = U.offsets_of([100, 28])
@@ -313,6 +329,7 @@ def test_another_stream():
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
     got = [P.grouped_mm(x, w, off, stream=st) for _ in range(4)]
+    got.append(P.grouped_mm(x, w, off, stream=st.cuda_stream))
     with torch.cuda.stream(st):
         got.append(P.grouped_mm(x, w, off))
     st.synchronize()

@@ -71,6 +71,14 @@ def _empty(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tenso
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _used_on(stream, *tensors: Optional[torch.Tensor]) -> None:
+    """Tells the allocator that a kernel on `stream` uses these tensors: their memory is not given out again
+    before it has run."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream)
+
+
 def products_status(device="cuda", stream=None) -> int:
     """Synchronises the stream and returns (and clears) the device status of its products:
     MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_INVALID (offsets that decrease or leave the rows)."""
@@ -175,6 +183,8 @@ def _by_row(fn: str, name: str, a: torch.Tensor, w: torch.Tensor, offsets: torch
         if out.dtype is not dtype:
             raise _types(fn, a, out)
         out_ld = _rows(out, "out", out_width, rows)
+    if stream is not None:
+        _used_on(stream, a, w, offsets, out)
     h = _handle(dev, stream)
     rc = B.function(fn)(code, a.data_ptr(), ld, w.data_ptr(), w_e, w_n, offsets.data_ptr(), E, rows, N, K,
                         out.data_ptr(), out_ld, _workspace(dev, h), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
@@ -223,6 +233,8 @@ def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out:
         if tuple(out.shape) != (E, N, K) or out.dtype is not out_dtype:
             raise ValueError(f"out: {out.dtype} {tuple(out.shape)}, expected {out_dtype} [{E}, {N}, {K}]")
         o_e, o_n = _bank(out, "out", out.shape)
+    if stream is not None:
+        _used_on(stream, dy, x, offsets, out)
     h = _handle(dev, stream)
     rc = B.function("moe_grouped_mm_dw")(
         code, dy.data_ptr(), ld, x.data_ptr(), x_ld, offsets.data_ptr(), E, rows, N, K,
@@ -237,22 +249,27 @@ class GroupedLinear(torch.autograd.Function):
     """grouped_mm with its gradients by x and w."""
 
     @staticmethod
-    def forward(ctx, x, w, offsets):
+    def forward(ctx, x, w, offsets, partial):
         ctx.save_for_backward(x, w, offsets)
-        return grouped_mm(x, w, offsets)
+        ctx.partial = partial
+        return grouped_mm(x, w, offsets, out=x.new_zeros((x.shape[0], w.shape[1])) if partial else None)
 
     @staticmethod
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dy = dy.contiguous()
-        dx = grouped_mm_dx(dy, w, offsets) if ctx.needs_input_grad[0] else None
-        dw = grouped_mm_dw(dy, x, offsets) if ctx.needs_input_grad[1] else None
-        return dx, dw, None
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            dx = grouped_mm_dx(dy, w, offsets, out=torch.zeros_like(x) if ctx.partial else None)
+        if ctx.needs_input_grad[1]:
+            dw = grouped_mm_dw(dy, x, offsets)
+        return dx, dw, None, None
 
 
-def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
-    """Differentiable grouped_mm.  Every row must belong to an expert (offsets from 0 to rows)."""
-    return GroupedLinear.apply(x, w, offsets)
+def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, partial: bool = False) -> torch.Tensor:
+    """Differentiable grouped_mm.  Every row must belong to an expert (offsets from 0 to rows), unless `partial`:
+    then the other rows, as of experts held elsewhere, give zeros and get zeros as their gradient."""
+    return GroupedLinear.apply(x, w, offsets, partial)
 
 
 def quant_fp8_block(x: torch.Tensor, rows: Optional[torch.Tensor] = None, gated: bool = False,
@@ -290,6 +307,8 @@ def quant_fp8_block(x: torch.Tensor, rows: Optional[torch.Tensor] = None, gated:
         if scale.dtype is not torch.float32 or tuple(scale.shape) != (R, G):
             raise ValueError(f"scale: {scale.dtype} {tuple(scale.shape)}, expected float32 [{R}, {G}]")
         s_m, s_g = scale.stride()
+    if stream is not None:
+        _used_on(stream, x, rows, out, scale)
     rc = B.function("moe_quant_fp8_block")(
         code, x.data_ptr(), ld, x_rows, index, R, K, 1 if gated else 0, out.data_ptr(), out_ld, scale.data_ptr(), s_m,
         s_g, _handle(dev, stream))
@@ -341,6 +360,8 @@ def gemm_fp8_block(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_sc
     else:
         out_ld = _rows(out, "out", N, R)
     s_m, s_g = x_scale.stride()
+    if stream is not None:
+        _used_on(stream, x, x_scale, w, w_scale, offsets, out)
     h = _handle(dev, stream)
     rc = B.function("moe_gemm_fp8_block")(
         x.data_ptr(), ld, x_scale.data_ptr(), s_m, s_g, w.data_ptr(), w_e, w_n, w_scale.data_ptr(),
