@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
                 stg128(dst + 8, make_uint4(o[4], o[5], o[6], o[7]));
               }
             }
-          } else {
+          } else if (left > 0) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               if (i < left) store_elem(g.out, at + 16 * c + i, g.out_type, v[i]);
