@@ -171,7 +171,7 @@ def check_fp8(out, xq, xs, wq, ws, off, K, what=""):
 FP8_SHAPES = [
     ([1], 16, 16), ([5], 128, 128), ([16, 0, 1, 33], 256, 256), ([64, 63, 65], 200, 144), ([128], 384, 2880),
     ([127, 129, 0, 256, 257], 512, 512), ([300, 1], 1000, 400), ([1000], 264, 1024), ([7] * 30, 136, 272),
-    ([2], 4096, 7168), ([700, 40, 900], 1024, 1536),
+    ([2], 4096, 7168), ([700, 40, 900], 1024, 1536), ([0, 1, 2, 5] * 16, 768, 272),
     # sizes and strides that 16-byte copies cannot address
     ([3], 5, 7), ([40, 0, 70], 130, 129), ([9], 33, 200),
 ]

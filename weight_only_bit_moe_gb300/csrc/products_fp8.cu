@@ -393,9 +393,13 @@ cudaError_t launch_fp8_tc(const ProdArgs& g, cudaStream_t st, bool* done) {
   if (!grid16b(g.a, g.a_ld) || !grid16b(g.w, g.w_ld) || !grid16b(g.out, g.out_ld * out_bytes)) return cudaSuccess;
   if (g.E > 1 && (g.w_se % 16 != 0 || g.w_se <= 0)) return cudaSuccess;
   if (((double)g.rows / 64 + g.E) * ((g.N + 127) / 128) > 1e9) return cudaSuccess;  // tile numbers are 32-bit
-  // 64 rows an expert on average: up to there one or two tiles of 64 rows stream the weights at the
-  // memory's rate, above it the row tiles of the other orientation do not run emptier than the memory
-  const bool rows_m = g.rows > (int64_t)64 * g.E;
+  // Rows on M wherever its tiles can fill the GPU: they stream the weights of few rows as fast (32
+  // experts of 8 and of 32 rows, 4096 x 4096: 94 and 95 us, rows on N 98 and 107).  With fewer tiles the
+  // smaller ones of rows on N are ahead up to 128 rows (one matrix 4096 x 7168: 16 rows 12.4 and 20.8 us,
+  // 128 rows 17.8 and 21.8, 200 rows 25.4 and 22.6).
+  const int sms = prod_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const bool rows_m = (int64_t)(g.E < g.rows ? g.E : g.rows) * ((g.N + 255) / 256) >= sms || g.rows > (int64_t)128 * g.E;
   Fp8TcArgs a;
   a.g = g;
   const uint64_t xd[2] = {(uint64_t)g.K, (uint64_t)g.rows}, xl = (uint64_t)g.a_ld;
@@ -408,8 +412,6 @@ cudaError_t launch_fp8_tc(const ProdArgs& g, cudaStream_t st, bool* done) {
     ok = make_prod_map(&a.map_x[i], kE4m3, g.a, 2, xd, &xl, box);
   }
   if (!ok) return cudaSuccess;  // (the plain kernel takes what a tensor map cannot describe)
-  const int sms = prod_sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
   a.wide_store = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0 && g.out_ld * out_bytes % 32 == 0;
   *done = true;
   return rows_m ? launch_orientation<true>(a, sms, st) : launch_orientation<false>(a, sms, st);
