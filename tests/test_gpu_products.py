@@ -238,6 +238,20 @@ def test_the_most_experts():
         U.assert_within(dw[e], ref, mag, m)
 
 
+def test_dw_of_skewed_experts():
+    # taken by falling size up to 512 experts, in their order beyond
+    P = products()
+    for E in (512, 513):
+        sizes = [0] * E
+        for e in range(E):
+            sizes[e] = 700 if e in (3, E - 1) else (e * 5) % 9
+        off = U.offsets_of(sizes)
+        x, dy = normal(sum(sizes), 40, dtype=torch.bfloat16, seed=49), normal(sum(sizes), 24, dtype=torch.bfloat16, seed=50)
+        dw = P.grouped_mm_dw(dy, x, off, out_dtype=torch.float32)
+        for e, (m, ref, mag) in enumerate(U.ref_dw(dy, x, off)):
+            U.assert_within(dw[e], ref, mag, m, f"expert {e} of {E}")
+
+
 def test_offsets_past_32_bits():
     # an expert whose weights start more than 2^32 bytes into the bank
     P = products()

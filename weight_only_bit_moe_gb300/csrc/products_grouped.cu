@@ -52,6 +52,7 @@ constexpr int kGtEpiWarp0 = 4, kGtEpiWarps = 8, kGtEpiThreads = 256;
 constexpr int kGtP = 256;             // P rows per pair
 constexpr int kGtN = 256;             // Q rows per pair, at most
 constexpr int kGtGran = 32;           // n is a multiple of this for cta_group::2, M = 256
+constexpr int kGtSorted = 512;        // dW: experts that are taken by falling size, at most
 constexpr int kGtOperandBytes = 128 * 128;              // 128 rows x 64 terms of 16 bits
 constexpr int kGtStageBytes = 2 * kGtOperandBytes;      // P and Q
 
@@ -79,12 +80,15 @@ struct GtSmem {
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;
-  static constexpr int kStatic = (MODE == kProdDw ? 0 : (kProdGroups + 1) * 4) + 64;
+  static constexpr int kStatic = (MODE == kProdDw ? kGtSorted * 2 : (kProdGroups + 1) * 4) + 64;
   static_assert(kAlloc + kStatic <= 227 * 1024, "shared memory over the per-CTA limit");
 };
 
 // Items of dW: a regular grid of tiles, x's columns fastest, each cut into S
-// slices.  A role steps from item to item with carries instead of divisions.
+// slices, the experts by falling size (order; none: in their own order).  Pairs take
+// items in turn, and then those of a turn cost about the same: experts drawn by
+// Zipf's law, 71 of 1160 x 1400, 459 rows on average, take 147 us by size and 159 by
+// number.  A role steps from item to item with carries instead of divisions.
 struct DwWalk {
   int p_tiles, q_tiles, S;
   int e, p, q, s;          // the item's expert, tile and slice
@@ -108,16 +112,16 @@ struct DwWalk {
     if (q >= q_tiles) q -= q_tiles, ++p;
     if (p >= p_tiles) p -= p_tiles, ++e;
   }
-  __device__ __forceinline__ ProdItem item(const ProdArgs& g) const {
+  __device__ __forceinline__ ProdItem item(const ProdArgs& g, const uint16_t* order) const {
     ProdItem it;
     it.tile = (e * p_tiles + p) * q_tiles + q;
     it.split = s;
-    it.e = e;
+    it.e = order ? order[e] : e;
     it.p0 = p * kGtP;
     it.q0 = q * kGtN;
     it.n = min(kGtN, g.K - it.q0);
     int r0, r1;
-    group_rows(g, e, r0, r1);
+    group_rows(g, it.e, r0, r1);
     const int stages = (r1 - r0 + 63) / 64;
     it.t0 = 0;
     it.t1 = stages;
@@ -137,8 +141,8 @@ struct GtWalk {
   __device__ __forceinline__ GtWalk(const RowPlan& pl, int q_tiles, int pair, int pairs) : w(pair), e(0), step(pairs) {
     if (MODE == kProdDw) dw.init(pl.p_tiles, q_tiles, pl.S, pair, pairs);
   }
-  __device__ __forceinline__ ProdItem item(const ProdArgs& g, const RowPlan& pl, const int* start) {
-    return MODE == kProdDw ? dw.item(g) : row_item<kGtN, kGtGran, kGtP>(g, pl, start, w, e);
+  __device__ __forceinline__ ProdItem item(const ProdArgs& g, const RowPlan& pl, const int* start, const uint16_t* order) {
+    return MODE == kProdDw ? dw.item(g, order) : row_item<kGtN, kGtGran, kGtP>(g, pl, start, w, e);
   }
   __device__ __forceinline__ void next() {
     w += step;
@@ -230,7 +234,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
   using SM = GtSmem<MODE>;
   constexpr int kStages = SM::kStages;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ int start[kProdGroups + 1];  // first tile of each group
+  __shared__ int start[MODE == kProdDw ? 1 : kProdGroups + 1];  // first tile of each group
+  __shared__ uint16_t sorted[MODE == kProdDw ? kGtSorted : 1];  // dW: experts by falling size
+  const uint16_t* order = nullptr;
   __shared__ int warp_tot[kGtThreads / 32];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smem_s = smem_u32(smem);
@@ -267,12 +273,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
   RowPlan pl;
   const int j_dim = MODE == kProdDx ? g.K : g.N;
   pl.p_tiles = (j_dim + kGtP - 1) / kGtP;
-  pl.stages = MODE == kProdDw ? g.rows / g.E / 64 : ((MODE == kProdDx ? g.N : g.K) + 63) / 64;  // (dW: on average)
+  pl.stages = ((MODE == kProdDx ? g.N : g.K) + 63) / 64;
   const int q_tiles = (g.K + kGtN - 1) / kGtN;  // dW
   if (MODE == kProdDw) {
     if (blockIdx.x == 0)
       for (int e = tid; e < g.E; e += kGtThreads)
         if (group_bad(g, e)) atomicOr(g.status, kStatusRouting);
+    // (With at most one tile to a pair the order does not matter, and with more than
+    // three tiles to four pairs two to four slices take as many rounds: there the sizes
+    // would cost 0.9 us for nothing.)
+    pl.tiles = g.E * pl.p_tiles * q_tiles;
+    if (g.E <= kGtSorted && (pl.tiles > a.pairs || 4 * pl.tiles <= 3 * a.pairs)) {
+      order = sorted;
+      int* size = reinterpret_cast<int*>(smem);  // (the ring, before its first copy)
+      for (int e = tid; e < g.E; e += kGtThreads) {
+        int r0, r1;
+        group_rows(g, e, r0, r1);
+        size[e] = r1 - r0;
+      }
+      __syncthreads();
+      for (int e = tid; e < g.E; e += kGtThreads) {
+        const int mine = size[e];
+        int larger = 0;
+#pragma unroll 8
+        for (int j = 0; j < g.E; ++j) larger += size[j] > mine || (size[j] == mine && j < e);
+        sorted[larger] = (uint16_t)e;
+      }
+      fence_async_proxy();
+    }
   } else {
     plan_groups<kGtN, kGtThreads>(g, pl.p_tiles, start, warp_tot);
   }
@@ -281,7 +309,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
   cluster_sync_all();  // both CTAs' barriers exist before either signals them
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  pl.tiles = MODE == kProdDw ? g.E * pl.p_tiles * q_tiles : start[g.E];
+  if (MODE == kProdDw) {  // slices for the longest sum, or the average one
+    int r0 = 0, r1 = g.rows / g.E;
+    if (order) group_rows(g, order[0], r0, r1);
+    pl.stages = (r1 - r0 + 63) / 64;
+  } else {
+    pl.tiles = start[g.E];
+  }
   pl.S = plan_slices(pl, a.pairs, 2, MODE == kProdDw ? 1 << 30 : g.rows, kGtN);
   const int items = pl.tiles * pl.S;
   const uint32_t full_s = map_to_rank(smem_u32(full), 0);
@@ -291,7 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     Ring<kStages> slot;
     uint32_t filled = 0;
     for (GtWalk<MODE> at(pl, q_tiles, pair, a.pairs); at.w < items; at.next()) {
-      const ProdItem it = at.item(g, pl, start);
+      const ProdItem it = at.item(g, pl, start, order);
       const int half = gt_half<MODE>(it.n);
       int r0 = 0, r1 = 0;
       if (MODE == kProdDw) group_rows(g, it.e, r0, r1);
@@ -329,7 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
       Ring<kStages> slot;
       Ring<2> acc;
       for (GtWalk<MODE> at(pl, q_tiles, pair, a.pairs); at.w < items; at.next()) {
-        const ProdItem it = at.item(g, pl, start);
+        const ProdItem it = at.item(g, pl, start, order);
         if (it.t0 >= it.t1) continue;  // (dW: no rows; the epilogue takes zeros)
         int r0 = 0, r1 = 0;
         if (MODE == kProdDw) group_rows(g, it.e, r0, r1);
@@ -368,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     uint4* partial = reinterpret_cast<uint4*>(g.scratch + kProdCounterBytes);
     uint32_t ic = 0, box = 0;
     for (GtWalk<MODE> at(pl, q_tiles, pair, a.pairs); at.w < items; at.next()) {
-      const ProdItem it = at.item(g, pl, start);
+      const ProdItem it = at.item(g, pl, start, order);
       const int p = it.p0 + rank * 128 + quarter * 32;  // this warp's first P row
       const bool none = it.t0 >= it.t1;                 // no terms: the sums are zeros
       const int acc = ic & 1;
