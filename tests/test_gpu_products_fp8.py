@@ -172,6 +172,8 @@ FP8_SHAPES = [
     ([1], 16, 16), ([5], 128, 128), ([16, 0, 1, 33], 256, 256), ([64, 63, 65], 200, 144), ([128], 384, 2880),
     ([127, 129, 0, 256, 257], 512, 512), ([300, 1], 1000, 400), ([1000], 264, 1024), ([7] * 30, 136, 272),
     ([2], 4096, 7168), ([700, 40, 900], 1024, 1536), ([0, 1, 2, 5] * 16, 768, 272),
+    # more tiles than SMs, and a sum long enough for slices: rows on the M side
+    ([127, 129, 0, 256, 257], 2056, 512), ([300, 1, 64] * 4, 1000, 400), ([1000], 1224, 1024), ([300], 2048, 6160),
     # sizes and strides that 16-byte copies cannot address
     ([3], 5, 7), ([40, 0, 70], 130, 129), ([9], 33, 200),
 ]
@@ -247,6 +249,38 @@ def test_fp8_special_values():
         x, w = xq.double() * U.spread_rows(xs, 256).double(), U.dequant_bank(wq, ws)
         (_, ref, mag), = U.ref_fwd(x[keep], w, U.offsets_of([rows - 1]))
         U.assert_within(out[keep], ref, mag, 256)
+
+
+def test_fp8_edges_with_rows_on_m():
+    # the three tests above at sizes whose tiles fill the GPU
+    P = products()
+    xq, xs, wq, ws = fp8_case([150], 5120, 384, 30, 2)
+    off = torch.tensor([7, 60, 140], dtype=torch.int32, device="cuda")
+    x_scale = xs.clone()
+    x_scale[:7], x_scale[140:] = float("nan"), float("nan")
+    out = torch.full((150, 5120), 9.0, dtype=torch.bfloat16, device="cuda")
+    P.gemm_fp8_block(xq, x_scale, wq, ws, off, out=out)
+    assert (out[:7] == 9).all() and (out[140:] == 9).all()
+    check_fp8(out, xq, xs, wq, ws, off, 384)
+
+    rows, N, K, pad = 1300, 1000, 528, 16
+    xq, xs, wq, ws = fp8_case([rows], N, K, 40, 1)
+    x2, w2 = U.strided(xq, pad, 0), U.strided(wq, pad, 0)
+    out = U.strided(torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda"), pad, 3.0)
+    P.gemm_fp8_block(x2, xs.t().contiguous().t(), w2[0], ws[0].t().contiguous().t(), out=out)
+    check_fp8(out, xq, xs, wq, ws, U.offsets_of([rows]), K)
+    assert (torch.as_strided(out, (rows - 1, pad), (N + pad, 1), N) == 3.0).all()
+
+    rows = 260
+    xq, xs, wq, ws = fp8_case([rows], 4096, 256, 50, 1)
+    xs = xs.clone()
+    xs[3, 1], xs[4], xs[5] = float("nan"), 0.0, -xs[5]
+    out = P.gemm_fp8_block(xq, xs, wq[0], ws[0])
+    assert torch.isnan(out[3]).all() and (out[4] == 0).all()
+    keep = [r for r in range(rows) if r != 3]
+    x, w = xq.double() * U.spread_rows(xs, 256).double(), U.dequant_bank(wq, ws)
+    (_, ref, mag), = U.ref_fwd(x[keep], w, U.offsets_of([rows - 1]))
+    U.assert_within(out[keep], ref, mag, 256)
 
 
 def test_fp8_offsets_past_32_bits():

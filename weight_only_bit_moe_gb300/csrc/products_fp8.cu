@@ -393,13 +393,18 @@ cudaError_t launch_fp8_tc(const ProdArgs& g, cudaStream_t st, bool* done) {
   if (!grid16b(g.a, g.a_ld) || !grid16b(g.w, g.w_ld) || !grid16b(g.out, g.out_ld * out_bytes)) return cudaSuccess;
   if (g.E > 1 && (g.w_se % 16 != 0 || g.w_se <= 0)) return cudaSuccess;
   if (((double)g.rows / 64 + g.E) * ((g.N + 127) / 128) > 1e9) return cudaSuccess;  // tile numbers are 32-bit
-  // Rows on M wherever its tiles can fill the GPU: they stream the weights of few rows as fast (32
-  // experts of 8 and of 32 rows, 4096 x 4096: 94 and 95 us, rows on N 98 and 107).  With fewer tiles the
-  // smaller ones of rows on N are ahead up to 128 rows (one matrix 4096 x 7168: 16 rows 12.4 and 20.8 us,
-  // 128 rows 17.8 and 21.8, 200 rows 25.4 and 22.6).
+  // Rows on N where its tiles, of half the rows and half the features, all run at one time: 1024 x 4096 (N x K),
+  // 256 rows 11.5 and 17.0 us with rows on M; 16384 x 4096, 16 rows 15.2 and 19.5; 4 experts of 100 rows, 2048 x
+  // 2048 11.9 and 12.3.  With more tiles rows on M are ahead for any rows: 24576 x 4096, 16 rows 28.6 and 21.3; 128
+  // experts of one row, 4096 x 4096 340 and 316.  Where rows on N are too many tiles for two slices and rows on M few
+  // enough for four, a long sum is faster in those: 8192 x 7168, 128 rows 25.7 and 23.2, 5120 x 16384 45.8 and 32.1;
+  // up to 40 blocks it is not (8192 x 5120 19.8 and 20.6).
   const int sms = prod_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const bool rows_m = (int64_t)(g.E < g.rows ? g.E : g.rows) * ((g.N + 255) / 256) >= sms || g.rows > (int64_t)128 * g.E;
+  const int64_t groups = g.E < g.rows ? g.E : g.rows, each = (g.rows + groups - 1) / groups;  // (rows > 0)
+  const int64_t tiles_n = groups * ((each + 63) / 64) * ((g.N + 127) / 128);
+  const int64_t tiles_m = groups * ((each + 127) / 128) * ((g.N + 255) / 256);
+  const bool rows_m = tiles_n > sms || (2 * tiles_n > sms && 4 * tiles_m <= sms && g.K > 40 * 128);
   Fp8TcArgs a;
   a.g = g;
   const uint64_t xd[2] = {(uint64_t)g.K, (uint64_t)g.rows}, xl = (uint64_t)g.a_ld;
