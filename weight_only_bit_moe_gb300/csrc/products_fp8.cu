@@ -66,7 +66,6 @@ struct Fp8TcArgs {
   CUtensorMap map_x[4];  // boxes of 128, 64, 32 and 16 rows of x
   CUtensorMap map_w;     // boxes of a tile's features
   ProdArgs g;
-  int wide_store;        // 32-byte stores are aligned
 };
 
 template <bool ROWS_M>
@@ -310,43 +309,52 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
         const int r = quarter * 32 + lane;
         const int j0 = it.p0 + sub * 128;
         const int64_t at = (int64_t)(it.q0 + r) * g.out_ld + j0;
+        const bool f32 = g.out_type == kFp32, bf = g.out_type == kBf16;
+        unsigned char* dst = static_cast<unsigned char*>(g.out) + at * (f32 ? 4 : 2);
+        const bool sector = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // (else 16 past one)
+        auto pack8 = [&](int f, uint32_t* o) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[i] = bf ? pack_bf16x2(sum[f + 2 * i], sum[f + 2 * i + 1]) : pack_half2(sum[f + 2 * i], sum[f + 2 * i + 1]);
+        };
 #pragma unroll
         for (int c = 0; c < C::kAcc / 16; ++c) {  // sixteen features at a time
           const int left = r < it.n ? g.N - j0 - 16 * c : 0;
-          const float* v = &sum[16 * c];
           if (left >= 16) {
-            if (g.out_type == kFp32) {
-              float* dst = static_cast<float*>(g.out) + at + 16 * c;
+            uint32_t o[8];
+            if (f32) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                uint32_t o[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(v[8 * h + i]);
-                if (a.wide_store) {
-                  stg256(dst + 8 * h, o);
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(sum[16 * c + 8 * h + i]);
+                if (sector) {
+                  stg256(dst + 64 * c + 32 * h, o);
                 } else {
-                  stg128(dst + 8 * h, make_uint4(o[0], o[1], o[2], o[3]));
-                  stg128(dst + 8 * h + 4, make_uint4(o[4], o[5], o[6], o[7]));
+                  stg128(dst + 64 * c + 32 * h, make_uint4(o[0], o[1], o[2], o[3]));
+                  stg128(dst + 64 * c + 32 * h + 16, make_uint4(o[4], o[5], o[6], o[7]));
                 }
               }
-            } else {
-              uint16_t* dst = static_cast<uint16_t*>(g.out) + at + 16 * c;
-              uint32_t o[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                o[i] = g.out_type == kBf16 ? pack_bf16x2(v[2 * i], v[2 * i + 1]) : pack_half2(v[2 * i], v[2 * i + 1]);
-              }
-              if (a.wide_store) {
-                stg256(dst, o);
-              } else {
+            } else if (sector) {
+              pack8(16 * c, o);
+              pack8(16 * c + 8, o + 4);
+              stg256(dst + 32 * c, o);
+            } else {  // eight features further, so that whole sectors are written here too
+              if (c == 0) {
+                pack8(0, o);
                 stg128(dst, make_uint4(o[0], o[1], o[2], o[3]));
-                stg128(dst + 8, make_uint4(o[4], o[5], o[6], o[7]));
+              }
+              pack8(16 * c + 8, o);
+              if (c + 1 < C::kAcc / 16 && left >= 32) {
+                pack8((16 * c + 16) % C::kAcc, o + 4);
+                stg256(dst + 32 * c + 16, o);
+              } else {
+                stg128(dst + 32 * c + 16, make_uint4(o[0], o[1], o[2], o[3]));
               }
             }
           } else if (left > 0) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              if (i < left) store_elem(g.out, at + 16 * c + i, g.out_type, v[i]);
+              if (i < left) store_elem(g.out, at + 16 * c + i, g.out_type, sum[16 * c + i]);
           }
         }
       } else {
@@ -417,7 +425,6 @@ cudaError_t launch_fp8_tc(const ProdArgs& g, cudaStream_t st, bool* done) {
     ok = make_prod_map(&a.map_x[i], kE4m3, g.a, 2, xd, &xl, box);
   }
   if (!ok) return cudaSuccess;  // (the plain kernel takes what a tensor map cannot describe)
-  a.wide_store = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0 && g.out_ld * out_bytes % 32 == 0;
   *done = true;
   return rows_m ? launch_orientation<true>(a, sms, st) : launch_orientation<false>(a, sms, st);
 }
