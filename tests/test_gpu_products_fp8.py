@@ -283,6 +283,21 @@ def test_fp8_edges_with_rows_on_m():
     U.assert_within(out[keep], ref, mag, 256)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("N", [1003, 1016, 977])
+def test_fp8_row_ends_inside_a_store(N, out_dtype):
+    # rows of the output start on 32 bytes and end anywhere
+    P = products()
+    rows, K = 1300, 272
+    xq, xs, wq, ws = fp8_case([rows], N, K, 70, 1)
+    if out_dtype == torch.float16:
+        ws = ws * 1e-2
+    out = U.strided(torch.zeros(rows, N, dtype=out_dtype, device="cuda"), 1024 - N, 3.0)
+    P.gemm_fp8_block(xq, xs, wq[0], ws[0], out=out)
+    check_fp8(out, xq, xs, wq, ws, U.offsets_of([rows]), K)
+    assert (torch.as_strided(out, (rows - 1, 1024 - N), (1024, 1), N) == 3.0).all()
+
+
 def test_fp8_offsets_past_32_bits():
     P = products()
     E, N, K = 3, 49152, 49152  # an expert's weights take 2^31.2 bytes
