@@ -11,11 +11,10 @@
 // the product where memory does not.
 //
 // Two orientations:
-//   rows on M (prompts): 128 rows x 256 features, a thread owns one row and the
+//   rows on M (many tiles): 128 rows x 256 features, a thread owns one row and the
 //     128 features of one weight block: one scale per thread and block.
-//   rows on N (decode): 128 features x up to 64 rows, a thread owns one feature
-//     and 32 rows, whose scales it reads from shared memory.  The tile moves the
-//     weights once.
+//   rows on N (few tiles): 128 features x up to 64 rows, a thread owns one feature
+//     and 32 rows, whose scales it reads from shared memory.
 // With rows on N a 256-row tile would read 32 scales from shared memory for 128
 // sums, more than the shared memory delivers in the time of the block's MMAs;
 // with rows on M a tile of few rows would run the MMA nearly empty.
@@ -25,11 +24,11 @@
 // longer than the block's MMAs (0.63 us a block and tile, here 0.44, of which the
 // MMAs alone take 0.34).  The 128 sums of a thread leave 40 registers for the rest:
 // 16 columns of tensor memory at a time and plain multiply-adds fit, packed ones or
-// 32 columns spill inside the loop (293 instead of 188 us for the prompt below).
+// 32 columns spill inside the loop (293 us when the prompt below took 188).
 //
-// Measured on GB300: 8191 x 4096 x 7168 188 us, 2550 TFLOP/s (the bf16 product of
-// these sizes at the measured peak takes 256); 32 experts of about 256 rows, 4096 x
-// 4096, 186 us; 5 rows x 4096 x 7168 12 us, 38912 x 7168 at 5.3 TB/s.
+// Measured on GB300: 8191 x 4096 x 7168 184 us, 2615 TFLOP/s (the bf16 product of
+// these sizes at the measured peak takes 256); 32 experts of 225 to 285 rows, 4096 x
+// 4096, 158 us; 5 rows x 4096 x 7168 12 us, 38912 x 7168 47 us, 6.0 TB/s.
 #include <atomic>
 
 #include "gemm.cuh"

@@ -14,8 +14,9 @@
 //   dW: P = dy's columns, Q = x's columns; the ragged dimension is the sum.
 // The operand order is the bank's own: forward reads both operands with the sum
 // innermost, dx reads W with j innermost and dW both operands so, through the
-// MN-major descriptors -- nothing is transposed in memory.  dW leaves through shared
-// memory by TMA, added to what is there when it accumulates.
+// MN-major descriptors -- nothing is transposed in memory.  Results leave through
+// shared memory: dW's by TMA, added to what is there when it accumulates, the others
+// as stores of 256 bytes of a row.
 //
 // A stage is 64 terms of the sum (128-byte lines, 128-byte swizzle), 32 KB per
 // CTA, six in flight (dW: five).  Roles: three producer warps per CTA issue TMA,

@@ -47,7 +47,8 @@ __device__ __forceinline__ uint64_t both(float v) { return pack2(__float_as_uint
 // A cheaper exponential as well (2^t on the special-function unit with a
 // correction) took 11.4 instead of 12.6 us for 4093 rows of 2880, but moved more
 // values across the boundary between two codes: 2.5e-4 relative error of the codes
-// against 64 bits instead of at most 7e-5.
+// against 64 bits instead of at most 8e-5 (10 of the 11.8 million codes differ; of
+// separate fp32 operations as many).
 __device__ __forceinline__ void silu_mul2(float& g0, float& g1, float u0, float u1) {
   const float d0 = fmin_nan(1.0f + expf(-g0), 1.7014118e38f), d1 = fmin_nan(1.0f + expf(-g1), 1.7014118e38f);
   float r0, r1;  // -1 / d
