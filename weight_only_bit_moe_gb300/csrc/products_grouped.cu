@@ -31,11 +31,12 @@
 // results do not depend on timing.
 //
 // Bounds and measurements (GB300; copy rate 6.8 TB/s, bf16 1880 TFLOP/s):
-//   8192 rows x 4096 x 4096, one expert: MMAs, 140 us = 1960 TFLOP/s (library 1980 to
-//     2050 at 8192^3); dx the same, dW 184 us.
+//   8192 rows x 4096 x 4096, one expert: MMAs, 140 to 144 us = 1910 to 1960 TFLOP/s
+//     (library 1980 to 2050 at 8192^3); dx the same, dW in 16 bits 164 us.
 //   128 rows over 128 experts of 4096 x 1536: weights from memory, 95 us = 6.5 TB/s.
-//   128 experts of 256 rows, 4096 x 1536: memory, 292 us (floor 292).
-//   32 experts of 256 and of 270 rows, 2880 x 2880: 113 and 154 us; past 256 rows the
+//   128 experts of 256 rows, 4096 x 1536: memory, 292 to 296 us (floor 292); of
+//     2048 x 768, 91 us (floor 86).
+//   32 experts of 256 and of 270 rows, 2880 x 2880: 114 and 136 us; past 256 rows the
 //     weights pass from L2 twice, once for each row tile.
 //   A stage takes at least 0.20 us whatever its rows (issue of its copies and MMAs).
 #include <atomic>
