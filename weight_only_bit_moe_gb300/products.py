@@ -84,6 +84,9 @@ def products_status(device="cuda", stream=None) -> int:
     MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_INVALID (offsets that decrease or leave the rows)."""
     index = torch.device(device).index
     index = torch.cuda.current_device() if index is None else index
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return products_status(torch.device("cuda", index), stream)
     handle = _handle(index, stream)
     return B.moe_get_status(_workspace(index, handle), handle)
 
@@ -135,6 +138,12 @@ def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
     return device
 
 
+def _current_device() -> int:
+    """The calling thread's device.  The library launches there, so a call with operands on another GPU starts
+    again with that one current."""
+    return torch._C._cuda_getDevice()
+
+
 def _check_offsets(offsets: torch.Tensor, E: int) -> None:
     if offsets.dtype is not torch.int32 or offsets.numel() != E + 1 or offsets.dim() != 1 or not offsets.is_contiguous():
         raise ValueError(f"offsets: expected contiguous int32 [{E + 1}], got {offsets.dtype} {tuple(offsets.shape)}")
@@ -162,6 +171,9 @@ def expert_order(topk_ids: torch.Tensor, num_experts: int, expert_base: int = 0)
 def _by_row(fn: str, name: str, a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
             out: Optional[torch.Tensor], stream, forward: bool) -> torch.Tensor:
     dev = _device(a, w, offsets, out)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return _by_row(fn, name, a, w, offsets, out, stream, forward)
     rows, a_width = _dims(a, name, 2)
     E, N, K = shape = _dims(w, "w", 3)
     width, out_width = (K, N) if forward else (N, K)
@@ -210,6 +222,9 @@ def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out:
     """Gradient of grouped_mm by w: dw[e] = sum over the rows of e of dy[r] x[r]^T; dy [rows, N], x [rows, K]
     -> [E, N, K], in out_dtype (the operands' type or float32).  accumulate adds to a float32 out."""
     dev = _device(dy, x, offsets, out)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return grouped_mm_dw(dy, x, offsets, out, out_dtype, accumulate, stream)
     rows, N = _dims(dy, "dy", 2)
     K = _dims(x, "x", 2)[1]
     E = _dims(offsets, "offsets", 1)[0] - 1
@@ -278,6 +293,9 @@ def quant_fp8_block(x: torch.Tensor, rows: Optional[torch.Tensor] = None, gated:
     scale per 128 columns; gated: of silu(x[:, :K]) * x[:, K:] with K half of x's columns.  scale has shape
     [rows, ceil(K / 128)], in any strides."""
     dev = _device(x, rows, out, scale)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return quant_fp8_block(x, rows, gated, out, scale, stream)
     code = _HALF.get(x.dtype)
     if code is None:
         raise _types("quant_fp8_block", x)
@@ -325,6 +343,9 @@ def gemm_fp8_block(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_sc
     out is given); with offsets, w and w_scale have a leading expert dimension and the rows of expert e take
     w[e].  Scales may have any strides."""
     dev = _device(x, x_scale, w, w_scale, offsets, out)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return gemm_fp8_block(x, x_scale, w, w_scale, offsets, out, out_dtype, stream)
     if x.dtype is not torch.float8_e4m3fn or w.dtype is not torch.float8_e4m3fn:
         raise ValueError(f"gemm_fp8_block: float8_e4m3fn operands expected, got {x.dtype} and {w.dtype}")
     if x_scale.dtype is not torch.float32 or w_scale.dtype is not torch.float32:
