@@ -1,0 +1,113 @@
+"""Products on several streams and in graphs, with sums cut into slices: the slices
+meet in a workspace's counters and partial tiles, so these calls notice one that
+is shared, not zeroed or given out again.  Results are compared bit for bit with
+those of the same calls made alone."""
+import pytest
+import torch
+
+from gpu_util import need_gpu
+import products_util as U
+
+pytestmark = pytest.mark.gpu
+F8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def products():
+    from weight_only_bit_moe_gb300 import products as P
+    return P
+
+
+class Sliced:
+    """Inputs of a decode step's product, an FP8 product of few rows and a gradient of few tiles."""
+
+    def __init__(self, seed):
+        g = torch.Generator("cuda").manual_seed(seed)
+
+        def normal(*shape):
+            return torch.randn(*shape, generator=g, device="cuda")
+
+        bf = torch.bfloat16
+        self.x, self.w, self.off = normal(5, 4096).to(bf), normal(1, 1024, 4096).to(bf), U.offsets_of([5])
+        self.q, self.wq = normal(6, 4096).to(F8), normal(512, 4096).to(F8)
+        self.s, self.ws = torch.exp(normal(6, 32)), torch.exp(normal(4, 32))
+        self.dy, self.rows, self.at = normal(2500, 264).to(bf), normal(2500, 200).to(bf), U.offsets_of([600, 1900])
+        torch.cuda.synchronize()
+
+    def __call__(self, stream=None):
+        P = products()
+        return [P.grouped_mm(self.x, self.w, self.off, stream=stream),
+                P.gemm_fp8_block(self.q, self.s, self.wq, self.ws, stream=stream),
+                P.grouped_mm_dw(self.dy, self.rows, self.at, out_dtype=torch.float32, stream=stream)]
+
+    def alone(self):
+        out = self()
+        torch.cuda.synchronize()
+        _, ref, mag = U.ref_fwd(self.x, self.w, self.off)[0]
+        U.assert_within(out[0], ref, mag, 4096)
+        return out
+
+
+def same(got, want):
+    assert len(got) == len(want)
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_two_streams_at_once():
+    a, b = Sliced(1), Sliced(2)
+    want_a, want_b = a.alone(), b.alone()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    got_a, got_b = [], []
+    for _ in range(30):
+        got_a.append(a(stream=one))
+        got_b.append(b(stream=two))
+    torch.cuda.synchronize()
+    for ga, gb in zip(got_a, got_b):
+        same(ga, want_a)
+        same(gb, want_b)
+
+
+def test_a_replay_beside_calls_on_the_captured_stream():
+    P = products()
+    a, b = Sliced(3), Sliced(4)
+    want_a, want_b = a.alone(), b.alone()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        a()  # the stream has a workspace of its own before the capture
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        captured = a()
+    for _ in range(30):
+        with torch.cuda.stream(other):
+            graph.replay()
+        with torch.cuda.stream(side):
+            got = b()
+        side.synchronize()
+        other.synchronize()
+        same(captured, want_a)
+        same(got, want_b)
+    assert P.products_status(stream=side) == 0
+
+
+def test_two_graphs_of_one_stream_at_once():
+    a, b = Sliced(5), Sliced(6)
+    want_a, want_b = a.alone(), b.alone()
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    for inputs in (a, b):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            outs.append(inputs())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(30):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        same(outs[0], want_a)
+        same(outs[1], want_b)

@@ -38,19 +38,24 @@ def _handle(device: int, stream) -> int:
 
 
 def _workspace(device: int, handle: int) -> int:
-    """Address of the workspace of this device and stream."""
+    """Address of the workspace of this device and stream.  A captured call never takes it: the graph may be
+    replayed on any stream, beside calls on this one."""
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return _captured_workspace(device)
     ws = _workspaces.get((device, handle))
     return ws[0] if ws is not None else _new_workspace(device, handle)
 
 
+def _captured_workspace(device: int) -> int:
+    # the graph's own memory, zeroed by the graph: not kept for calls outside it.  The tensor lives until the
+    # next one is made, which is after the call's launch.
+    ws = torch.empty(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=torch.device("cuda", device))
+    ws[:B.MOE_PRODUCTS_WORKSPACE_HEAD_BYTES].zero_()
+    _workspaces["capture"] = (ws.data_ptr(), ws)
+    return ws.data_ptr()
+
+
 def _new_workspace(device: int, handle: int) -> int:
-    if torch.cuda.is_current_stream_capturing():
-        # the graph's own memory, zeroed by the graph: not kept for calls outside it.  The tensor lives until the
-        # next one is made, which is after the call's launch.
-        ws = torch.empty(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=torch.device("cuda", device))
-        ws[:B.MOE_PRODUCTS_WORKSPACE_HEAD_BYTES].zero_()
-        _workspaces["capture"] = (ws.data_ptr(), ws)
-        return ws.data_ptr()
     with _workspace_lock:
         if (device, handle) not in _workspaces:
             ws = torch.zeros(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=torch.device("cuda", device))
