@@ -116,6 +116,25 @@ int moe_gemm_fp8_block(const void* x, int64_t x_stride, const float* x_scale, in
                        const int32_t* offsets, int num_experts, int rows, int N, int K, int out_dtype,
                        void* out, int64_t out_stride, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* Calls that are captured into a CUDA graph.  A replay runs on whatever stream it is
+ * launched on, so a captured call takes a workspace that no call outside the graph
+ * uses, one for each stream of the capture, kept until the graph is gone.  These
+ * tell the owner of workspaces what that takes.
+ *
+ * The capture that `stream` is in: its number into *id (never used again in the
+ * process), 0 if it is in none. */
+int moe_capture_id(void* stream, uint64_t* id);
+
+/* Exchanges the calling thread's capture interaction mode (cudaStreamCaptureMode) with
+ * *mode: in mode 2, relaxed, a thread that captures may allocate, and zero and wait
+ * for a workspace on a stream outside the capture. */
+int moe_capture_mode(int* mode);
+
+/* A word on the host that is 0 and becomes 1 once the graph that `stream` is being
+ * captured into and every executable graph made of it are gone and their replays
+ * have finished.  The word is never freed. */
+int moe_capture_watch(void* stream, const int32_t** gone);
+
 #ifdef __cplusplus
 }
 #endif

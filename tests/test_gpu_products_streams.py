@@ -2,6 +2,8 @@
 meet in a workspace's counters and partial tiles, so these calls notice one that
 is shared, not zeroed or given out again.  Results are compared bit for bit with
 those of the same calls made alone."""
+import time
+
 import pytest
 import torch
 
@@ -111,3 +113,66 @@ def test_two_graphs_of_one_stream_at_once():
         torch.cuda.synchronize()
         same(outs[0], want_a)
         same(outs[1], want_b)
+
+
+def test_branches_of_a_capture():
+    # products on a stream that joined the capture, beside products on the captured one
+    P = products()
+    a, b = Sliced(7), Sliced(8)
+    want_a, want_b = a.alone(), b.alone()
+    main, branch = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        branch.wait_stream(main)
+        on_branch = [b(stream=branch) for _ in range(3)]
+        on_main = [a() for _ in range(3)]
+        main.wait_stream(branch)
+        after = b()
+    graph.replay()
+    for _ in range(20):
+        for outs in on_branch + on_main + [after]:
+            for t in outs:
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for outs in on_branch + [after]:
+            same(outs, want_b)
+        for outs in on_main:
+            same(outs, want_a)
+    same(a(), want_a)
+
+
+def test_a_workspace_made_in_a_capture_outlives_it():
+    # memory that the graph's own nodes use before is not taken for counters; a graph's end frees its workspace
+    P = products()
+    a = Sliced(9)
+    want = a.alone()
+
+    def capture():
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(4):
+                torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")  # (dropped: its memory is used again)
+            out = a()
+            torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+        return graph, out
+
+    graph, out = capture()
+    for _ in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        same(out, want)
+    torch.cuda.synchronize()
+    held = len(P._captured)
+    for _ in range(3):
+        del graph, out
+        torch.cuda.synchronize()
+        for _ in range(200):  # (the graph's end is reported from another thread)
+            if any(gone.contents.value for _, _, gone in P._captured.values()):
+                break
+            time.sleep(0.01)
+        graph, out = capture()
+        assert len(P._captured) <= held
+        graph.replay()
+        torch.cuda.synchronize()
+        same(out, want)

@@ -25,3 +25,54 @@ def test_a_captured_call_does_not_share_the_streams_workspace(capturing):
     assert P._workspace(0, HANDLE) == OWN
     capturing[0] = False
     assert P._workspace(0, HANDLE) == EAGER
+
+
+def test_the_capture_that_counts_is_that_of_the_calls_stream(capturing, monkeypatch):
+    captured = set()
+    monkeypatch.setattr(P.B, "moe_capture_id", lambda stream: 9 if stream in captured else 0, raising=False)
+    capturing[0] = True  # the current stream, but not the one that the call names
+    assert P._workspace(0, HANDLE, HANDLE) == EAGER
+    capturing[0] = False
+    captured.add(HANDLE)
+    assert P._workspace(0, HANDLE, HANDLE) == OWN
+
+
+class Word:
+    def __init__(self):
+        self.contents = self
+        self.value = 0
+
+
+def test_one_workspace_for_each_stream_of_a_capture(monkeypatch):
+    capture, made, words = [1], [], []
+
+    def zeroed(device, ws=None):
+        made.append(ws)
+        return torch.zeros(16, dtype=torch.uint8) if ws is None else ws
+
+    monkeypatch.setattr(P.B, "moe_capture_id", lambda stream: capture[0], raising=False)
+    monkeypatch.setattr(P.B, "moe_capture_watch", lambda stream: words.append(Word()) or words[-1], raising=False)
+    monkeypatch.setattr(P, "_zeroed", zeroed, raising=False)
+    monkeypatch.setattr(P, "_captured", {}, raising=False)
+    first = P._captured_workspace(0, HANDLE)
+    assert P._captured_workspace(0, HANDLE) == first and len(made) == 1  # zeroed once
+    branch = P._captured_workspace(0, HANDLE + 1)
+    capture[0] = 2
+    second = P._captured_workspace(0, HANDLE)
+    assert len({first, branch, second}) == 3 and made == [None] * 3  # the first graph may still be replayed
+    words[0].value = 1
+    capture[0] = 3
+    assert P._captured_workspace(0, HANDLE) == first  # it is gone, its workspace is zeroed and used again
+    assert len(made) == 4 and made[3] is not None
+
+
+def test_refusals():
+    from weight_only_bit_moe_gb300 import build
+    build.build()
+    B = P.B
+    L = B.load()
+    assert L.moe_capture_id(None, None) == B.MOE_ERR_INVALID
+    assert L.moe_capture_watch(None, None) == B.MOE_ERR_INVALID
+    for mode in (-1, 3):
+        with pytest.raises(B.MoeError):
+            B.moe_capture_mode(mode)

@@ -24,7 +24,7 @@ EXPORTED = ("moe_repack_size", "moe_repack_weights", "moe_repack_weights_ex", "m
             "moe_workspace_size", "moe_w4a16_forward", "moe_w4a16_forward_noalloc", "moe_get_status",
             "moe_set_trace_events", "moe_set_test_starve_wait", "moe_status_string", "moe_requant_fp8",
             "moe_requant_launch_geometry", "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw",
-            "moe_quant_fp8_block", "moe_gemm_fp8_block")
+            "moe_quant_fp8_block", "moe_gemm_fp8_block", "moe_capture_id", "moe_capture_mode", "moe_capture_watch")
 MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
 MOE_PRODUCTS_WORKSPACE_BYTES = 48 << 20  # workspace of the products in moe_products.h
 MOE_PRODUCTS_WORKSPACE_HEAD_BYTES = 8192  # of which these are zeroed before the first use
@@ -95,6 +95,9 @@ def load(path: str = ""):
                 "moe_quant_fp8_block": (i32, [i32, p, i64, i32, p, i32, i32, i32, p, i64, p, i64, i64, p]),
                 "moe_gemm_fp8_block": (i32, [p, i64, p, i64, i64, p, i64, i64, p, i64, i64, i64, p, i32, i32, i32,
                                              i32, i32, p, i64, p, i64, p]),
+                "moe_capture_id": (i32, [p, ctypes.POINTER(ctypes.c_uint64)]),
+                "moe_capture_mode": (i32, [ctypes.POINTER(i32)]),
+                "moe_capture_watch": (i32, [p, ctypes.POINTER(ctypes.POINTER(ctypes.c_int32))]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -252,6 +255,27 @@ def moe_requant_launch_geometry(num_experts: int, K: int, expected_rows: int, sm
     _check("moe_requant_launch_geometry", load().moe_requant_launch_geometry(
         num_experts, K, expected_rows, sm_count, ctypes.byref(c), ctypes.byref(t)))
     return c.value, t.value
+
+
+def moe_capture_id(stream=None) -> int:
+    """The number of the capture that the stream is in, 0 if it is in none."""
+    n = ctypes.c_uint64(0)
+    _check("moe_capture_id", load().moe_capture_id(_stream(stream), ctypes.byref(n)))
+    return n.value
+
+
+def moe_capture_mode(mode: int) -> int:
+    """Sets the calling thread's capture interaction mode and returns the one it had."""
+    m = ctypes.c_int(mode)
+    _check("moe_capture_mode", load().moe_capture_mode(ctypes.byref(m)))
+    return m.value
+
+
+def moe_capture_watch(stream=None):
+    """A word (``.contents.value``) that becomes 1 once the graph being captured on the stream is gone."""
+    word = ctypes.POINTER(ctypes.c_int32)()
+    _check("moe_capture_watch", load().moe_capture_watch(_stream(stream), ctypes.byref(word)))
+    return word
 
 
 def moe_grouped_mm(dtype, x, x_stride, w, w_stride_e, w_stride_n, offsets, num_experts, rows, N, K, out, out_stride,

@@ -1,4 +1,6 @@
 // Entry points of moe_products.h: argument rules and the choice of the kernel.
+#include <new>
+
 #include "products_tc.cuh"
 
 using namespace moe;
@@ -122,4 +124,57 @@ extern "C" int moe_gemm_fp8_block(const void* x, int64_t x_stride, const float* 
   g.offsets = offsets, g.in_type = kE4m3, g.out_type = out_dtype, g.out = out, g.out_ld = out_stride;
   set_workspace(g, workspace);
   return run(g, kProdFwd, stream);
+}
+
+// ---------------------------------------------------------------- captured calls
+namespace moe {
+
+// The capture's number (0: none) and graph.
+static bool capture_of(void* stream, unsigned long long* id, cudaGraph_t* graph) {
+  cudaStreamCaptureStatus status;
+  if (cudaStreamGetCaptureInfo((cudaStream_t)stream, &status, id, graph) != cudaSuccess) return false;
+  if (status == cudaStreamCaptureStatusInvalidated) return false;
+  if (status == cudaStreamCaptureStatusNone) *id = 0;
+  return true;
+}
+
+}  // namespace moe
+
+extern "C" int moe_capture_id(void* stream, uint64_t* id) {
+  unsigned long long n = 0;
+  if (!id) return MOE_ERR_INVALID;
+  if (!capture_of(stream, &n, nullptr)) return MOE_ERR_CUDA;
+  *id = n;
+  return MOE_OK;
+}
+
+extern "C" int moe_capture_mode(int* mode) {
+  if (!mode || *mode < 0 || *mode > 2) return MOE_ERR_INVALID;
+  static_assert(cudaStreamCaptureModeRelaxed == 2, "the header names this value");
+  cudaStreamCaptureMode m = (cudaStreamCaptureMode)*mode;
+  if (cudaThreadExchangeStreamCaptureMode(&m) != cudaSuccess) return MOE_ERR_CUDA;
+  *mode = (int)m;
+  return MOE_OK;
+}
+
+extern "C" int moe_capture_watch(void* stream, const int32_t** gone) {
+  if (!gone) return MOE_ERR_INVALID;
+  unsigned long long id = 0;
+  cudaGraph_t graph = nullptr;
+  if (!capture_of(stream, &id, &graph)) return MOE_ERR_CUDA;
+  if (id == 0) return MOE_ERR_INVALID;
+  int32_t* word = new (std::nothrow) int32_t(0);
+  if (!word) return MOE_ERR_CUDA;
+  cudaUserObject_t object;
+  const cudaHostFn_t set = [](void* p) { __atomic_store_n(static_cast<int32_t*>(p), 1, __ATOMIC_RELEASE); };
+  if (cudaUserObjectCreate(&object, word, set, 1, cudaUserObjectNoDestructorSync) != cudaSuccess) {
+    delete word;
+    return MOE_ERR_CUDA;
+  }
+  if (cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove) != cudaSuccess) {
+    cudaUserObjectRelease(object, 1);  // (sets the word some time from now: it stays)
+    return MOE_ERR_CUDA;
+  }
+  *gone = word;
+  return MOE_OK;
 }

@@ -27,6 +27,8 @@ _DTYPE = {torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_FP16, torch.float32: 
 
 # One workspace per device and stream, as the kernels of one stream run one after another: (address, tensor).
 _workspaces = {}
+# Those of captured calls, by device, stream and capture: (address, tensor, word that tells whether the graph is gone).
+_captured = {}
 _workspace_lock = threading.Lock()
 
 
@@ -37,32 +39,53 @@ def _handle(device: int, stream) -> int:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _workspace(device: int, handle: int) -> int:
-    """Address of the workspace of this device and stream.  A captured call never takes it: the graph may be
-    replayed on any stream, beside calls on this one."""
-    if torch._C._cuda_isCurrentStreamCapturing():
-        return _captured_workspace(device)
+def _workspace(device: int, handle: int, stream=None) -> int:
+    """Address of the workspace of this device and stream (`stream` as the caller gave it).  A captured call never
+    takes it: the graph may be replayed on any stream, beside calls on this one."""
+    if torch._C._cuda_isCurrentStreamCapturing() if stream is None else B.moe_capture_id(handle):
+        return _captured_workspace(device, handle)
     ws = _workspaces.get((device, handle))
     return ws[0] if ws is not None else _new_workspace(device, handle)
-
-
-def _captured_workspace(device: int) -> int:
-    # the graph's own memory, zeroed by the graph: not kept for calls outside it.  The tensor lives until the
-    # next one is made, which is after the call's launch.
-    ws = torch.empty(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=torch.device("cuda", device))
-    ws[:B.MOE_PRODUCTS_WORKSPACE_HEAD_BYTES].zero_()
-    _workspaces["capture"] = (ws.data_ptr(), ws)
-    return ws.data_ptr()
 
 
 def _new_workspace(device: int, handle: int) -> int:
     with _workspace_lock:
         if (device, handle) not in _workspaces:
-            ws = torch.zeros(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=torch.device("cuda", device))
-            # the zeros are written on the current stream, the kernels run on `handle`
-            torch.cuda.current_stream(device).synchronize()
+            ws = _zeroed(device)
             _workspaces[(device, handle)] = (ws.data_ptr(), ws)
         return _workspaces[(device, handle)][0]
+
+
+def _captured_workspace(device: int, handle: int) -> int:
+    """Address of the workspace of the capture that the stream is in, on that stream: branches of a graph may run
+    at one time.  It is kept until the graph is gone, and then serves another capture."""
+    key = (device, handle, B.moe_capture_id(handle))
+    ws = _captured.get(key)
+    if ws is None:
+        with _workspace_lock:
+            ended = next((k for k, (_, _, gone) in _captured.items() if k[0] == device and gone.contents.value), None)
+            ws = _zeroed(device, None if ended is None else _captured.pop(ended)[1])
+            ws = _captured[key] = (ws.data_ptr(), ws, B.moe_capture_watch(handle))
+    return ws[0]
+
+
+def _zeroed(device: int, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A workspace (a new one unless given) whose head is zeros when this returns.  Also while the thread captures:
+    the kernels leave their counters at zero, so a graph needs no fill of its own, and memory that is not the
+    graph's is not shared with its other nodes."""
+    mode = B.moe_capture_mode(2)  # relaxed
+    try:
+        side = torch.cuda.Stream(device)
+        while B.moe_capture_id(side):  # (streams are handed out in turn)
+            side = torch.cuda.Stream(device)
+        with torch.cuda.stream(side):
+            if ws is None:
+                ws = torch.empty(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=torch.device("cuda", device))
+            ws[:B.MOE_PRODUCTS_WORKSPACE_HEAD_BYTES].zero_()
+        side.synchronize()
+    finally:
+        B.moe_capture_mode(mode)
+    return ws
 
 
 def _empty(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
@@ -204,7 +227,7 @@ def _by_row(fn: str, name: str, a: torch.Tensor, w: torch.Tensor, offsets: torch
         _used_on(stream, a, w, offsets, out)
     h = _handle(dev, stream)
     rc = B.function(fn)(code, a.data_ptr(), ld, w.data_ptr(), w_e, w_n, offsets.data_ptr(), E, rows, N, K,
-                        out.data_ptr(), out_ld, _workspace(dev, h), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+                        out.data_ptr(), out_ld, _workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
     if rc:
         raise B.MoeError(fn, rc)
     return out
@@ -259,7 +282,7 @@ def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out:
     rc = B.function("moe_grouped_mm_dw")(
         code, dy.data_ptr(), ld, x.data_ptr(), x_ld, offsets.data_ptr(), E, rows, N, K,
         code if out_dtype is dtype else B.MOE_FP32, 1 if accumulate else 0, out.data_ptr(), o_e, o_n,
-        _workspace(dev, h), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+        _workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
     if rc:
         raise B.MoeError("moe_grouped_mm_dw", rc)
     return out
@@ -392,7 +415,7 @@ def gemm_fp8_block(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_sc
     rc = B.function("moe_gemm_fp8_block")(
         x.data_ptr(), ld, x_scale.data_ptr(), s_m, s_g, w.data_ptr(), w_e, w_n, w_scale.data_ptr(),
         0 if offsets is None else ws[0], ws[-2], ws[-1], at, E, R, N, K, code, out.data_ptr(), out_ld,
-        _workspace(dev, h), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+        _workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
     if rc:
         raise B.MoeError("moe_gemm_fp8_block", rc)
     return out
