@@ -176,3 +176,34 @@ def test_a_workspace_made_in_a_capture_outlives_it():
         graph.replay()
         torch.cuda.synchronize()
         same(out, want)
+
+
+def test_broken_offsets_in_a_replay_are_reported():
+    P, B = products(), __import__("weight_only_bit_moe_gb300.binding", fromlist=["binding"])
+    a = Sliced(10)
+    want = a.alone()
+    assert P.products_status() == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = a()
+    graph.replay()
+    assert P.products_status() == 0
+    a.off.copy_(U.offsets_of([6]))  # past the rows
+    graph.replay()
+    a.off.copy_(U.offsets_of([5]))
+    graph.replay()  # and right again: what the replay before it found is kept
+    assert P.products_status() == B.MOE_ERR_INVALID
+    assert P.products_status() == 0
+    same(out, want)
+    a.off.copy_(U.offsets_of([6]))
+    graph.replay()
+    torch.cuda.synchronize()
+    del graph, out  # nor does the graph's end take it away
+    a.off.copy_(U.offsets_of([5]))
+    time.sleep(0.2)
+    again = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(again):
+        out = a()
+    again.replay()
+    assert P.products_status() == B.MOE_ERR_INVALID
+    same(out, want)

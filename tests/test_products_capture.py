@@ -76,3 +76,25 @@ def test_refusals():
     for mode in (-1, 3):
         with pytest.raises(B.MoeError):
             B.moe_capture_mode(mode)
+
+
+def test_the_status_of_graphs_is_reported(monkeypatch):
+    B = P.B
+    words = {EAGER: B.MOE_OK, OWN: B.MOE_ERR_INVALID, 3 << 20: B.MOE_ERR_TIMEOUT, 4 << 20: B.MOE_ERR_CUDA}
+
+    def status(workspace, stream):
+        word, words[workspace] = words[workspace], B.MOE_OK
+        return word
+
+    waited = []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: HANDLE, raising=False)
+    monkeypatch.setattr(torch.cuda, "synchronize", waited.append)
+    monkeypatch.setattr(P, "_workspace", lambda *a: EAGER)
+    monkeypatch.setattr(P, "_captured", {(0, HANDLE, 1): (OWN, None, Word()), (0, HANDLE, 2): (3 << 20, None, Word()),
+                                         (1, HANDLE, 3): (4 << 20, None, Word())}, raising=False)
+    monkeypatch.setattr(B, "moe_get_status", status)
+    assert P.products_status("cuda:0") == B.MOE_ERR_TIMEOUT and waited == [0]  # (device 1's is not asked for)
+    assert P.products_status("cuda:0") == B.MOE_OK  # every word was cleared
+    words[OWN] = B.MOE_ERR_INVALID
+    assert P.products_status("cuda:0") == B.MOE_ERR_INVALID

@@ -70,18 +70,20 @@ def _captured_workspace(device: int, handle: int) -> int:
 
 
 def _zeroed(device: int, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """A workspace (a new one unless given) whose head is zeros when this returns.  Also while the thread captures:
-    the kernels leave their counters at zero, so a graph needs no fill of its own, and memory that is not the
-    graph's is not shared with its other nodes."""
+    """A workspace (a new one unless given) whose head is zeros when this returns; one that is given keeps its
+    status, which nobody may have read.  Also while the thread captures: the kernels leave their counters at zero,
+    so a graph needs no fill of its own, and memory that is not the graph's is not shared with its other nodes."""
     mode = B.moe_capture_mode(2)  # relaxed
     try:
         side = torch.cuda.Stream(device)
         while B.moe_capture_id(side):  # (streams are handed out in turn)
             side = torch.cuda.Stream(device)
         with torch.cuda.stream(side):
+            first = 4  # past the status word
             if ws is None:
                 ws = torch.empty(B.MOE_PRODUCTS_WORKSPACE_BYTES, dtype=torch.uint8, device=torch.device("cuda", device))
-            ws[:B.MOE_PRODUCTS_WORKSPACE_HEAD_BYTES].zero_()
+                first = 0
+            ws[first:B.MOE_PRODUCTS_WORKSPACE_HEAD_BYTES].zero_()
         side.synchronize()
     finally:
         B.moe_capture_mode(mode)
@@ -108,15 +110,22 @@ def _used_on(stream, *tensors: Optional[torch.Tensor]) -> None:
 
 
 def products_status(device="cuda", stream=None) -> int:
-    """Synchronises the stream and returns (and clears) the device status of its products:
-    MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_INVALID (offsets that decrease or leave the rows)."""
+    """Synchronises the stream and returns (and clears) the device status of its products and of those in the
+    device's graphs, whose replays it waits for on every stream: MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_INVALID
+    (offsets that decrease or leave the rows)."""
     index = torch.device(device).index
     index = torch.cuda.current_device() if index is None else index
     if index != _current_device():
         with torch.cuda.device(index):
             return products_status(torch.device("cuda", index), stream)
     handle = _handle(index, stream)
-    return B.moe_get_status(_workspace(index, handle), handle)
+    status = [B.moe_get_status(_workspace(index, handle), handle)]
+    graphs = [ws for key, (ws, _, _) in list(_captured.items()) if key[0] == index]
+    if graphs:
+        torch.cuda.synchronize(index)
+        status += [B.moe_get_status(ws, handle) for ws in graphs]
+    return next((s for s in (B.MOE_ERR_CUDA, B.MOE_ERR_TIMEOUT) if s in status),
+                next((s for s in status if s != B.MOE_OK), B.MOE_OK))
 
 
 # The checks below read each attribute of a tensor once: for a decode step they are most of a call's host time.
