@@ -297,6 +297,30 @@ def grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out:
     return out
 
 
+# y = grouped_mm(x, w), dx = grouped_mm_dx(dy, w) and dw = grouped_mm_dw(dy, x) are bilinear, and the gradients of each
+# are the other two, so the three have derivatives of any order.  In an ordinary backward pass autograd records
+# nothing, and the kernels are called without its bookkeeping.
+
+def _by_row_zeroed(fn, a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, partial: bool, width: int):
+    return fn(a, w, offsets, out=a.new_zeros((a.shape[0], width)) if partial else None)
+
+
+def _mm(x, w, offsets, partial):
+    if torch.is_grad_enabled():
+        return GroupedLinear.apply(x, w, offsets, partial)
+    return _by_row_zeroed(grouped_mm, x, w, offsets, partial, w.shape[1])
+
+
+def _mm_dx(dy, w, offsets, partial):
+    if torch.is_grad_enabled():
+        return GroupedLinearDx.apply(dy, w, offsets, partial)
+    return _by_row_zeroed(grouped_mm_dx, dy, w, offsets, partial, w.shape[2])
+
+
+def _mm_dw(dy, x, offsets, partial):
+    return GroupedLinearDw.apply(dy, x, offsets, partial) if torch.is_grad_enabled() else grouped_mm_dw(dy, x, offsets)
+
+
 class GroupedLinear(torch.autograd.Function):
     """grouped_mm with its gradients by x and w."""
 
@@ -304,23 +328,57 @@ class GroupedLinear(torch.autograd.Function):
     def forward(ctx, x, w, offsets, partial):
         ctx.save_for_backward(x, w, offsets)
         ctx.partial = partial
-        return grouped_mm(x, w, offsets, out=x.new_zeros((x.shape[0], w.shape[1])) if partial else None)
+        return _by_row_zeroed(grouped_mm, x, w, offsets, partial, w.shape[1])
 
     @staticmethod
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dy = dy.contiguous()
-        dx = dw = None
-        if ctx.needs_input_grad[0]:
-            dx = grouped_mm_dx(dy, w, offsets, out=torch.zeros_like(x) if ctx.partial else None)
-        if ctx.needs_input_grad[1]:
-            dw = grouped_mm_dw(dy, x, offsets)
+        dx = _mm_dx(dy, w, offsets, ctx.partial) if ctx.needs_input_grad[0] else None
+        dw = _mm_dw(dy, x, offsets, ctx.partial) if ctx.needs_input_grad[1] else None
         return dx, dw, None, None
 
 
+class GroupedLinearDx(torch.autograd.Function):
+    """grouped_mm_dx with its gradients by dy and w."""
+
+    @staticmethod
+    def forward(ctx, dy, w, offsets, partial):
+        ctx.save_for_backward(dy, w, offsets)
+        ctx.partial = partial
+        return _by_row_zeroed(grouped_mm_dx, dy, w, offsets, partial, w.shape[2])
+
+    @staticmethod
+    def backward(ctx, g):
+        dy, w, offsets = ctx.saved_tensors
+        g = g.contiguous()
+        d_dy = _mm(g, w, offsets, ctx.partial) if ctx.needs_input_grad[0] else None
+        d_w = _mm_dw(dy, g, offsets, ctx.partial) if ctx.needs_input_grad[1] else None
+        return d_dy, d_w, None, None
+
+
+class GroupedLinearDw(torch.autograd.Function):
+    """grouped_mm_dw with its gradients by dy and x."""
+
+    @staticmethod
+    def forward(ctx, dy, x, offsets, partial):
+        ctx.save_for_backward(dy, x, offsets)
+        ctx.partial = partial
+        return grouped_mm_dw(dy, x, offsets)
+
+    @staticmethod
+    def backward(ctx, g):
+        dy, x, offsets = ctx.saved_tensors
+        g = g.contiguous()
+        d_dy = _mm(x, g, offsets, ctx.partial) if ctx.needs_input_grad[0] else None
+        d_x = _mm_dx(dy, g, offsets, ctx.partial) if ctx.needs_input_grad[1] else None
+        return d_dy, d_x, None, None
+
+
 def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, partial: bool = False) -> torch.Tensor:
-    """Differentiable grouped_mm.  Every row must belong to an expert (offsets from 0 to rows), unless `partial`:
-    then the other rows, as of experts held elsewhere, give zeros and get zeros as their gradient."""
+    """Differentiable grouped_mm, its derivatives too.  Every row must belong to an expert (offsets from 0 to rows),
+    unless `partial`: then the other rows, as of experts held elsewhere, give zeros and get zeros as their gradient.
+    (The calls that take `out` are the kernels alone: what they return has no gradient.)"""
     return GroupedLinear.apply(x, w, offsets, partial)
 
 
