@@ -67,7 +67,8 @@ int moe_grouped_mm_dx(int dtype, const void* dy, int64_t dy_stride, const void* 
  *   dw          [num_experts, N, K], strides dw_stride_e, dw_stride_n >= K, of
  *               type dw_dtype: dtype or MOE_FP32
  *   accumulate  0: dw is written; 1 (MOE_FP32 only): the gradient is added to it
- *               (values below 2^-126 may count as zeros there)
+ *               (values below 2^-126 may count as zeros there; the part of an
+ *               expert without rows is left as it is)
  * The same inputs give the same bits. */
 int moe_grouped_mm_dw(int dtype, const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
                       const int32_t* offsets, int num_experts, int rows, int N, int K, int dw_dtype,

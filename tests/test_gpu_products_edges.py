@@ -1,0 +1,59 @@
+"""Values at the ends of fp32's range in the products: small ones in a buffer that a
+gradient is added to, scales of opposite size, gates whose exponential nearly
+overflows.  Each for operands that the tensor-core kernels take and for others."""
+import pytest
+import torch
+
+from gpu_util import need_gpu
+import products_util as U
+
+pytestmark = pytest.mark.gpu
+F8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def products():
+    from weight_only_bit_moe_gb300 import products as P
+    return P
+
+
+def normal(*shape, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("sizes,N,K", [
+    ([0, 1900, 0], 264, 200),          # few tiles, sums in slices
+    ([0, 40, 0, 0, 300, 0], 1024, 520),
+    ([0] * 80 + [3], 512, 256),        # more tiles than CTA pairs
+    ([0, 70, 0], 65, 33),              # operands off the 16-byte grid
+    ([0, 0], 128, 64),                 # no rows at all
+])
+def test_accumulation_leaves_experts_without_rows_alone(sizes, N, K):
+    """Their gradient is zero, so their part of the buffer keeps its bits: values below fp32's normal range, zeros
+    with a sign, infinities and NaN included."""
+    P = products()
+    dy, x = normal(sum(sizes), N, seed=1).bfloat16(), normal(sum(sizes), K, seed=2).bfloat16()
+    start = normal(len(sizes), N, K, seed=3)
+    start[:, 1::2] *= 2.0 ** -130
+    start[:, 0, 0], start[:, 0, 1], start[:, 0, 2] = -0.0, float("inf"), float("nan")
+    out = start.clone()
+    P.grouped_mm_dw(dy, x, U.offsets_of(sizes), out=out, accumulate=True)
+    for e, m in enumerate(sizes):
+        if m == 0:
+            assert torch.equal(out[e].view(torch.int32), start[e].view(torch.int32)), f"expert {e}"
+        else:
+            ref, mag = dy_x(dy, x, sizes, e)
+            part = slice(2, None, 2)  # (values that stay in fp32's normal range)
+            U.assert_within(out[e][part], (ref + start[e].double())[part], (mag + start[e].double().abs())[part], m + 1)
+    assert P.products_status() == 0
+
+
+def dy_x(dy, x, sizes, e):
+    a = sum(sizes[:e])
+    d, v = dy[a:a + sizes[e]].double(), x[a:a + sizes[e]].double()
+    return d.t() @ v, d.abs().t() @ v.abs()

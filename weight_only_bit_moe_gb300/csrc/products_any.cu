@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kAnyThreads) products_any_dw_kernel(const __gr
   int r0, r1;
   group_rows(g, e, r0, r1);
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && group_bad(g, e)) atomicOr(g.status, kStatusRouting);
+  if (g.accumulate && r0 == r1) return;  // nothing is added: the expert's part keeps its bits
   float acc[4][4] = {};
   any_tile<kProdDw>(g, e, i0, g.N, j0, g.K, r0, r1, s, acc);
 #pragma unroll

@@ -406,6 +406,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     uint32_t ic = 0, box = 0;
     for (GtWalk<MODE> at(pl, q_tiles, pair, a.pairs); at.w < items; at.next()) {
       const ProdItem it = at.item(g, pl, start, order);
+      if (MODE == kProdDw && g.accumulate) {  // nothing is added for an expert without rows: its part keeps its bits
+        int r0, r1;
+        group_rows(g, it.e, r0, r1);
+        if (r0 == r1) continue;  // (in every warp and slice: no accumulator or counter moves)
+      }
       const int p = it.p0 + rank * 128 + quarter * 32;  // this warp's first P row
       const bool none = it.t0 >= it.t1;                 // no terms: the sums are zeros
       const int acc = ic & 1;
