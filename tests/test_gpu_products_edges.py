@@ -57,3 +57,19 @@ def dy_x(dy, x, sizes, e):
     a = sum(sizes[:e])
     d, v = dy[a:a + sizes[e]].double(), x[a:a + sizes[e]].double()
     return d.t() @ v, d.abs().t() @ v.abs()
+
+
+@pytest.mark.parametrize("rows,N", [(12, 264), (300, 2056)])  # rows on the N and on the M side
+@pytest.mark.parametrize("pad", [0, 1])                       # 1: off the 16-byte grid
+@pytest.mark.parametrize("up", [120, -120])
+def test_fp8_scales_of_opposite_size(rows, N, pad, up):
+    """Each block's sum is multiplied by xs * ws: with scales of 2^120 and 2^-120 the result is that of scales of 1,
+    although x * xs (up to 2^128.8) or w * ws lies outside fp32."""
+    P = products()
+    K = 528
+    x, w = (normal(rows, K, seed=4) * 150).clamp(-448, 448).to(F8), (normal(N, K, seed=5) * 150).clamp(-448, 448).to(F8)
+    xs = torch.full((rows, 5), 2.0 ** up, device="cuda")
+    ws = torch.full((-(-N // 128), 5), 2.0 ** -up, device="cuda")
+    x, w = (U.strided(t, pad, 0) if pad else t for t in (x, w))
+    out = P.gemm_fp8_block(x, xs, w, ws, out_dtype=torch.float32)
+    U.assert_within(out, x.double() @ w.double().t(), x.double().abs() @ w.double().abs().t(), K)

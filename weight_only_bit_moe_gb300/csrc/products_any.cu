@@ -5,8 +5,10 @@
 //   dW:            out[e][n, k] = sum_{r in e} dy[r, n] x[r, k]
 //
 // A 64 x 64 output tile per CTA, 4 x 4 sums per thread in fp32, operands
-// converted to fp32 (FP8: times their block's scale) on their way into shared
-// memory, 16 terms of the sum at a time.  Plain loads of single elements: this
+// converted to fp32 on their way into shared memory, 16 terms of the sum at a
+// time.  FP8: each block's sum is multiplied by xs ws, as on the tensor cores; the
+// elements times their scales could leave fp32's range where the product of the
+// scales does not.  Plain loads of single elements: this
 // kernel takes the operands that TMA cannot address, and is bound by its fp32
 // multiply-adds and these loads.
 #include "products.cuh"
@@ -24,17 +26,13 @@ struct AnyTiles {
 template <int MODE>
 __device__ __forceinline__ float any_a(const ProdArgs& g, int64_t i, int t) {
   if (MODE == kProdDw) return load_elem(g.a, (int64_t)t * g.a_ld + i, g.in_type);
-  float v = load_elem(g.a, i * g.a_ld + t, g.in_type);
-  if (g.in_type == kE4m3) v *= g.xs[i * g.xs_m + (int64_t)(t >> 7) * g.xs_g];
-  return v;
+  return load_elem(g.a, i * g.a_ld + t, g.in_type);
 }
 template <int MODE>
 __device__ __forceinline__ float any_b(const ProdArgs& g, int e, int64_t j, int t) {
   if (MODE == kProdDw) return load_elem(g.w, (int64_t)t * g.w_ld + j, g.in_type);
   if (MODE == kProdDx) return load_elem(g.w, e * g.w_se + (int64_t)t * g.w_ld + j, g.in_type);
-  float v = load_elem(g.w, e * g.w_se + j * g.w_ld + t, g.in_type);
-  if (g.in_type == kE4m3) v *= g.ws[e * g.ws_e + (j >> 7) * g.ws_n + (int64_t)(t >> 7) * g.ws_k];
-  return v;
+  return load_elem(g.w, e * g.w_se + j * g.w_ld + t, g.in_type);
 }
 
 // acc[y][x] += sum over t in [t0, t1) of A(i0 + 4 ty + y, t) B(j0 + 4 tx + x, t); rows at or
@@ -78,7 +76,22 @@ __global__ void __launch_bounds__(kAnyThreads) products_any_rows_kernel(const __
     const int i0 = max(row0, r0), i1 = min(row1, r1);
     if (i0 >= i1) continue;
     float acc[4][4] = {};
-    any_tile<MODE>(g, e, i0, i1, j0, cols, 0, terms, s, acc);
+    if (MODE == kProdFwd && g.in_type == kE4m3) {
+      for (int b = 0; 128 * b < terms; ++b) {
+        float part[4][4] = {};
+        any_tile<MODE>(g, e, i0, i1, j0, cols, 128 * b, min(128 * b + 128, terms), s, part);
+        const float ws = g.ws[e * g.ws_e + (int64_t)(j0 >> 7) * g.ws_n + (int64_t)b * g.ws_k];  // (64 columns: one block)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int i = i0 + 4 * ty + y;
+          const float scale = i < i1 ? g.xs[i * g.xs_m + (int64_t)b * g.xs_g] * ws : 0.0f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[y][x] = fmaf(part[y][x], scale, acc[y][x]);
+        }
+      }
+    } else {
+      any_tile<MODE>(g, e, i0, i1, j0, cols, 0, terms, s, acc);
+    }
 #pragma unroll
     for (int y = 0; y < 4; ++y)
 #pragma unroll
