@@ -81,7 +81,7 @@ int moe_grouped_mm_dw(int dtype, const void* dy, int64_t dy_stride, const void* 
  * with, per block of 128 columns (the last may be shorter),
  *   s = max(max |v| / 448, 2^-126),  q = e4m3(v * (1 / s)),
  * each operation rounded to fp32, q to nearest even; silu(g) = g / (1 + exp(-g)),
- * 0 below g = -87.3.
+ * 0 below g = -88.72, where exp(-g) passes the largest fp32 number.
  * A NaN or an infinity in a block makes s a NaN or an infinity, so
  * the block's values q * s are not finite.
  *   dtype   MOE_BF16 or MOE_FP16: the type of x [x_rows, K or 2K], row stride

@@ -73,3 +73,39 @@ def test_fp8_scales_of_opposite_size(rows, N, pad, up):
     x, w = (U.strided(t, pad, 0) if pad else t for t in (x, w))
     out = P.gemm_fp8_block(x, xs, w, ws, out_dtype=torch.float32)
     U.assert_within(out, x.double() @ w.double().t(), x.double().abs() @ w.double().abs().t(), K)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("K", [512, 130, 200])  # 130: off the 16-byte grid
+def test_gates_near_the_exponentials_overflow(dtype, K):
+    """silu of -88.69 to -87 in fp32: exp(-g) is finite (up to 88.72), the quotient of the order of 1e-37 and in the
+    normal range.  The bounds are those of ordinary gates: half a code step, and 2^-20 for the steps in fp32."""
+    P = products()
+    g = torch.linspace(-88.6, -87.0, 6 * K, device="cuda").view(6, K).to(dtype)
+    g[0, :3] = torch.tensor([-88.5, -88.0, -87.5], device="cuda").to(dtype)
+    u = (normal(6, K, seed=6).abs() * 100 + 100).to(dtype)
+    q, s = P.quant_fp8_block(torch.cat([g, u], 1), gated=True)
+    v = g.double() * torch.sigmoid(g.double()) * u.double()
+    top = torch.nn.functional.pad(v, (0, -K % 128)).unflatten(1, (-1, 128)).abs().amax(2) / 448.0
+    assert (top > 2.0 ** -126).all()
+    assert ((s.double() - top).abs() <= 2.0 ** -20 * top).all()
+    sw = U.spread_rows(s, K).double()
+    err = (q.double() * sw - v).abs()
+    assert (err <= torch.maximum(v.abs() * 2.0 ** -4, sw * 2.0 ** -10) + 2.0 ** -20 * v.abs()).all()
+
+
+@pytest.mark.parametrize("K", [128, 130])
+def test_gated_rows_that_are_not_finite(K):
+    """A NaN or an infinity in either half makes its block's values not finite, and no other block's; gates far
+    below the overflow give zeros."""
+    P = products()
+    for value in (float("nan"), float("inf"), float("-inf")):
+        for half in (0, 1):
+            x = torch.ones(3, 2 * K, dtype=torch.bfloat16, device="cuda")
+            x[1, half * K + 5] = value
+            x[2, :K] = -100.0
+            q, s = P.quant_fp8_block(x, gated=True)
+            v = q.float() * U.spread_rows(s, K)
+            assert not torch.isfinite(v[1, :128]).any()
+            assert torch.isfinite(v[1, 128:]).all() and torch.isfinite(v[0]).all() and (v[0] > 0).all()
+            assert (v[2] == 0).all()
