@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_tc_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  pl.tiles = start[g.E];
+  pl.tiles = min(start[g.E], kProdItems);
   pl.S = plan_slices(pl, gridDim.x, 1, ROWS_M ? 1 << 30 : 0, 256);
   const int items = pl.tiles * pl.S;
 
@@ -470,7 +470,7 @@ cudaError_t launch_fp8_tc(const ProdArgs& g, cudaStream_t st, bool* done) {
   // enough for four, a long sum is faster in those: 8192 x 7168, 128 rows 25.7 and 23.2, 5120 x 16384 45.8 and 32.1;
   // up to 40 blocks it is not (8192 x 5120 19.8 and 20.6).
   const int sms = prod_sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
+  if (sms <= 0 || sms > kProdWidth) return cudaErrorInvalidDevice;
   const int64_t groups = g.E < g.rows ? g.E : g.rows, each = (g.rows + groups - 1) / groups;  // (rows > 0)
   const int64_t tiles_n = groups * ((each + 63) / 64) * ((g.N + 127) / 128);
   const int64_t tiles_m = groups * ((each + 127) / 128) * ((g.N + 255) / 256);

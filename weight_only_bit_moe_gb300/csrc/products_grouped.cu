@@ -316,7 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
     if (order) group_rows(g, order[0], r0, r1);
     pl.stages = (r1 - r0 + 63) / 64;
   } else {
-    pl.tiles = start[g.E];
+    pl.tiles = min(start[g.E], kProdItems);
   }
   pl.S = plan_slices(pl, a.pairs, 2, MODE == kProdDw ? 1 << 30 : g.rows, kGtN);
   const int items = pl.tiles * pl.S;
@@ -698,7 +698,7 @@ cudaError_t launch_grouped_tc(const ProdArgs& g, int mode, cudaStream_t st, bool
   if (mode != kProdDw) a.map_out = a.map_dw_q = a.map_p;
   if (!ok) return cudaSuccess;  // (the plain kernel takes what a tensor map cannot describe)
   const int sms = prod_sm_count();
-  if (sms < 2) return cudaErrorInvalidDevice;
+  if (sms < 2 || sms > kProdWidth) return cudaErrorInvalidDevice;
   a.pairs = sms / 2;
   a.wide_store = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0 && g.out_ld % 8 == 0 && g.out_se % 8 == 0;
   *done = true;

@@ -287,6 +287,12 @@ constexpr int kProdGroups = 1024;       // groups, at most
 constexpr int kProdTokenChunk = 8;      // row tiles that run next to each other through a group's features
 constexpr int kProdPartials = 320;      // partial tiles of 128 x 256 sums that the scratch holds
 constexpr int kProdCounterBytes = 4096; // scratch: arrival counters, then partial tiles
+// Items of a launch, at most.  Offsets that do not overlap give 1e9 of them (the host's limit); others can count up
+// to 2^31, and a role's position, which passes the last item by up to a launch's width, must not wrap to numbers
+// below 0 that would be taken for items again.
+constexpr int kProdWidth = 65536;       // CTAs of a launch, at most
+constexpr int kProdItems = 0x7FFFFFFF - kProdWidth;
+static_assert(kProdItems > 1000000000, "offsets that keep the rule would lose tiles");
 
 struct RowPlan {
   int tiles, S, stages, p_tiles;
