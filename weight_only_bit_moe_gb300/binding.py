@@ -276,41 +276,3 @@ def moe_capture_watch(stream=None):
     word = ctypes.POINTER(ctypes.c_int32)()
     _check("moe_capture_watch", load().moe_capture_watch(_stream(stream), ctypes.byref(word)))
     return word
-
-
-def moe_grouped_mm(dtype, x, x_stride, w, w_stride_e, w_stride_n, offsets, num_experts, rows, N, K, out, out_stride,
-                   workspace, workspace_bytes, stream=None):
-    return _check("moe_grouped_mm", load().moe_grouped_mm(
-        dtype, _p(x), x_stride, _p(w), w_stride_e, w_stride_n, _p(offsets), num_experts, rows, N, K, _p(out),
-        out_stride, _p(workspace), workspace_bytes, _stream(stream)))
-
-
-def moe_grouped_mm_dx(dtype, dy, dy_stride, w, w_stride_e, w_stride_n, offsets, num_experts, rows, N, K, dx,
-                      dx_stride, workspace, workspace_bytes, stream=None):
-    return _check("moe_grouped_mm_dx", load().moe_grouped_mm_dx(
-        dtype, _p(dy), dy_stride, _p(w), w_stride_e, w_stride_n, _p(offsets), num_experts, rows, N, K, _p(dx),
-        dx_stride, _p(workspace), workspace_bytes, _stream(stream)))
-
-
-def moe_grouped_mm_dw(dtype, dy, dy_stride, x, x_stride, offsets, num_experts, rows, N, K, dw_dtype, accumulate, dw,
-                      dw_stride_e, dw_stride_n, workspace, workspace_bytes, stream=None):
-    return _check("moe_grouped_mm_dw", load().moe_grouped_mm_dw(
-        dtype, _p(dy), dy_stride, _p(x), x_stride, _p(offsets), num_experts, rows, N, K, dw_dtype, accumulate,
-        _p(dw), dw_stride_e, dw_stride_n, _p(workspace), workspace_bytes, _stream(stream)))
-
-
-def moe_quant_fp8_block(dtype, x, x_stride, x_rows, row_index, rows, K, gated, q, q_stride, scale, scale_strides,
-                        stream=None):
-    """scale_strides = (m, g) element strides of the fp32 scale buffer."""
-    return _check("moe_quant_fp8_block", load().moe_quant_fp8_block(
-        dtype, _p(x), x_stride, x_rows, _p(row_index), rows, K, gated, _p(q), q_stride, _p(scale),
-        scale_strides[0], scale_strides[1], _stream(stream)))
-
-
-def moe_gemm_fp8_block(x, x_stride, x_scale, xs_strides, w, w_strides, w_scale, ws_strides, offsets, num_experts,
-                       rows, N, K, out_dtype, out, out_stride, workspace, workspace_bytes, stream=None):
-    """xs_strides = (m, g), w_strides = (e, n), ws_strides = (e, n, k)."""
-    return _check("moe_gemm_fp8_block", load().moe_gemm_fp8_block(
-        _p(x), x_stride, _p(x_scale), xs_strides[0], xs_strides[1], _p(w), w_strides[0], w_strides[1], _p(w_scale),
-        ws_strides[0], ws_strides[1], ws_strides[2], _p(offsets), num_experts, rows, N, K, out_dtype, _p(out),
-        out_stride, _p(workspace), workspace_bytes, _stream(stream)))
