@@ -8,9 +8,12 @@
 // between the maximum and the rounding.  Operands off the 16-byte grid run a
 // form of the same with single elements.
 //
-// Bound by instructions where rows come from L2 (16384 rows of 4096 gathered from
-// 2048: 19.4 us, 201 MB moved, ALU 65 % busy; floor by memory 12.7) and between them
-// and memory when gated (4093 rows of 2880: 12.5 us; floor 8.7).
+// Gathered rows are bound by instructions (16384 rows of 4096 from 2048: 17.5 us with
+// the tokens in L2, 19.9 from memory, 201 MB moved, ALU 65 % busy; floor by memory
+// 12.7): each token is quantised as often as it is gathered.  Gated rows fill no unit
+// (4093 rows of 2880: 10.9 us in L2, 13.3 from memory, where ALU 36 %, FMA 47 % and
+// DRAM 37 % are busy; floor 8.7): a warp's loads, arithmetic and stores follow one
+// another.
 #include "products_tc.cuh"
 
 namespace moe {
