@@ -1,0 +1,92 @@
+/*
+ * moe_adapters.h -- C ABI of the low-rank adapters beside a shared projection
+ * (GB300, sm_103a): what tuning frozen 4-bit, FP8 or 16-bit weights trains, and what
+ * serving many tuned variants of them at once adds to each projection.
+ *
+ * Conventions as in moe_products.h: device pointers owned by the caller, no
+ * allocation, no synchronisation, `stream` a cudaStream_t passed as void*, return
+ * values from moe_status, strides in elements with the innermost dimension
+ * contiguous, and its workspace, which serves both.
+ *
+ * Adapter l holds A[l] [rank, K] and B[l] [N, rank] and changes a projection's
+ * output y = W x to y + scale[l] B[l] (A[l] x).
+ *
+ * Rows.  Adapter l has the positions [offsets[l], offsets[l + 1]), offsets int32
+ * [num_adapters + 1] on the device, not decreasing, inside [0, rows]; position i
+ * stands for the row order[i] of the row matrices (order NULL: for row i).  order is
+ * int32 [rows] and names each row once.  The rows of the other positions have no
+ * adapter.  Offsets that break the rule and entries outside [0, rows) never lead to
+ * an access outside the arguments; the workspace's status then holds
+ * MOE_ERR_INVALID and the rows concerned are unspecified, as are rows that order
+ * names more than once or not at all.
+ *
+ * Sizes.  num_adapters 1 .. 4096, rank 1 .. 256, 1 <= N, K <= 2^21, 0 <= rows <
+ * 2^31 - 1024.  Any strides and alignment are computed; the fast kernels take
+ * matrices whose base addresses and strides are multiples of 16 bytes.
+ */
+#ifndef MOE_ADAPTERS_H
+#define MOE_ADAPTERS_H
+
+#include <stdint.h>
+
+#include "moe_products.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define MOE_MAX_ADAPTERS 4096
+#define MOE_MAX_RANK 256
+#define MOE_ADAPTER_MID_VALUES ((int64_t)1 << 22)
+
+/* out[r] = base[r] + scale[l] B[l] mid[i],  mid[i] = A[l] x[r]   for the rows r of
+ * adapter l (r at position i); out[r] = base[r] for the others.
+ *   dtype   MOE_BF16 or MOE_FP16: the type of x, a, b, base and out
+ *   x       [rows, K], a [num_adapters, rank, K] with strides a_stride_l,
+ *           a_stride_r >= K, b [num_adapters, N, rank] with strides b_stride_l,
+ *           b_stride_n >= rank
+ *   scale   fp32 [num_adapters], or NULL for ones
+ *   base    [rows, N] or NULL for zeros; may be out itself (same strides: then the
+ *           rows without an adapter are not touched), else does not overlap it
+ *   out     [rows, N], or NULL: then only mid is computed (b, base and scale are not
+ *           read)
+ *   mid     fp32 [rows, rank], contiguous: written at the positions of adapters (for
+ *           moe_adapter_mm_dw), unspecified at the others.  NULL: kept in the
+ *           workspace, for rows * rank <= MOE_ADAPTER_MID_VALUES
+ * mid is summed in fp32 and enters the second product with at least 16 significant
+ * bits; sums are fp32, rounded once to dtype.  rows == 0 is a no-op. */
+int moe_adapter_mm(int dtype, const void* x, int64_t x_stride, const void* a, int64_t a_stride_l, int64_t a_stride_r,
+                   const void* b, int64_t b_stride_l, int64_t b_stride_n, const int32_t* offsets,
+                   const int32_t* order, const float* scale, int num_adapters, int rows, int N, int K, int rank,
+                   const void* base, int64_t base_stride, void* out, int64_t out_stride, float* mid,
+                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The gradient by the rows: dx[r] = base[r] + scale[l] A[l]^T mid[i], mid[i] =
+ * B[l]^T dy[r].  dy [rows, N]; base and dx [rows, K]; otherwise as moe_adapter_mm. */
+int moe_adapter_mm_dx(int dtype, const void* dy, int64_t dy_stride, const void* a, int64_t a_stride_l,
+                      int64_t a_stride_r, const void* b, int64_t b_stride_l, int64_t b_stride_n,
+                      const int32_t* offsets, const int32_t* order, const float* scale, int num_adapters, int rows,
+                      int N, int K, int rank, const void* base, int64_t base_stride, void* dx, int64_t dx_stride,
+                      float* mid, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The gradients by the adapters:
+ *   dA[l] = scale[l] sum over i of mid_dy[i] x[r]^T,  dB[l] = scale[l] sum over i of dy[r] mid_x[i]^T
+ * with mid_x of moe_adapter_mm and mid_dy of moe_adapter_mm_dx; zero for an adapter
+ * without rows.  One of the two may be left out: da NULL (x and mid_dy are then not
+ * read) or db NULL (dy and mid_x).
+ *   da, db   of grad_dtype: dtype or MOE_FP32; strides as of a and b
+ *   accumulate  0: written; 1 (MOE_FP32 only): added to (the part of an adapter
+ *            without rows keeps its bits)
+ * Sums are fp32.  The same inputs give the same bits. */
+int moe_adapter_mm_dw(int dtype, const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                      const float* mid_x, const float* mid_dy, const int32_t* offsets, const int32_t* order,
+                      const float* scale, int num_adapters, int rows, int N, int K, int rank, int grad_dtype,
+                      int accumulate, void* da, int64_t da_stride_l, int64_t da_stride_r, void* db,
+                      int64_t db_stride_l, int64_t db_stride_n, void* workspace, int64_t workspace_bytes,
+                      void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MOE_ADAPTERS_H */

@@ -1,0 +1,101 @@
+/*
+ * moe_routing.h -- C ABI of what decides and balances the routing of the layer of
+ * moe_w4a16.h (GB300, sm_103a): the experts of each token with their weights, the
+ * pairs of each expert, the balance loss, and the gradients by the logits.
+ *
+ * Conventions as in moe_w4a16.h: device pointers owned by the caller, no
+ * allocation, no synchronisation, `stream` a cudaStream_t passed as void*,
+ * return values from moe_status.  Strides count elements; the experts of a token
+ * and the slots of a token are contiguous.  Logits are MOE_BF16, MOE_FP16 or
+ * MOE_FP32 (moe_products.h); everything is computed in 32 bits, or in 64 where
+ * said.  1 <= num_experts <= 1024, 0 <= tokens (0 is a no-op where nothing but
+ * token rows is written), tokens * num_experts < 2^40.
+ *
+ * Workspace (where there is one): as in moe_products.h, and the same one serves.
+ */
+#ifndef MOE_ROUTING_H
+#define MOE_ROUTING_H
+
+#include <stdint.h>
+
+#include "moe_products.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+#define MOE_MAX_TOP_K 32
+
+/* The top_k experts of each token and their weights.
+ *   p      = softmax of the token's logits, or the sigmoid of each
+ *   chosen: the top_k largest p + bias, largest first, equal ones by ascending
+ *          expert; without bias the largest logits.  Sums that 32 bits cannot tell
+ *          apart are compared in 64.
+ *   weight = scale * p[chosen], divided by the sum of the token's chosen p when
+ *          renormalize is 1
+ * An expert whose logit or bias is -infinity is never chosen; slots without an
+ * expert get id -1 and weight 0.  A token with a NaN or +infinity among its logits
+ * or biases gets ids -1 and weights NaN.
+ *   logits  [tokens, num_experts], row stride logits_stride >= num_experts
+ *   bias    fp32 [num_experts] or NULL
+ *   top_k   1 .. min(num_experts, MOE_MAX_TOP_K)
+ *   weights fp32 [tokens, top_k], ids int32 [tokens, top_k], both contiguous
+ * The same inputs give the same bits. */
+int moe_route(int dtype, const void* logits, int64_t logits_stride, const float* bias, int tokens, int num_experts,
+              int top_k, int score, int renormalize, float scale, float* weights, int32_t* ids, void* stream);
+
+/* The gradient of moe_route's weights by the logits, the choice held fixed: written
+ * for every expert of every token.  ids as moe_route gave them, or other ones: ids
+ * outside [0, num_experts) take no part (nor do their dweights), an id that stands
+ * twice counts twice.  A token without ids gets zeros.  A NaN that the formula meets
+ * gives NaN.
+ *   dweights fp32 [tokens, top_k], row stride dweights_stride >= top_k
+ *   ids      int32 [tokens, top_k], contiguous
+ *   dlogits  [tokens, num_experts] of the logits' type, row stride dlogits_stride */
+int moe_route_grad(int dtype, const float* dweights, int64_t dweights_stride, const void* logits,
+                   int64_t logits_stride, const int32_t* ids, int tokens, int num_experts, int top_k, int score,
+                   int renormalize, float scale, void* dlogits, int64_t dlogits_stride, void* stream);
+
+/* counts[s, e]: how often e stands among the ids of the tokens of sequence s.
+ * Sequence s has the tokens [offsets[s], offsets[s + 1]), offsets int32
+ * [num_sequences + 1] on the device, not decreasing, inside [0, tokens]; NULL: one
+ * sequence of all tokens.  Ids outside [0, num_experts) are not counted.  Offsets
+ * that break the rule never lead to an access outside the arguments; the
+ * workspace's status then holds MOE_ERR_INVALID and the results are unspecified.
+ *   ids     int32 [tokens, top_k], row stride ids_stride >= top_k; top_k >= 1,
+ *           tokens * top_k < 2^31
+ *   counts  int32 [num_sequences, num_experts], contiguous, written whole
+ *   1 <= num_sequences <= 2^20 */
+int moe_expert_counts(const int32_t* ids, int64_t ids_stride, int tokens, int top_k, const int32_t* offsets,
+                      int num_sequences, int num_experts, int32_t* counts, void* workspace, int64_t workspace_bytes,
+                      void* stream);
+
+/* loss[s] = num_experts / (C T) * sum over the T tokens t of s, over e, of
+ *           counts[s, e] * p[t, e],   C = sum over e of counts[s, e],
+ * p the softmax of the token's logits, or their sigmoids divided by the sigmoids'
+ * sum.  1 for even counts; 0 for a sequence without tokens or counts.  A token all
+ * of whose logits are -infinity has p = 0.  counts may hold more than the tokens'
+ * own pairs (of other batches or ranks), each >= 0.  Sequences as in
+ * moe_expert_counts.  Sums over tokens are in 64 bits past some hundred terms; the
+ * same inputs give the same bits.
+ *   counts  int32 [num_sequences, num_experts], contiguous
+ *   loss    fp32 [num_sequences] */
+int moe_balance_loss(int dtype, const void* logits, int64_t logits_stride, int tokens, int num_experts,
+                     const int32_t* counts, const int32_t* offsets, int num_sequences, int score, float* loss,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The gradient of sum over s of dloss[s] * loss[s] by the logits, the counts held
+ * fixed; zero for tokens of no sequence.  dlogits as in moe_route_grad, dloss fp32
+ * [num_sequences]. */
+int moe_balance_loss_grad(int dtype, const float* dloss, const void* logits, int64_t logits_stride, int tokens,
+                          int num_experts, const int32_t* counts, const int32_t* offsets, int num_sequences,
+                          int score, void* dlogits, int64_t dlogits_stride, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MOE_ROUTING_H */

@@ -1,0 +1,222 @@
+"""PyTorch-facing calls of the low-rank adapters in include/moe_adapters.h: what many
+tuned variants add to a shared projection, and the gradients that tuning them takes.
+
+Adapter l holds a[l] [rank, K] and b[l] [N, rank] and adds scale[l] * b[l] (a[l] x)
+to the projection of its rows.  ``products.expert_order`` says which rows are whose,
+once for all projections of a step::
+
+    order, offsets = P.expert_order(adapter_of_row, len(a))     # -1: no adapter
+    y = P.gemm_fp8_block(q, s, w, w_scale)                       # the shared projection
+    adapter_mm(x, a, b, offsets, order, scale, base=y, out=y)    # the adapters', in place
+
+    y = adapter_linear(x, a, b, offsets, base=y)                 # differentiable; rows in adapter order
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import binding as B
+from . import products as P
+
+
+def _bank(t: torch.Tensor, name: str) -> Tuple[Tuple[int, int, int], int, int]:
+    """Shape and (adapter, row) strides of a bank of factors."""
+    shape = P._dims(t, name, 3)
+    return (shape, *P._bank(t, name, shape))
+
+
+def _positions(offsets: torch.Tensor, order: Optional[torch.Tensor], scale: Optional[torch.Tensor], adapters: int,
+               rows: int) -> Tuple[Optional[int], Optional[int]]:
+    """Addresses of order and scale, which may be None."""
+    P._check_offsets(offsets, adapters)
+    if order is not None and (order.dtype is not torch.int32 or order.shape != (rows,) or not order.is_contiguous()):
+        raise ValueError(f"order: expected contiguous int32 [{rows}], got {order.dtype} {tuple(order.shape)}")
+    if scale is not None and (scale.dtype is not torch.float32 or scale.shape != (adapters,) or
+                              not scale.is_contiguous()):
+        raise ValueError(f"scale: expected contiguous float32 [{adapters}], got {scale.dtype} {tuple(scale.shape)}")
+    return None if order is None else order.data_ptr(), None if scale is None else scale.data_ptr()
+
+
+def _mid(mid: torch.Tensor, name: str, rows: int, rank: int) -> int:
+    if mid.dtype is not torch.float32 or mid.shape != (rows, rank) or not mid.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous float32 [{rows}, {rank}], got {mid.dtype} {tuple(mid.shape)}")
+    return mid.data_ptr()
+
+
+def _by_row(fn: str, name: str, rows_in: torch.Tensor, a, b, offsets, order, scale, base, out, mid, stream,
+            forward: bool, only_mid: bool = False):
+    dev = P._device(rows_in, a, b, offsets, order, scale, base, out, mid)
+    if dev != P._current_device():
+        with torch.cuda.device(dev):
+            return _by_row(fn, name, rows_in, a, b, offsets, order, scale, base, out, mid, stream, forward, only_mid)
+    rows, width = P._dims(rows_in, name, 2)
+    (L, R, K), a_l, a_r = _bank(a, "a")
+    (b_L, N, b_R), b_l, b_n = _bank(b, "b")
+    if (b_L, b_R) != (L, R):
+        raise ValueError(f"b: {tuple(b.shape)}, expected [{L}, N, {R}] beside a of {tuple(a.shape)}")
+    if R > B.MOE_MAX_RANK or L > B.MOE_MAX_ADAPTERS:
+        raise ValueError(f"a: {L} adapters of rank {R}, at most {B.MOE_MAX_ADAPTERS} of {B.MOE_MAX_RANK}")
+    out_width = N if forward else K
+    dtype = rows_in.dtype
+    code = P._HALF.get(dtype)
+    if code is None or a.dtype is not dtype or b.dtype is not dtype:
+        raise P._types(fn, rows_in, a, b)
+    ld = P._rows(rows_in, name, K if forward else N, rows)
+    order_at, scale_at = _positions(offsets, order, scale, L, rows)
+    base_at, base_ld = None, 0
+    if base is not None:
+        if base.dtype is not dtype:
+            raise P._types(fn, rows_in, base)
+        base_at, base_ld = base.data_ptr(), P._rows(base, "base", out_width, rows)
+    if only_mid:
+        out_at, out_ld = None, 0
+    elif out is None:
+        out = P._empty((rows, out_width), dtype, rows_in, stream)
+        out_at, out_ld = out.data_ptr(), out_width
+    else:
+        if out.dtype is not dtype:
+            raise P._types(fn, rows_in, out)
+        out_at, out_ld = out.data_ptr(), P._rows(out, "out", out_width, rows)
+    if mid is not None:
+        mid_at = _mid(mid, "mid", rows, R)
+    elif rows * R <= B.MOE_ADAPTER_MID_VALUES:
+        mid_at = None  # in the workspace
+    else:
+        mid = P._empty((rows, R), torch.float32, rows_in, stream)
+        mid_at = mid.data_ptr()
+    if stream is not None:
+        P._used_on(stream, rows_in, a, b, offsets, order, scale, base, out, mid)
+    h = P._handle(dev, stream)
+    rc = B.function(fn)(code, rows_in.data_ptr(), ld, a.data_ptr(), a_l, a_r, b.data_ptr(), b_l, b_n,
+                        offsets.data_ptr(), order_at, scale_at, L, rows, N, K, R, base_at, base_ld, out_at, out_ld,
+                        mid_at, P._workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    if rc:
+        raise B.MoeError(fn, rc)
+    return out
+
+
+def adapter_mm(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor,
+               order: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+               base: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               mid: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[r] = base[r] + scale[l] * b[l] (a[l] x[r]) for the rows r of adapter l, base[r] (zeros without base) for
+    rows without one: x [rows, K], a [L, rank, K], b [L, N, rank] -> [rows, N].
+
+    offsets int32 [L + 1] and order int32 [rows] as ``products.expert_order`` makes them: adapter l has the rows
+    order[offsets[l]:offsets[l + 1]]; without order, the rows offsets[l]:offsets[l + 1].  order names every row once.
+    scale float32 [L].  base may be out, which then is added to in place.  mid, float32 [rows, rank], gets a[l] x of
+    the adapters' rows in the positions' order, for adapter_mm_dw."""
+    return _by_row("moe_adapter_mm", "x", x, a, b, offsets, order, scale, base, out, mid, stream, True)
+
+
+def adapter_mm_dx(dy: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor,
+                  order: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                  base: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  mid: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of adapter_mm by x, added to base: dy [rows, N] -> [rows, K]; zeros (or base) for rows without an
+    adapter.  mid gets b[l]^T dy."""
+    return _by_row("moe_adapter_mm_dx", "dy", dy, a, b, offsets, order, scale, base, out, mid, stream, False)
+
+
+def adapter_mm_dw(dy: Optional[torch.Tensor], x: Optional[torch.Tensor], mid_x: Optional[torch.Tensor],
+                  mid_dy: Optional[torch.Tensor], offsets: torch.Tensor, order: Optional[torch.Tensor] = None,
+                  scale: Optional[torch.Tensor] = None, out=(None, None), out_dtype: Optional[torch.dtype] = None,
+                  accumulate: bool = False, stream=None):
+    """Gradients (da [L, rank, K], db [L, N, rank]) of adapter_mm by a and b, from the mids of adapter_mm and
+    adapter_mm_dx, in out_dtype (the operands' type or float32): da = scale[l] mid_dy^T x, db = scale[l] dy^T mid_x
+    over the rows of each adapter.  Without x and mid_dy there is no da, without dy and mid_x no db (None in its
+    place).  out: (da, db) to write, or with accumulate to add to (float32)."""
+    rows_in, mids = (x, dy), (mid_dy, mid_x)
+    names, mid_names = ("x", "dy"), ("mid_dy", "mid_x")
+    sides = [i for i in range(2) if rows_in[i] is not None]
+    if not sides or any((rows_in[i] is None) != (mids[i] is None) for i in range(2)):
+        raise ValueError("adapter_mm_dw: x with mid_dy, dy with mid_x, or both pairs expected")
+    first = rows_in[sides[0]]
+    dev = P._device(first, *rows_in, *mids, offsets, order, scale, *out)
+    if dev != P._current_device():
+        with torch.cuda.device(dev):
+            return adapter_mm_dw(dy, x, mid_x, mid_dy, offsets, order, scale, out, out_dtype, accumulate, stream)
+    rows = P._dims(first, names[sides[0]], 2)[0]
+    R = P._dims(mids[sides[0]], mid_names[sides[0]], 2)[1]
+    L = P._dims(offsets, "offsets", 1)[0] - 1
+    if not 1 <= R <= B.MOE_MAX_RANK or not 1 <= L <= B.MOE_MAX_ADAPTERS:
+        raise ValueError(f"adapter_mm_dw: {L} adapters of rank {R}, at most {B.MOE_MAX_ADAPTERS} of {B.MOE_MAX_RANK}")
+    order_at, scale_at = _positions(offsets, order, scale, L, rows)
+    dtype = first.dtype
+    code = P._HALF.get(dtype)
+    if code is None or any(rows_in[i].dtype is not dtype for i in sides):
+        raise P._types("adapter_mm_dw", *(rows_in[i] for i in sides))
+    given = [t for t in out if t is not None]
+    if out_dtype is None:
+        out_dtype = given[0].dtype if given else dtype
+    if out_dtype is not dtype and out_dtype is not torch.float32:
+        raise ValueError(f"adapter_mm_dw: {out_dtype} gradients, expected {dtype} or float32")
+    if accumulate and (out_dtype is not torch.float32 or any(out[i] is None for i in sides)):
+        raise ValueError("adapter_mm_dw: accumulate needs float32 out")
+    widths, lds, mid_at, grads, args = [1, 1], [0, 0], [None, None], [None, None], []
+    for i in range(2):
+        if rows_in[i] is None:
+            args += [None, 0, 0]
+            continue
+        widths[i] = P._dims(rows_in[i], names[i], 2)[1]
+        lds[i] = P._rows(rows_in[i], names[i], widths[i], rows)
+        mid_at[i] = _mid(mids[i], mid_names[i], rows, R)
+        shape = (L, R, widths[i]) if i == 0 else (L, widths[i], R)
+        grads[i] = out[i]
+        if grads[i] is None:
+            grads[i] = P._empty(shape, out_dtype, first, stream)
+        elif tuple(grads[i].shape) != shape or grads[i].dtype is not out_dtype:
+            raise ValueError(f"out: {grads[i].dtype} {tuple(grads[i].shape)}, expected {out_dtype} {list(shape)}")
+        args += [grads[i].data_ptr(), *P._bank(grads[i], "out", shape)]
+    if stream is not None:
+        P._used_on(stream, *rows_in, *mids, offsets, order, scale, *grads)
+    h = P._handle(dev, stream)
+    at = [None if t is None else t.data_ptr() for t in rows_in]
+    rc = B.function("moe_adapter_mm_dw")(
+        code, at[1], lds[1], at[0], lds[0], mid_at[1], mid_at[0], offsets.data_ptr(), order_at, scale_at, L, rows,
+        widths[1], widths[0], R, code if out_dtype is dtype else B.MOE_FP32, 1 if accumulate else 0, *args,
+        P._workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    if rc:
+        raise B.MoeError("moe_adapter_mm_dw", rc)
+    return tuple(grads)
+
+
+class AdapterLinear(torch.autograd.Function):
+    """adapter_mm with its gradients by x, a, b and base."""
+
+    @staticmethod
+    def forward(ctx, x, a, b, offsets, order, scale, base):
+        mid = x.new_empty((x.shape[0], a.shape[1]), dtype=torch.float32)
+        out = adapter_mm(x, a, b, offsets, order, scale, base=base, mid=mid)
+        ctx.save_for_backward(x, a, b, offsets, order, scale, mid)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, a, b, offsets, order, scale, mid = ctx.saved_tensors
+        need_x, need_a, need_b = ctx.needs_input_grad[:3]
+        dx = da = db = mid_dy = None
+        rows = dy.contiguous()
+        if need_a:
+            mid_dy = torch.empty_like(mid)
+        if need_x or need_a:
+            dx = _by_row("moe_adapter_mm_dx", "dy", rows, a, b, offsets, order, scale, None, None, mid_dy, None, False,
+                         only_mid=not need_x)
+        if need_a or need_b:
+            da, db = adapter_mm_dw(rows if need_b else None, x if need_a else None, mid if need_b else None, mid_dy,
+                                   offsets, order, scale)
+        return dx, da, db, None, None, None, dy if ctx.needs_input_grad[6] else None
+
+
+def adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor,
+                   order: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                   base: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Differentiable adapter_mm, by x, a, b and base (not by scale; first derivatives).  (The calls that take `out`
+    are the kernels alone: what they return has no gradient.)"""
+    if scale is not None and scale.requires_grad:
+        raise ValueError("adapter_linear: scale has no gradient; it must not require one")
+    return AdapterLinear.apply(x, a, b, offsets, order, scale, base)

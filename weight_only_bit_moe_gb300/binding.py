@@ -1,5 +1,5 @@
 """ctypes binding of the C ABI declared in include/ (moe_w4a16.h, moe_requant.h,
-moe_products.h).
+moe_products.h, moe_routing.h, moe_adapters.h).
 
 Argument marshalling only: torch tensors are passed as their data pointers,
 streams as their CUDA handles; every step of the layer runs in the library's
@@ -24,8 +24,14 @@ EXPORTED = ("moe_repack_size", "moe_repack_weights", "moe_repack_weights_ex", "m
             "moe_workspace_size", "moe_w4a16_forward", "moe_w4a16_forward_noalloc", "moe_get_status",
             "moe_set_trace_events", "moe_set_test_starve_wait", "moe_status_string", "moe_requant_fp8",
             "moe_requant_launch_geometry", "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw",
-            "moe_quant_fp8_block", "moe_gemm_fp8_block", "moe_capture_id", "moe_capture_mode", "moe_capture_watch")
+            "moe_quant_fp8_block", "moe_gemm_fp8_block", "moe_capture_id", "moe_capture_mode", "moe_capture_watch",
+            "moe_route", "moe_route_grad", "moe_expert_counts", "moe_balance_loss", "moe_balance_loss_grad",
+            "moe_adapter_mm", "moe_adapter_mm_dx", "moe_adapter_mm_dw")
 MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_MAX_TOP_K = 32
+MOE_MAX_ADAPTERS, MOE_MAX_RANK = 4096, 256
+MOE_ADAPTER_MID_VALUES = 1 << 22  # mid values that an adapter product keeps in the workspace
 MOE_PRODUCTS_WORKSPACE_BYTES = 48 << 20  # workspace of the products in moe_products.h
 MOE_PRODUCTS_WORKSPACE_HEAD_BYTES = 8192  # of which these are zeroed before the first use
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20  # fixed workspace of moe_w4a16_forward_noalloc
@@ -95,6 +101,17 @@ def load(path: str = ""):
                 "moe_quant_fp8_block": (i32, [i32, p, i64, i32, p, i32, i32, i32, p, i64, p, i64, i64, p]),
                 "moe_gemm_fp8_block": (i32, [p, i64, p, i64, i64, p, i64, i64, p, i64, i64, i64, p, i32, i32, i32,
                                              i32, i32, p, i64, p, i64, p]),
+                "moe_route": (i32, [i32, p, i64, p, i32, i32, i32, i32, i32, f32, p, p, p]),
+                "moe_route_grad": (i32, [i32, p, i64, p, i64, p, i32, i32, i32, i32, i32, f32, p, i64, p]),
+                "moe_expert_counts": (i32, [p, i64, i32, i32, p, i32, i32, p, p, i64, p]),
+                "moe_balance_loss": (i32, [i32, p, i64, i32, i32, p, p, i32, i32, p, p, i64, p]),
+                "moe_balance_loss_grad": (i32, [i32, p, p, i64, i32, i32, p, p, i32, i32, p, i64, p, i64, p]),
+                "moe_adapter_mm": (i32, [i32, p, i64, p, i64, i64, p, i64, i64, p, p, p, i32, i32, i32, i32, i32, p,
+                                         i64, p, i64, p, p, i64, p]),
+                "moe_adapter_mm_dx": (i32, [i32, p, i64, p, i64, i64, p, i64, i64, p, p, p, i32, i32, i32, i32, i32,
+                                            p, i64, p, i64, p, p, i64, p]),
+                "moe_adapter_mm_dw": (i32, [i32, p, i64, p, i64, p, p, p, p, p, i32, i32, i32, i32, i32, i32, i32, p,
+                                            i64, i64, p, i64, i64, p, i64, p]),
                 "moe_capture_id": (i32, [p, ctypes.POINTER(ctypes.c_uint64)]),
                 "moe_capture_mode": (i32, [ctypes.POINTER(i32)]),
                 "moe_capture_watch": (i32, [p, ctypes.POINTER(ctypes.POINTER(ctypes.c_int32))]),

@@ -1,0 +1,110 @@
+// Entry points of moe_adapters.h: argument rules and the choice of the kernels.
+#include "adapters.cuh"
+
+namespace moe {
+
+constexpr int kAdMaxRows = 0x7FFFFFFF - 1024;
+constexpr int kAdMaxDim = 1 << 21;  // (gridDim.y of the plain kernels counts 64-column tiles)
+
+static bool on_elements(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+static int check_sizes(int dtype, int L, int rows, int N, int K, int R, const void* workspace, int64_t bytes) {
+  if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_INVALID;
+  if (L < 1 || L > kAdAdapters || rows < 0 || rows > kAdMaxRows || N < 1 || N > kAdMaxDim || K < 1 || K > kAdMaxDim ||
+      R < 1 || R > kAdRank)
+    return MOE_ERR_INVALID;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return MOE_ERR_INVALID;
+  return bytes < MOE_PRODUCTS_WORKSPACE_BYTES ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+static int run(const AdapterArgs& a, bool fwd, void* stream) {
+  const cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t rc = launch_adapter_any(a, fwd, st);
+  if (rc == cudaSuccess && a.out && a.base != a.out) rc = launch_adapter_rest(a, st);
+  return rc == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+static int by_row(int dtype, const void* in, int64_t in_stride, const void* a, int64_t a_l, int64_t a_r, const void* b,
+                  int64_t b_l, int64_t b_n, const int32_t* offsets, const int32_t* order, const float* scale, int L,
+                  int rows, int N, int K, int R, const void* base, int64_t base_stride, void* out, int64_t out_stride,
+                  float* mid, void* workspace, int64_t workspace_bytes, void* stream, bool fwd) {
+  const int rc = check_sizes(dtype, L, rows, N, K, R, workspace, workspace_bytes);
+  if (rc != MOE_OK) return rc;
+  const int P = fwd ? K : N, Q = fwd ? N : K;
+  if (in_stride < P || a_r < K || b_n < R || a_l < 0 || b_l < 0) return MOE_ERR_INVALID;
+  if (out && (out_stride < Q || (base && base_stride < Q) || (base == out && base_stride != out_stride)))
+    return MOE_ERR_INVALID;
+  if (rows == 0) return MOE_OK;
+  if (!in || !a || !b || !offsets || (!out && !mid)) return MOE_ERR_INVALID;
+  if (!mid && (int64_t)rows * R > MOE_ADAPTER_MID_VALUES) return MOE_ERR_WORKSPACE;
+  if (!on_elements(in, 2) || !on_elements(a, 2) || !on_elements(b, 2) || !on_elements(base, 2) || !on_elements(out, 2) ||
+      !on_elements(offsets, 4) || !on_elements(order, 4) || !on_elements(scale, 4) || !on_elements(mid, 4))
+    return MOE_ERR_INVALID;
+  AdapterArgs g{};
+  g.in = in, g.in_ld = in_stride;
+  g.f = fwd ? a : b, g.f_l = fwd ? a_l : b_l, g.f_r = fwd ? a_r : b_n;
+  g.s = fwd ? b : a, g.s_l = fwd ? b_l : a_l, g.s_r = fwd ? b_n : a_r;
+  g.offsets = offsets, g.order = order, g.scale = scale;
+  g.L = L, g.rows = rows, g.P = P, g.Q = Q, g.R = R, g.type = dtype;
+  uint8_t* const w = static_cast<uint8_t*>(workspace);
+  g.base = base, g.base_ld = base_stride, g.out = out, g.out_ld = out_stride;
+  g.mid = mid ? mid : reinterpret_cast<float*>(w + MOE_PRODUCTS_WORKSPACE_HEAD_BYTES);
+  g.status = reinterpret_cast<unsigned*>(w);
+  return run(g, fwd, stream);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_adapter_mm(int dtype, const void* x, int64_t x_stride, const void* a, int64_t a_stride_l,
+                              int64_t a_stride_r, const void* b, int64_t b_stride_l, int64_t b_stride_n,
+                              const int32_t* offsets, const int32_t* order, const float* scale, int num_adapters,
+                              int rows, int N, int K, int rank, const void* base, int64_t base_stride, void* out,
+                              int64_t out_stride, float* mid, void* workspace, int64_t workspace_bytes, void* stream) {
+  return by_row(dtype, x, x_stride, a, a_stride_l, a_stride_r, b, b_stride_l, b_stride_n, offsets, order, scale,
+                num_adapters, rows, N, K, rank, base, base_stride, out, out_stride, mid, workspace, workspace_bytes,
+                stream, true);
+}
+
+extern "C" int moe_adapter_mm_dx(int dtype, const void* dy, int64_t dy_stride, const void* a, int64_t a_stride_l,
+                                 int64_t a_stride_r, const void* b, int64_t b_stride_l, int64_t b_stride_n,
+                                 const int32_t* offsets, const int32_t* order, const float* scale, int num_adapters,
+                                 int rows, int N, int K, int rank, const void* base, int64_t base_stride, void* dx,
+                                 int64_t dx_stride, float* mid, void* workspace, int64_t workspace_bytes,
+                                 void* stream) {
+  return by_row(dtype, dy, dy_stride, a, a_stride_l, a_stride_r, b, b_stride_l, b_stride_n, offsets, order, scale,
+                num_adapters, rows, N, K, rank, base, base_stride, dx, dx_stride, mid, workspace, workspace_bytes,
+                stream, false);
+}
+
+extern "C" int moe_adapter_mm_dw(int dtype, const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                 const float* mid_x, const float* mid_dy, const int32_t* offsets,
+                                 const int32_t* order, const float* scale, int num_adapters, int rows, int N, int K,
+                                 int rank, int grad_dtype, int accumulate, void* da, int64_t da_stride_l,
+                                 int64_t da_stride_r, void* db, int64_t db_stride_l, int64_t db_stride_n,
+                                 void* workspace, int64_t workspace_bytes, void* stream) {
+  const int rc = check_sizes(dtype, num_adapters, rows, N, K, rank, workspace, workspace_bytes);
+  if (rc != MOE_OK) return rc;
+  if ((grad_dtype != dtype && grad_dtype != MOE_FP32) || accumulate < 0 || accumulate > 1) return MOE_ERR_INVALID;
+  if (accumulate && grad_dtype != MOE_FP32) return MOE_ERR_INVALID;
+  const int each = grad_dtype == MOE_FP32 ? 4 : 2;
+  if (!offsets || !on_elements(offsets, 4) || !on_elements(order, 4) || !on_elements(scale, 4)) return MOE_ERR_INVALID;
+  if (da && (x_stride < K || da_stride_r < K || !on_elements(da, each) ||
+             (num_adapters > 1 && da_stride_l < (rank - 1) * da_stride_r + K)))
+    return MOE_ERR_INVALID;
+  if (db && (dy_stride < N || db_stride_n < rank || !on_elements(db, each) ||
+             (num_adapters > 1 && db_stride_l < (N - 1) * db_stride_n + rank)))
+    return MOE_ERR_INVALID;
+  if (rows > 0 && da && (!x || !mid_dy || !on_elements(x, 2) || !on_elements(mid_dy, 4))) return MOE_ERR_INVALID;
+  if (rows > 0 && db && (!dy || !mid_x || !on_elements(dy, 2) || !on_elements(mid_x, 4))) return MOE_ERR_INVALID;
+  AdapterGradArgs g{};
+  g.side[0] = {da ? x : nullptr, x_stride, mid_dy, K, da, da_stride_l, da_stride_r, 1};
+  g.side[1] = {db ? dy : nullptr, dy_stride, mid_x, N, db, db_stride_l, 1, db_stride_n};
+  g.offsets = offsets, g.order = order, g.scale = scale;
+  g.L = num_adapters, g.rows = rows, g.R = rank, g.type = dtype, g.out_type = grad_dtype, g.accumulate = accumulate;
+  g.status = static_cast<unsigned*>(workspace);
+  for (int side = 0; side < 2; ++side)
+    if (g.side[side].out && launch_adapter_grad_any(g, side, (cudaStream_t)stream) != cudaSuccess) return MOE_ERR_CUDA;
+  return MOE_OK;
+}

@@ -1,0 +1,196 @@
+// The adapters of moe_adapters.h for any size, stride and alignment, in three plain
+// kernels: the first product (mid), the second (out) and the gradients.  64 x 64
+// values to a CTA, 4 x 4 fp32 sums to a thread, 16 terms at a time in shared memory,
+// single elements loaded: bound by these loads and the fp32 multiply-adds.
+#include "adapters.cuh"
+
+namespace moe {
+
+constexpr int kAaTile = 64, kAaTerms = 16, kAaThreads = 256;
+
+struct AaTiles {
+  float a[kAaTerms][kAaTile + 4], b[kAaTerms][kAaTile + 4];
+  int row[kAaTile];
+};
+
+__device__ __forceinline__ void aa_multiply(const AaTiles& s, int tx, int ty, float (&acc)[4][4]) {
+#pragma unroll
+  for (int k = 0; k < kAaTerms; ++k)
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[y][x] = fmaf(s.a[k][4 * ty + y], s.b[k][4 * tx + x], acc[y][x]);
+}
+
+// The first adapter that ends past position i; L: none.
+__device__ __forceinline__ int first_adapter(const int32_t* offsets, int rows, int L, int i) {
+  int lo = 0, hi = L;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    int i0, i1;
+    adapter_rows(offsets, rows, mid, i0, i1);
+    if (i1 > i) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+template <bool FWD>
+__global__ void __launch_bounds__(kAaThreads) adapter_any_mid_kernel(const __grid_constant__ AdapterArgs a) {
+  __shared__ AaTiles s;
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  const int pos0 = blockIdx.x * kAaTile, pos1 = min(pos0 + kAaTile, a.rows), j0 = blockIdx.y * kAaTile;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int l = tid; l < a.L; l += kAaThreads)
+      if (adapter_bad(a.offsets, a.rows, l)) atomicOr(a.status, kStatusRouting);
+  for (int l = first_adapter(a.offsets, a.rows, a.L, pos0); l < a.L; ++l) {
+    int i0, i1;
+    adapter_rows(a.offsets, a.rows, l, i0, i1);
+    if (i0 >= pos1) break;
+    i0 = max(i0, pos0), i1 = min(i1, pos1);
+    if (i0 >= i1) continue;
+    __syncthreads();
+    if (tid < kAaTile) s.row[tid] = i0 + tid < i1 ? row_of(a.order, a.rows, i0 + tid, a.status) : -1;
+    float acc[4][4] = {};
+    for (int p0 = 0; p0 < a.P; p0 += kAaTerms) {
+      __syncthreads();
+      for (int u = tid; u < kAaTile * kAaTerms; u += kAaThreads) {
+        const int i = u / kAaTerms, p = u % kAaTerms;
+        const int r = s.row[i];
+        s.a[p][i] = r >= 0 && p0 + p < a.P ? load_elem(a.in, r * a.in_ld + p0 + p, a.type) : 0.0f;
+        const int j = FWD ? u / kAaTerms : u % kAaTile, t = FWD ? u % kAaTerms : u / kAaTile;
+        s.b[t][j] = j0 + j < a.R && p0 + t < a.P
+                        ? load_elem(a.f, l * a.f_l + (FWD ? (j0 + j) * a.f_r + p0 + t : (p0 + t) * a.f_r + j0 + j), a.type)
+                        : 0.0f;
+      }
+      __syncthreads();
+      aa_multiply(s, tx, ty, acc);
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int i = i0 + 4 * ty + y, j = j0 + 4 * tx + x;
+        if (i < i1 && j < a.R) a.mid[(int64_t)i * a.R + j] = acc[y][x];
+      }
+  }
+}
+
+template <bool FWD>
+__global__ void __launch_bounds__(kAaThreads) adapter_any_out_kernel(const __grid_constant__ AdapterArgs a) {
+  __shared__ AaTiles s;
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  const int pos0 = blockIdx.x * kAaTile, pos1 = min(pos0 + kAaTile, a.rows), q0 = blockIdx.y * kAaTile;
+  for (int l = first_adapter(a.offsets, a.rows, a.L, pos0); l < a.L; ++l) {
+    int i0, i1;
+    adapter_rows(a.offsets, a.rows, l, i0, i1);
+    if (i0 >= pos1) break;
+    i0 = max(i0, pos0), i1 = min(i1, pos1);
+    if (i0 >= i1) continue;
+    __syncthreads();
+    if (tid < kAaTile) s.row[tid] = i0 + tid < i1 ? row_of(a.order, a.rows, i0 + tid, a.status) : -1;
+    float acc[4][4] = {};
+    for (int j0 = 0; j0 < a.R; j0 += kAaTerms) {
+      __syncthreads();
+      for (int u = tid; u < kAaTile * kAaTerms; u += kAaThreads) {
+        const int i = u / kAaTerms, j = u % kAaTerms;
+        s.a[j][i] = i0 + i < i1 && j0 + j < a.R ? a.mid[(int64_t)(i0 + i) * a.R + j0 + j] : 0.0f;
+        const int q = FWD ? u / kAaTerms : u % kAaTile, t = FWD ? u % kAaTerms : u / kAaTile;
+        s.b[t][q] = q0 + q < a.Q && j0 + t < a.R
+                        ? load_elem(a.s, l * a.s_l + (FWD ? (q0 + q) * a.s_r + j0 + t : (j0 + t) * a.s_r + q0 + q), a.type)
+                        : 0.0f;
+      }
+      __syncthreads();
+      aa_multiply(s, tx, ty, acc);
+    }
+    const float scale = a.scale ? a.scale[l] : 1.0f;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int r = s.row[4 * ty + y];
+      if (r < 0) continue;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int q = q0 + 4 * tx + x;
+        if (q >= a.Q) continue;
+        const float base = a.base ? load_elem(a.base, r * a.base_ld + q, a.type) : 0.0f;
+        store_elem(a.out, r * a.out_ld + q, a.type, fmaf(scale, acc[y][x], base));
+      }
+    }
+  }
+}
+
+// out = base for the rows without an adapter: positions before the first adapter's and
+// from the last one's end on.  A CTA per position, in turn.
+__global__ void __launch_bounds__(kAaThreads) adapter_rest_kernel(const __grid_constant__ AdapterArgs a) {
+  const int before = min(max(__ldg(a.offsets), 0), a.rows), from = max(before, min(max(__ldg(a.offsets + a.L), 0), a.rows));
+  const int rest = before + a.rows - from;
+  for (int n = blockIdx.x; n < rest; n += gridDim.x) {
+    const int r = row_of(a.order, a.rows, n < before ? n : from + n - before, a.status);
+    if (r < 0) continue;
+    const uint16_t* b = static_cast<const uint16_t*>(a.base) + r * a.base_ld;
+    uint16_t* o = static_cast<uint16_t*>(a.out) + r * a.out_ld;
+    for (int q = threadIdx.x; q < a.Q; q += kAaThreads) o[q] = a.base ? b[q] : (uint16_t)0;
+  }
+}
+
+__global__ void __launch_bounds__(kAaThreads) adapter_any_grad_kernel(const __grid_constant__ AdapterGradArgs a, int side) {
+  __shared__ AaTiles s;
+  const AdapterGradSide& g = a.side[side];
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  const int l = blockIdx.z, j0 = blockIdx.y * kAaTile, p0 = blockIdx.x * kAaTile;
+  int i0, i1;
+  adapter_rows(a.offsets, a.rows, l, i0, i1);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0 && adapter_bad(a.offsets, a.rows, l)) atomicOr(a.status, kStatusRouting);
+  if (a.accumulate && i0 == i1) return;
+  float acc[4][4] = {};
+  for (int i = i0; i < i1; i += kAaTerms) {
+    __syncthreads();
+    if (tid < kAaTerms) s.row[tid] = i + tid < i1 ? row_of(a.order, a.rows, i + tid, a.status) : -1;
+    __syncthreads();
+    for (int u = tid; u < kAaTile * kAaTerms; u += kAaThreads) {
+      const int c = u % kAaTile, t = u / kAaTile, r = s.row[t];
+      s.a[t][c] = r >= 0 && j0 + c < a.R ? g.mid[(int64_t)(i + t) * a.R + j0 + c] : 0.0f;
+      s.b[t][c] = r >= 0 && p0 + c < g.P ? load_elem(g.in, r * g.in_ld + p0 + c, a.type) : 0.0f;
+    }
+    __syncthreads();
+    aa_multiply(s, tx, ty, acc);
+  }
+  const float scale = a.scale ? a.scale[l] : 1.0f;
+#pragma unroll
+  for (int y = 0; y < 4; ++y)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int j = j0 + 4 * ty + y, p = p0 + 4 * tx + x;
+      if (j >= a.R || p >= g.P) continue;
+      const int64_t at = l * g.out_l + j * g.out_j + p * g.out_p;
+      float v = scale * acc[y][x];
+      if (a.accumulate) v += static_cast<const float*>(g.out)[at];
+      store_elem(g.out, at, a.out_type, v);
+    }
+}
+
+static unsigned aa_tiles(int n) { return (unsigned)((n + kAaTile - 1) / kAaTile); }
+
+cudaError_t launch_adapter_any(const AdapterArgs& a, bool fwd, cudaStream_t st) {
+  const dim3 mid(aa_tiles(a.rows), aa_tiles(a.R)), out(aa_tiles(a.rows), aa_tiles(a.Q));
+  if (fwd) {
+    adapter_any_mid_kernel<true><<<mid, kAaThreads, 0, st>>>(a);
+    if (a.out) adapter_any_out_kernel<true><<<out, kAaThreads, 0, st>>>(a);
+  } else {
+    adapter_any_mid_kernel<false><<<mid, kAaThreads, 0, st>>>(a);
+    if (a.out) adapter_any_out_kernel<false><<<out, kAaThreads, 0, st>>>(a);
+  }
+  return cudaPeekAtLastError();
+}
+
+cudaError_t launch_adapter_rest(const AdapterArgs& a, cudaStream_t st) {
+  adapter_rest_kernel<<<min(a.rows, 1216), kAaThreads, 0, st>>>(a);
+  return cudaPeekAtLastError();
+}
+
+cudaError_t launch_adapter_grad_any(const AdapterGradArgs& a, int side, cudaStream_t st) {
+  adapter_any_grad_kernel<<<dim3(aa_tiles(a.side[side].P), aa_tiles(a.R), a.L), kAaThreads, 0, st>>>(a, side);
+  return cudaPeekAtLastError();
+}
+
+}  // namespace moe
