@@ -17,8 +17,9 @@
  * int32 [rows] and names each row once.  The rows of the other positions have no
  * adapter.  Offsets that break the rule and entries outside [0, rows) never lead to
  * an access outside the arguments; the workspace's status then holds
- * MOE_ERR_INVALID and the rows concerned are unspecified, as are rows that order
- * names more than once or not at all.
+ * MOE_ERR_INVALID and the results are unspecified (an entry outside: those of its
+ * row and of its adapter's gradients).  Rows that order names more than once or not
+ * at all are unspecified.
  *
  * Sizes.  num_adapters 1 .. 4096, rank 1 .. 256, 1 <= N, K <= 2^21, 0 <= rows <
  * 2^31 - 1024.  Any strides and alignment are computed; the fast kernels take

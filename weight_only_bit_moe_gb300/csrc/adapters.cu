@@ -17,10 +17,32 @@ static int check_sizes(int dtype, int L, int rows, int N, int K, int R, const vo
   return bytes < MOE_PRODUCTS_WORKSPACE_BYTES ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 
-static int run(const AdapterArgs& a, bool fwd, void* stream) {
+// Matrices that the fast kernels take: whole eights of columns on 16-byte boundaries.
+static bool grid16(const void* p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; }
+static bool on_grid(const AdapterArgs& a, const float* mid) {
+  return a.P % 8 == 0 && a.Q % 8 == 0 && a.R % 8 == 0 && grid16(a.in, a.in_ld) && grid16(a.f, a.f_l) && a.f_r % 8 == 0 &&
+         grid16(a.s, a.s_l) && a.s_r % 8 == 0 && (reinterpret_cast<uintptr_t>(mid) & 15) == 0 &&
+         (!a.out || (grid16(a.out, a.out_ld) && (!a.base || grid16(a.base, a.base_ld))));
+}
+
+// The workspace behind its head: the plan, mid where the caller keeps none, slices of mid.
+constexpr int64_t kAdMidAt = MOE_PRODUCTS_WORKSPACE_HEAD_BYTES + 256, kAdPartAt = kAdMidAt + MOE_ADAPTER_MID_VALUES * 4;
+constexpr int64_t kAdPartValues = (MOE_PRODUCTS_WORKSPACE_BYTES - kAdPartAt) / 4;
+
+static int run(AdapterArgs& a, bool fwd, float* mid, uint8_t* workspace, void* stream) {
   const cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t rc = launch_adapter_any(a, fwd, st);
-  if (rc == cudaSuccess && a.out && a.base != a.out) rc = launch_adapter_rest(a, st);
+  a.mid = mid ? mid : reinterpret_cast<float*>(workspace + kAdMidAt);
+  a.part = reinterpret_cast<float*>(workspace + kAdPartAt);
+  a.plan = reinterpret_cast<int*>(workspace + MOE_PRODUCTS_WORKSPACE_HEAD_BYTES);
+  cudaError_t rc;
+  if (on_grid(a, mid)) {
+    const int64_t room = kAdPartValues / ((int64_t)a.rows * a.R);
+    a.slices = (int)(room < 1 ? 1 : room > 32 ? 32 : room);
+    rc = fwd && a.rows <= kAdFewRows ? launch_adapter_few(a, mid != nullptr, st) : launch_adapter_tc(a, fwd, mid != nullptr, st);
+  } else {
+    rc = launch_adapter_any(a, fwd, st);
+    if (rc == cudaSuccess && a.out && a.base != a.out) rc = launch_adapter_rest(a, st);
+  }
   return rc == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -48,9 +70,8 @@ static int by_row(int dtype, const void* in, int64_t in_stride, const void* a, i
   g.L = L, g.rows = rows, g.P = P, g.Q = Q, g.R = R, g.type = dtype;
   uint8_t* const w = static_cast<uint8_t*>(workspace);
   g.base = base, g.base_ld = base_stride, g.out = out, g.out_ld = out_stride;
-  g.mid = mid ? mid : reinterpret_cast<float*>(w + MOE_PRODUCTS_WORKSPACE_HEAD_BYTES);
   g.status = reinterpret_cast<unsigned*>(w);
-  return run(g, fwd, stream);
+  return run(g, fwd, mid, w, stream);
 }
 
 }  // namespace moe

@@ -1,6 +1,8 @@
 // What the kernels of moe_adapters.h share: the arguments and the rows of an adapter.
 #pragma once
 
+#include <atomic>
+
 #include "../../include/moe_adapters.h"
 #include "products_tc.cuh"
 
@@ -26,6 +28,10 @@ struct AdapterArgs {
   void* out;
   int64_t out_ld;
   float* mid;                // [rows, R]
+  float* part;               // partial sums of mid, [slices, rows, R]
+  int* plan;                 // device: the slices that the first product was cut into
+  int slices;                // at most (few rows: exactly)
+  int want_mid;              // mid is the caller's
   unsigned* status;
 };
 
@@ -65,8 +71,126 @@ __device__ __forceinline__ int row_of(const int32_t* order, int rows, int i, uns
   return -1;
 }
 
+// Values of mid of two lanes' columns as 16-bit operands: high parts and what they leave.
+template <int TYPE>
+__device__ __forceinline__ uint32_t pack_type(float lo, float hi) {
+  return TYPE == kBf16 ? pack_bf16x2(lo, hi) : pack_half2(lo, hi);
+}
+template <int TYPE>
+__device__ __forceinline__ float2 unpack_type(uint32_t w) {
+  if (TYPE == kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// hi + lo = v to 16 (bf16) or 22 (fp16, inside its range) significant bits; infinities keep lo = 0.
+template <int TYPE>
+__device__ __forceinline__ void split_type(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_type<TYPE>(v0, v1);
+  const float2 h = unpack_type<TYPE>(hi);
+  lo = pack_type<TYPE>(fabsf(h.x) < INFINITY ? v0 - h.x : 0.0f, fabsf(h.y) < INFINITY ? v1 - h.y : 0.0f);
+}
+
+// D (16 x 8) += A (16 x 16) B (16 x 8) of 16-bit operands, as mma_16816.
+template <int TYPE>
+__device__ __forceinline__ void mma_type(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if (TYPE == kFp16) {
+    mma_16816(d, a0, a1, a2, a3, b0, b1);
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+
+// Asynchronous copies of the thread: `bytes` of 16 (the rest zeros), and four at a time.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// First tile of each adapter into start[0 .. L], tiles of ROWS positions (none, and a report, where offsets break the
+// rule); all THREADS threads of the CTA (warp_tot: an int for each warp).
+template <int ROWS, int THREADS>
+__device__ __forceinline__ void plan_adapters(const int32_t* offsets, int rows, int L, int* start, int* warp_tot,
+                                              unsigned* status) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (L + THREADS - 1) / THREADS;
+  int run = 0, bad = 0;
+  for (int i = 0; i < per; ++i) {
+    const int l = tid * per + i;
+    if (l >= L) break;
+    int i0, i1;
+    adapter_rows(offsets, rows, l, i0, i1);
+    run += (i1 - i0 + ROWS - 1) / ROWS;
+    bad |= adapter_bad(offsets, rows, l);
+  }
+  if (__syncthreads_or(bad)) {  // overlapping adapters could make any number of tiles
+    if (bad && blockIdx.x == 0) atomicOr(status, kStatusRouting);
+    for (int l = tid; l <= L; l += THREADS) start[l] = 0;
+    __syncthreads();
+    return;
+  }
+  int incl = run;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) warp_tot[warp] = incl;
+  __syncthreads();
+  int pos = incl - run;
+  for (int w = 0; w < warp; ++w) pos += warp_tot[w];
+  for (int i = 0; i < per; ++i) {
+    const int l = tid * per + i;
+    if (l >= L) break;
+    int i0, i1;
+    adapter_rows(offsets, rows, l, i0, i1);
+    start[l] = pos;
+    pos += (i1 - i0 + ROWS - 1) / ROWS;
+    if (l == L - 1) start[L] = pos;
+  }
+  __syncthreads();
+}
+
+constexpr int kAtRows = 128;  // positions of a tile
+
+// Power-of-two columns of tensor memory that hold n.
+__host__ __device__ constexpr uint32_t tmem_columns(uint32_t n) {
+  uint32_t c = 32;
+  while (c < n) c *= 2;
+  return c;
+}
+
+// ---------------------------------------------------------------- host
+// The kernel may take that much shared memory; once a device.
+template <typename F>
+inline cudaError_t allow_smem(F* kernel, int bytes, std::atomic<bool>* ready) {
+  int dev = 0;
+  cudaError_t rc = cudaGetDevice(&dev);
+  if (rc != cudaSuccess) return rc;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (rc == cudaSuccess) ready[dev].store(true, std::memory_order_release);
+  return rc;
+}
+
 cudaError_t launch_adapter_any(const AdapterArgs& a, bool fwd, cudaStream_t st);
 cudaError_t launch_adapter_grad_any(const AdapterGradArgs& a, int side, cudaStream_t st);
 cudaError_t launch_adapter_rest(const AdapterArgs& a, cudaStream_t st);
+// Operands on the 16-byte grid: up to kAdFewRows rows of the forward product, and any number of both.
+constexpr int kAdFewRows = 256;
+cudaError_t launch_adapter_few(AdapterArgs& a, bool mid_wanted, cudaStream_t st);
+cudaError_t launch_adapter_tc(AdapterArgs& a, bool fwd, bool mid_wanted, cudaStream_t st);
+cudaError_t launch_adapter_out_fwd(const AdapterArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_adapter_out_dx(const AdapterArgs& a, int sms, cudaStream_t st);
 
 }  // namespace moe

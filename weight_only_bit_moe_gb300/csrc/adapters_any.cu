@@ -35,14 +35,20 @@ __device__ __forceinline__ int first_adapter(const int32_t* offsets, int rows, i
   return lo;
 }
 
+// Whether offsets break the rule (reported; overlapping adapters could repeat a row any number of times); all threads.
+__device__ __forceinline__ bool aa_broken(const int32_t* offsets, int rows, int L, unsigned* status) {
+  bool bad = false;
+  for (int l = threadIdx.x; l < L; l += kAaThreads) bad |= adapter_bad(offsets, rows, l);
+  if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(status, kStatusRouting);
+  return __syncthreads_or(bad);
+}
+
 template <bool FWD>
 __global__ void __launch_bounds__(kAaThreads) adapter_any_mid_kernel(const __grid_constant__ AdapterArgs a) {
   __shared__ AaTiles s;
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
   const int pos0 = blockIdx.x * kAaTile, pos1 = min(pos0 + kAaTile, a.rows), j0 = blockIdx.y * kAaTile;
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int l = tid; l < a.L; l += kAaThreads)
-      if (adapter_bad(a.offsets, a.rows, l)) atomicOr(a.status, kStatusRouting);
+  if (aa_broken(a.offsets, a.rows, a.L, a.status)) return;
   for (int l = first_adapter(a.offsets, a.rows, a.L, pos0); l < a.L; ++l) {
     int i0, i1;
     adapter_rows(a.offsets, a.rows, l, i0, i1);
@@ -81,6 +87,7 @@ __global__ void __launch_bounds__(kAaThreads) adapter_any_out_kernel(const __gri
   __shared__ AaTiles s;
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
   const int pos0 = blockIdx.x * kAaTile, pos1 = min(pos0 + kAaTile, a.rows), q0 = blockIdx.y * kAaTile;
+  if (aa_broken(a.offsets, a.rows, a.L, a.status)) return;
   for (int l = first_adapter(a.offsets, a.rows, a.L, pos0); l < a.L; ++l) {
     int i0, i1;
     adapter_rows(a.offsets, a.rows, l, i0, i1);
@@ -140,7 +147,7 @@ __global__ void __launch_bounds__(kAaThreads) adapter_any_grad_kernel(const __gr
   const int l = blockIdx.z, j0 = blockIdx.y * kAaTile, p0 = blockIdx.x * kAaTile;
   int i0, i1;
   adapter_rows(a.offsets, a.rows, l, i0, i1);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0 && adapter_bad(a.offsets, a.rows, l)) atomicOr(a.status, kStatusRouting);
+  if (aa_broken(a.offsets, a.rows, a.L, a.status)) return;
   if (a.accumulate && i0 == i1) return;
   float acc[4][4] = {};
   for (int i = i0; i < i1; i += kAaTerms) {

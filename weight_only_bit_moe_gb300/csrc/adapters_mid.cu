@@ -1,0 +1,268 @@
+// The adapters of many rows: each adapter's positions in tiles of 128, in two launches.
+//
+//   mid[i, j] = sum_p in[r, p] F[l](j, p)                       adapter_mid_kernel
+//   out[r, q] = base[r, q] + scale[l] sum_j mid[i, j] S[l](q, j)  adapter_out_kernel
+//
+// (forward: F = A, S = B; gradient by the rows: F = B^T, S = A^T, read where they lie.)
+// Both are streams: 2 P bytes a row in, then 2 Q in and out, against 2 R (P + 2 Q)
+// operations, R of 8 to 256.
+#include "adapters.cuh"
+
+namespace moe {
+
+// Four MMAs of 16 terms of one CTA; the descriptors advance by DA and DB (16-byte units) a step.
+template <int DA, int DB>
+__device__ __forceinline__ void umma1_f16_stage_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "add.u64 a1, %1, %3;\n\tadd.u64 a2, a1, %3;\n\tadd.u64 a3, a2, %3;\n\t"
+      "add.u64 b1, %2, %4;\n\tadd.u64 b2, b1, %4;\n\tadd.u64 b3, b2, %4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %5, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %5, 1;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "n"(DA), "n"(DB), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// A persistent CTA per SM on tcgen05: 128 rows on the MMA's M side, the ranks on its N
+// side, a stage of 64 terms of the sum in 128-byte swizzled lines.  Four loader warps
+// gather the rows (and F) with 16-byte asynchronous copies, which take any order of
+// the rows and leave zeros past the ends; an MMA warp; four epilogue warps.  F enters
+// as it lies: terms innermost (A) or ranks innermost (B^T) through MN-major
+// descriptors.  With few tiles the sum is cut into slices, whose parts of mid the
+// second launch adds in their order.
+constexpr int kMdThreads = 288, kMdLoaders = 128;
+
+template <int RB>  // blocks of 64 ranks
+struct MidCfg {
+  static constexpr int kStages = RB == 1 ? 8 : RB == 2 ? 6 : 4;
+  static constexpr int kLag = RB == 1 ? 6 : RB == 2 ? 4 : 3;  // stages of copies in flight
+  static constexpr int kFBytes = RB * 8192;
+  static constexpr int kStageBytes = 16384 + kFBytes;
+  static constexpr int kAlloc = kStages * kStageBytes + 1024;
+  static_assert(kLag < kStages, "a loader would wait for a stage that it has not signalled");
+  static_assert(kAlloc + (kAdAdapters + 1) * 4 + 512 <= 227 * 1024, "shared memory over the per-CTA limit");
+};
+
+struct MidItem {
+  int l, pos, n;  // adapter, first position, rows
+  int t0, t1;     // stages
+  int split;
+};
+
+// Item w = tile * S + slice; items are walked in ascending order, l goes on from the last one's.
+__device__ __forceinline__ MidItem mid_item(const AdapterArgs& a, const int* start, int w, int S, int stages, int& l) {
+  MidItem it;
+  const int tile = w / S;
+  it.split = w - tile * S;
+  while (start[l + 1] <= tile) ++l;
+  it.l = l;
+  int i0, i1;
+  adapter_rows(a.offsets, a.rows, l, i0, i1);
+  it.pos = i0 + (tile - start[l]) * kAtRows;
+  it.n = min(kAtRows, i1 - it.pos);
+  it.t0 = (int)((int64_t)it.split * stages / S);
+  it.t1 = (int)((int64_t)(it.split + 1) * stages / S);
+  return it;
+}
+
+// Slices of the sum: the number that minimises rounds * (stages of a slice + 4) + 2 S, in stages; a lane per number.
+__device__ __forceinline__ int mid_slices(int tiles, int stages, int ctas, int most) {
+  const int s = (threadIdx.x & 31) + 1;
+  uint32_t cost = 0xFFFFFFu;
+  if (s <= most && s <= stages) {
+    const int64_t rounds = ((int64_t)tiles * s + ctas - 1) / ctas;
+    cost = (uint32_t)min((int64_t)0xFFFFFF, rounds * ((stages + s - 1) / s + 4) + (s > 1 ? 2 * s : 0));
+  }
+  return (int)(__reduce_min_sync(0xffffffffu, cost * 64 + s) & 63);
+}
+
+template <int RB, bool FWD>
+__global__ void __launch_bounds__(kMdThreads, 1) adapter_mid_kernel(const __grid_constant__ AdapterArgs a) {
+  using C = MidCfg<RB>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ int start[kAdAdapters + 1];
+  __shared__ int warp_tot[kMdThreads / 32];
+  __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], drain_bar;
+  __shared__ uint32_t misc[2];  // tensor memory, abort
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(&misc[1]);
+  const uint32_t smem_s = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const uint32_t ranks = (a.R + 15) / 16 * 16, columns = tmem_columns(2 * ranks);
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) { mbar_init(&full[i], kMdLoaders); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
+    mbar_init(&drain_bar, 1);
+    misc[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&misc[0], columns);
+    tmem_relinquish();
+  }
+  grid_dependents_launch();
+  grid_dependency_wait();
+  plan_adapters<kAtRows, kMdThreads>(a.offsets, a.rows, a.L, start, warp_tot, a.status);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const int stages = (a.P + 63) / 64, tiles = start[a.L];
+  const int S = mid_slices(tiles, stages, gridDim.x, a.slices);
+  const int64_t items = (int64_t)tiles * S;
+  if (blockIdx.x == 0 && tid == 0) *a.plan = S;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ loaders
+    const int c = tid & 7, line0 = tid >> 3;               // 16-byte column, first line
+    const uint32_t sw = (uint32_t)((c ^ (line0 & 7)) << 4);  // (lines 16 apart share it)
+    const uint16_t* in = static_cast<const uint16_t*>(a.in);
+    int filled = 0, signalled = 0;
+    Ring<C::kStages> slot, done;
+    bool ok = true;
+    int l = 0;
+    for (int64_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      const MidItem it = mid_item(a, start, (int)w, S, stages, l);
+      const uint16_t* row[8];
+      uint32_t there = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = line0 + 16 * i;
+        const int r = at < it.n ? row_of(a.order, a.rows, it.pos + at, a.status) : -1;
+        row[i] = in + (int64_t)max(r, 0) * a.in_ld;
+        there |= (r >= 0 ? 1u : 0u) << i;
+      }
+      const uint16_t* f = static_cast<const uint16_t*>(a.f) + it.l * a.f_l;
+      for (int t = it.t0; t < it.t1; ++t) {
+        if (!mbar_wait(&empty[slot.i], slot.phase ^ 1, abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = smem_s + slot.i * C::kStageBytes + line0 * 128 + sw;
+        const int p = 64 * t + 8 * c;
+        const int whole = p < a.P ? 16 : 0, q = whole ? p : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cp_async16(dst + i * 2048, row[i] + q, (there >> i) & 1 ? whole : 0);
+        if (FWD) {
+#pragma unroll
+          for (int i = 0; i < 4 * RB; ++i) {
+            const int j = line0 + 16 * i;
+            if (j < a.R) cp_async16(dst + 16384 + i * 2048, f + j * a.f_r + q, whole);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int term = 64 * t + line0 + 16 * i;
+            const uint16_t* line = f + (int64_t)(term < a.P ? term : 0) * a.f_r;
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+              if (64 * b + 8 * c < a.R)
+                cp_async16(dst + 16384 + b * 8192 + i * 2048, line + 64 * b + 8 * c, term < a.P ? 16 : 0);
+          }
+        }
+        cp_async_commit();
+        slot.next();
+        if (++filled > C::kLag) {
+          cp_async_wait<C::kLag>();
+          fence_async_proxy();
+          mbar_arrive(&full[done.i]);
+          done.next();
+          ++signalled;
+        }
+      }
+    }
+    cp_async_wait<0>();
+    fence_async_proxy();
+    for (; signalled < filled; ++signalled) {
+      mbar_arrive(&full[done.i]);
+      done.next();
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA
+    const uint32_t idesc = idesc_f16_f32(kAtRows, ranks, a.type == kBf16 ? 1u : 0u) | (FWD ? 0u : kIdescMajorB);
+    const uint64_t xd0 = smem_desc_sw128(smem_s);
+    const uint64_t fd0 = FWD ? smem_desc_sw128(smem_s + 16384) : smem_desc_sw128_mn(smem_s + 16384, 8192);
+    Ring<C::kStages> slot;
+    Ring<2> acc;
+    bool ok = true;
+    int l = 0;
+    for (int64_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      const MidItem it = mid_item(a, start, (int)w, S, stages, l);
+      if (!warp_wait(&acc_empty[acc.i], acc.phase ^ 1, abort_flag, a.status)) break;
+      tc_fence_after();
+      for (int t = it.t0; t < it.t1; ++t) {
+        if (!(ok = warp_wait(&full[slot.i], slot.phase, abort_flag, a.status))) break;
+        tc_fence_after();
+        const uint32_t at = slot.i * (C::kStageBytes >> 4);
+        umma1_f16_stage_elect<2, FWD ? 2 : 128>(tmem + acc.i * ranks, xd0 + at, fd0 + at, idesc, t > it.t0 ? 1u : 0u);
+        umma_commit_elect(&empty[slot.i]);
+        slot.next();
+      }
+      umma_commit_elect(&acc_full[acc.i]);
+      acc.next();
+    }
+    umma_commit_elect(&drain_bar);
+    mbar_drain(&drain_bar, 0, a.status);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue: a row to a thread
+    Ring<2> acc;
+    int l = 0;
+    for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
+      const MidItem it = mid_item(a, start, (int)w, S, stages, l);
+      if (!warp_wait(&acc_full[acc.i], acc.phase, abort_flag, a.status)) break;
+      tc_fence_after();
+      const int at = (warp & 3) * 32 + lane;
+      float* out = (S == 1 ? a.mid : a.part + (int64_t)it.split * a.rows * a.R) + (int64_t)(it.pos + at) * a.R;
+      const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc.i * ranks;
+      for (int j = 0; j < a.R; j += 16) {
+        uint32_t v[16];
+        tmem_ld16(src + j, v);
+        tmem_ld_wait();
+        if (at < it.n) {
+#pragma unroll
+          for (int u = 0; u < 16; u += 4)
+            if (j + u < a.R) *reinterpret_cast<uint4*>(out + j + u) = make_uint4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[acc.i]);
+      acc.next();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, columns);
+}
+
+// ---------------------------------------------------------------- host
+template <int RB, bool FWD>
+static cudaError_t launch_mid(const AdapterArgs& a, int sms, cudaStream_t st) {
+  static std::atomic<bool> ready[64] = {};
+  const cudaError_t rc = allow_smem(adapter_mid_kernel<RB, FWD>, MidCfg<RB>::kAlloc, ready);
+  if (rc != cudaSuccess) return rc;
+  return launch_dependent(adapter_mid_kernel<RB, FWD>, dim3(sms), dim3(kMdThreads), MidCfg<RB>::kAlloc, st, a);
+}
+
+template <bool FWD>
+static cudaError_t launch_mid(const AdapterArgs& a, int sms, cudaStream_t st) {
+  return a.R <= 64 ? launch_mid<1, FWD>(a, sms, st) : a.R <= 128 ? launch_mid<2, FWD>(a, sms, st) : launch_mid<4, FWD>(a, sms, st);
+}
+
+cudaError_t launch_adapter_tc(AdapterArgs& a, bool fwd, bool mid_wanted, cudaStream_t st) {
+  const int sms = prod_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  a.want_mid = mid_wanted;
+  if (!a.out) a.slices = 1;
+  const cudaError_t rc = fwd ? launch_mid<true>(a, sms, st) : launch_mid<false>(a, sms, st);
+  if (rc != cudaSuccess || !a.out) return rc;
+  return fwd ? launch_adapter_out_fwd(a, sms, st) : launch_adapter_out_dx(a, sms, st);
+}
+
+}  // namespace moe
