@@ -120,11 +120,19 @@ extern "C" int moe_adapter_mm_dw(int dtype, const void* dy, int64_t dy_stride, c
   if (rows > 0 && da && (!x || !mid_dy || !on_elements(x, 2) || !on_elements(mid_dy, 4))) return MOE_ERR_INVALID;
   if (rows > 0 && db && (!dy || !mid_x || !on_elements(dy, 2) || !on_elements(mid_x, 4))) return MOE_ERR_INVALID;
   AdapterGradArgs g{};
-  g.side[0] = {da ? x : nullptr, x_stride, mid_dy, K, da, da_stride_l, da_stride_r, 1};
-  g.side[1] = {db ? dy : nullptr, dy_stride, mid_x, N, db, db_stride_l, 1, db_stride_n};
+  g.side[0] = {da ? x : nullptr, x_stride, mid_dy, K, da, da_stride_l, da_stride_r, 1, 0};
+  g.side[1] = {db ? dy : nullptr, dy_stride, mid_x, N, db, db_stride_l, 1, db_stride_n, 0};
   g.offsets = offsets, g.order = order, g.scale = scale;
   g.L = num_adapters, g.rows = rows, g.R = rank, g.type = dtype, g.out_type = grad_dtype, g.accumulate = accumulate;
   g.status = static_cast<unsigned*>(workspace);
+  bool fast = rank % 8 == 0 && rows > 0;
+  for (const AdapterGradSide& s : g.side)
+    if (s.out) fast = fast && s.P % 8 == 0 && grid16(s.in, s.in_ld) && grid16(s.mid, 0);
+  if (fast) {
+    g.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + MOE_PRODUCTS_WORKSPACE_HEAD_BYTES);
+    const int64_t room = (MOE_PRODUCTS_WORKSPACE_BYTES - MOE_PRODUCTS_WORKSPACE_HEAD_BYTES) / 4;
+    return launch_adapter_grad_tc(g, room, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
   for (int side = 0; side < 2; ++side)
     if (g.side[side].out && launch_adapter_grad_any(g, side, (cudaStream_t)stream) != cudaSuccess) return MOE_ERR_CUDA;
   return MOE_OK;

@@ -43,6 +43,7 @@ struct AdapterGradSide {
   int P;
   void* out;
   int64_t out_l, out_j, out_p;  // strides
+  int tiles;                 // of columns p
 };
 struct AdapterGradArgs {
   AdapterGradSide side[2];
@@ -50,6 +51,8 @@ struct AdapterGradArgs {
   const int32_t* order;
   const float* scale;
   int L, rows, R, type, out_type, accumulate;
+  int slice_rows;            // positions of a slice
+  float* part;               // partial tiles
   unsigned* status;
 };
 
@@ -162,6 +165,23 @@ __device__ __forceinline__ void plan_adapters(const int32_t* offsets, int rows, 
 
 constexpr int kAtRows = 128;  // positions of a tile
 
+// Four MMAs of 16 terms of one CTA; the descriptors advance by DA and DB (16-byte units) a step.
+template <int DA, int DB>
+__device__ __forceinline__ void umma1_f16_stage_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "add.u64 a1, %1, %3;\n\tadd.u64 a2, a1, %3;\n\tadd.u64 a3, a2, %3;\n\t"
+      "add.u64 b1, %2, %4;\n\tadd.u64 b2, b1, %4;\n\tadd.u64 b3, b2, %4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %5, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %5, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %5, 1;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "n"(DA), "n"(DB), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
 // Power-of-two columns of tensor memory that hold n.
 __host__ __device__ constexpr uint32_t tmem_columns(uint32_t n) {
   uint32_t c = 32;
@@ -184,6 +204,7 @@ inline cudaError_t allow_smem(F* kernel, int bytes, std::atomic<bool>* ready) {
 }
 
 cudaError_t launch_adapter_any(const AdapterArgs& a, bool fwd, cudaStream_t st);
+cudaError_t launch_adapter_grad_tc(AdapterGradArgs& a, int64_t part_values, cudaStream_t st);
 cudaError_t launch_adapter_grad_any(const AdapterGradArgs& a, int side, cudaStream_t st);
 cudaError_t launch_adapter_rest(const AdapterArgs& a, cudaStream_t st);
 // Operands on the 16-byte grid: up to kAdFewRows rows of the forward product, and any number of both.

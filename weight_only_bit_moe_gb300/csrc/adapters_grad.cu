@@ -1,0 +1,418 @@
+// The gradients of the adapters' factors:
+//   dF[l](j, p) = scale[l] sum_i mid[i, j] in[r, p]      dA: in = x, mid of dy;  dB: in = dy, mid of x
+//
+// On tcgen05: 128 columns p of the rows on the MMA's M side, the ranks on its N side,
+// the sum over positions in stages of 64; both operands lie with the sum outermost and
+// enter through MN-major descriptors.  mid is fp32 and enters as a high and a low
+// 16-bit part, two MMAs on one accumulator (fp16: divided by a power of two that
+// brings the item's largest value to 2^13 .. 2^14, so that values 2^-27 of it still
+// keep 11 bits).  Roles: four warps gather rows with asynchronous copies, four warps
+// convert mid, an MMA warp, four epilogue warps.
+//
+// Items: an adapter's positions are cut into slices of a.slice_rows, times the tiles
+// of p of both sides in one launch.  An adapter of one slice is written at once; the
+// slices of others go to the workspace, and a second launch adds them in their order,
+// so the same inputs give the same bits.
+#include <climits>
+
+#include "adapters.cuh"
+
+namespace moe {
+
+constexpr int kDwThreads = 416, kDwLoaders = 128;  // warps 0-3 loaders, 4-7 epilogue, 8-11 converters, 12 MMA
+constexpr int kDwCols = 128;
+
+template <int RB>  // blocks of 64 ranks
+struct DwCfg {
+  static constexpr int kStages = RB == 1 ? 6 : RB == 2 ? 4 : 2;
+  static constexpr int kLag = RB == 1 ? 4 : RB == 2 ? 3 : 1;
+  static constexpr int kMidBytes = RB * 8192;  // of one part
+  static constexpr int kStageBytes = 16384 + 2 * kMidBytes;
+  static constexpr int kAlloc = kStages * kStageBytes + 1024;
+  static constexpr int kVec = RB * 8;  // float4 of a stage that a converter holds
+  static_assert(kLag < kStages, "a loader would wait for a stage that it has not signalled");
+  static_assert(kAlloc + 2 * (kAdAdapters + 1) * 4 + 512 <= 227 * 1024, "shared memory over the per-CTA limit");
+};
+
+struct DwItem {
+  int l, side, p0;
+  int pos, n;       // positions
+  int slices;       // of the adapter
+  int64_t part;     // partial tile, for adapters of several slices
+};
+
+// Slices of adapter l.
+__device__ __forceinline__ int dw_slices(const AdapterGradArgs& a, int l) {
+  int i0, i1;
+  adapter_rows(a.offsets, a.rows, l, i0, i1);
+  return i0 == i1 ? 1 : (i1 - i0 + a.slice_rows - 1) / a.slice_rows;
+}
+
+// First slice of each adapter into start, and first one that goes to the workspace into part (their numbers to part[L]).
+// False, and no slices, where offsets break the rule.
+template <int THREADS>
+__device__ __forceinline__ bool plan_dw(const AdapterGradArgs& a, int* start, int* part, int* warp_tot) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (a.L + THREADS - 1) / THREADS;
+  int run = 0, run_part = 0, bad = 0;
+  for (int i = 0; i < per; ++i) {
+    const int l = tid * per + i;
+    if (l >= a.L) break;
+    bad |= adapter_bad(a.offsets, a.rows, l);
+    const int n = dw_slices(a, l);
+    run += n;
+    if (n > 1) run_part += n;
+  }
+  if (__syncthreads_or(bad)) {
+    if (bad && blockIdx.x == 0) atomicOr(a.status, kStatusRouting);
+    return false;
+  }
+  int incl = run, incl_part = run_part;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, incl_part, o);
+    if (lane >= o) incl += u, incl_part += v;
+  }
+  if (lane == 31) warp_tot[2 * warp] = incl, warp_tot[2 * warp + 1] = incl_part;
+  __syncthreads();
+  int at = incl - run, at_part = incl_part - run_part;
+  for (int w = 0; w < warp; ++w) at += warp_tot[2 * w], at_part += warp_tot[2 * w + 1];
+  for (int i = 0; i < per; ++i) {
+    const int l = tid * per + i;
+    if (l >= a.L) break;
+    const int n = dw_slices(a, l);
+    start[l] = at;
+    part[l] = at_part;
+    at += n;
+    if (n > 1) at_part += n;
+    if (l == a.L - 1) start[a.L] = at, part[a.L] = at_part;
+  }
+  __syncthreads();
+  return true;
+}
+
+// Item w: tiles of p fastest, then slices.
+__device__ __forceinline__ DwItem dw_item(const AdapterGradArgs& a, const int* start, const int* part, int64_t w, int& l) {
+  DwItem it;
+  const int tiles = a.side[0].tiles + a.side[1].tiles;
+  const int slice = (int)(w / tiles), tile = (int)(w - (int64_t)slice * tiles);
+  while (start[l + 1] <= slice) ++l;
+  it.l = l;
+  it.side = tile >= a.side[0].tiles;
+  it.p0 = (tile - (it.side ? a.side[0].tiles : 0)) * kDwCols;
+  int i0, i1;
+  adapter_rows(a.offsets, a.rows, l, i0, i1);
+  const int s = slice - start[l];
+  it.pos = i0 + s * a.slice_rows;
+  it.n = min(a.slice_rows, i1 - it.pos);
+  it.slices = start[l + 1] - start[l];
+  it.part = (int64_t)(part[l] + s) * tiles + tile;
+  return it;
+}
+
+// A value of the gradient: scaled, rounded, written or added.
+__device__ __forceinline__ void dw_store(const AdapterGradArgs& a, void* out, int64_t at, float v) {
+  if (a.accumulate) v += static_cast<const float*>(out)[at];
+  store_elem(out, at, a.out_type, v);
+}
+
+template <int RB>
+__global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_constant__ AdapterGradArgs a) {
+  using C = DwCfg<RB>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ int start[kAdAdapters + 1], part[kAdAdapters + 1];
+  __shared__ int warp_tot[2 * kDwThreads / 32];
+  __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], drain_bar;
+  __shared__ uint32_t misc[2];
+  __shared__ float factor[2];      // of the accumulators (fp16)
+  __shared__ float warp_top[4];
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(&misc[1]);
+  const uint32_t smem_s = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const uint32_t ranks = (a.R + 15) / 16 * 16, columns = tmem_columns(2 * ranks);
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) { mbar_init(&full[i], 2 * kDwLoaders); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
+    mbar_init(&drain_bar, 1);
+    misc[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&misc[0], columns);
+    tmem_relinquish();
+  }
+  grid_dependents_launch();
+  grid_dependency_wait();
+  const bool good = plan_dw<kDwThreads>(a, start, part, warp_tot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const int64_t items = good ? (int64_t)start[a.L] * (a.side[0].tiles + a.side[1].tiles) : 0;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ loaders: 64 lines of 128 columns, two blocks of 64
+    const int c = tid & 15, line0 = tid >> 4;  // lines 8 apart
+    const uint32_t to = (uint32_t)((c >> 3) * 8192 + line0 * 128 + (((c & 7) ^ (line0 & 7)) << 4));
+    int filled = 0, signalled = 0;
+    Ring<C::kStages> slot, done;
+    bool ok = true;
+    int l = 0;
+    for (int64_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      const DwItem it = dw_item(a, start, part, w, l);
+      const AdapterGradSide& g = a.side[it.side];
+      const uint16_t* in = static_cast<const uint16_t*>(g.in);
+      const int p = it.p0 + 8 * c;
+      int r[8];  // rows of the next stage, on their way while this one is copied
+      auto load_rows = [&](int i) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int at = i + line0 + 8 * u;
+          r[u] = at < it.n ? (a.order ? __ldg(a.order + it.pos + at) : it.pos + at) : INT_MIN;
+        }
+      };
+      load_rows(0);
+      for (int i = 0; i < it.n; i += 64) {
+        if (!mbar_wait(&empty[slot.i], slot.phase ^ 1, abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = smem_s + slot.i * C::kStageBytes + to;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const bool have = (unsigned)r[u] < (unsigned)a.rows;
+          if (!have && i + line0 + 8 * u < it.n) atomicOr(a.status, kStatusRouting);
+          cp_async16(dst + u * 1024, in + (have && p < g.P ? r[u] * g.in_ld + p : 0), have && p < g.P ? 16 : 0);
+        }
+        cp_async_commit();
+        if (i + 64 < it.n) load_rows(i + 64);
+        slot.next();
+        if (++filled > C::kLag) {
+          cp_async_wait<C::kLag>();
+          fence_async_proxy();
+          mbar_arrive(&full[done.i]);
+          done.next();
+          ++signalled;
+        }
+      }
+    }
+    cp_async_wait<0>();
+    fence_async_proxy();
+    for (; signalled < filled; ++signalled) {
+      mbar_arrive(&full[done.i]);
+      done.next();
+    }
+  } else if (warp >= 8 && warp < 12) {
+    // ------------------------------------------------------------ converters: mid to two 16-bit parts
+    const int ct = tid - 8 * 32;
+    const int quads = a.R / 4;  // float4 of a position
+    Ring<C::kStages> slot;
+    Ring<2> acc;
+    bool ok = true;
+    int l = 0;
+    for (int64_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      const DwItem it = dw_item(a, start, part, w, l);
+      if (it.n == 0) continue;
+      const float4* mid = reinterpret_cast<const float4*>(a.side[it.side].mid + (int64_t)it.pos * a.R);
+      float inv = 1.0f;
+      if (a.type == kFp16) {
+        float top = 0.0f;
+        const int64_t all = (int64_t)it.n * quads;
+#pragma unroll 4
+        for (int64_t u = ct; u < all; u += kDwLoaders) {
+          const float4 v = __ldg(mid + u);
+          top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+        }
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // (not negative)
+        if (lane == 0) warp_top[warp - 8] = top;
+        named_bar_sync(1, kDwLoaders);
+        top = fmaxf(fmaxf(warp_top[0], warp_top[1]), fmaxf(warp_top[2], warp_top[3]));
+        float f = 1.0f;
+        const int e = max((int)((__float_as_uint(top) >> 23) & 255) - 13, 1);
+        if (top > 0.0f && top < INFINITY) f = __uint_as_float((uint32_t)e << 23);
+        inv = 1.0f / f;
+        // the accumulator's last reader is done before its factor changes
+        if (!(ok = warp_wait(&acc_empty[acc.i], acc.phase ^ 1, abort_flag, a.status))) break;
+        if (ct == 0) factor[acc.i] = f;
+        acc.next();
+        named_bar_sync(1, kDwLoaders);
+      }
+      // a stage holds 64 quads float4, dealt to the threads in turn
+      float4 v[C::kVec];
+      auto load = [&](int i) {
+#pragma unroll
+        for (int u = 0; u < C::kVec; ++u) {
+          const int at = u * kDwLoaders + ct, line = at / quads;
+          v[u] = line < 64 && i + line < it.n ? __ldg(mid + (int64_t)i * quads + at) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+      };
+      load(0);
+      for (int i = 0; i < it.n; i += 64) {
+        if (!mbar_wait(&empty[slot.i], slot.phase ^ 1, abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = smem_s + slot.i * C::kStageBytes + 16384;
+#pragma unroll
+        for (int u = 0; u < C::kVec; ++u) {
+          const int at = u * kDwLoaders + ct, line = at / quads, j = (at - line * quads) * 4;
+          if (line >= 64) break;
+          uint32_t h0, h1, l0, l1;
+          if (a.type == kBf16) {
+            split_type<kBf16>(v[u].x, v[u].y, h0, l0);
+            split_type<kBf16>(v[u].z, v[u].w, h1, l1);
+          } else {
+            split_type<kFp16>(v[u].x * inv, v[u].y * inv, h0, l0);
+            split_type<kFp16>(v[u].z * inv, v[u].w * inv, h1, l1);
+          }
+          const uint32_t to = dst + (j >> 6) * 8192 + line * 128 + ((((j & 63) >> 3) ^ (line & 7)) << 4) + (j & 4) * 2;
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(h0), "r"(h1) : "memory");
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + C::kMidBytes), "r"(l0), "r"(l1) : "memory");
+        }
+        fence_async_proxy();
+        mbar_arrive(&full[slot.i]);
+        slot.next();
+        if (i + 64 < it.n) load(i + 64);
+      }
+    }
+  } else if (warp == 12) {
+    // ------------------------------------------------------------ MMA
+    const uint32_t idesc = idesc_f16_f32(kDwCols, ranks, a.type == kBf16 ? 1u : 0u) | kIdescMajorA | kIdescMajorB;
+    const uint64_t xd0 = smem_desc_sw128_mn(smem_s, 8192), hd0 = smem_desc_sw128_mn(smem_s + 16384, 8192),
+                   ld0 = smem_desc_sw128_mn(smem_s + 16384 + C::kMidBytes, 8192);
+    Ring<C::kStages> slot;
+    Ring<2> acc;
+    bool ok = true;
+    int l = 0;
+    for (int64_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      const DwItem it = dw_item(a, start, part, w, l);
+      if (it.n == 0) continue;
+      if (!warp_wait(&acc_empty[acc.i], acc.phase ^ 1, abort_flag, a.status)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + acc.i * ranks;
+      for (int i = 0; i < it.n; i += 64) {
+        if (!(ok = warp_wait(&full[slot.i], slot.phase, abort_flag, a.status))) break;
+        tc_fence_after();
+        const uint32_t at = slot.i * (C::kStageBytes >> 4);
+        umma1_f16_stage_elect<128, 128>(d, xd0 + at, hd0 + at, idesc, i > 0 ? 1u : 0u);
+        umma1_f16_stage_elect<128, 128>(d, xd0 + at, ld0 + at, idesc, 1u);
+        umma_commit_elect(&empty[slot.i]);
+        slot.next();
+      }
+      umma_commit_elect(&acc_full[acc.i]);
+      acc.next();
+    }
+    umma_commit_elect(&drain_bar);
+    mbar_drain(&drain_bar, 0, a.status);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue: a column p to a thread
+    Ring<2> acc;
+    int l = 0;
+    const int at = (warp & 3) * 32 + lane;
+    for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
+      const DwItem it = dw_item(a, start, part, w, l);
+      const AdapterGradSide& g = a.side[it.side];
+      const bool some = it.n > 0;
+      if (!some && a.accumulate) continue;  // nothing is added: the adapter's part keeps its bits
+      if (some && !warp_wait(&acc_full[acc.i], acc.phase, abort_flag, a.status)) break;
+      tc_fence_after();
+      const bool whole = it.slices == 1;
+      float mul = whole && a.scale ? a.scale[it.l] : 1.0f;
+      if (a.type == kFp16 && some) mul *= *(volatile float*)&factor[acc.i];
+      const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc.i * ranks;
+      const bool there = it.p0 + at < g.P;
+      const int64_t first = it.l * g.out_l + (it.p0 + at) * g.out_p;
+      float* const partial = a.part + (it.part * a.R) * kDwCols + at;
+      for (int j = 0; j < a.R; j += 16) {
+        uint32_t v[16] = {};
+        if (some) {
+          tmem_ld16(src + j, v);
+          tmem_ld_wait();
+        }
+        if (there) {
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            if (j + u >= a.R) break;
+            const float f = some ? mul * __uint_as_float(v[u]) : 0.0f;
+            if (whole) dw_store(a, g.out, first + (j + u) * g.out_j, f);
+            else partial[(j + u) * kDwCols] = f;
+          }
+        }
+        __syncwarp();
+      }
+      if (some) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[acc.i]);
+        acc.next();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, columns);
+}
+
+// Adds the slices of the adapters that have several: a CTA to a tile of 128 columns, in turn.
+__global__ void __launch_bounds__(256) adapter_dw_sum_kernel(const __grid_constant__ AdapterGradArgs a) {
+  __shared__ int start[kAdAdapters + 1], part[kAdAdapters + 1];
+  __shared__ int warp_tot[16];
+  grid_dependents_launch();
+  grid_dependency_wait();
+  if (!plan_dw<256>(a, start, part, warp_tot)) return;
+  const int tiles = a.side[0].tiles + a.side[1].tiles;
+  int turn = 0;
+  for (int l = 0; l < a.L; ++l) {
+    const int n = start[l + 1] - start[l];
+    if (n == 1) continue;
+    for (int tile = 0; tile < tiles; ++tile, ++turn) {
+      if (turn % gridDim.x != blockIdx.x) continue;
+      const int side = tile >= a.side[0].tiles;
+      const AdapterGradSide& g = a.side[side];
+      const int p0 = (tile - (side ? a.side[0].tiles : 0)) * kDwCols;
+      const float scale = a.scale ? a.scale[l] : 1.0f;
+      for (int u = threadIdx.x; u < a.R * kDwCols; u += 256) {
+        // neighbours in the output to neighbouring threads
+        const int j = side ? u % a.R : u / kDwCols, c = side ? u / a.R : u % kDwCols;
+        if (p0 + c >= g.P) continue;
+        float sum = 0.0f;
+        for (int s = 0; s < n; ++s) sum += a.part[(((int64_t)(part[l] + s) * tiles + tile) * a.R + j) * kDwCols + c];
+        dw_store(a, g.out, l * g.out_l + j * g.out_j + (p0 + c) * g.out_p, scale * sum);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host
+template <int RB>
+static cudaError_t launch_dw(const AdapterGradArgs& a, int sms, cudaStream_t st) {
+  static std::atomic<bool> ready[64] = {};
+  const cudaError_t rc = allow_smem(adapter_dw_kernel<RB>, DwCfg<RB>::kAlloc, ready);
+  if (rc != cudaSuccess) return rc;
+  return launch_dependent(adapter_dw_kernel<RB>, dim3(sms), dim3(kDwThreads), DwCfg<RB>::kAlloc, st, a);
+}
+
+// part_values: what the workspace holds of partial sums.
+cudaError_t launch_adapter_grad_tc(AdapterGradArgs& a, int64_t part_values, cudaStream_t st) {
+  const int sms = prod_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  for (int i = 0; i < 2; ++i) a.side[i].tiles = a.side[i].out ? (a.side[i].P + kDwCols - 1) / kDwCols : 0;
+  const int64_t tiles = a.side[0].tiles + a.side[1].tiles;
+  // Six items to a CTA, of 256 rows at least, if one adapter had all rows; n rows in slices make fewer than
+  // 2 n / slice of them where there is more than one, all of which the workspace has to hold.
+  const int64_t items = (int64_t)sms * 6, room = part_values / (tiles * a.R * kDwCols);
+  int64_t rows = (a.rows * tiles + items - 1) / items;
+  if (rows < 256) rows = 256;
+  if (room < 2) rows = a.rows;
+  else if (rows * room < 2 * (int64_t)a.rows) rows = (2 * (int64_t)a.rows + room - 1) / room;
+  rows = (rows + 63) / 64 * 64;
+  a.slice_rows = (int)(rows > a.rows ? a.rows : rows);
+  if (a.slice_rows < 1) a.slice_rows = 1;
+  cudaError_t rc = a.R <= 64 ? launch_dw<1>(a, sms, st) : a.R <= 128 ? launch_dw<2>(a, sms, st) : launch_dw<4>(a, sms, st);
+  if (rc != cudaSuccess || a.slice_rows >= a.rows) return rc;
+  return launch_dependent(adapter_dw_sum_kernel, dim3(sms * 4), dim3(256), 0, st, a);
+}
+
+}  // namespace moe

@@ -10,23 +10,6 @@
 
 namespace moe {
 
-// Four MMAs of 16 terms of one CTA; the descriptors advance by DA and DB (16-byte units) a step.
-template <int DA, int DB>
-__device__ __forceinline__ void umma1_f16_stage_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "add.u64 a1, %1, %3;\n\tadd.u64 a2, a1, %3;\n\tadd.u64 a3, a2, %3;\n\t"
-      "add.u64 b1, %2, %4;\n\tadd.u64 b2, b1, %4;\n\tadd.u64 b3, b2, %4;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %5, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %5, 1;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %5, 1;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %5, 1;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "n"(DA), "n"(DB), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
 // A persistent CTA per SM on tcgen05: 128 rows on the MMA's M side, the ranks on its N
 // side, a stage of 64 terms of the sum in 128-byte swizzled lines.  Four loader warps
 // gather the rows (and F) with 16-byte asynchronous copies, which take any order of
