@@ -29,7 +29,7 @@ struct DwCfg {
   static constexpr int kMidBytes = RB * 8192;  // of one part
   static constexpr int kStageBytes = 16384 + 2 * kMidBytes;
   static constexpr int kAlloc = kStages * kStageBytes + 1024;
-  static constexpr int kVec = RB * 8;  // float4 of a stage that a converter holds
+  static constexpr int kVec = RB * 8;  // float4 of a stage that a converter holds, at most
   static_assert(kLag < kStages, "a loader would wait for a stage that it has not signalled");
   static_assert(kAlloc + 2 * (kAdAdapters + 1) * 4 + 512 <= 227 * 1024, "shared memory over the per-CTA limit");
 };
@@ -237,13 +237,17 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
         acc.next();
         named_bar_sync(1, kDwLoaders);
       }
-      // a stage holds 64 quads float4, dealt to the threads in turn
+      // two threads to a position, which take its groups of eight values in turn, half a group each
+      const int line = ct >> 1, half = ct & 1, groups = a.R / 8;
+      const float4* const from = mid + (int64_t)line * quads + half;
+      const uint32_t to = smem_s + 16384 + line * 128 + half * 8;
       float4 v[C::kVec];
       auto load = [&](int i) {
+        const bool in = i + line < it.n;
 #pragma unroll
         for (int u = 0; u < C::kVec; ++u) {
-          const int at = u * kDwLoaders + ct, line = at / quads;
-          v[u] = line < 64 && i + line < it.n ? __ldg(mid + (int64_t)i * quads + at) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (u >= groups) break;
+          v[u] = in ? __ldg(from + (int64_t)i * quads + 2 * u) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
       };
       load(0);
@@ -252,11 +256,10 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
           ok = false;
           break;
         }
-        const uint32_t dst = smem_s + slot.i * C::kStageBytes + 16384;
+        const uint32_t dst = to + slot.i * C::kStageBytes;
 #pragma unroll
         for (int u = 0; u < C::kVec; ++u) {
-          const int at = u * kDwLoaders + ct, line = at / quads, j = (at - line * quads) * 4;
-          if (line >= 64) break;
+          if (u >= groups) break;
           uint32_t h0, h1, l0, l1;
           if (a.type == kBf16) {
             split_type<kBf16>(v[u].x, v[u].y, h0, l0);
@@ -265,9 +268,9 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
             split_type<kFp16>(v[u].x * inv, v[u].y * inv, h0, l0);
             split_type<kFp16>(v[u].z * inv, v[u].w * inv, h1, l1);
           }
-          const uint32_t to = dst + (j >> 6) * 8192 + line * 128 + ((((j & 63) >> 3) ^ (line & 7)) << 4) + (j & 4) * 2;
-          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(h0), "r"(h1) : "memory");
-          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + C::kMidBytes), "r"(l0), "r"(l1) : "memory");
+          const uint32_t at = dst + (u >> 3) * 8192 + (((u & 7) ^ (line & 7)) << 4);
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(h0), "r"(h1) : "memory");
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + C::kMidBytes), "r"(l0), "r"(l1) : "memory");
         }
         fence_async_proxy();
         mbar_arrive(&full[slot.i]);

@@ -1,10 +1,10 @@
 // Routing and its balance (moe_routing.h): the experts of each token, the pairs of
 // each expert, the balance loss and the gradients by the logits.
 //
-// A warp owns a token.  Lane l holds the experts (32 i + l) V .. + V - 1 for i = 0,
-// 1, ..: V = 4 where the rows allow vector loads, so a token of 128 experts is one
-// load of a lane.  PER registers a lane serve up to 32 PER experts.
-#include "products_tc.cuh"
+// Routing: a warp owns a token, lane l the PER experts from l PER on, so that among
+// equal lanes the lowest has the lowest expert; rows on the vectors' grid are loaded
+// four values at a time (V = 4).  Balance: a team of G lanes owns a token.
+#include "adapters.cuh"
 #include "../../include/moe_routing.h"
 
 namespace moe {
@@ -63,38 +63,40 @@ __device__ __forceinline__ float sigmoid(float l) {
 // What is subtracted before exponentials: the largest value, or 0 for a token of -infinities.
 __device__ __forceinline__ float finite_or_0(float v) { return v == -INFINITY ? 0.0f : v; }
 
-template <int V>
-__device__ __forceinline__ int expert_of(int i, int lane) {
-  return ((i / V) * 32 + lane) * V + i % V;
+// Four consecutive values.
+template <int TYPE>
+__device__ __forceinline__ void load_four(const void* base, int64_t at, float* v) {
+  if (TYPE == kFp32) {
+    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
+    const float2 f = unpack_type<TYPE>(u.x), g = unpack_type<TYPE>(u.y);
+    v[0] = f.x, v[1] = f.y, v[2] = g.x, v[3] = g.y;
+  }
 }
-
-// A token's logits, -infinity past the last.  V = 4: rows on a boundary of four elements, E a multiple of four.
+template <int TYPE>
+__device__ __forceinline__ void store_four(void* base, int64_t at, const float* v) {
+  if (TYPE == kFp32)
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + at) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at) =
+        make_uint2(pack_type<TYPE>(v[0], v[1]), pack_type<TYPE>(v[2], v[3]));
+}
+// The lane's experts of a token, -infinity past the last.  V = 4: rows on a boundary of four elements, E a multiple
+// of four.
 template <int TYPE, int PER, int V>
 __device__ __forceinline__ void load_row(const void* base, int64_t row_at, int E, int lane, float (&v)[PER]) {
 #pragma unroll
   for (int i = 0; i < PER; i += V) {
-    const int e = expert_of<V>(i, lane);
-    if constexpr (V == 1) {
-      v[i] = e < E ? load_elem(base, row_at + e, TYPE) : -INFINITY;
-    } else if (e >= E) {
-      v[i] = v[i + 1] = v[i + 2] = v[i + 3] = -INFINITY;
-    } else if (TYPE == kFp32) {
-      const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + row_at + e);
-      v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
-    } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + row_at + e);
-      const uint32_t w[2] = {u.x, u.y};
+    const int e = lane * PER + i;
+    if (e >= E) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (TYPE == kBf16) {
-          v[i + 2 * j] = __uint_as_float(w[j] << 16);
-          v[i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        } else {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-          v[i + 2 * j] = f.x;
-          v[i + 2 * j + 1] = f.y;
-        }
-      }
+      for (int u = 0; u < V; ++u) v[i + u] = -INFINITY;
+    } else if constexpr (V == 1) {
+      v[i] = load_elem(base, row_at + e, TYPE);
+    } else {
+      load_four<TYPE>(base, row_at + e, v + i);
     }
   }
 }
@@ -102,57 +104,66 @@ template <int TYPE, int PER, int V>
 __device__ __forceinline__ void store_row(void* base, int64_t row_at, int E, int lane, const float (&v)[PER]) {
 #pragma unroll
   for (int i = 0; i < PER; i += V) {
-    const int e = expert_of<V>(i, lane);
+    const int e = lane * PER + i;
     if (e >= E) continue;
-    if constexpr (V == 1) {
-      store_elem(base, row_at + e, TYPE, v[i]);
-    } else if (TYPE == kFp32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(base) + row_at + e) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    } else {
-      const uint2 u = TYPE == kBf16 ? make_uint2(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]))
-                                    : make_uint2(pack_half2(v[i], v[i + 1]), pack_half2(v[i + 2], v[i + 3]));
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + row_at + e) = u;
-    }
+    if constexpr (V == 1) store_elem(base, row_at + e, TYPE, v[i]);
+    else store_four<TYPE>(base, row_at + e, v + i);
   }
 }
 
 // ---------------------------------------------------------------- choice
-// The choice of a token whose p + bias lie too close for 32 bits, from its logits
-// again: lane j gets the j-th expert or -1.
-__device__ __noinline__ int choose_in_64(const RouteArgs& a, int type, int64_t row_at, int lane) {
-  double key[32];
-  double top = -INFINITY, z = 0.0;
-  if (a.score == MOE_SCORE_SOFTMAX) {
+// p + bias of an expert in 64 bits; without bias the logit.
+__device__ __forceinline__ double key_in_64(const RouteArgs& a, double l, int e, double top, double z) {
+  if (l == -INFINITY) return -INFINITY;
+  if (!a.bias) return l;
+  const double u = exp(a.score == MOE_SCORE_SOFTMAX ? l - top : -fabs(l));
+  const double p = a.score == MOE_SCORE_SOFTMAX ? u / z : (l >= 0.0 ? 1.0 : u) / (1.0 + u);
+  return p + (double)a.bias[e];
+}
+
+// The choice of a token in 64 bits: lane j gets the j-th expert or -1.  Lane c < n brings the candidate `e` (all
+// experts that can be chosen are among them), or with n = 0 every expert is looked at.
+__device__ __noinline__ int choose_in_64(const RouteArgs& a, int type, int64_t row_at, int lane, int e, int n) {
+  double top = 0.0, z = 1.0;
+  if (a.bias && a.score == MOE_SCORE_SOFTMAX) {
+    top = -INFINITY;
 #pragma unroll 1
-    for (int e = lane; e < a.E; e += 32) top = fmax(top, (double)load_elem(a.logits, row_at + e, type));
+    for (int i = lane; i < a.E; i += 32) top = fmax(top, (double)load_elem(a.logits, row_at + i, type));
     for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+    z = 0.0;
 #pragma unroll 1
-    for (int e = lane; e < a.E; e += 32) z += exp((double)load_elem(a.logits, row_at + e, type) - top);
+    for (int i = lane; i < a.E; i += 32) z += exp((double)load_elem(a.logits, row_at + i, type) - top);
     z = warp_sum(z);
   }
-#pragma unroll 1
-  for (int i = 0; i < 32; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = -INFINITY;
-    if (e >= a.E) continue;
-    const double l = load_elem(a.logits, row_at + e, type);
-    if (l == -INFINITY) continue;
-    double p;
-    if (a.score == MOE_SCORE_SOFTMAX) {
-      p = exp(l - top) / z;
-    } else {
-      const double u = exp(-fabs(l));
-      p = (l >= 0.0 ? 1.0 : u) / (1.0 + u);
-    }
-    key[i] = p + (double)a.bias[e];
-  }
   int mine = -1;
+  if (n > 0) {
+    const double key = lane < n ? key_in_64(a, load_elem(a.logits, row_at + e, type), e, top, z) : 0.0;
+    int rank = 0;
+#pragma unroll 1
+    for (int c = 0; c < n; ++c) {
+      const double other = __shfl_sync(0xffffffffu, key, c);
+      const int other_e = __shfl_sync(0xffffffffu, e, c);
+      rank += other > key || (other == key && other_e < e);
+    }
+#pragma unroll 1
+    for (int c = 0; c < n; ++c) {
+      const int at = __shfl_sync(0xffffffffu, rank, c), other_e = __shfl_sync(0xffffffffu, e, c);
+      if (at == lane) mine = other_e;
+    }
+    return lane < a.k ? mine : -1;
+  }
+  double key[kProdGroups / 32];
+#pragma unroll 1
+  for (int i = 0; i < kProdGroups / 32; ++i) {
+    const int x = lane + 32 * i;
+    key[i] = x < a.E ? key_in_64(a, load_elem(a.logits, row_at + x, type), x, top, z) : -INFINITY;
+  }
 #pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
     double best = -INFINITY;
     int at = 1 << 30;
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < kProdGroups / 32; ++i)
       if (key[i] > best) {
         best = key[i];
         at = lane + 32 * i;
@@ -168,49 +179,79 @@ __device__ __noinline__ int choose_in_64(const RouteArgs& a, int type, int64_t r
     if (best == -INFINITY) break;
     if (lane == j) mine = at;
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < kProdGroups / 32; ++i)
       if (lane + 32 * i == at) key[i] = -INFINITY;
   }
   return mine;
 }
 
-template <int TYPE, int PER, int V>
+// Descending order of a lane's keys, by merging sorted halves (Batcher's odd-even merge).
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
+#pragma unroll
+  for (int lp = 0; (1 << lp) < N; ++lp)
+#pragma unroll
+    for (int lq = lp; lq >= 0; --lq)
+#pragma unroll
+      for (int x = 0; x < N; ++x) {
+        const int p = 1 << lp, q = 1 << lq, from = q % p;
+        if (x >= from && ((x - from) / q) % 2 == 0 && x + q < N && x / (2 * p) == (x + q) / (2 * p)) {
+          const uint32_t hi = max(k[x], k[x + q]);
+          k[x + q] = min(k[x], k[x + q]);
+          k[x] = hi;
+        }
+      }
+}
+
+// A key is a value's order in its upper 22 bits and the expert, lowest best, in the
+// lower ten: the largest of the lanes' heads, by one reduction of the warp, names the
+// next expert, and the lane that held it moves its list up.
+//
+// Logits of 16 bits fit the 22 and decide as they are.  Logits of fp32, and p + bias,
+// are taken relative to the token's largest, which keeps 2^-14 of their distance from
+// it.  Where two neighbours among the first k + 1 come closer than the key resolves,
+// or than 32 bits know p + bias, the experts from there on that could be chosen are
+// ranked in 64 bits.
+template <int TYPE, int PER, int V, bool BIAS>
 __global__ void __launch_bounds__(kRtThreads) route_kernel(const __grid_constant__ RouteArgs a) {
+  constexpr bool kExact = TYPE != kFp32 && !BIAS;
+  constexpr uint32_t kLow = kProdGroups - 1;
   grid_dependents_launch();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int64_t token = (int64_t)blockIdx.x * kRtWarps + (threadIdx.x >> 5);
   if (token >= a.tokens) return;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  const int64_t row_at = token * a.ld;
   float v[PER];
-  load_row<TYPE, PER, V>(a.logits, token * a.ld, a.E, lane, v);
+  load_row<TYPE, PER, V>(a.logits, row_at, a.E, lane, v);
   float most = v[0];  // (NaN passes on)
 #pragma unroll
   for (int i = 1; i < PER; ++i) most = fmax_nan(most, v[i]);
   bool bad = !(most < INFINITY);
-  const float top = warp_max(most);
-  const float shift = finite_or_0(top);
+  const float shift = finite_or_0(warp_max(most));
   // softmax: the sum over all experts, where a weight or a key needs it
   float z = 1.0f;
-  if (softmax && (a.bias || !a.renorm)) {
+  if (softmax && (BIAS || !a.renorm)) {
     z = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) z += expf(v[i] - shift);
     z = warp_sum(z);
   }
-  uint32_t key[PER];
+  float largest = shift;  // of what is chosen by
+  if (BIAS) {
+    most = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    float c = v[i];
-    if (a.bias) {
-      const int e = expert_of<V>(i, lane);
+    for (int i = 0; i < PER; ++i) {
+      const int e = lane * PER + i;
       if (e < a.E) {
         const float b = __ldg(a.bias + e);
         bad |= !(b < INFINITY);
-        if (c != -INFINITY) c = (softmax ? expf(c - shift) / z : sigmoid(c)) + b;
+        if (v[i] != -INFINITY) v[i] = (softmax ? __fdividef(expf(v[i] - shift), z) : sigmoid(v[i])) + b;
+        most = fmaxf(most, v[i]);
       }
     }
-    key[i] = c == -INFINITY ? 0u : order_key(c);
+    largest = finite_or_0(warp_max(most));
   }
   int32_t* ids = a.ids + token * a.k;
   float* weights = a.weights + token * a.k;
@@ -221,70 +262,71 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const __grid_constant
     }
     return;
   }
-  // The largest key k times over, and with a bias once more: a 32-bit p is off by at
-  // most 2^-17 of the largest p (softmax: the exponentials' and the sum's rounding;
-  // p |ln p| < 1/e keeps the difference's small) or 2^-20 (sigmoid), the sum with the
-  // bias by 2^-24 of itself, so keys further apart than twice that are in order.
-  const float slack = !a.bias ? 0.0f : softmax ? 7.6293945e-6f / z : 9.5367432e-7f;
-  const int rounds = a.bias ? min(a.k + 1, a.E) : a.k;
-  int mine = -1;
-  float picked = 0.0f, before = 0.0f;
+  uint32_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const float x = kExact ? v[i] : v[i] - largest;
+    key[i] = v[i] == -INFINITY ? 0u : (order_key(x) & ~kLow) | (kLow - (lane * PER + i));
+  }
+  sort_keys(key);
+  // A 32-bit p is off by at most 2^-17 of the largest p (softmax: the exponentials' and
+  // the sum's rounding; p |ln p| < 1/e keeps the difference's small) or 2^-20 (sigmoid),
+  // the sum with the bias and the distance from the largest by 2^-24 of themselves.
+  const float slack = !BIAS ? 0.0f : 2.0f * (softmax ? 7.6293945e-6f / z : 9.5367432e-7f) + 2.3841858e-7f * fabsf(largest);
+  uint32_t mine = 0, before = 0;
+  float reach = -INFINITY;  // what is not below this could still be chosen
   bool close = false;
-  for (int j = 0; j < rounds; ++j) {
-    uint32_t local = key[0];
-#pragma unroll
-    for (int i = 1; i < PER; ++i) local = max(local, key[i]);
-    const uint32_t best = __reduce_max_sync(0xffffffffu, local);
+  int n = 0;
+  for (; n < 32; ++n) {
+    const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
     if (best == 0u) break;
-    const float now = key_value(best);
-    if (a.bias) {
-      if (j > 0 && before - now <= 2.0f * slack + 2.3841858e-7f * fmaxf(fabsf(before), fabsf(now))) close = true;
-      before = now;
-      if (j == a.k) break;
-    }
-    int at = 1 << 30;
-#pragma unroll
-    for (int i = PER - 1; i >= 0; --i)
-      if (key[i] == best) at = expert_of<V>(i, lane);
-    at = __reduce_min_sync(0xffffffffu, at);
-    float logit = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (expert_of<V>(i, lane) == at) {
-        key[i] = 0u;
-        logit = v[i];
+    if (kExact) {
+      if (n == a.k) break;
+    } else {
+      if (n > 0 && n <= a.k) {
+        const float low = key_value(before & ~kLow), high = key_value(best | kLow);
+        const float margin = BIAS ? slack + 2.3841858e-7f * fabsf(high) : 0.0f;
+        close |= BIAS ? low - high <= margin : (before ^ best) <= kLow;
+        if (n == a.k) reach = low - margin;
       }
-    logit = __shfl_sync(0xffffffffu, logit, (at / V) % 32);
-    if (lane == j) {
-      mine = at;
-      picked = logit;
+      if (n >= a.k && (!close || key_value(best | kLow) < reach)) break;
+      before = best;
+    }
+    if (lane == n) mine = best;
+    if (key[0] == best) {
+#pragma unroll
+      for (int i = 0; i + 1 < PER; ++i) key[i] = key[i + 1];
+      key[PER - 1] = 0u;
     }
   }
-  if (close) {
-    mine = choose_in_64(a, TYPE, token * a.ld, lane);
-    if (mine >= 0) picked = load_elem(a.logits, token * a.ld + mine, TYPE);
+  int id = mine && lane < a.k ? (int)(kLow - (mine & kLow)) : -1;
+  if (!kExact && close) {
+    // (32 candidates and perhaps more: look at all)
+    const int e = mine ? (int)(kLow - (mine & kLow)) : 0;
+    id = choose_in_64(a, TYPE, row_at, lane, e, n < 32 ? n : 0);
   }
+  const float picked = id >= 0 ? load_elem(a.logits, row_at + id, TYPE) : -INFINITY;
   float w = 0.0f;
   if (softmax) {
     if (a.renorm) {
-      const float first = finite_or_0(warp_max(mine >= 0 ? picked : -INFINITY));
-      if (mine >= 0) w = expf(picked - first);
-    } else if (mine >= 0) {
+      const float first = finite_or_0(warp_max(picked));
+      if (id >= 0) w = expf(picked - first);
+    } else if (id >= 0) {
       w = expf(picked - shift) / z;
     }
   } else if (a.renorm) {
-    const float floor = fminf(finite_or_0(warp_max(mine >= 0 ? picked : -INFINITY)), 0.0f);
-    if (mine >= 0) w = shifted_sigmoid(picked, floor);
-  } else if (mine >= 0) {
+    const float floor = fminf(finite_or_0(warp_max(picked)), 0.0f);
+    if (id >= 0) w = shifted_sigmoid(picked, floor);
+  } else if (id >= 0) {
     w = sigmoid(picked);
   }
   if (a.renorm) {
     const float sum = warp_sum(w);
-    if (mine >= 0) w = w / sum;
+    if (id >= 0) w = w / sum;
   }
   if (lane < a.k) {
-    ids[lane] = mine;
-    weights[lane] = mine >= 0 ? a.scale * w : 0.0f;
+    ids[lane] = id;
+    weights[lane] = id >= 0 ? a.scale * w : 0.0f;
   }
 }
 
@@ -294,48 +336,52 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const __grid_constant
 //   sigmoid, renormalised   dl_j = w_j (g_j - sum g w / c) (1 - p_j)
 //   sigmoid                 dl_j = c g_j p_j (1 - p_j)
 // Only the softmax over all experts reads the row; the others read the chosen logits.
+// The chosen experts' parts find their lanes through shared memory.
 template <int TYPE, int PER, int V>
 __global__ void __launch_bounds__(kRtThreads) route_grad_kernel(const __grid_constant__ RouteArgs a) {
+  __shared__ __align__(16) float rows[kRtWarps][32 * PER];
   grid_dependents_launch();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int64_t token = (int64_t)blockIdx.x * kRtWarps + (threadIdx.x >> 5);
   if (token >= a.tokens) return;
+  float* const row = rows[threadIdx.x >> 5];
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
   int id = -1;
   float g = 0.0f, l = -INFINITY;
   if (lane < a.k) {
     id = a.in_ids[token * a.k + lane];
-    if (id < 0 || id >= a.E) id = -1;
-    if (id >= 0) {
-      g = a.dw[token * a.dw_ld + lane];
-      l = load_elem(a.logits, token * a.ld + id, TYPE);
-    }
+    g = a.dw[token * a.dw_ld + lane];
   }
   float out[PER];
+  const bool whole = softmax && !a.renorm;
+  if (whole) load_row<TYPE, PER, V>(a.logits, token * a.ld, a.E, lane, out);
+  if (id < 0 || id >= a.E) id = -1, g = 0.0f;
+  if (id >= 0) l = load_elem(a.logits, token * a.ld + id, TYPE);
 #pragma unroll
-  for (int i = 0; i < PER; ++i) out[i] = 0.0f;
+  for (int i = 0; i < PER; i += 4) {
+    if constexpr (PER >= 4) *reinterpret_cast<float4*>(row + lane * PER + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    else for (int u = i; u < PER; ++u) row[lane * PER + u] = 0.0f;
+  }
   float part = 0.0f;  // what the lane's slot adds to its expert
-  if (__any_sync(0xffffffffu, id >= 0)) {
-    if (softmax && !a.renorm) {
-      float v[PER];
-      load_row<TYPE, PER, V>(a.logits, token * a.ld, a.E, lane, v);
-      float most = v[0];
+  float add = 0.0f;   // what p times it adds to every expert
+  const bool some = __any_sync(0xffffffffu, id >= 0);
+  if (some) {
+    if (whole) {
+      float most = out[0];
 #pragma unroll
-      for (int i = 1; i < PER; ++i) most = fmaxf(most, v[i]);
+      for (int i = 1; i < PER; ++i) most = fmaxf(most, out[i]);
       const float shift = finite_or_0(warp_max(most));
       float z = 0.0f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        v[i] = expf(v[i] - shift);
-        z += v[i];
+        out[i] = expf(out[i] - shift);
+        z += out[i];
       }
       z = warp_sum(z);
       const float p = id >= 0 ? expf(l - shift) / z : 0.0f;
-      const float mean = warp_sum(g * p), c = a.scale;
-      part = c * p * g;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) out[i] = -c * (v[i] / z) * mean;
+      add = -a.scale * warp_sum(g * p) / z;
+      part = a.scale * p * g;
     } else if (a.renorm) {
       const float first = finite_or_0(warp_max(l));
       const float e = id < 0 ? 0.0f : softmax ? expf(l - first) : shifted_sigmoid(l, fminf(first, 0.0f));
@@ -347,16 +393,20 @@ __global__ void __launch_bounds__(kRtThreads) route_grad_kernel(const __grid_con
     } else {
       part = a.scale * g * sigmoid(l) * sigmoid(-l);
     }
-    if (id < 0) part = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-      const int at = __shfl_sync(0xffffffffu, id, j);
-      const float add = __shfl_sync(0xffffffffu, part, j);
-      if (at < 0) continue;
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (expert_of<V>(i, lane) == at) out[i] += add;
+    __syncwarp();
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
+    if (__any_sync(0xffffffffu, id >= 0 && (same & (same - 1)))) {  // an expert stands twice: in the slots' order
+      for (int j = 0; j < a.k; ++j) {
+        if (lane == j && id >= 0) row[id] += part;
+        __syncwarp();
+      }
+    } else if (id >= 0) {
+      row[id] = part;
     }
   }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < PER; ++i) out[i] = (whole && some ? out[i] * add : 0.0f) + row[lane * PER + i];
   store_row<TYPE, PER, V>(a.out, token * a.out_ld, a.E, lane, out);
 }
 
@@ -445,200 +495,304 @@ struct BalanceArgs {
   int64_t out_ld;
   unsigned* status;
   int32_t* counter;
-  float* partial;        // [warps + S]: warp w, sequence s at w + s
-  int rows_per_warp;
+  float* partial;        // a part of a sequence's loss for each CTA
+  int chunk;             // tokens of a CTA, at most
 };
 
-// The sequence of a token, from the first one that may hold it on; S: none.
-struct SequenceWalk {
-  int s, r0, r1;
-  __device__ __forceinline__ void start(const BalanceArgs& a, int token) {
-    int lo = 0, hi = a.S;  // the first sequence that ends past the token
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      int b0, b1;
-      sequence_rows(a.offsets, mid, a.tokens, b0, b1);
-      if (b1 > token) hi = mid;
-      else lo = mid + 1;
-    }
-    s = lo;
-    if (s < a.S) sequence_rows(a.offsets, s, a.tokens, r0, r1);
-  }
-  // On to the sequence that ends past the token; true where it is another one.
-  __device__ __forceinline__ bool reach(const BalanceArgs& a, int token) {
-    bool moved = false;
-    while (s < a.S && r1 <= token) {
-      ++s;
-      moved = true;
-      if (s < a.S) sequence_rows(a.offsets, s, a.tokens, r0, r1);
-    }
-    return moved;
-  }
+// A CTA has the tokens that a sequence shares with a chunk [n chunk, (n + 1) chunk):
+// one sequence, so one set of counts.  Going through the tokens, either the sequence or
+// the chunk moves on by one, so sequence s of chunk n is CTA s + n.  The tokens before
+// the first sequence and behind the last are sequences of their own, without a loss.
+// Their bounds: start(0) = 0, the offsets, start(spans) = tokens.
+__device__ __forceinline__ int balance_spans(const BalanceArgs& a) { return a.offsets ? a.S + 2 : 1; }
+__device__ __forceinline__ int balance_start(const BalanceArgs& a, int i) {
+  if (i <= 0) return 0;
+  if (!a.offsets || i >= a.S + 2) return a.tokens;
+  return min(max(__ldg(a.offsets + i - 1), 0), a.tokens);
+}
+struct BalanceItem {
+  int s;       // sequence, -1: none
+  int t0, t1;  // tokens
+  int length;  // of the sequence
 };
-
-// Counts of the sequence, times num_experts / (C T).
-template <int PER, int V>
-__device__ __forceinline__ void load_counts(const BalanceArgs& a, const SequenceWalk& q, int lane, float (&c)[PER]) {
-  double sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = expert_of<V>(i, lane);
-    c[i] = e < a.E ? (float)a.counts[(int64_t)q.s * a.E + e] : 0.0f;
-    sum += c[i];
+// Item x, by every warp: a search in steps of 32.
+__device__ __forceinline__ BalanceItem balance_item(const BalanceArgs& a, int x, int lane) {
+  int lo = 0, hi = balance_spans(a);  // the last span that starts at or before x
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const bool before = at < hi && balance_start(a, at) / a.chunk + at <= x;
+    lo += (31 - __clz(__ballot_sync(0xffffffffu, before) | 1u)) * step;
+    hi = min(hi, lo + step);
   }
-  sum = warp_sum(sum) * (q.r1 - q.r0);
-  const float factor = sum > 0.0 ? (float)(a.E / sum) : 0.0f;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) c[i] *= factor;
+  const int r0 = balance_start(a, lo), r1 = balance_start(a, lo + 1), n = x - lo;
+  BalanceItem it;
+  it.s = !a.offsets ? 0 : lo >= 1 && lo <= a.S ? lo - 1 : -1;
+  it.length = r1 - r0;
+  const int64_t c0 = (int64_t)n * a.chunk;
+  it.t0 = (int)max((int64_t)r0, c0);
+  it.t1 = (int)min((int64_t)r1, c0 + a.chunk);
+  return it;
 }
 
-// p of a token in v's place (times z), returns 1 / z; `rest` gets 1 - sigmoid.
-template <int PER>
+// Teams: G lanes to a token, lane u of them the experts (G i + u) V .. + V - 1, i = 0, 1, ..
+template <int G>
+__device__ __forceinline__ float team_sum(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float team_max(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int TYPE, int G, int PER, int V>
+__device__ __forceinline__ void load_team(const void* base, int64_t row_at, int E, int u, bool on, float (&v)[PER]) {
+#pragma unroll
+  for (int i = 0; i < PER; i += V) {
+    const int e = (i / V * G + u) * V;
+    if (!on || e >= E) {
+#pragma unroll
+      for (int x = 0; x < V; ++x) v[i + x] = -INFINITY;
+    } else if constexpr (V == 1) {
+      v[i] = load_elem(base, row_at + e, TYPE);
+    } else if constexpr (V == 4) {
+      load_four<TYPE>(base, row_at + e, v + i);
+    } else {
+      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + row_at + e);
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float2 f = unpack_type<TYPE>(ws[x]);
+        v[i + 2 * x] = f.x, v[i + 2 * x + 1] = f.y;
+      }
+    }
+  }
+}
+// Counts of the sequence; the factor num_experts / (C T) that goes with them.
+template <int G, int PER, int V>
+__device__ __forceinline__ float load_counts(const BalanceArgs& a, const BalanceItem& it, int u, float (&c)[PER]) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = (i / V * G + u) * V + i % V;
+    c[i] = e < a.E ? (float)__ldg(a.counts + (int64_t)it.s * a.E + e) : 0.0f;
+    sum += c[i];
+  }
+  sum = team_sum<G>(sum);
+  return sum > 0.0f ? a.E / sum / it.length : 0.0f;
+}
+// 2^x.
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// p of a token in v's place, times z; returns 1 / z.  `rest` gets 1 - sigmoid.  exp(l - top) = 2^(l log2 e - top log2 e),
+// one rounding of 2^-24 of the exponent more than the function, for a quarter of its instructions; what is rounded in
+// top log2 e is common to numerator and sum.
+template <int G, int PER>
 __device__ __forceinline__ float probabilities(float (&v)[PER], bool softmax, float* rest) {
+  constexpr float kLog2e = 1.44269504f;
   float most = v[0];
 #pragma unroll
   for (int i = 1; i < PER; ++i) most = fmaxf(most, v[i]);
-  const float shift = finite_or_0(warp_max(most)), floor = fminf(shift, 0.0f);
+  const float shift = finite_or_0(team_max<G>(most));
   float z = 0.0f;
+  if (softmax) {
+    const float s = shift * kLog2e;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (softmax) {
-      v[i] = expf(v[i] - shift);
-    } else {
-      const float u = expf(-fabsf(v[i])), inv = __fdividef(1.0f, 1.0f + u);
-      if (rest) rest[i] = (v[i] >= 0.0f ? u : 1.0f) * inv;
-      v[i] = expf(fminf(v[i], 0.0f) - floor) * inv;
+    for (int i = 0; i < PER; ++i) {
+      v[i] = exp2_of(fmaf(v[i], kLog2e, -s));
+      z += v[i];
     }
-    z += v[i];
+  } else {
+    const float s = fminf(shift, 0.0f) * kLog2e;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const float u = exp2_of(-fabsf(v[i]) * kLog2e), inv = __fdividef(1.0f, 1.0f + u);
+      if (rest) rest[i] = (v[i] >= 0.0f ? u : 1.0f) * inv;
+      v[i] = exp2_of(fmaf(fminf(v[i], 0.0f), kLog2e, -s)) * inv;
+      z += v[i];
+    }
   }
-  z = warp_sum(z);
+  z = team_sum<G>(z);
   return z == 0.0f ? 0.0f : 1.0f / z;
 }
 
-template <int TYPE, int PER, int V>
+template <int TYPE, int G, int PER, int V>
 __global__ void __launch_bounds__(kRtThreads) balance_kernel(const __grid_constant__ BalanceArgs a) {
+  constexpr int kTeams = kRtThreads / G;
+  __shared__ double parts[kTeams];
   __shared__ int last;
-  const int lane = threadIdx.x & 31, warp = blockIdx.x * kRtWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, u = lane % G, team = threadIdx.x / G;
   grid_dependents_launch();
   grid_dependency_wait();
-  if (a.offsets)
-    for (int s = blockIdx.x * kRtThreads + threadIdx.x; s < a.S; s += gridDim.x * kRtThreads)
-      if (sequence_bad(a.offsets, s, a.tokens)) atomicOr(a.status, kStatusRouting);
-  const int64_t first = (int64_t)warp * a.rows_per_warp;
-  const int end = (int)min((int64_t)a.tokens, first + a.rows_per_warp);
-  if (first < end) {
-    SequenceWalk q;
-    q.start(a, (int)first);
+  const BalanceItem it = balance_item(a, blockIdx.x, lane);
+  const bool any = it.s >= 0 && it.t0 < it.t1;
+  if (any) {
     float c[PER], sum = 0.0f;
-    bool have = false;
-    for (int token = (int)first; token < end; ++token) {
-      const int old = q.s;
-      if (q.reach(a, token)) {
-        if (have && lane == 0) a.partial[warp + old] = sum;
-        have = false;
-        sum = 0.0f;
-      }
-      if (q.s == a.S) break;
-      if (token < q.r0) continue;
-      if (!have) load_counts<PER, V>(a, q, lane, c);
-      have = true;
+    const float factor = load_counts<G, PER, V>(a, it, u, c);
+    double total = 0.0;
+    int n = 0;
+    for (int t = it.t0; t < it.t1; t += kTeams, ++n) {
+      const int token = t + team;
       float v[PER], inner = 0.0f;
-      load_row<TYPE, PER, V>(a.logits, token * a.ld, a.E, lane, v);
-      const float inv = probabilities<PER>(v, a.score == MOE_SCORE_SOFTMAX, nullptr);
+      load_team<TYPE, G, PER, V>(a.logits, token * a.ld, a.E, u, token < it.t1, v);
+      const float inv = probabilities<G, PER>(v, a.score == MOE_SCORE_SOFTMAX, nullptr);
 #pragma unroll
       for (int i = 0; i < PER; ++i) inner = fmaf(v[i], c[i], inner);
-      sum += warp_sum(inner) * inv;
+      sum = fmaf(inner, inv, sum);
+      if (n % 64 == 63) total += sum, sum = 0.0f;
     }
-    if (have && lane == 0) a.partial[warp + q.s] = sum;
+    // (each lane has its experts' part; lanes of a team in the order of the exchange)
+    total += sum;
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (u == 0) parts[team] = total * factor;
   }
   __syncthreads();
-  if (threadIdx.x == 0) last = slice_arrive_last(a.counter, gridDim.x);
+  if (threadIdx.x == 0) {
+    if (any) {
+      double sum = 0.0;
+      for (int i = 0; i < kTeams; ++i) sum += parts[i];
+      a.partial[blockIdx.x] = (float)sum;
+    }
+    __threadfence();
+    last = slice_arrive_last(a.counter, gridDim.x);
+  }
   __syncthreads();
   if (!last) return;
-  // the last CTA: a warp per sequence adds the warps' parts in their order
+  // the last CTA adds the parts of each sequence in their order, a warp to a sequence
+  bool bad = false;
+  if (a.offsets)
+    for (int s = threadIdx.x; s < a.S; s += kRtThreads) bad |= sequence_bad(a.offsets, s, a.tokens);
+  if (bad) atomicOr(a.status, kStatusRouting);
+  if (__syncthreads_or(bad)) return;  // (parts of overlapping sequences are not where they are looked for)
+  const int first = a.offsets ? 1 : 0;
   for (int s = threadIdx.x >> 5; s < a.S; s += kRtWarps) {
-    int r0, r1;
-    sequence_rows(a.offsets, s, a.tokens, r0, r1);
+    const int r0 = balance_start(a, s + first), r1 = balance_start(a, s + first + 1);
     double sum = 0.0;
-    if (r0 < r1)
-      for (int w = r0 / a.rows_per_warp + lane; w <= (r1 - 1) / a.rows_per_warp; w += 32)
-        sum += *(volatile float*)(a.partial + w + s);
+    if (r0 < r1) {
+      const int end = (r1 - 1) / a.chunk + s + first;
+#pragma unroll 8
+      for (int x = r0 / a.chunk + s + first + lane; x <= end; x += 32) sum += __ldcg(a.partial + x);
+    }
     sum = warp_sum(sum);
     if (lane == 0) a.loss[s] = (float)sum;
   }
 }
 
-// dl_e = dloss p_e (c_e - sum c p), c the counts times num_experts / (C T); sigmoid: p_e (1 - sigmoid_e) in
-// the place of p_e.
-template <int TYPE, int PER, int V>
+// dl_e = dloss num_experts / (C T) p_e (c_e - sum c p), c the counts; sigmoid: p_e (1 - sigmoid_e) in the place of p_e.
+template <int TYPE, int G, int PER, int V>
 __global__ void __launch_bounds__(kRtThreads) balance_grad_kernel(const __grid_constant__ BalanceArgs a) {
-  const int lane = threadIdx.x & 31, warp = blockIdx.x * kRtWarps + (threadIdx.x >> 5);
+  constexpr int kTeams = kRtThreads / G;
+  const int lane = threadIdx.x & 31, u = lane % G, team = threadIdx.x / G;
   grid_dependents_launch();
   grid_dependency_wait();
   if (a.offsets)
     for (int s = blockIdx.x * kRtThreads + threadIdx.x; s < a.S; s += gridDim.x * kRtThreads)
       if (sequence_bad(a.offsets, s, a.tokens)) atomicOr(a.status, kStatusRouting);
-  const int64_t first = (int64_t)warp * a.rows_per_warp;
-  const int end = (int)min((int64_t)a.tokens, first + a.rows_per_warp);
-  if (first >= end) return;
+  const BalanceItem it = balance_item(a, blockIdx.x, lane);
+  if (it.t0 >= it.t1) return;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-  SequenceWalk q;
-  q.start(a, (int)first);
-  float c[PER], dloss = 0.0f;
-  bool have = false;
-  for (int token = (int)first; token < end; ++token) {
-    if (q.reach(a, token)) have = false;
+  float c[PER], factor = 0.0f;
+  if (it.s >= 0) factor = load_counts<G, PER, V>(a, it, u, c) * a.dloss[it.s];
+  for (int t = it.t0; t < it.t1; t += kTeams) {
+    const int token = t + team;
+    const bool on = token < it.t1;
     float v[PER];
-    if (q.s == a.S || token < q.r0) {
+    if (it.s < 0) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[i] = 0.0f;
     } else {
-      if (!have) {
-        load_counts<PER, V>(a, q, lane, c);
-        dloss = a.dloss[q.s];
-        have = true;
-      }
       float rest[PER], inner = 0.0f;
-      load_row<TYPE, PER, V>(a.logits, token * a.ld, a.E, lane, v);
-      const float inv = probabilities<PER>(v, softmax, rest);
+      load_team<TYPE, G, PER, V>(a.logits, token * a.ld, a.E, u, on, v);
+      const float inv = probabilities<G, PER>(v, softmax, rest);
 #pragma unroll
       for (int i = 0; i < PER; ++i) inner = fmaf(v[i], c[i], inner);
-      inner = warp_sum(inner) * inv;
-      const float g = dloss * inv;
+      inner = team_sum<G>(inner) * inv;
+      const float g = factor * inv;
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[i] = g * (softmax ? v[i] : v[i] * rest[i]) * (c[i] - inner);
     }
-    store_row<TYPE, PER, V>(a.out, token * a.out_ld, a.E, lane, v);
+    if (!on) continue;
+#pragma unroll
+    for (int i = 0; i < PER; i += V) {
+      const int e = (i / V * G + u) * V;
+      if (e >= a.E) continue;
+      const int64_t at = token * a.out_ld + e;
+      if constexpr (V == 1) {
+        store_elem(a.out, at, TYPE, v[i]);
+      } else if constexpr (V == 4) {
+        store_four<TYPE>(a.out, at, v + i);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) w[x] = pack_type<TYPE>(v[i + 2 * x], v[i + 2 * x + 1]);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
   }
 }
 
 // ---------------------------------------------------------------- host
-// The instance of KERNEL for a type, a number of experts and the rows' alignment.
-#define MOE_ROUTING_PICK_V(KERNEL, T, V)                                                  \
-  (E <= 32 ? (const void*)KERNEL<T, (V == 4 ? 4 : 1), V>                                   \
-           : E <= 64 ? (const void*)KERNEL<T, (V == 4 ? 4 : 2), V>                         \
-                     : E <= 128 ? (const void*)KERNEL<T, 4, V>                             \
-                                : E <= 256 ? (const void*)KERNEL<T, 8, V>                  \
-                                           : E <= 512 ? (const void*)KERNEL<T, 16, V>      \
-                                                      : (const void*)KERNEL<T, 32, V>)
-#define MOE_ROUTING_PICK(KERNEL)                                                          \
-  static const void* pick_##KERNEL(int type, int E, bool four) {                          \
-    if (type == kBf16) return four ? MOE_ROUTING_PICK_V(KERNEL, kBf16, 4) : MOE_ROUTING_PICK_V(KERNEL, kBf16, 1); \
-    if (type == kFp16) return four ? MOE_ROUTING_PICK_V(KERNEL, kFp16, 4) : MOE_ROUTING_PICK_V(KERNEL, kFp16, 1); \
-    return four ? MOE_ROUTING_PICK_V(KERNEL, kFp32, 4) : MOE_ROUTING_PICK_V(KERNEL, kFp32, 1);                    \
-  }
-MOE_ROUTING_PICK(route_kernel)
-MOE_ROUTING_PICK(route_grad_kernel)
-MOE_ROUTING_PICK(balance_kernel)
-MOE_ROUTING_PICK(balance_grad_kernel)
+// The instance of a kernel for a number of experts.
+template <int TYPE, int V, bool BIAS>
+static const void* pick_route(int E) {
+  if (E <= 32 && V == 1) return (const void*)route_kernel<TYPE, 1, 1, BIAS>;
+  if (E <= 64 && V == 1) return (const void*)route_kernel<TYPE, 2, 1, BIAS>;
+  if (E <= 128) return (const void*)route_kernel<TYPE, 4, V, BIAS>;
+  if (E <= 256) return (const void*)route_kernel<TYPE, 8, V, BIAS>;
+  if (E <= 512) return (const void*)route_kernel<TYPE, 16, V, BIAS>;
+  return (const void*)route_kernel<TYPE, 32, V, BIAS>;
+}
+template <int TYPE, int V>
+static const void* pick_route_grad(int E) {
+  if (E <= 32 && V == 1) return (const void*)route_grad_kernel<TYPE, 1, 1>;
+  if (E <= 64 && V == 1) return (const void*)route_grad_kernel<TYPE, 2, 1>;
+  if (E <= 128) return (const void*)route_grad_kernel<TYPE, 4, V>;
+  if (E <= 256) return (const void*)route_grad_kernel<TYPE, 8, V>;
+  if (E <= 512) return (const void*)route_grad_kernel<TYPE, 16, V>;
+  return (const void*)route_grad_kernel<TYPE, 32, V>;
+}
+template <int TYPE, int V>
+static const void* pick_balance(int E, bool grad) {
+  if (E <= 64) return grad ? (const void*)balance_grad_kernel<TYPE, 8, 8, V> : (const void*)balance_kernel<TYPE, 8, 8, V>;
+  if (E <= 128) return grad ? (const void*)balance_grad_kernel<TYPE, 8, 16, V> : (const void*)balance_kernel<TYPE, 8, 16, V>;
+  if (E <= 256) return grad ? (const void*)balance_grad_kernel<TYPE, 16, 16, V> : (const void*)balance_kernel<TYPE, 16, 16, V>;
+  if (E <= 512) return grad ? (const void*)balance_grad_kernel<TYPE, 32, 16, V> : (const void*)balance_kernel<TYPE, 32, 16, V>;
+  return grad ? (const void*)balance_grad_kernel<TYPE, 32, 32, V> : (const void*)balance_kernel<TYPE, 32, 32, V>;
+}
+// vec: rows on the grid of 4 elements (routing) or of 16 bytes (balance)
+static const void* route_instance(int type, int E, bool vec, bool bias) {
+  if (type == kBf16)
+    return vec ? (bias ? pick_route<kBf16, 4, true>(E) : pick_route<kBf16, 4, false>(E))
+               : (bias ? pick_route<kBf16, 1, true>(E) : pick_route<kBf16, 1, false>(E));
+  if (type == kFp16)
+    return vec ? (bias ? pick_route<kFp16, 4, true>(E) : pick_route<kFp16, 4, false>(E))
+               : (bias ? pick_route<kFp16, 1, true>(E) : pick_route<kFp16, 1, false>(E));
+  return vec ? (bias ? pick_route<kFp32, 4, true>(E) : pick_route<kFp32, 4, false>(E))
+             : (bias ? pick_route<kFp32, 1, true>(E) : pick_route<kFp32, 1, false>(E));
+}
+static const void* route_grad_instance(int type, int E, bool vec) {
+  if (type == kBf16) return vec ? pick_route_grad<kBf16, 4>(E) : pick_route_grad<kBf16, 1>(E);
+  if (type == kFp16) return vec ? pick_route_grad<kFp16, 4>(E) : pick_route_grad<kFp16, 1>(E);
+  return vec ? pick_route_grad<kFp32, 4>(E) : pick_route_grad<kFp32, 1>(E);
+}
+static const void* balance_instance(int type, int E, bool vec, bool grad) {
+  if (type == kBf16) return vec ? pick_balance<kBf16, 8>(E, grad) : pick_balance<kBf16, 1>(E, grad);
+  if (type == kFp16) return vec ? pick_balance<kFp16, 8>(E, grad) : pick_balance<kFp16, 1>(E, grad);
+  return vec ? pick_balance<kFp32, 4>(E, grad) : pick_balance<kFp32, 1>(E, grad);
+}
 
 static int elem_bytes(int type) { return type == kFp32 ? 4 : 2; }
 static bool on_elements(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-// Rows that four elements at a time can be read from (NULL: none to read).
-static bool in_fours(const void* p, int64_t ld, int E, int type) {
-  return !p || (E % 4 == 0 && ld % 4 == 0 && on_elements(p, 4 * elem_bytes(type)));
+// Rows that n elements at a time can be read from.
+static bool in_vectors(const void* p, int64_t ld, int E, int type, int n) {
+  return E % n == 0 && ld % n == 0 && on_elements(p, n * elem_bytes(type));
 }
-// (Below 128 experts four a lane leave most of the lanes without work, but the loads are fewer.)
 
 static bool good_rows(const void* p, int64_t ld, int E, int type) { return p && ld >= E && on_elements(p, elem_bytes(type)); }
 static bool good_logits(int type, int tokens, int E) {
@@ -648,9 +802,9 @@ static bool good_logits(int type, int tokens, int E) {
 static bool good_score(int score) { return score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID; }
 
 template <typename Args>
-static int launch_routing(const void* kernel, int grid, const Args& a, void* stream) {
+static int launch_routing(const void* kernel, int64_t grid, const Args& a, void* stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kRtThreads);
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[1];
@@ -667,16 +821,16 @@ static int check_workspace(const void* workspace, int64_t bytes) {
   return bytes < MOE_PRODUCTS_WORKSPACE_BYTES ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 
-// Tokens a warp takes one after the other: one until the GPU is full four times over.
-static int plan_balance(BalanceArgs& a, int* grid) {
+// Tokens to a CTA: four CTAs to an SM, but a token to a team at least; as many parts as the workspace holds.
+static int plan_balance(BalanceArgs& a, int64_t* grid) {
   const int sms = prod_sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
-  const int64_t warps = (int64_t)sms * 4 * kRtWarps;
-  a.rows_per_warp = (int)((a.tokens + warps - 1) / warps);
-  if (a.rows_per_warp < 1) a.rows_per_warp = 1;
-  const int64_t used = ((int64_t)a.tokens + a.rows_per_warp - 1) / a.rows_per_warp;
-  *grid = (int)((used + kRtWarps - 1) / kRtWarps);
-  if (*grid < 1) *grid = 1;
+  const int64_t most = (MOE_PRODUCTS_WORKSPACE_BYTES - MOE_PRODUCTS_WORKSPACE_HEAD_BYTES) / 8 - kRtSequences;
+  int64_t chunk = ((int64_t)a.tokens + 4 * sms - 1) / (4 * sms);
+  if (chunk < a.tokens / most + 1) chunk = a.tokens / most + 1;
+  a.chunk = (int)((chunk + 31) / 32 * 32);
+  if (a.chunk < 32) a.chunk = 32;
+  *grid = ((int64_t)a.tokens + a.chunk - 1) / a.chunk + (a.offsets ? a.S + 2 : 1);
   return MOE_OK;
 }
 
@@ -704,8 +858,8 @@ extern "C" int moe_route(int dtype, const void* logits, int64_t logits_stride, c
   RouteArgs a{};
   a.logits = logits, a.ld = logits_stride, a.bias = bias, a.tokens = tokens, a.E = num_experts, a.k = top_k;
   a.score = score, a.renorm = renormalize, a.scale = scale, a.weights = weights, a.ids = ids;
-  const bool four = in_fours(logits, logits_stride, num_experts, dtype);
-  return launch_routing(pick_route_kernel(dtype, num_experts, four), (tokens - 1) / kRtWarps + 1, a, stream);
+  const bool vec = in_vectors(logits, logits_stride, num_experts, dtype, 4);
+  return launch_routing(route_instance(dtype, num_experts, vec, bias != nullptr), (tokens - 1) / kRtWarps + 1, a, stream);
 }
 
 extern "C" int moe_route_grad(int dtype, const float* dweights, int64_t dweights_stride, const void* logits,
@@ -725,9 +879,9 @@ extern "C" int moe_route_grad(int dtype, const float* dweights, int64_t dweights
   a.logits = logits, a.ld = logits_stride, a.tokens = tokens, a.E = num_experts, a.k = top_k;
   a.score = score, a.renorm = renormalize, a.scale = scale, a.dw = dweights, a.dw_ld = dweights_stride;
   a.in_ids = ids, a.out = dlogits, a.out_ld = dlogits_stride;
-  const bool four = in_fours(logits, logits_stride, num_experts, dtype) &&
-                    in_fours(dlogits, dlogits_stride, num_experts, dtype);
-  return launch_routing(pick_route_grad_kernel(dtype, num_experts, four), (tokens - 1) / kRtWarps + 1, a, stream);
+  const bool vec = in_vectors(logits, logits_stride, num_experts, dtype, 4) &&
+                   in_vectors(dlogits, dlogits_stride, num_experts, dtype, 4);
+  return launch_routing(route_grad_instance(dtype, num_experts, vec), (tokens - 1) / kRtWarps + 1, a, stream);
 }
 
 extern "C" int moe_expert_counts(const int32_t* ids, int64_t ids_stride, int tokens, int top_k,
@@ -785,10 +939,10 @@ extern "C" int moe_balance_loss(int dtype, const void* logits, int64_t logits_st
   a.logits = logits, a.ld = logits_stride, a.tokens = tokens, a.E = num_experts, a.S = num_sequences, a.score = score;
   a.counts = counts, a.offsets = offsets, a.loss = loss;
   set_balance_workspace(a, workspace);
-  int grid;
+  int64_t grid;
   if ((rc = plan_balance(a, &grid)) != MOE_OK) return rc;
-  const bool four = in_fours(logits, logits_stride, num_experts, dtype);
-  return launch_routing(pick_balance_kernel(dtype, num_experts, four), grid, a, stream);
+  const bool vec = in_vectors(logits, logits_stride, num_experts, dtype, 16 / elem_bytes(dtype));
+  return launch_routing(balance_instance(dtype, num_experts, vec, false), grid, a, stream);
 }
 
 extern "C" int moe_balance_loss_grad(int dtype, const float* dloss, const void* logits, int64_t logits_stride,
@@ -805,9 +959,9 @@ extern "C" int moe_balance_loss_grad(int dtype, const float* dloss, const void* 
   a.logits = logits, a.ld = logits_stride, a.tokens = tokens, a.E = num_experts, a.S = num_sequences, a.score = score;
   a.counts = counts, a.offsets = offsets, a.dloss = dloss, a.out = dlogits, a.out_ld = dlogits_stride;
   set_balance_workspace(a, workspace);
-  int grid;
+  int64_t grid;
   if ((rc = plan_balance(a, &grid)) != MOE_OK) return rc;
-  const bool four = in_fours(logits, logits_stride, num_experts, dtype) &&
-                    in_fours(dlogits, dlogits_stride, num_experts, dtype);
-  return launch_routing(pick_balance_grad_kernel(dtype, num_experts, four), grid, a, stream);
+  const bool vec = in_vectors(logits, logits_stride, num_experts, dtype, 16 / elem_bytes(dtype)) &&
+                   in_vectors(dlogits, dlogits_stride, num_experts, dtype, 16 / elem_bytes(dtype));
+  return launch_routing(balance_instance(dtype, num_experts, vec, true), grid, a, stream);
 }
