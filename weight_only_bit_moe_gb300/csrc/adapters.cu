@@ -17,11 +17,13 @@ static int check_sizes(int dtype, int L, int rows, int N, int K, int R, const vo
   return bytes < MOE_PRODUCTS_WORKSPACE_BYTES ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 
-// Matrices that the fast kernels take: whole eights of columns on 16-byte boundaries.
-static bool grid16(const void* p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; }
+// Matrices that the fast kernels take: whole eights of columns on 16-byte boundaries, rows less than 4 GB apart.
+static bool grid16(const void* p, int64_t stride) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0 && stride < (int64_t)1 << 31;
+}
 static bool on_grid(const AdapterArgs& a, const float* mid) {
-  return a.P % 8 == 0 && a.Q % 8 == 0 && a.R % 8 == 0 && grid16(a.in, a.in_ld) && grid16(a.f, a.f_l) && a.f_r % 8 == 0 &&
-         grid16(a.s, a.s_l) && a.s_r % 8 == 0 && (reinterpret_cast<uintptr_t>(mid) & 15) == 0 &&
+  return a.P % 8 == 0 && a.Q % 8 == 0 && a.R % 8 == 0 && grid16(a.in, a.in_ld) && grid16(a.f, a.f_r) && a.f_l % 8 == 0 &&
+         grid16(a.s, a.s_r) && a.s_l % 8 == 0 && (reinterpret_cast<uintptr_t>(mid) & 15) == 0 &&
          (!a.out || (grid16(a.out, a.out_ld) && (!a.base || grid16(a.base, a.base_ld))));
 }
 

@@ -6,30 +6,29 @@
 // enter through MN-major descriptors.  mid is fp32 and enters as a high and a low
 // 16-bit part, two MMAs on one accumulator (fp16: divided by a power of two that
 // brings the item's largest value to 2^13 .. 2^14, so that values 2^-27 of it still
-// keep 11 bits).  Roles: four warps gather rows with asynchronous copies, four warps
-// convert mid, an MMA warp, four epilogue warps.
+// keep 11 bits).  Roles: eight warps gather rows with asynchronous copies, eight convert
+// mid, an MMA warp, four epilogue warps.
 //
 // Items: an adapter's positions are cut into slices of a.slice_rows, times the tiles
 // of p of both sides in one launch.  An adapter of one slice is written at once; the
 // slices of others go to the workspace, and a second launch adds them in their order,
 // so the same inputs give the same bits.
-#include <climits>
-
 #include "adapters.cuh"
 
 namespace moe {
 
-constexpr int kDwThreads = 416, kDwLoaders = 128;  // warps 0-3 loaders, 4-7 epilogue, 8-11 converters, 12 MMA
+constexpr int kDwThreads = 672, kDwLoaders = 256, kDwConverters = 256;  // warps 0-7, 12-19; 8-11 epilogue, 20 MMA
 constexpr int kDwCols = 128;
 
-template <int RB>  // blocks of 64 ranks
+template <int VEC>  // float4 of a stage's mid to a converter: ceil(R / 16)
 struct DwCfg {
+  static constexpr int RB = (VEC + 3) / 4;  // blocks of 64 ranks
+  static constexpr int kAhead = VEC == 1 ? 8 : 16 / VEC;  // stages of mid on their way in registers
   static constexpr int kStages = RB == 1 ? 6 : RB == 2 ? 4 : 2;
   static constexpr int kLag = RB == 1 ? 4 : RB == 2 ? 3 : 1;
   static constexpr int kMidBytes = RB * 8192;  // of one part
   static constexpr int kStageBytes = 16384 + 2 * kMidBytes;
   static constexpr int kAlloc = kStages * kStageBytes + 1024;
-  static constexpr int kVec = RB * 8;  // float4 of a stage that a converter holds, at most
   static_assert(kLag < kStages, "a loader would wait for a stage that it has not signalled");
   static_assert(kAlloc + 2 * (kAdAdapters + 1) * 4 + 512 <= 227 * 1024, "shared memory over the per-CTA limit");
 };
@@ -116,28 +115,28 @@ __device__ __forceinline__ void dw_store(const AdapterGradArgs& a, void* out, in
   store_elem(out, at, a.out_type, v);
 }
 
-template <int RB>
+template <int VEC>
 __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_constant__ AdapterGradArgs a) {
-  using C = DwCfg<RB>;
+  using C = DwCfg<VEC>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ int start[kAdAdapters + 1], part[kAdAdapters + 1];
   __shared__ int warp_tot[2 * kDwThreads / 32];
   __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], drain_bar;
   __shared__ uint32_t misc[2];
   __shared__ float factor[2];      // of the accumulators (fp16)
-  __shared__ float warp_top[4];
+  __shared__ float warp_top[8];
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&misc[1]);
   const uint32_t smem_s = (smem_u32(smem_raw) + 1023) & ~1023u;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t ranks = (a.R + 15) / 16 * 16, columns = tmem_columns(2 * ranks);
   if (tid == 0) {
-    for (int i = 0; i < C::kStages; ++i) { mbar_init(&full[i], 2 * kDwLoaders); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < C::kStages; ++i) { mbar_init(&full[i], kDwLoaders + kDwConverters); mbar_init(&empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
     mbar_init(&drain_bar, 1);
     misc[1] = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 20) {
     tmem_alloc(&misc[0], columns);
     tmem_relinquish();
   }
@@ -150,25 +149,29 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
   const uint32_t tmem = misc[0];
   const int64_t items = good ? (int64_t)start[a.L] * (a.side[0].tiles + a.side[1].tiles) : 0;
 
-  if (warp < 4) {
+  if (warp < 8) {
     // ------------------------------------------------------------ loaders: 64 lines of 128 columns, two blocks of 64
-    const int c = tid & 15, line0 = tid >> 4;  // lines 8 apart
+    constexpr int kLines = 64 * 16 / kDwLoaders;  // of a thread, 16 apart
+    const int c = tid & 15, line0 = tid >> 4;
     const uint32_t to = (uint32_t)((c >> 3) * 8192 + line0 * 128 + (((c & 7) ^ (line0 & 7)) << 4));
     int filled = 0, signalled = 0;
     Ring<C::kStages> slot, done;
-    bool ok = true;
+    bool ok = true, bad = false;
     int l = 0;
     for (int64_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
       const DwItem it = dw_item(a, start, part, w, l);
       const AdapterGradSide& g = a.side[it.side];
-      const uint16_t* in = static_cast<const uint16_t*>(g.in);
       const int p = it.p0 + 8 * c;
-      int r[8];  // rows of the next stage, on their way while this one is copied
+      const bool column = p < g.P;
+      const uint8_t* const in = static_cast<const uint8_t*>(g.in) + (column ? 2 * p : 0);
+      const uint32_t ld = (uint32_t)(2 * g.in_ld), rows = (uint32_t)a.rows;
+      uint32_t r[kLines];  // rows of the next stage, on their way while this one is copied; past the end 2^32 - 1
       auto load_rows = [&](int i) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int at = i + line0 + 8 * u;
-          r[u] = at < it.n ? (a.order ? __ldg(a.order + it.pos + at) : it.pos + at) : INT_MIN;
+        for (int u = 0; u < kLines; ++u) {
+          const int at = i + line0 + 16 * u;
+          r[u] = 0xFFFFFFFFu;
+          if (at < it.n) r[u] = a.order ? min((uint32_t)__ldg(a.order + it.pos + at), 0xFFFFFFFEu) : it.pos + at;
         }
       };
       load_rows(0);
@@ -179,13 +182,13 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
         }
         const uint32_t dst = smem_s + slot.i * C::kStageBytes + to;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const bool have = (unsigned)r[u] < (unsigned)a.rows;
-          if (!have && i + line0 + 8 * u < it.n) atomicOr(a.status, kStatusRouting);
-          cp_async16(dst + u * 1024, in + (have && p < g.P ? r[u] * g.in_ld + p : 0), have && p < g.P ? 16 : 0);
+        for (int u = 0; u < kLines; ++u) {
+          const bool have = r[u] < rows;
+          bad |= !have && r[u] != 0xFFFFFFFFu;
+          cp_async16(dst + u * 2048, in + (uint64_t)(have ? r[u] : 0u) * ld, have && column ? 16 : 0);
         }
         cp_async_commit();
-        if (i + 64 < it.n) load_rows(i + 64);
+        load_rows(i + 64);
         slot.next();
         if (++filled > C::kLag) {
           cp_async_wait<C::kLag>();
@@ -196,15 +199,16 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
         }
       }
     }
+    if (bad) atomicOr(a.status, kStatusRouting);
     cp_async_wait<0>();
     fence_async_proxy();
     for (; signalled < filled; ++signalled) {
       mbar_arrive(&full[done.i]);
       done.next();
     }
-  } else if (warp >= 8 && warp < 12) {
+  } else if (warp >= 12 && warp < 20) {
     // ------------------------------------------------------------ converters: mid to two 16-bit parts
-    const int ct = tid - 8 * 32;
+    const int ct = tid - 12 * 32;
     const int quads = a.R / 4;  // float4 of a position
     Ring<C::kStages> slot;
     Ring<2> acc;
@@ -219,14 +223,15 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
         float top = 0.0f;
         const int64_t all = (int64_t)it.n * quads;
 #pragma unroll 4
-        for (int64_t u = ct; u < all; u += kDwLoaders) {
+        for (int64_t u = ct; u < all; u += kDwConverters) {
           const float4 v = __ldg(mid + u);
           top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
         }
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // (not negative)
-        if (lane == 0) warp_top[warp - 8] = top;
-        named_bar_sync(1, kDwLoaders);
-        top = fmaxf(fmaxf(warp_top[0], warp_top[1]), fmaxf(warp_top[2], warp_top[3]));
+        if (lane == 0) warp_top[warp - 12] = top;
+        named_bar_sync(1, kDwConverters);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) top = fmaxf(top, warp_top[u]);
         float f = 1.0f;
         const int e = max((int)((__float_as_uint(top) >> 23) & 255) - 13, 1);
         if (top > 0.0f && top < INFINITY) f = __uint_as_float((uint32_t)e << 23);
@@ -235,50 +240,56 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
         if (!(ok = warp_wait(&acc_empty[acc.i], acc.phase ^ 1, abort_flag, a.status))) break;
         if (ct == 0) factor[acc.i] = f;
         acc.next();
-        named_bar_sync(1, kDwLoaders);
+        named_bar_sync(1, kDwConverters);
       }
-      // two threads to a position, which take its groups of eight values in turn, half a group each
-      const int line = ct >> 1, half = ct & 1, groups = a.R / 8;
-      const float4* const from = mid + (int64_t)line * quads + half;
-      const uint32_t to = smem_s + 16384 + line * 128 + half * 8;
-      float4 v[C::kVec];
-      auto load = [&](int i) {
+      // four threads to a position, which take its float4 in turn; the loads run some stages ahead (one stage ahead, a
+      // stage took as long as memory answers: 205 us where this takes less than half)
+      const int line = ct >> 2, first = ct & 3;
+      const float4* const from = mid + (int64_t)line * quads + first;
+      const uint32_t to = smem_s + 16384 + line * 128 + (first & 1) * 8;
+      float4 v[C::kAhead][VEC];
+      auto load = [&](float4 (&x)[VEC], int i) {
         const bool in = i + line < it.n;
 #pragma unroll
-        for (int u = 0; u < C::kVec; ++u) {
-          if (u >= groups) break;
-          v[u] = in ? __ldg(from + (int64_t)i * quads + 2 * u) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
+        for (int u = 0; u < VEC; ++u)
+          x[u] = in && first + 4 * u < quads ? __ldg(from + (int64_t)i * quads + 4 * u) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       };
-      load(0);
-      for (int i = 0; i < it.n; i += 64) {
-        if (!mbar_wait(&empty[slot.i], slot.phase ^ 1, abort_flag, a.status)) {
-          ok = false;
-          break;
-        }
-        const uint32_t dst = to + slot.i * C::kStageBytes;
 #pragma unroll
-        for (int u = 0; u < C::kVec; ++u) {
-          if (u >= groups) break;
-          uint32_t h0, h1, l0, l1;
-          if (a.type == kBf16) {
-            split_type<kBf16>(v[u].x, v[u].y, h0, l0);
-            split_type<kBf16>(v[u].z, v[u].w, h1, l1);
-          } else {
-            split_type<kFp16>(v[u].x * inv, v[u].y * inv, h0, l0);
-            split_type<kFp16>(v[u].z * inv, v[u].w * inv, h1, l1);
+      for (int d = 0; d < C::kAhead; ++d) load(v[d], 64 * d);
+      for (int i0 = 0; i0 < it.n && ok; i0 += 64 * C::kAhead) {
+#pragma unroll
+        for (int d = 0; d < C::kAhead; ++d) {
+          const int i = i0 + 64 * d;
+          if (i >= it.n) break;
+          if (!mbar_wait(&empty[slot.i], slot.phase ^ 1, abort_flag, a.status)) {
+            ok = false;
+            break;
           }
-          const uint32_t at = dst + (u >> 3) * 8192 + (((u & 7) ^ (line & 7)) << 4);
-          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(h0), "r"(h1) : "memory");
-          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + C::kMidBytes), "r"(l0), "r"(l1) : "memory");
+          const uint32_t dst = to + slot.i * C::kStageBytes;
+#pragma unroll
+          for (int u = 0; u < VEC; ++u) {
+            const float4 x = v[d][u];
+            uint32_t h0, h1, l0, l1;
+            if (a.type == kBf16) {
+              split_type<kBf16>(x.x, x.y, h0, l0);
+              split_type<kBf16>(x.z, x.w, h1, l1);
+            } else {
+              split_type<kFp16>(x.x * inv, x.y * inv, h0, l0);
+              split_type<kFp16>(x.z * inv, x.w * inv, h1, l1);
+            }
+            const int c = 2 * u + (first >> 1);  // 16-byte column
+            const uint32_t at = dst + (c >> 3) * 8192 + (((c & 7) ^ (line & 7)) << 4);
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(h0), "r"(h1) : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + C::kMidBytes), "r"(l0), "r"(l1) : "memory");
+          }
+          fence_async_proxy();
+          mbar_arrive(&full[slot.i]);
+          slot.next();
+          load(v[d], i + 64 * C::kAhead);
         }
-        fence_async_proxy();
-        mbar_arrive(&full[slot.i]);
-        slot.next();
-        if (i + 64 < it.n) load(i + 64);
       }
     }
-  } else if (warp == 12) {
+  } else if (warp == 20) {
     // ------------------------------------------------------------ MMA
     const uint32_t idesc = idesc_f16_f32(kDwCols, ranks, a.type == kBf16 ? 1u : 0u) | kIdescMajorA | kIdescMajorB;
     const uint64_t xd0 = smem_desc_sw128_mn(smem_s, 8192), hd0 = smem_desc_sw128_mn(smem_s + 16384, 8192),
@@ -326,7 +337,9 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
       const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc.i * ranks;
       const bool there = it.p0 + at < g.P;
       const int64_t first = it.l * g.out_l + (it.p0 + at) * g.out_p;
-      float* const partial = a.part + (it.part * a.R) * kDwCols + at;
+      // partial tiles lie as the gradient does: [rank, 128] of dA, [128, rank] of dB
+      const int step = it.side ? 1 : kDwCols;
+      float* const partial = a.part + it.part * a.R * kDwCols + (it.side ? at * a.R : at);
       for (int j = 0; j < a.R; j += 16) {
         uint32_t v[16] = {};
         if (some) {
@@ -339,7 +352,7 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
             if (j + u >= a.R) break;
             const float f = some ? mul * __uint_as_float(v[u]) : 0.0f;
             if (whole) dw_store(a, g.out, first + (j + u) * g.out_j, f);
-            else partial[(j + u) * kDwCols] = f;
+            else partial[(j + u) * step] = f;
           }
         }
         __syncwarp();
@@ -355,46 +368,55 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, columns);
+  if (warp == 20) tmem_dealloc(tmem, columns);
 }
 
-// Adds the slices of the adapters that have several: a CTA to a tile of 128 columns, in turn.
-__global__ void __launch_bounds__(256) adapter_dw_sum_kernel(const __grid_constant__ AdapterGradArgs a) {
+// Adds the slices of the adapters that have several, four values to a thread.
+constexpr int kDsThreads = 256;
+__global__ void __launch_bounds__(kDsThreads) adapter_dw_sum_kernel(const __grid_constant__ AdapterGradArgs a) {
   __shared__ int start[kAdAdapters + 1], part[kAdAdapters + 1];
-  __shared__ int warp_tot[16];
+  __shared__ int warp_tot[2 * kDsThreads / 32];
   grid_dependents_launch();
   grid_dependency_wait();
-  if (!plan_dw<256>(a, start, part, warp_tot)) return;
-  const int tiles = a.side[0].tiles + a.side[1].tiles;
-  int turn = 0;
+  if (!plan_dw<kDsThreads>(a, start, part, warp_tot)) return;
+  const int tiles = a.side[0].tiles + a.side[1].tiles, quads = a.R * kDwCols / 4;  // of a tile
+  const int64_t slice = (int64_t)tiles * quads;
+  int64_t u = (int64_t)blockIdx.x * kDsThreads + threadIdx.x;  // from the first quad of adapter l on
   for (int l = 0; l < a.L; ++l) {
     const int n = start[l + 1] - start[l];
     if (n == 1) continue;
-    for (int tile = 0; tile < tiles; ++tile, ++turn) {
-      if (turn % gridDim.x != blockIdx.x) continue;
+    const float scale = a.scale ? a.scale[l] : 1.0f;
+    for (; u < slice; u += (int64_t)gridDim.x * kDsThreads) {
+      const int tile = (int)(u / quads), at = (int)(u - (int64_t)tile * quads) * 4;
       const int side = tile >= a.side[0].tiles;
       const AdapterGradSide& g = a.side[side];
       const int p0 = (tile - (side ? a.side[0].tiles : 0)) * kDwCols;
-      const float scale = a.scale ? a.scale[l] : 1.0f;
-      for (int u = threadIdx.x; u < a.R * kDwCols; u += 256) {
-        // neighbours in the output to neighbouring threads
-        const int j = side ? u % a.R : u / kDwCols, c = side ? u / a.R : u % kDwCols;
-        if (p0 + c >= g.P) continue;
-        float sum = 0.0f;
-        for (int s = 0; s < n; ++s) sum += a.part[(((int64_t)(part[l] + s) * tiles + tile) * a.R + j) * kDwCols + c];
-        dw_store(a, g.out, l * g.out_l + j * g.out_j + (p0 + c) * g.out_p, scale * sum);
+      const int j = side ? at % a.R : at / kDwCols, p = p0 + (side ? at / a.R : at % kDwCols);
+      if (p >= g.P) continue;  // (P and R are whole eights)
+      const float4* from = reinterpret_cast<const float4*>(a.part) + part[l] * slice + u;
+      float4 sum = from[0];
+#pragma unroll 4
+      for (int s = 1; s < n; ++s) {
+        const float4 v = from[s * slice];
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
       }
+      const int64_t out = l * g.out_l + j * g.out_j + p * g.out_p;  // the four are neighbours there
+      dw_store(a, g.out, out, scale * sum.x);
+      dw_store(a, g.out, out + 1, scale * sum.y);
+      dw_store(a, g.out, out + 2, scale * sum.z);
+      dw_store(a, g.out, out + 3, scale * sum.w);
     }
+    u -= slice;
   }
 }
 
 // ---------------------------------------------------------------- host
-template <int RB>
+template <int VEC>
 static cudaError_t launch_dw(const AdapterGradArgs& a, int sms, cudaStream_t st) {
   static std::atomic<bool> ready[64] = {};
-  const cudaError_t rc = allow_smem(adapter_dw_kernel<RB>, DwCfg<RB>::kAlloc, ready);
+  const cudaError_t rc = allow_smem(adapter_dw_kernel<VEC>, DwCfg<VEC>::kAlloc, ready);
   if (rc != cudaSuccess) return rc;
-  return launch_dependent(adapter_dw_kernel<RB>, dim3(sms), dim3(kDwThreads), DwCfg<RB>::kAlloc, st, a);
+  return launch_dependent(adapter_dw_kernel<VEC>, dim3(sms), dim3(kDwThreads), DwCfg<VEC>::kAlloc, st, a);
 }
 
 // part_values: what the workspace holds of partial sums.
@@ -413,7 +435,11 @@ cudaError_t launch_adapter_grad_tc(AdapterGradArgs& a, int64_t part_values, cuda
   rows = (rows + 63) / 64 * 64;
   a.slice_rows = (int)(rows > a.rows ? a.rows : rows);
   if (a.slice_rows < 1) a.slice_rows = 1;
-  cudaError_t rc = a.R <= 64 ? launch_dw<1>(a, sms, st) : a.R <= 128 ? launch_dw<2>(a, sms, st) : launch_dw<4>(a, sms, st);
+  const cudaError_t rc = a.R <= 16    ? launch_dw<1>(a, sms, st)
+                         : a.R <= 32  ? launch_dw<2>(a, sms, st)
+                         : a.R <= 64  ? launch_dw<4>(a, sms, st)
+                         : a.R <= 128 ? launch_dw<8>(a, sms, st)
+                                      : launch_dw<16>(a, sms, st);
   if (rc != cudaSuccess || a.slice_rows >= a.rows) return rc;
   return launch_dependent(adapter_dw_sum_kernel, dim3(sms * 4), dim3(256), 0, st, a);
 }

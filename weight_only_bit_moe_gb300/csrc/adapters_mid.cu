@@ -11,13 +11,13 @@
 namespace moe {
 
 // A persistent CTA per SM on tcgen05: 128 rows on the MMA's M side, the ranks on its N
-// side, a stage of 64 terms of the sum in 128-byte swizzled lines.  Four loader warps
+// side, a stage of 64 terms of the sum in 128-byte swizzled lines.  Eight loader warps
 // gather the rows (and F) with 16-byte asynchronous copies, which take any order of
 // the rows and leave zeros past the ends; an MMA warp; four epilogue warps.  F enters
 // as it lies: terms innermost (A) or ranks innermost (B^T) through MN-major
 // descriptors.  With few tiles the sum is cut into slices, whose parts of mid the
 // second launch adds in their order.
-constexpr int kMdThreads = 288, kMdLoaders = 128;
+constexpr int kMdThreads = 416, kMdLoaders = 256;  // warps 0-7; 8-11 epilogue, 12 MMA
 
 template <int RB>  // blocks of 64 ranks
 struct MidCfg {
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kMdThreads, 1) adapter_mid_kernel(const __grid
     misc[1] = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == 12) {
     tmem_alloc(&misc[0], columns);
     tmem_relinquish();
   }
@@ -98,10 +98,10 @@ __global__ void __launch_bounds__(kMdThreads, 1) adapter_mid_kernel(const __grid
   const int64_t items = (int64_t)tiles * S;
   if (blockIdx.x == 0 && tid == 0) *a.plan = S;
 
-  if (warp < 4) {
+  if (warp < 8) {
     // ------------------------------------------------------------ loaders
-    const int c = tid & 7, line0 = tid >> 3;               // 16-byte column, first line
-    const uint32_t sw = (uint32_t)((c ^ (line0 & 7)) << 4);  // (lines 16 apart share it)
+    const int c = tid & 7, line0 = tid >> 3;               // 16-byte column, first line (others 32 apart)
+    const uint32_t sw = (uint32_t)((c ^ (line0 & 7)) << 4);  // (lines 32 apart share it)
     const uint16_t* in = static_cast<const uint16_t*>(a.in);
     int filled = 0, signalled = 0;
     Ring<C::kStages> slot, done;
@@ -109,41 +109,41 @@ __global__ void __launch_bounds__(kMdThreads, 1) adapter_mid_kernel(const __grid
     int l = 0;
     for (int64_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
       const MidItem it = mid_item(a, start, (int)w, S, stages, l);
-      const uint16_t* row[8];
-      uint32_t there = 0;
+      const uint16_t* row[4];
+      int there[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int at = line0 + 16 * i;
+      for (int i = 0; i < 4; ++i) {
+        const int at = line0 + 32 * i;
         const int r = at < it.n ? row_of(a.order, a.rows, it.pos + at, a.status) : -1;
-        row[i] = in + (int64_t)max(r, 0) * a.in_ld;
-        there |= (r >= 0 ? 1u : 0u) << i;
+        row[i] = in + (int64_t)max(r, 0) * a.in_ld + 8 * c;
+        there[i] = r >= 0 ? 16 : 0;
       }
-      const uint16_t* f = static_cast<const uint16_t*>(a.f) + it.l * a.f_l;
+      const uint16_t* const f = static_cast<const uint16_t*>(a.f) + it.l * a.f_l;
       for (int t = it.t0; t < it.t1; ++t) {
         if (!mbar_wait(&empty[slot.i], slot.phase ^ 1, abort_flag, a.status)) {
           ok = false;
           break;
         }
         const uint32_t dst = smem_s + slot.i * C::kStageBytes + line0 * 128 + sw;
-        const int p = 64 * t + 8 * c;
-        const int whole = p < a.P ? 16 : 0, q = whole ? p : 0;
+        const bool whole = 64 * t + 8 * c < a.P;
+        const int q = whole ? 64 * t : -8 * c;  // (past the sum's end: the row's start, of which nothing is copied)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cp_async16(dst + i * 2048, row[i] + q, (there >> i) & 1 ? whole : 0);
+        for (int i = 0; i < 4; ++i) cp_async16(dst + i * 4096, row[i] + q, whole ? there[i] : 0);
         if (FWD) {
 #pragma unroll
-          for (int i = 0; i < 4 * RB; ++i) {
-            const int j = line0 + 16 * i;
-            if (j < a.R) cp_async16(dst + 16384 + i * 2048, f + j * a.f_r + q, whole);
+          for (int i = 0; i < 2 * RB; ++i) {
+            const int j = line0 + 32 * i;
+            if (j < a.R) cp_async16(dst + 16384 + i * 4096, f + j * a.f_r + 8 * c + q, whole ? 16 : 0);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int term = 64 * t + line0 + 16 * i;
+          for (int i = 0; i < 2; ++i) {
+            const int term = 64 * t + line0 + 32 * i;
             const uint16_t* line = f + (int64_t)(term < a.P ? term : 0) * a.f_r;
 #pragma unroll
             for (int b = 0; b < RB; ++b)
               if (64 * b + 8 * c < a.R)
-                cp_async16(dst + 16384 + b * 8192 + i * 2048, line + 64 * b + 8 * c, term < a.P ? 16 : 0);
+                cp_async16(dst + 16384 + b * 8192 + i * 4096, line + 64 * b + 8 * c, term < a.P ? 16 : 0);
           }
         }
         cp_async_commit();
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kMdThreads, 1) adapter_mid_kernel(const __grid
       mbar_arrive(&full[done.i]);
       done.next();
     }
-  } else if (warp == 8) {
+  } else if (warp == 12) {
     // ------------------------------------------------------------ MMA
     const uint32_t idesc = idesc_f16_f32(kAtRows, ranks, a.type == kBf16 ? 1u : 0u) | (FWD ? 0u : kIdescMajorB);
     const uint64_t xd0 = smem_desc_sw128(smem_s);
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kMdThreads, 1) adapter_mid_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, columns);
+  if (warp == 12) tmem_dealloc(tmem, columns);
 }
 
 // ---------------------------------------------------------------- host
