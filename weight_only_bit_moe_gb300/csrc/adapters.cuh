@@ -106,6 +106,22 @@ __device__ __forceinline__ void mma_type(float (&d)[4], uint32_t a0, uint32_t a1
   }
 }
 
+// D = A B, nothing added.
+template <int TYPE>
+__device__ __forceinline__ void mma_type_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  if (TYPE == kFp16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // Asynchronous copies of the thread: `bytes` of 16 (the rest zeros), and four at a time.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -130,10 +146,9 @@ __device__ __forceinline__ void plan_adapters(const int32_t* offsets, int rows, 
   for (int i = 0; i < per; ++i) {
     const int l = tid * per + i;
     if (l >= L) break;
-    int i0, i1;
-    adapter_rows(offsets, rows, l, i0, i1);
+    const int i0 = __ldg(offsets + l), i1 = __ldg(offsets + l + 1);
+    bad |= i0 < 0 || i1 < i0 || i1 > rows;
     run += (i1 - i0 + ROWS - 1) / ROWS;
-    bad |= adapter_bad(offsets, rows, l);
   }
   if (__syncthreads_or(bad)) {  // overlapping adapters could make any number of tiles
     if (bad && blockIdx.x == 0) atomicOr(status, kStatusRouting);
@@ -154,10 +169,8 @@ __device__ __forceinline__ void plan_adapters(const int32_t* offsets, int rows, 
   for (int i = 0; i < per; ++i) {
     const int l = tid * per + i;
     if (l >= L) break;
-    int i0, i1;
-    adapter_rows(offsets, rows, l, i0, i1);
     start[l] = pos;
-    pos += (i1 - i0 + ROWS - 1) / ROWS;
+    pos += per == 1 ? run : (__ldg(offsets + l + 1) - __ldg(offsets + l) + ROWS - 1) / ROWS;
     if (l == L - 1) start[L] = pos;
   }
   __syncthreads();

@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(kMdThreads, 1) adapter_mid_kernel(const __grid
     tmem_alloc(&misc[0], columns);
     tmem_relinquish();
   }
-  grid_dependents_launch();
   grid_dependency_wait();
+  grid_dependents_launch();  // (after the wait: the second launch reads operands before its own)
   plan_adapters<kAtRows, kMdThreads>(a.offsets, a.rows, a.L, start, warp_tot, a.status);
   tc_fence_before();
   __syncthreads();

@@ -16,11 +16,15 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t& r0, u
 // Register-fed: a CTA holds 128 rows' mid as MMA operands, high and low 16-bit parts
 // (fp16: of the row divided by a power of two that brings its largest value below
 // 2^14), and walks over columns, 128 at a time.  S passes through shared memory in an
-// order that leaves eight consecutive columns of a row in each lane: base comes
-// straight from memory into the lane that adds to it, and the sum goes straight back,
-// 16 bytes each and 64 of a row by four lanes.  Rows without an adapter are tiles
-// whose sums are zero (none of them where out is base).
-constexpr int kOuThreads = 256, kOuCols = 128;
+// order that leaves eight consecutive columns of a row in each lane: base goes through
+// shared memory, a chunk ahead, to the lane that copied it and adds to it, and the sum
+// goes straight back, 16 bytes each and 64 of a row by four lanes.  Rows without an adapter
+// are tiles whose sums are zero (none of them where out is base).
+//
+// What does not come from the first launch -- the plan, the rows' numbers, the first
+// chunk of S and of base -- is read before that has finished: it starts this one only
+// after its own predecessors are done.
+constexpr int kOuThreads = 256, kOuCols = 128, kOuGroups = kOuCols / 32;
 
 template <int KS>  // steps of 16 ranks, at most
 struct OutCfg {
@@ -29,9 +33,12 @@ struct OutCfg {
   static constexpr int kFwdPitch = (2 * KS + 1) * 16, kGradPitch = kOuCols * 2 + 16;  // odd in 16 bytes
   static constexpr int kSBytes = kOuCols * kFwdPitch > 16 * KS * kGradPitch ? kOuCols * kFwdPitch : 16 * KS * kGradPitch;
   static constexpr int kMidBytes = kRegs ? 0 : 8 * KS * 2 * 512;
-  static constexpr int kAlloc = kBuffers * kSBytes + kMidBytes;
-  static constexpr int kCtas = KS <= 4 ? 2 : 1;
-  static_assert(kCtas * (kAlloc + (kAdAdapters + 1) * 4 + 1024) <= 227 * 1024, "shared memory over the SM's");
+  static constexpr int kBaseBytes = KS <= 8 ? kOuGroups * 2 * kOuThreads * 16 : 0;  // of a chunk (0: read when it is added)
+  static constexpr int kMidAt = kBuffers * kSBytes, kBaseAt = kMidAt + kMidBytes, kStartAt = kBaseAt + 2 * kBaseBytes;
+  static constexpr int kCtas = KS <= 4 ? 2 : 1;  // (with thousands of adapters one: their tiles' numbers come on top)
+  static constexpr int bytes(int adapters) { return kStartAt + (adapters + 1) * 4; }
+  static_assert(kStartAt + (kAdAdapters + 1) * 4 + 64 <= 227 * 1024, "shared memory over the per-CTA limit");
+  static_assert(kCtas * (kStartAt + 4096 + 1024) <= 227 * 1024, "shared memory over the SM's");
 };
 
 struct OutPlan {
@@ -39,19 +46,72 @@ struct OutPlan {
   int rest0, rest1;         // tiles of those
   int chunks, ranges;       // column chunks, cut into ranges
 };
+struct OutItem {
+  bool has;       // an adapter
+  int l, pos, n;
+  int range, c0, c1;
+};
+__device__ __forceinline__ OutItem out_item(const AdapterArgs& a, const OutPlan& pl, const int* start, int64_t w, int& l) {
+  OutItem it;
+  const int tile = (int)(w / pl.ranges);
+  it.range = (int)(w - (int64_t)tile * pl.ranges);
+  it.c0 = (int)((int64_t)it.range * pl.chunks / pl.ranges);
+  it.c1 = (int)((int64_t)(it.range + 1) * pl.chunks / pl.ranges);
+  it.has = tile < pl.tiles;
+  if (it.has) {
+    while (start[l + 1] <= tile) ++l;
+    int i0, i1;
+    adapter_rows(a.offsets, a.rows, l, i0, i1);
+    it.pos = i0 + (tile - start[l]) * kAtRows;
+    it.n = min(kAtRows, i1 - it.pos);
+  } else {
+    const int k = tile - pl.tiles;
+    it.pos = k < pl.rest0 ? k * kAtRows : pl.from + (k - pl.rest0) * kAtRows;
+    it.n = min(kAtRows, (k < pl.rest0 ? pl.before : a.rows) - it.pos);
+  }
+  it.l = l;
+  return it;
+}
+
+// S of a chunk into shared memory, zeros past the last column and rank.
+template <int KS, bool FWD>
+__device__ __forceinline__ void out_fetch(const AdapterArgs& a, const uint16_t* s, int q0, int steps, uint32_t dst) {
+  const int tid = threadIdx.x;
+  if (FWD) {  // two threads to a column, which take its eights of ranks in turn
+    const int q = tid >> 1, c = tid & 1;
+    const int line = (q & ~31) + ((q >> 1) & 3) * 8 + ((q >> 3) & 3) * 2 + (q & 1);
+    const uint16_t* from = s + (int64_t)min(q0 + q, a.Q - 1) * a.s_r + 8 * c;
+    const uint32_t to = dst + line * OutCfg<KS>::kFwdPitch + 16 * c;
+    const bool in = q0 + q < a.Q;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      if (i >= steps) break;
+      const bool have = in && 8 * c + 16 * i < a.R;
+      cp_async16(to + 32 * i, from + (have ? 16 * i : 0), have ? 16 : 0);
+    }
+  } else {  // a thread has a pair of columns of every fourth rank
+    const int v = tid & 63, j = tid >> 6;
+    const bool in = q0 + 2 * v < a.Q;
+    const uint16_t* from = s + (in ? q0 + 2 * v : 0);
+    const uint32_t to = dst + j * OutCfg<KS>::kGradPitch + (v & ~15) * 4 + ((v & 3) * 4 + ((v >> 2) & 3)) * 4;
+#pragma unroll
+    for (int i = 0; i < 4 * KS; ++i) {
+      if (i >= 4 * steps) break;
+      const bool have = in && j + 4 * i < a.R;
+      cp_async4(to + 4 * i * OutCfg<KS>::kGradPitch, from + (have ? (j + 4 * i) * a.s_r : 0), have ? 4 : 0);
+    }
+  }
+}
 
 template <int TYPE, int KS, bool FWD>
 __global__ void __launch_bounds__(kOuThreads, OutCfg<KS>::kCtas) adapter_out_kernel(const __grid_constant__ AdapterArgs a) {
   using C = OutCfg<KS>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ int start[kAdAdapters + 1];
+  int* const start = reinterpret_cast<int*>(smem_raw + C::kStartAt);
   __shared__ int warp_tot[kOuThreads / 32];
   const uint32_t smem_s = smem_u32(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  grid_dependents_launch();
-  grid_dependency_wait();
   plan_adapters<kAtRows, kOuThreads>(a.offsets, a.rows, a.L, start, warp_tot, a.status);
-  const int S = *(volatile int*)a.plan;
   OutPlan pl;
   pl.tiles = start[a.L];
   pl.before = pl.from = pl.rest0 = pl.rest1 = 0;
@@ -73,96 +133,111 @@ __global__ void __launch_bounds__(kOuThreads, OutCfg<KS>::kCtas) adapter_out_ker
     pl.ranges = (int)(__reduce_min_sync(0xffffffffu, cost * 64 + n) & 63);
   }
   const int64_t items = (int64_t)tiles * pl.ranges;
-  const float* part = S == 1 ? a.mid : a.part;
   const int64_t slice = (int64_t)a.rows * a.R;
   const int steps = (a.R + 15) / 16;
-  const uint16_t* base = static_cast<const uint16_t*>(a.base);
-  uint16_t* out = static_cast<uint16_t*>(a.out);
+  const bool added = a.base != nullptr;
+  const float* part = nullptr;
+  int S = 0;  // slices of mid; 0 before the first launch is known to be done
 
   int l = 0;
   for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
-    const int tile = (int)(w / pl.ranges), range = (int)(w - (int64_t)tile * pl.ranges);
-    const int c0 = (int)((int64_t)range * pl.chunks / pl.ranges), c1 = (int)((int64_t)(range + 1) * pl.chunks / pl.ranges);
-    int pos, n;
-    const bool has = tile < pl.tiles;
-    if (has) {
-      while (start[l + 1] <= tile) ++l;
-      int i0, i1;
-      adapter_rows(a.offsets, a.rows, l, i0, i1);
-      pos = i0 + (tile - start[l]) * kAtRows;
-      n = min(kAtRows, i1 - pos);
-    } else {
-      const int k = tile - pl.tiles;
-      pos = k < pl.rest0 ? k * kAtRows : pl.from + (k - pl.rest0) * kAtRows;
-      n = min(kAtRows, (k < pl.rest0 ? pl.before : a.rows) - pos);
-    }
-    const uint16_t* s = static_cast<const uint16_t*>(a.s) + (has ? l * a.s_l : 0);
-
-    // S of a chunk into buffer b
-    auto fetch = [&](int chunk, int b) {
-      if (!has) return;
-      const uint32_t dst = smem_s + b * C::kSBytes;
-      const int q0 = chunk * kOuCols;
-      if (FWD) {
-        for (int u = tid; u < kOuCols * 2 * steps; u += kOuThreads) {
-          const int q = u / (2 * steps), c = u - q * 2 * steps;
-          const int line = (q & ~31) + ((q >> 1) & 3) * 8 + ((q >> 3) & 3) * 2 + (q & 1);
-          const bool in = q0 + q < a.Q && 8 * c < a.R;
-          cp_async16(dst + line * C::kFwdPitch + c * 16, s + (in ? (q0 + q) * a.s_r + 8 * c : 0), in ? 16 : 0);
-        }
-      } else {
-        for (int u = tid; u < 16 * steps * (kOuCols / 2); u += kOuThreads) {
-          const int j = u / (kOuCols / 2), v = u % (kOuCols / 2);
-          const bool in = q0 + 2 * v < a.Q && j < a.R;
-          cp_async4(dst + j * C::kGradPitch + (v & ~15) * 4 + ((v & 3) * 4 + ((v >> 2) & 3)) * 4,
-                    s + (in ? j * a.s_r + q0 + 2 * v : 0), in ? 4 : 0);
-        }
-      }
-    };
+    const OutItem it = out_item(a, pl, start, w, l);
+    const uint16_t* const s = static_cast<const uint16_t*>(a.s) + (it.has ? it.l * a.s_l : 0);
     __syncthreads();  // the last item's reads of S are done
-    if (C::kBuffers == 2) {
-      fetch(c0, 0);
-      cp_async_commit();
-    }
+    if (it.has) out_fetch<KS, FWD>(a, s, it.c0 * kOuCols, steps, smem_s);
 
-    // rows 16 warp + g and + 8 of the tile, and their mid
-    int row[2];
-    float factor[2] = {1.0f, 1.0f};
-    const float* m[2];
-    bool held[2];
+    // rows 16 warp + g and + 8 of the tile
+    const bool work = 16 * warp < it.n;  // of the warp
+    bool ok[2];
+    const uint16_t* from[2];
+    uint16_t* to[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int at = 16 * warp + g + 8 * h;
-      held[h] = at < n;
-      row[h] = held[h] ? row_of(a.order, a.rows, pos + at, a.status) : -1;
-      m[h] = part + (int64_t)(pos + (held[h] ? at : 0)) * a.R;
+      const int row = at < it.n ? row_of(a.order, a.rows, it.pos + at, a.status) : -1;
+      ok[h] = row >= 0;
+      const int64_t q = it.c0 * kOuCols + 8 * t;
+      from[h] = static_cast<const uint16_t*>(a.base) + (added ? (int64_t)max(row, 0) * a.base_ld + q : 0);
+      to[h] = static_cast<uint16_t*>(a.out) + (int64_t)max(row, 0) * a.out_ld + q;
     }
-    auto mid2 = [&](int h, int j) {
-      float2 v = make_float2(0.0f, 0.0f);
-      if (held[h] && j < a.R) {
-        v = *reinterpret_cast<const float2*>(m[h] + j);
-        for (int k = 1; k < S; ++k) {
-          const float2 u = *reinterpret_cast<const float2*>(m[h] + k * slice + j);
-          v.x += u.x;
-          v.y += u.y;
-        }
-        if (S > 1 && a.want_mid && range == 0) *reinterpret_cast<float2*>(a.mid + (int64_t)(pos + 16 * warp + g + 8 * h) * a.R + j) = v;
-      }
-      return v;
+    // base of the chunk that `from` is at, of which `left` columns remain, into buffer b
+    const uint32_t base_s = smem_s + C::kBaseAt + tid * 16;
+    auto fetch_base = [&](int b, int left) {
+#pragma unroll
+      for (int u = 0; u < kOuGroups; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (ok[h] && 32 * u < left) cp_async16(base_s + b * C::kBaseBytes + (2 * u + h) * kOuThreads * 16, from[h] + 32 * u, 16);
     };
+    if (C::kBaseBytes > 0 && added) fetch_base(0, a.Q - it.c0 * kOuCols - 8 * t);
+    cp_async_commit();
+    if (S == 0) {
+      grid_dependency_wait();
+      grid_dependents_launch();
+      S = *(volatile int*)a.plan;
+      part = S == 1 ? a.mid : a.part;
+    }
+
+    float factor[2] = {1.0f, 1.0f};
     uint32_t mh[C::kRegs ? KS : 1][4], ml[C::kRegs ? KS : 1][4];
-    uint4* kept = reinterpret_cast<uint4*>(smem_raw + C::kBuffers * C::kSBytes) + warp * KS * 2 * 32;
-    if (has) {
-      if (TYPE == kFp16) {
-        float top[2] = {0.0f, 0.0f};
-        for (int ks = 0; ks < steps; ++ks)
+    uint4* const kept = reinterpret_cast<uint4*>(smem_raw + C::kMidAt) + warp * KS * 2 * 32;
+    if (it.has && work) {
+      // mid of four steps of ranks from step k0 on, the sum of its slices in their order: x & 1 the row, x >> 1 the
+      // half of a step.  A slice's loads are on their way together.
+      constexpr int kBlock = KS < 4 ? KS : 4;
+      float2 v[kBlock][4];
+      auto load_mid = [&](int k0) {
+        const float* m[2];
+        bool in[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+          in[h] = 16 * warp + g + 8 * h < it.n;
+          m[h] = part + (int64_t)(it.pos + (in[h] ? 16 * warp + g + 8 * h : 0)) * a.R + 16 * k0 + 2 * t;
+        }
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const float2 v = mid2(h, 16 * ks + 8 * o + 2 * t);
-              top[h] = fmaxf(top[h], fmaxf(fabsf(v.x), fabsf(v.y)));
+        for (int k = 0; k < kBlock; ++k)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v[k][x] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+        for (int n = 0; n < S; ++n) {
+          float2 u[kBlock][4];
+#pragma unroll
+          for (int k = 0; k < kBlock; ++k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              u[k][x] = make_float2(0.0f, 0.0f);
+              const int j = 16 * k + 8 * (x >> 1);
+              if (in[x & 1] && 16 * k0 + j < a.R) u[k][x] = *reinterpret_cast<const float2*>(m[x & 1] + j);
             }
+#pragma unroll
+          for (int k = 0; k < kBlock; ++k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[k][x].x += u[k][x].x, v[k][x].y += u[k][x].y;
+          m[0] += slice, m[1] += slice;
+        }
+        if (S > 1 && a.want_mid && it.range == 0) {
+#pragma unroll
+          for (int k = 0; k < kBlock; ++k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int j = 16 * (k0 + k) + 8 * (x >> 1) + 2 * t;
+              if (in[x & 1] && j < a.R)
+                *reinterpret_cast<float2*>(a.mid + (int64_t)(it.pos + 16 * warp + g + 8 * (x & 1)) * a.R + j) = v[k][x];
+            }
+        }
+      };
+      float top[2] = {0.0f, 0.0f};  // fp16: the largest of a row
+      if (C::kRegs || TYPE == kFp16) {
+#pragma unroll 1
+        for (int k0 = 0; k0 < steps; k0 += kBlock) {
+          load_mid(k0);
+#pragma unroll
+          for (int k = 0; k < kBlock; ++k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) top[x & 1] = fmaxf(top[x & 1], fmaxf(fabsf(v[k][x].x), fabsf(v[k][x].y)));
+        }
+      }
+      if (TYPE == kFp16) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
@@ -174,101 +249,123 @@ __global__ void __launch_bounds__(kOuThreads, OutCfg<KS>::kCtas) adapter_out_ker
       }
       const float inv[2] = {1.0f / factor[0], 1.0f / factor[1]};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if (ks >= steps) break;
-        uint32_t hi[4], lo[4];
+      for (int k0 = 0; k0 < KS; k0 += kBlock) {
+        if (k0 >= steps) break;
+        if (!C::kRegs) load_mid(k0);
 #pragma unroll
-        for (int o = 0; o < 2; ++o)
+        for (int k = 0; k < kBlock; ++k) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float2 m = v[k][x];
+            if (TYPE == kFp16) m.x *= inv[x & 1], m.y *= inv[x & 1];
+            split_type<TYPE>(m.x, m.y, hi[x], lo[x]);
+            if (C::kRegs) mh[C::kRegs ? k : 0][x] = hi[x], ml[C::kRegs ? k : 0][x] = lo[x];
+          }
+          if (!C::kRegs) {
+            kept[(2 * (k0 + k)) * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            kept[(2 * (k0 + k) + 1) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+      }
+    }
+    const float scale = it.has ? (a.scale ? __ldg(a.scale + it.l) : 1.0f) : 0.0f;
+    uint64_t mul[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) mul[h] = pack2(__float_as_uint(scale * factor[h]), __float_as_uint(scale * factor[h]));
+
+    for (int chunk = it.c0; chunk < it.c1; ++chunk) {
+      const int b = C::kBuffers == 2 ? (chunk - it.c0) & 1 : 0;
+      const int left = a.Q - chunk * kOuCols - 8 * t;  // columns from the lane's first on
+      cp_async_wait<0>();
+      __syncthreads();  // S of this chunk is there; the other buffer's readers are done
+      const int half = (chunk - it.c0) & 1;
+      if (chunk + 1 < it.c1) {
+        if (C::kBuffers == 2 && it.has) out_fetch<KS, FWD>(a, s, (chunk + 1) * kOuCols, steps, smem_s + (b ^ 1) * C::kSBytes);
+        if (C::kBaseBytes > 0 && added) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) from[h] += kOuCols;
+          fetch_base(half ^ 1, left - kOuCols);
+        }
+        cp_async_commit();
+      }
+      if (work) {
+        const uint32_t buf = smem_s + b * C::kSBytes +
+                             (FWD ? ((lane >> 4) * 8 + (lane & 7)) * C::kFwdPitch + ((lane >> 3) & 1) * 16
+                                  : (lane & 15) * C::kGradPitch + (lane >> 4) * 16);
+#pragma unroll
+        for (int u = 0; u < kOuGroups; ++u) {
+          float acc[4][4];
+          if (it.has) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              if (ks >= steps) break;
+              uint4 hi, lo;
+              if (C::kRegs) {
+                const uint32_t* hp = mh[C::kRegs ? ks : 0];
+                const uint32_t* lp = ml[C::kRegs ? ks : 0];
+                hi = make_uint4(hp[0], hp[1], hp[2], hp[3]);
+                lo = make_uint4(lp[0], lp[1], lp[2], lp[3]);
+              } else {
+                hi = kept[(2 * ks) * 32 + lane];
+                lo = kept[(2 * ks + 1) * 32 + lane];
+              }
+#pragma unroll
+              for (int v = 0; v < 4; v += 2) {
+                uint32_t f0, f1, f2, f3;
+                if (FWD) ldmatrix_x4(buf + (32 * u + 8 * v) * C::kFwdPitch + 32 * ks, f0, f1, f2, f3);
+                else ldmatrix_x4_trans(buf + 16 * ks * C::kGradPitch + 64 * u + 16 * v, f0, f1, f2, f3);
+                if (ks == 0) {
+                  mma_type_first<TYPE>(acc[v], hi.x, hi.y, hi.z, hi.w, f0, f1);
+                  mma_type_first<TYPE>(acc[v + 1], hi.x, hi.y, hi.z, hi.w, f2, f3);
+                } else {
+                  mma_type<TYPE>(acc[v], hi.x, hi.y, hi.z, hi.w, f0, f1);
+                  mma_type<TYPE>(acc[v + 1], hi.x, hi.y, hi.z, hi.w, f2, f3);
+                }
+                mma_type<TYPE>(acc[v], lo.x, lo.y, lo.z, lo.w, f0, f1);
+                mma_type<TYPE>(acc[v + 1], lo.x, lo.y, lo.z, lo.w, f2, f3);
+              }
+            }
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float2 v = mid2(h, 16 * ks + 8 * o + 2 * t);
-            if (TYPE == kFp16) v.x *= inv[h], v.y *= inv[h];
-            split_type<TYPE>(v.x, v.y, hi[2 * o + h], lo[2 * o + h]);
-          }
-        if (C::kRegs) {
+            uint4 o = make_uint4(0, 0, 0, 0);
+            if (added && ok[h] && 32 * u < left)
+              o = C::kBaseBytes > 0 ? lds128(base_s + half * C::kBaseBytes + (2 * u + h) * kOuThreads * 16)
+                                    : *reinterpret_cast<const uint4*>(from[h] + 32 * u);
+            if (it.has) {
+              const uint32_t wd[4] = {o.x, o.y, o.z, o.w};
+              uint32_t r[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mh[C::kRegs ? ks : 0][u] = hi[u], ml[C::kRegs ? ks : 0][u] = lo[u];
-        } else {
-          kept[(2 * ks) * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          kept[(2 * ks + 1) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-    }
-    const float scale = has ? (a.scale ? a.scale[l] : 1.0f) : 0.0f;
-    const float mul[2] = {scale * factor[0], scale * factor[1]};
-
-    for (int chunk = c0; chunk < c1; ++chunk) {
-      const int b = C::kBuffers == 2 ? (chunk - c0) & 1 : 0;
-      const int q0 = chunk * kOuCols + 8 * t;
-      uint4 was[kOuCols / 32][2];
-#pragma unroll
-      for (int u = 0; u < kOuCols / 32; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int q = q0 + 32 * u;
-          was[u][h] = base && row[h] >= 0 && q < a.Q ? *reinterpret_cast<const uint4*>(base + (int64_t)row[h] * a.base_ld + q)
-                                                     : make_uint4(0, 0, 0, 0);
-        }
-      if (C::kBuffers == 2) {
-        if (chunk + 1 < c1) fetch(chunk + 1, b ^ 1);
-        cp_async_commit();
-        cp_async_wait<1>();
-      } else {
-        fetch(chunk, 0);
-        cp_async_commit();
-        cp_async_wait<0>();
-      }
-      __syncthreads();
-      const uint32_t buf = smem_s + b * C::kSBytes;
-#pragma unroll
-      for (int u = 0; u < kOuCols / 32; ++u) {
-        float acc[4][4] = {};
-        if (has) {
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            if (ks >= steps) break;
-            uint4 hi, lo;
-            if (C::kRegs) {
-              const uint32_t* hp = mh[C::kRegs ? ks : 0];
-              const uint32_t* lp = ml[C::kRegs ? ks : 0];
-              hi = make_uint4(hp[0], hp[1], hp[2], hp[3]);
-              lo = make_uint4(lp[0], lp[1], lp[2], lp[3]);
-            } else {
-              hi = kept[(2 * ks) * 32 + lane];
-              lo = kept[(2 * ks + 1) * 32 + lane];
+              for (int v = 0; v < 4; ++v) {
+                const float2 f = unpack_type<TYPE>(wd[v]);
+                uint64_t sum = pack2(__float_as_uint(f.x), __float_as_uint(f.y));
+                fma2(sum, pack2(__float_as_uint(acc[v][2 * h]), __float_as_uint(acc[v][2 * h + 1])), mul[h]);
+                uint32_t x, y;
+                unpack2(sum, x, y);
+                r[v] = pack_type<TYPE>(__uint_as_float(x), __uint_as_float(y));
+              }
+              o = make_uint4(r[0], r[1], r[2], r[3]);
             }
-#pragma unroll
-            for (int v = 0; v < 4; v += 2) {
-              uint32_t f0, f1, f2, f3;
-              if (FWD)
-                ldmatrix_x4(buf + (32 * u + (v + (lane >> 4)) * 8 + (lane & 7)) * C::kFwdPitch + (2 * ks + ((lane >> 3) & 1)) * 16,
-                            f0, f1, f2, f3);
-              else
-                ldmatrix_x4_trans(buf + (16 * ks + (lane & 15)) * C::kGradPitch + 64 * u + (v + (lane >> 4)) * 16, f0, f1, f2, f3);
-              mma_type<TYPE>(acc[v], hi.x, hi.y, hi.z, hi.w, f0, f1);
-              mma_type<TYPE>(acc[v + 1], hi.x, hi.y, hi.z, hi.w, f2, f3);
-              mma_type<TYPE>(acc[v], lo.x, lo.y, lo.z, lo.w, f0, f1);
-              mma_type<TYPE>(acc[v + 1], lo.x, lo.y, lo.z, lo.w, f2, f3);
-            }
+            if (ok[h] && 32 * u < left) *reinterpret_cast<uint4*>(to[h] + 32 * u) = o;
           }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int q = q0 + 32 * u;
-          if (row[h] < 0 || q >= a.Q) continue;
-          const uint32_t wd[4] = {was[u][h].x, was[u][h].y, was[u][h].z, was[u][h].w};
-          uint32_t o[4];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float2 f = unpack_type<TYPE>(wd[v]);
-            o[v] = has ? pack_type<TYPE>(fmaf(mul[h], acc[v][2 * h], f.x), fmaf(mul[h], acc[v][2 * h + 1], f.y)) : wd[v];
-          }
-          *reinterpret_cast<uint4*>(out + (int64_t)row[h] * a.out_ld + q) = make_uint4(o[0], o[1], o[2], o[3]);
+          if (C::kBaseBytes == 0 && added) from[h] += kOuCols;
+          to[h] += kOuCols;
         }
       }
-      __syncthreads();  // before the buffer is filled again
+      if (C::kBuffers == 1 && it.has && chunk + 1 < it.c1) {
+        __syncthreads();
+        out_fetch<KS, FWD>(a, s, (chunk + 1) * kOuCols, steps, smem_s);
+        cp_async_commit();
+      }
     }
-    cp_async_wait<0>();
+  }
+  if (S == 0) {
+    grid_dependency_wait();
+    grid_dependents_launch();
   }
 }
 
@@ -276,9 +373,9 @@ template <int TYPE, int KS, bool FWD>
 static cudaError_t launch_out(const AdapterArgs& a, int sms, cudaStream_t st) {
   static std::atomic<bool> ready[64] = {};
   using C = OutCfg<KS>;
-  const cudaError_t rc = allow_smem(adapter_out_kernel<TYPE, KS, FWD>, C::kAlloc, ready);
+  const cudaError_t rc = allow_smem(adapter_out_kernel<TYPE, KS, FWD>, C::bytes(kAdAdapters), ready);
   if (rc != cudaSuccess) return rc;
-  return launch_dependent(adapter_out_kernel<TYPE, KS, FWD>, dim3(sms * C::kCtas), dim3(kOuThreads), C::kAlloc, st, a);
+  return launch_dependent(adapter_out_kernel<TYPE, KS, FWD>, dim3(sms * C::kCtas), dim3(kOuThreads), C::bytes(a.L), st, a);
 }
 
 template <int TYPE, bool FWD>
