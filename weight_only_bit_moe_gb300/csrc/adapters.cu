@@ -27,20 +27,20 @@ static bool on_grid(const AdapterArgs& a, const float* mid) {
          (!a.out || (grid16(a.out, a.out_ld) && (!a.base || grid16(a.base, a.base_ld))));
 }
 
-// The workspace behind its head: the plan, mid where the caller keeps none, slices of mid.
-constexpr int64_t kAdMidAt = MOE_PRODUCTS_WORKSPACE_HEAD_BYTES + 256, kAdPartAt = kAdMidAt + MOE_ADAPTER_MID_VALUES * 4;
+// The workspace behind its head: mid where the caller keeps none, parts of mid.
+constexpr int64_t kAdMidAt = MOE_PRODUCTS_WORKSPACE_HEAD_BYTES, kAdPartAt = kAdMidAt + MOE_ADAPTER_MID_VALUES * 4;
 constexpr int64_t kAdPartValues = (MOE_PRODUCTS_WORKSPACE_BYTES - kAdPartAt) / 4;
 
 static int run(AdapterArgs& a, bool fwd, float* mid, uint8_t* workspace, void* stream) {
   const cudaStream_t st = (cudaStream_t)stream;
   a.mid = mid ? mid : reinterpret_cast<float*>(workspace + kAdMidAt);
   a.part = reinterpret_cast<float*>(workspace + kAdPartAt);
-  a.plan = reinterpret_cast<int*>(workspace + MOE_PRODUCTS_WORKSPACE_HEAD_BYTES);
   cudaError_t rc;
   if (on_grid(a, mid)) {
     const int64_t room = kAdPartValues / ((int64_t)a.rows * a.R);
     a.slices = (int)(room < 1 ? 1 : room > 32 ? 32 : room);
-    rc = fwd && a.rows <= kAdFewRows ? launch_adapter_few(a, mid != nullptr, st) : launch_adapter_tc(a, fwd, mid != nullptr, st);
+    rc = fwd && a.rows <= kAdFewRows ? launch_adapter_few(a, mid != nullptr, st)
+                                     : launch_adapter_tc(a, fwd, mid != nullptr, kAdPartValues, st);
   } else {
     rc = launch_adapter_any(a, fwd, st);
     if (rc == cudaSuccess && a.out && a.base != a.out) rc = launch_adapter_rest(a, st);

@@ -28,9 +28,9 @@ struct AdapterArgs {
   void* out;
   int64_t out_ld;
   float* mid;                // [rows, R]
-  float* part;               // partial sums of mid, [slices, rows, R]
-  int* plan;                 // device: the slices that the first product was cut into
-  int slices;                // at most (few rows: exactly)
+  float* part;               // partial sums of mid
+  int slices;                // few rows: of mid, [slices, rows, R]
+  int mid_ctas;              // many rows: CTAs of the first launch; 0: they take whole tiles
   int want_mid;              // mid is the caller's
   unsigned* status;
 };
@@ -178,6 +178,19 @@ __device__ __forceinline__ void plan_adapters(const int32_t* offsets, int rows, 
 
 constexpr int kAtRows = 128;  // positions of a tile
 
+// The first product's work on many rows, in units of a tile's stage of 64 terms, laid end to end and cut evenly: CTA b
+// of `ctas` has the units from b units / ctas on.  A tile that one CTA has whole goes to mid, the parts of others to
+// part, where CTA b's of tile t is at (b + t) [128, R]: going through the units either b or t moves on by one.
+struct MidSplit {
+  int stages, ctas;
+  int64_t units;
+  __device__ __forceinline__ MidSplit(const AdapterArgs& a, int tiles) : stages((a.P + 63) / 64), units((int64_t)tiles * stages) {
+    ctas = (int)max((int64_t)1, min((int64_t)a.mid_ctas, units / 4));  // (four stages at least)
+  }
+  __device__ __forceinline__ int64_t begin(int b) const { return units * b / ctas; }
+  __device__ __forceinline__ int owner(int64_t unit) const { return (int)(((unit + 1) * ctas + units - 1) / units) - 1; }
+};
+
 // Four MMAs of 16 terms of one CTA; the descriptors advance by DA and DB (16-byte units) a step.
 template <int DA, int DB>
 __device__ __forceinline__ void umma1_f16_stage_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -223,7 +236,8 @@ cudaError_t launch_adapter_rest(const AdapterArgs& a, cudaStream_t st);
 // Operands on the 16-byte grid: up to kAdFewRows rows of the forward product, and any number of both.
 constexpr int kAdFewRows = 256;
 cudaError_t launch_adapter_few(AdapterArgs& a, bool mid_wanted, cudaStream_t st);
-cudaError_t launch_adapter_tc(AdapterArgs& a, bool fwd, bool mid_wanted, cudaStream_t st);
+// part_values: what a.part holds.
+cudaError_t launch_adapter_tc(AdapterArgs& a, bool fwd, bool mid_wanted, int64_t part_values, cudaStream_t st);
 cudaError_t launch_adapter_out_fwd(const AdapterArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_adapter_out_dx(const AdapterArgs& a, int sms, cudaStream_t st);
 

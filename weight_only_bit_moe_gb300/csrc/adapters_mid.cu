@@ -15,8 +15,8 @@ namespace moe {
 // gather the rows (and F) with 16-byte asynchronous copies, which take any order of
 // the rows and leave zeros past the ends; an MMA warp; four epilogue warps.  F enters
 // as it lies: terms innermost (A) or ranks innermost (B^T) through MN-major
-// descriptors.  With few tiles the sum is cut into slices, whose parts of mid the
-// second launch adds in their order.
+// descriptors.  The tiles' stages are cut evenly over the CTAs; what several CTAs have
+// of a tile the second launch adds in their order.
 constexpr int kMdThreads = 416, kMdLoaders = 256;  // warps 0-7; 8-11 epilogue, 12 MMA
 
 template <int RB>  // blocks of 64 ranks
@@ -30,38 +30,45 @@ struct MidCfg {
   static_assert(kAlloc + (kAdAdapters + 1) * 4 + 512 <= 227 * 1024, "shared memory over the per-CTA limit");
 };
 
+// A role's position among the CTA's pieces of tiles.
 struct MidItem {
   int l, pos, n;  // adapter, first position, rows
   int t0, t1;     // stages
-  int split;
+  float* out;     // of the first row
 };
-
-// Item w = tile * S + slice; items are walked in ascending order, l goes on from the last one's.
-__device__ __forceinline__ MidItem mid_item(const AdapterArgs& a, const int* start, int w, int S, int stages, int& l) {
-  MidItem it;
-  const int tile = w / S;
-  it.split = w - tile * S;
-  while (start[l + 1] <= tile) ++l;
-  it.l = l;
-  int i0, i1;
-  adapter_rows(a.offsets, a.rows, l, i0, i1);
-  it.pos = i0 + (tile - start[l]) * kAtRows;
-  it.n = min(kAtRows, i1 - it.pos);
-  it.t0 = (int)((int64_t)it.split * stages / S);
-  it.t1 = (int)((int64_t)(it.split + 1) * stages / S);
-  return it;
-}
-
-// Slices of the sum: the number that minimises rounds * (stages of a slice + 4) + 2 S, in stages; a lane per number.
-__device__ __forceinline__ int mid_slices(int tiles, int stages, int ctas, int most) {
-  const int s = (threadIdx.x & 31) + 1;
-  uint32_t cost = 0xFFFFFFu;
-  if (s <= most && s <= stages) {
-    const int64_t rounds = ((int64_t)tiles * s + ctas - 1) / ctas;
-    cost = (uint32_t)min((int64_t)0xFFFFFF, rounds * ((stages + s - 1) / s + 4) + (s > 1 ? 2 * s : 0));
+struct MidWalk {
+  const AdapterArgs& a;
+  const int* start;
+  MidSplit split;
+  int64_t unit, end;
+  int l = 0;
+  __device__ __forceinline__ MidWalk(const AdapterArgs& a_, const int* start_, int tiles)
+      : a(a_), start(start_), split(a_, tiles) {
+    if (a.mid_ctas > 0) {
+      unit = (int)blockIdx.x < split.ctas ? split.begin(blockIdx.x) : 0;
+      end = (int)blockIdx.x < split.ctas ? split.begin(blockIdx.x + 1) : 0;
+    } else {  // whole tiles, spread evenly
+      unit = (int64_t)tiles * blockIdx.x / gridDim.x * split.stages;
+      end = (int64_t)tiles * (blockIdx.x + 1) / gridDim.x * split.stages;
+    }
   }
-  return (int)(__reduce_min_sync(0xffffffffu, cost * 64 + s) & 63);
-}
+  __device__ __forceinline__ bool next(MidItem& it) {
+    if (unit >= end) return false;
+    const int tile = (int)(unit / split.stages);
+    while (start[l + 1] <= tile) ++l;
+    it.l = l;
+    int i0, i1;
+    adapter_rows(a.offsets, a.rows, l, i0, i1);
+    it.pos = i0 + (tile - start[l]) * kAtRows;
+    it.n = min(kAtRows, i1 - it.pos);
+    it.t0 = (int)(unit - (int64_t)tile * split.stages);
+    it.t1 = (int)min((int64_t)split.stages, it.t0 + end - unit);
+    unit += it.t1 - it.t0;
+    it.out = it.t1 - it.t0 == split.stages ? a.mid + (int64_t)it.pos * a.R
+                                           : a.part + (int64_t)(blockIdx.x + tile) * kAtRows * a.R;
+    return true;
+  }
+};
 
 template <int RB, bool FWD>
 __global__ void __launch_bounds__(kMdThreads, 1) adapter_mid_kernel(const __grid_constant__ AdapterArgs a) {
@@ -93,10 +100,7 @@ __global__ void __launch_bounds__(kMdThreads, 1) adapter_mid_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  const int stages = (a.P + 63) / 64, tiles = start[a.L];
-  const int S = mid_slices(tiles, stages, gridDim.x, a.slices);
-  const int64_t items = (int64_t)tiles * S;
-  if (blockIdx.x == 0 && tid == 0) *a.plan = S;
+  const int tiles = start[a.L];
 
   if (warp < 8) {
     // ------------------------------------------------------------ loaders
@@ -106,15 +110,14 @@ __global__ void __launch_bounds__(kMdThreads, 1) adapter_mid_kernel(const __grid
     int filled = 0, signalled = 0;
     Ring<C::kStages> slot, done;
     bool ok = true;
-    int l = 0;
-    for (int64_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
-      const MidItem it = mid_item(a, start, (int)w, S, stages, l);
+    MidItem it;
+    for (MidWalk at(a, start, tiles); ok && at.next(it);) {
       const uint16_t* row[4];
       int there[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int at = line0 + 32 * i;
-        const int r = at < it.n ? row_of(a.order, a.rows, it.pos + at, a.status) : -1;
+        const int n = line0 + 32 * i;
+        const int r = n < it.n ? row_of(a.order, a.rows, it.pos + n, a.status) : -1;
         row[i] = in + (int64_t)max(r, 0) * a.in_ld + 8 * c;
         there[i] = r >= 0 ? 16 : 0;
       }
@@ -171,16 +174,15 @@ __global__ void __launch_bounds__(kMdThreads, 1) adapter_mid_kernel(const __grid
     Ring<C::kStages> slot;
     Ring<2> acc;
     bool ok = true;
-    int l = 0;
-    for (int64_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
-      const MidItem it = mid_item(a, start, (int)w, S, stages, l);
+    MidItem it;
+    for (MidWalk at(a, start, tiles); ok && at.next(it);) {
       if (!warp_wait(&acc_empty[acc.i], acc.phase ^ 1, abort_flag, a.status)) break;
       tc_fence_after();
       for (int t = it.t0; t < it.t1; ++t) {
         if (!(ok = warp_wait(&full[slot.i], slot.phase, abort_flag, a.status))) break;
         tc_fence_after();
-        const uint32_t at = slot.i * (C::kStageBytes >> 4);
-        umma1_f16_stage_elect<2, FWD ? 2 : 128>(tmem + acc.i * ranks, xd0 + at, fd0 + at, idesc, t > it.t0 ? 1u : 0u);
+        const uint32_t by = slot.i * (C::kStageBytes >> 4);
+        umma1_f16_stage_elect<2, FWD ? 2 : 128>(tmem + acc.i * ranks, xd0 + by, fd0 + by, idesc, t > it.t0 ? 1u : 0u);
         umma_commit_elect(&empty[slot.i]);
         slot.next();
       }
@@ -193,13 +195,12 @@ __global__ void __launch_bounds__(kMdThreads, 1) adapter_mid_kernel(const __grid
   } else {
     // ------------------------------------------------------------ epilogue: a row to a thread
     Ring<2> acc;
-    int l = 0;
-    for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
-      const MidItem it = mid_item(a, start, (int)w, S, stages, l);
+    MidItem it;
+    for (MidWalk walk(a, start, tiles); walk.next(it);) {
       if (!warp_wait(&acc_full[acc.i], acc.phase, abort_flag, a.status)) break;
       tc_fence_after();
       const int at = (warp & 3) * 32 + lane;
-      float* out = (S == 1 ? a.mid : a.part + (int64_t)it.split * a.rows * a.R) + (int64_t)(it.pos + at) * a.R;
+      float* out = it.out + (int64_t)at * a.R;
       const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc.i * ranks;
       for (int j = 0; j < a.R; j += 16) {
         uint32_t v[16];
@@ -238,11 +239,13 @@ static cudaError_t launch_mid(const AdapterArgs& a, int sms, cudaStream_t st) {
   return a.R <= 64 ? launch_mid<1, FWD>(a, sms, st) : a.R <= 128 ? launch_mid<2, FWD>(a, sms, st) : launch_mid<4, FWD>(a, sms, st);
 }
 
-cudaError_t launch_adapter_tc(AdapterArgs& a, bool fwd, bool mid_wanted, cudaStream_t st) {
+cudaError_t launch_adapter_tc(AdapterArgs& a, bool fwd, bool mid_wanted, int64_t part_values, cudaStream_t st) {
   const int sms = prod_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   a.want_mid = mid_wanted;
-  if (!a.out) a.slices = 1;
+  // parts of tiles, where they are added up and the workspace holds them
+  const int64_t tiles = (int64_t)a.rows / kAtRows + a.L;
+  a.mid_ctas = a.out && (sms + tiles) * kAtRows * a.R <= part_values ? sms : 0;
   const cudaError_t rc = fwd ? launch_mid<true>(a, sms, st) : launch_mid<false>(a, sms, st);
   if (rc != cudaSuccess || !a.out) return rc;
   return fwd ? launch_adapter_out_fwd(a, sms, st) : launch_adapter_out_dx(a, sms, st);

@@ -44,26 +44,39 @@ struct OutCfg {
 struct OutPlan {
   int tiles, before, from;  // tiles of adapters; positions [0, before) and [from, rows) have none
   int rest0, rest1;         // tiles of those
-  int chunks, ranges;       // column chunks, cut into ranges
+  int chunks;               // of columns
 };
 struct OutItem {
   bool has;       // an adapter
   int l, pos, n;
-  int range, c0, c1;
+  int c0, c1;     // chunks
+  int parts;      // of mid: 1 where it lies in mid
+  const float* mid;
+  int64_t step;   // from one part to the next
 };
-__device__ __forceinline__ OutItem out_item(const AdapterArgs& a, const OutPlan& pl, const int* start, int64_t w, int& l) {
+// The piece of a tile from unit on; l: the adapter of the last one, or 0.
+__device__ __forceinline__ OutItem out_item(const AdapterArgs& a, const OutPlan& pl, const MidSplit& split, const int* start,
+                                            int64_t unit, int64_t end, int& l) {
   OutItem it;
-  const int tile = (int)(w / pl.ranges);
-  it.range = (int)(w - (int64_t)tile * pl.ranges);
-  it.c0 = (int)((int64_t)it.range * pl.chunks / pl.ranges);
-  it.c1 = (int)((int64_t)(it.range + 1) * pl.chunks / pl.ranges);
+  const int tile = (int)(unit / pl.chunks);
+  it.c0 = (int)(unit - (int64_t)tile * pl.chunks);
+  it.c1 = (int)min((int64_t)pl.chunks, it.c0 + end - unit);
   it.has = tile < pl.tiles;
+  it.parts = 0;
   if (it.has) {
     while (start[l + 1] <= tile) ++l;
     int i0, i1;
     adapter_rows(a.offsets, a.rows, l, i0, i1);
     it.pos = i0 + (tile - start[l]) * kAtRows;
     it.n = min(kAtRows, i1 - it.pos);
+    int first = 0, last = 0;
+    if (a.mid_ctas > 0) {
+      first = split.owner((int64_t)tile * split.stages);
+      last = split.owner((int64_t)(tile + 1) * split.stages - 1);
+    }
+    it.parts = last - first + 1;
+    it.mid = it.parts == 1 ? a.mid + (int64_t)it.pos * a.R : a.part + (int64_t)(first + tile) * kAtRows * a.R;
+    it.step = (int64_t)kAtRows * a.R;
   } else {
     const int k = tile - pl.tiles;
     it.pos = k < pl.rest0 ? k * kAtRows : pl.from + (k - pl.rest0) * kAtRows;
@@ -122,26 +135,18 @@ __global__ void __launch_bounds__(kOuThreads, OutCfg<KS>::kCtas) adapter_out_ker
     pl.rest1 = (a.rows - pl.from + kAtRows - 1) / kAtRows;
   }
   pl.chunks = (a.Q + kOuCols - 1) / kOuCols;
-  const int tiles = pl.tiles + pl.rest0 + pl.rest1;
-  {  // ranges of columns to a tile: the number that minimises rounds * (chunks of a range + 2), a lane per number
-    const int n = lane + 1;
-    uint32_t cost = 0xFFFFFFu;
-    if (n <= pl.chunks) {
-      const int64_t rounds = ((int64_t)tiles * n + gridDim.x - 1) / gridDim.x;
-      cost = (uint32_t)min((int64_t)0xFFFFFF, rounds * ((pl.chunks + n - 1) / n + 2));
-    }
-    pl.ranges = (int)(__reduce_min_sync(0xffffffffu, cost * 64 + n) & 63);
-  }
-  const int64_t items = (int64_t)tiles * pl.ranges;
-  const int64_t slice = (int64_t)a.rows * a.R;
+  // units of a tile's chunk, cut evenly over the CTAs
+  const MidSplit split(a, pl.tiles);
+  const int64_t units = (int64_t)(pl.tiles + pl.rest0 + pl.rest1) * pl.chunks;
+  int64_t unit = units * blockIdx.x / gridDim.x;
+  const int64_t end = units * (blockIdx.x + 1) / gridDim.x;
   const int steps = (a.R + 15) / 16;
   const bool added = a.base != nullptr;
-  const float* part = nullptr;
-  int S = 0;  // slices of mid; 0 before the first launch is known to be done
+  bool done = false;  // the first launch
 
-  int l = 0;
-  for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
-    const OutItem it = out_item(a, pl, start, w, l);
+  for (int l = 0; unit < end;) {
+    const OutItem it = out_item(a, pl, split, start, unit, end, l);
+    unit += it.c1 - it.c0;
     const uint16_t* const s = static_cast<const uint16_t*>(a.s) + (it.has ? it.l * a.s_l : 0);
     __syncthreads();  // the last item's reads of S are done
     if (it.has) out_fetch<KS, FWD>(a, s, it.c0 * kOuCols, steps, smem_s);
@@ -171,35 +176,34 @@ __global__ void __launch_bounds__(kOuThreads, OutCfg<KS>::kCtas) adapter_out_ker
     };
     if (C::kBaseBytes > 0 && added) fetch_base(0, a.Q - it.c0 * kOuCols - 8 * t);
     cp_async_commit();
-    if (S == 0) {
+    if (!done) {
       grid_dependency_wait();
       grid_dependents_launch();
-      S = *(volatile int*)a.plan;
-      part = S == 1 ? a.mid : a.part;
+      done = true;
     }
 
     float factor[2] = {1.0f, 1.0f};
     uint32_t mh[C::kRegs ? KS : 1][4], ml[C::kRegs ? KS : 1][4];
     uint4* const kept = reinterpret_cast<uint4*>(smem_raw + C::kMidAt) + warp * KS * 2 * 32;
     if (it.has && work) {
-      // mid of four steps of ranks from step k0 on, the sum of its slices in their order: x & 1 the row, x >> 1 the
-      // half of a step.  A slice's loads are on their way together.
-      constexpr int kBlock = KS < 4 ? KS : 4;
+      // mid of two steps of ranks from step k0 on, the sum of its parts in their order: x & 1 the row, x >> 1 the
+      // half of a step.  A part's loads are on their way together.
+      constexpr int kBlock = KS < 2 ? KS : 2;  // (four spill, and what spills comes back from L2)
       float2 v[kBlock][4];
-      auto load_mid = [&](int k0) {
+      auto load_mid = [&](int k0, bool keep) {
         const float* m[2];
         bool in[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           in[h] = 16 * warp + g + 8 * h < it.n;
-          m[h] = part + (int64_t)(it.pos + (in[h] ? 16 * warp + g + 8 * h : 0)) * a.R + 16 * k0 + 2 * t;
+          m[h] = it.mid + (int64_t)(in[h] ? 16 * warp + g + 8 * h : 0) * a.R + 16 * k0 + 2 * t;
         }
 #pragma unroll
         for (int k = 0; k < kBlock; ++k)
 #pragma unroll
           for (int x = 0; x < 4; ++x) v[k][x] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
-        for (int n = 0; n < S; ++n) {
+        for (int n = 0; n < it.parts; ++n) {
           float2 u[kBlock][4];
 #pragma unroll
           for (int k = 0; k < kBlock; ++k)
@@ -213,9 +217,9 @@ __global__ void __launch_bounds__(kOuThreads, OutCfg<KS>::kCtas) adapter_out_ker
           for (int k = 0; k < kBlock; ++k)
 #pragma unroll
             for (int x = 0; x < 4; ++x) v[k][x].x += u[k][x].x, v[k][x].y += u[k][x].y;
-          m[0] += slice, m[1] += slice;
+          m[0] += it.step, m[1] += it.step;
         }
-        if (S > 1 && a.want_mid && it.range == 0) {
+        if (keep && it.parts > 1 && a.want_mid && it.c0 == 0) {
 #pragma unroll
           for (int k = 0; k < kBlock; ++k)
 #pragma unroll
@@ -226,11 +230,11 @@ __global__ void __launch_bounds__(kOuThreads, OutCfg<KS>::kCtas) adapter_out_ker
             }
         }
       };
-      float top[2] = {0.0f, 0.0f};  // fp16: the largest of a row
-      if (C::kRegs || TYPE == kFp16) {
+      float top[2] = {0.0f, 0.0f};  // fp16: the largest of a row, by reading it once more
+      if (TYPE == kFp16) {
 #pragma unroll 1
         for (int k0 = 0; k0 < steps; k0 += kBlock) {
-          load_mid(k0);
+          load_mid(k0, false);
 #pragma unroll
           for (int k = 0; k < kBlock; ++k)
 #pragma unroll
@@ -251,7 +255,7 @@ __global__ void __launch_bounds__(kOuThreads, OutCfg<KS>::kCtas) adapter_out_ker
 #pragma unroll
       for (int k0 = 0; k0 < KS; k0 += kBlock) {
         if (k0 >= steps) break;
-        if (!C::kRegs) load_mid(k0);
+        load_mid(k0, true);
 #pragma unroll
         for (int k = 0; k < kBlock; ++k) {
           uint32_t hi[4], lo[4];
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(kOuThreads, OutCfg<KS>::kCtas) adapter_out_ker
             float2 m = v[k][x];
             if (TYPE == kFp16) m.x *= inv[x & 1], m.y *= inv[x & 1];
             split_type<TYPE>(m.x, m.y, hi[x], lo[x]);
-            if (C::kRegs) mh[C::kRegs ? k : 0][x] = hi[x], ml[C::kRegs ? k : 0][x] = lo[x];
+            if (C::kRegs) mh[C::kRegs ? k0 + k : 0][x] = hi[x], ml[C::kRegs ? k0 + k : 0][x] = lo[x];
           }
           if (!C::kRegs) {
             kept[(2 * (k0 + k)) * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(kOuThreads, OutCfg<KS>::kCtas) adapter_out_ker
       }
     }
   }
-  if (S == 0) {
+  if (!done) {
     grid_dependency_wait();
     grid_dependents_launch();
   }
