@@ -122,8 +122,9 @@ extern "C" int moe_adapter_mm_dw(int dtype, const void* dy, int64_t dy_stride, c
   if (rows > 0 && da && (!x || !mid_dy || !on_elements(x, 2) || !on_elements(mid_dy, 4))) return MOE_ERR_INVALID;
   if (rows > 0 && db && (!dy || !mid_x || !on_elements(dy, 2) || !on_elements(mid_x, 4))) return MOE_ERR_INVALID;
   AdapterGradArgs g{};
-  g.side[0] = {da ? x : nullptr, x_stride, mid_dy, K, da, da_stride_l, da_stride_r, 1, 0};
-  g.side[1] = {db ? dy : nullptr, dy_stride, mid_x, N, db, db_stride_l, 1, db_stride_n, 0};
+  g.side[0] = {da ? x : nullptr, x_stride, mid_dy, K, da, da_stride_l, da_stride_r, 1, 0, 0};
+  g.side[1] = {db ? dy : nullptr, dy_stride, mid_x, N, db, db_stride_l, 1, db_stride_n, 0,
+               (reinterpret_cast<uintptr_t>(db) & 15) == 0 && db_stride_l % 8 == 0 && db_stride_n % 8 == 0};
   g.offsets = offsets, g.order = order, g.scale = scale;
   g.L = num_adapters, g.rows = rows, g.R = rank, g.type = dtype, g.out_type = grad_dtype, g.accumulate = accumulate;
   g.status = static_cast<unsigned*>(workspace);

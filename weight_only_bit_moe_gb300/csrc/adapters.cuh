@@ -44,6 +44,7 @@ struct AdapterGradSide {
   void* out;
   int64_t out_l, out_j, out_p;  // strides
   int tiles;                 // of columns p
+  int vec;                   // dB: rows of eight ranks can be written 16 bytes at a time
 };
 struct AdapterGradArgs {
   AdapterGradSide side[2];

@@ -13,6 +13,8 @@
 // of p of both sides in one launch.  An adapter of one slice is written at once; the
 // slices of others go to the workspace, and a second launch adds them in their order,
 // so the same inputs give the same bits.
+#include <type_traits>
+
 #include "adapters.cuh"
 
 namespace moe {
@@ -23,7 +25,7 @@ constexpr int kDwCols = 128;
 template <int VEC>  // float4 of a stage's mid to a converter: ceil(R / 16)
 struct DwCfg {
   static constexpr int RB = (VEC + 3) / 4;  // blocks of 64 ranks
-  static constexpr int kAhead = VEC == 1 ? 8 : 16 / VEC;  // stages of mid on their way in registers
+  static constexpr int kAhead = VEC <= 8 ? 8 / VEC : 1;  // stages of mid on their way in registers
   static constexpr int kStages = RB == 1 ? 6 : RB == 2 ? 4 : 2;
   static constexpr int kLag = RB == 1 ? 4 : RB == 2 ? 3 : 1;
   static constexpr int kMidBytes = RB * 8192;  // of one part
@@ -113,6 +115,62 @@ __device__ __forceinline__ DwItem dw_item(const AdapterGradArgs& a, const int* s
 __device__ __forceinline__ void dw_store(const AdapterGradArgs& a, void* out, int64_t at, float v) {
   if (a.accumulate) v += static_cast<const float*>(out)[at];
   store_elem(out, at, a.out_type, v);
+}
+
+// Sixteen ranks, of which `left` are there, of a column: `step` elements apart, from `at` on.  Their types and places
+// are told apart once for the sixteen (a value at a time took four fifths of the kernel's time).
+template <int OUT, bool ADD>
+__device__ __forceinline__ void dw_put(void* out, int64_t at, int64_t step, const uint32_t (&v)[16], float mul, int left) {
+  using T = typename std::conditional<OUT == kFp32, float, uint16_t>::type;
+  T* p = static_cast<T*>(out) + at;
+  float was[16];
+  if (ADD) {
+#pragma unroll
+    for (int u = 0; u < 16; ++u) was[u] = u < left ? static_cast<float*>(out)[at + u * step] : 0.0f;
+  }
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    if (u >= left) break;
+    const float f = mul * __uint_as_float(v[u]);
+    store_elem(p, 0, OUT, ADD ? was[u] + f : f);
+    p += step;
+  }
+}
+template <int OUT, bool ADD>
+__device__ __forceinline__ void dw_put_row(void* out, int64_t at, const uint32_t (&v)[16], float mul, int left) {
+#pragma unroll
+  for (int u = 0; u < 16; u += 8) {
+    if (u >= left) break;
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = mul * __uint_as_float(v[u + i]);
+    if constexpr (OUT == kFp32) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at + u);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 was = ADD ? p[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        p[i] = ADD ? make_float4(was.x + f[4 * i], was.y + f[4 * i + 1], was.z + f[4 * i + 2], was.w + f[4 * i + 3])
+                   : make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+      }
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at + u) =
+          make_uint4(pack_type<OUT>(f[0], f[1]), pack_type<OUT>(f[2], f[3]), pack_type<OUT>(f[4], f[5]), pack_type<OUT>(f[6], f[7]));
+    }
+  }
+}
+__device__ __forceinline__ void dw_put_any(const AdapterGradArgs& a, const AdapterGradSide& g, bool row, int64_t at,
+                                           const uint32_t (&v)[16], float mul, int left) {
+  if (row && g.vec) {
+    if (a.accumulate) dw_put_row<kFp32, true>(g.out, at, v, mul, left);
+    else if (a.out_type == kFp32) dw_put_row<kFp32, false>(g.out, at, v, mul, left);
+    else if (a.out_type == kBf16) dw_put_row<kBf16, false>(g.out, at, v, mul, left);
+    else dw_put_row<kFp16, false>(g.out, at, v, mul, left);
+  } else {
+    if (a.accumulate) dw_put<kFp32, true>(g.out, at, g.out_j, v, mul, left);
+    else if (a.out_type == kFp32) dw_put<kFp32, false>(g.out, at, g.out_j, v, mul, left);
+    else if (a.out_type == kBf16) dw_put<kBf16, false>(g.out, at, g.out_j, v, mul, left);
+    else dw_put<kFp16, false>(g.out, at, g.out_j, v, mul, left);
+  }
 }
 
 template <int VEC>
@@ -332,13 +390,12 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
       if (some && !warp_wait(&acc_full[acc.i], acc.phase, abort_flag, a.status)) break;
       tc_fence_after();
       const bool whole = it.slices == 1;
-      float mul = whole && a.scale ? a.scale[it.l] : 1.0f;
+      float mul = whole && a.scale && some ? a.scale[it.l] : 1.0f;
       if (a.type == kFp16 && some) mul *= *(volatile float*)&factor[acc.i];
       const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc.i * ranks;
       const bool there = it.p0 + at < g.P;
       const int64_t first = it.l * g.out_l + (it.p0 + at) * g.out_p;
       // partial tiles lie as the gradient does: [rank, 128] of dA, [128, rank] of dB
-      const int step = it.side ? 1 : kDwCols;
       float* const partial = a.part + it.part * a.R * kDwCols + (it.side ? at * a.R : at);
       for (int j = 0; j < a.R; j += 16) {
         uint32_t v[16] = {};
@@ -347,13 +404,9 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
           tmem_ld_wait();
         }
         if (there) {
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            if (j + u >= a.R) break;
-            const float f = some ? mul * __uint_as_float(v[u]) : 0.0f;
-            if (whole) dw_store(a, g.out, first + (j + u) * g.out_j, f);
-            else partial[(j + u) * step] = f;
-          }
+          if (whole) dw_put_any(a, g, it.side, first + j * g.out_j, v, mul, a.R - j);
+          else if (it.side) dw_put_row<kFp32, false>(partial, j, v, mul, a.R - j);
+          else dw_put<kFp32, false>(partial, (int64_t)j * kDwCols, kDwCols, v, mul, a.R - j);
         }
         __syncwarp();
       }
