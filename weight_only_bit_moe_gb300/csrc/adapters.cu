@@ -37,8 +37,6 @@ static int run(AdapterArgs& a, bool fwd, float* mid, uint8_t* workspace, void* s
   a.part = reinterpret_cast<float*>(workspace + kAdPartAt);
   cudaError_t rc;
   if (on_grid(a, mid)) {
-    const int64_t room = kAdPartValues / ((int64_t)a.rows * a.R);
-    a.slices = (int)(room < 1 ? 1 : room > 32 ? 32 : room);
     rc = fwd && a.rows <= kAdFewRows ? launch_adapter_few(a, mid != nullptr, st)
                                      : launch_adapter_tc(a, fwd, mid != nullptr, kAdPartValues, st);
   } else {

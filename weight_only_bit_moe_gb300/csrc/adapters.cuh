@@ -29,7 +29,7 @@ struct AdapterArgs {
   int64_t out_ld;
   float* mid;                // [rows, R]
   float* part;               // partial sums of mid
-  int slices;                // few rows: of mid, [slices, rows, R]
+  int few_ctas;              // few rows: CTAs of a cluster
   int mid_ctas;              // many rows: CTAs of the first launch; 0: they take whole tiles
   int want_mid;              // mid is the caller's
   unsigned* status;
