@@ -75,6 +75,9 @@ def test_many_tokens_with_a_bias(R):
     bias = torch.randn(256, device="cuda") * 0.05
     for score in ("softmax", "sigmoid"):
         check_route(R, logits, 8, score, bias, True, 1.0)
+    for top_k in (31, 32):  # as many as a warp has lanes: the next one decides too
+        check_route(R, logits, top_k, "sigmoid", bias, True, 1.0)
+    check_route(R, logits, 32, "softmax", None, False, 1.0)
 
 
 def test_keys_next_to_each_other(R):

@@ -22,28 +22,40 @@ from . import binding as B
 from . import products as P
 
 
-def _bank(t: torch.Tensor, name: str) -> Tuple[Tuple[int, int, int], int, int]:
-    """Shape and (adapter, row) strides of a bank of factors."""
-    shape = P._dims(t, name, 3)
-    return (shape, *P._bank(t, name, shape))
-
+# As in ``products``, the checks read each attribute of a tensor once: for a decode step they are most of a call's time.
 
 def _positions(offsets: torch.Tensor, order: Optional[torch.Tensor], scale: Optional[torch.Tensor], adapters: int,
                rows: int) -> Tuple[Optional[int], Optional[int]]:
     """Addresses of order and scale, which may be None."""
-    P._check_offsets(offsets, adapters)
-    if order is not None and (order.dtype is not torch.int32 or order.shape != (rows,) or not order.is_contiguous()):
-        raise ValueError(f"order: expected contiguous int32 [{rows}], got {order.dtype} {tuple(order.shape)}")
-    if scale is not None and (scale.dtype is not torch.float32 or scale.shape != (adapters,) or
-                              not scale.is_contiguous()):
-        raise ValueError(f"scale: expected contiguous float32 [{adapters}], got {scale.dtype} {tuple(scale.shape)}")
-    return None if order is None else order.data_ptr(), None if scale is None else scale.data_ptr()
+    if offsets.dtype is not torch.int32 or offsets.shape != (adapters + 1,) or not offsets.is_contiguous():
+        P._check_offsets(offsets, adapters)
+    order_at = scale_at = None
+    if order is not None:
+        if order.dtype is not torch.int32 or order.shape != (rows,) or not order.is_contiguous():
+            raise ValueError(f"order: expected contiguous int32 [{rows}], got {order.dtype} {tuple(order.shape)}")
+        order_at = order.data_ptr()
+    if scale is not None:
+        if scale.dtype is not torch.float32 or scale.shape != (adapters,) or not scale.is_contiguous():
+            raise ValueError(f"scale: expected contiguous float32 [{adapters}], got {scale.dtype} {tuple(scale.shape)}")
+        scale_at = scale.data_ptr()
+    return order_at, scale_at
 
 
 def _mid(mid: torch.Tensor, name: str, rows: int, rank: int) -> int:
     if mid.dtype is not torch.float32 or mid.shape != (rows, rank) or not mid.is_contiguous():
         raise ValueError(f"{name}: expected contiguous float32 [{rows}, {rank}], got {mid.dtype} {tuple(mid.shape)}")
     return mid.data_ptr()
+
+
+def _ld(t: torch.Tensor, name: str, dtype: torch.dtype, width: int, rows: int) -> int:
+    """Row stride of a matrix of that type and shape."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+    if t.shape == (rows, width):
+        ld, step = t.stride()
+        if step == 1 and ld >= width:
+            return ld
+    return P._rows(t, name, width, rows)
 
 
 def _by_row(fn: str, name: str, rows_in: torch.Tensor, a, b, offsets, order, scale, base, out, mid, stream,
@@ -53,38 +65,39 @@ def _by_row(fn: str, name: str, rows_in: torch.Tensor, a, b, offsets, order, sca
         with torch.cuda.device(dev):
             return _by_row(fn, name, rows_in, a, b, offsets, order, scale, base, out, mid, stream, forward, only_mid)
     rows, width = P._dims(rows_in, name, 2)
-    (L, R, K), a_l, a_r = _bank(a, "a")
-    (b_L, N, b_R), b_l, b_n = _bank(b, "b")
-    if (b_L, b_R) != (L, R):
-        raise ValueError(f"b: {tuple(b.shape)}, expected [{L}, N, {R}] beside a of {tuple(a.shape)}")
+    L, R, K = shape = P._dims(a, "a", 3)
+    b_L, N, b_R = b_shape = P._dims(b, "b", 3)
+    if b_L != L or b_R != R:
+        raise ValueError(f"b: {tuple(b_shape)}, expected [{L}, N, {R}] beside a of {tuple(shape)}")
     if R > B.MOE_MAX_RANK or L > B.MOE_MAX_ADAPTERS:
         raise ValueError(f"a: {L} adapters of rank {R}, at most {B.MOE_MAX_ADAPTERS} of {B.MOE_MAX_RANK}")
-    out_width = N if forward else K
     dtype = rows_in.dtype
     code = P._HALF.get(dtype)
     if code is None or a.dtype is not dtype or b.dtype is not dtype:
         raise P._types(fn, rows_in, a, b)
-    ld = P._rows(rows_in, name, K if forward else N, rows)
+    a_l, a_r, step = a.stride()
+    if step != 1 or a_r < K:
+        a_l, a_r = P._bank(a, "a", shape)
+    b_l, b_n, step = b.stride()
+    if step != 1 or b_n < R:
+        b_l, b_n = P._bank(b, "b", b_shape)
+    ld, step = rows_in.stride()
+    in_width, out_width = (K, N) if forward else (N, K)
+    if width != in_width or step != 1 or ld < width:
+        ld = P._rows(rows_in, name, in_width, rows)
     order_at, scale_at = _positions(offsets, order, scale, L, rows)
-    base_at, base_ld = None, 0
+    base_at = out_at = mid_at = None
+    base_ld = out_ld = 0
     if base is not None:
-        if base.dtype is not dtype:
-            raise P._types(fn, rows_in, base)
-        base_at, base_ld = base.data_ptr(), P._rows(base, "base", out_width, rows)
-    if only_mid:
-        out_at, out_ld = None, 0
-    elif out is None:
+        base_at, base_ld = base.data_ptr(), _ld(base, "base", dtype, out_width, rows)
+    if out is not None:
+        out_at, out_ld = out.data_ptr(), _ld(out, "out", dtype, out_width, rows)
+    elif not only_mid:
         out = P._empty((rows, out_width), dtype, rows_in, stream)
         out_at, out_ld = out.data_ptr(), out_width
-    else:
-        if out.dtype is not dtype:
-            raise P._types(fn, rows_in, out)
-        out_at, out_ld = out.data_ptr(), P._rows(out, "out", out_width, rows)
     if mid is not None:
         mid_at = _mid(mid, "mid", rows, R)
-    elif rows * R <= B.MOE_ADAPTER_MID_VALUES:
-        mid_at = None  # in the workspace
-    else:
+    elif rows * R > B.MOE_ADAPTER_MID_VALUES:  # (else in the workspace)
         mid = P._empty((rows, R), torch.float32, rows_in, stream)
         mid_at = mid.data_ptr()
     if stream is not None:

@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const __grid_constant
   float reach = -INFINITY;  // what is not below this could still be chosen
   bool close = false;
   int n = 0;
-  for (; n < 32; ++n) {
+  for (;; ++n) {
     const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
     if (best == 0u) break;
     if (kExact) {
@@ -290,6 +290,7 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const __grid_constant
         if (n == a.k) reach = low - margin;
       }
       if (n >= a.k && (!close || key_value(best | kLow) < reach)) break;
+      if (n == 32) break;  // (more candidates than lanes)
       before = best;
     }
     if (lane == n) mine = best;
@@ -547,29 +548,44 @@ __device__ __forceinline__ float team_max(float v) {
   for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
+// A team's row on its way: 16 bytes at a time (V = 8 or 4 elements), or single values; nothing past the last expert.
 template <int TYPE, int G, int PER, int V>
-__device__ __forceinline__ void load_team(const void* base, int64_t row_at, int E, int u, bool on, float (&v)[PER]) {
+struct TeamRow {
+  uint4 w[V == 1 ? 1 : PER / V];
+  float f[V == 1 ? PER : 1];
+  __device__ __forceinline__ void fetch(const void* base, int64_t row_at, int E, int u, bool on) {
+    const char* const row = static_cast<const char*>(base) + row_at * (TYPE == kFp32 ? 4 : 2);
 #pragma unroll
-  for (int i = 0; i < PER; i += V) {
-    const int e = (i / V * G + u) * V;
-    if (!on || e >= E) {
+    for (int i = 0; i < PER / V; ++i) {
+      const int e = (i * G + u) * V;
+      if constexpr (V == 1) f[i] = on && e < E ? load_elem(row, e, TYPE) : -INFINITY;
+      else if (on && e < E) w[i] = __ldg(reinterpret_cast<const uint4*>(row + 16 * (i * G + u)));
+    }
+  }
+  __device__ __forceinline__ void widen(int E, int u, bool on, float (&v)[PER]) const {
 #pragma unroll
-      for (int x = 0; x < V; ++x) v[i + x] = -INFINITY;
-    } else if constexpr (V == 1) {
-      v[i] = load_elem(base, row_at + e, TYPE);
-    } else if constexpr (V == 4) {
-      load_four<TYPE>(base, row_at + e, v + i);
-    } else {
-      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + row_at + e);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    for (int i = 0; i < PER; i += V) {
+      const bool in = on && (i / V * G + u) * V < E;
+      if constexpr (V == 1) {
+        v[i] = f[i];
+      } else if (!in) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float2 f = unpack_type<TYPE>(ws[x]);
-        v[i + 2 * x] = f.x, v[i + 2 * x + 1] = f.y;
+        for (int x = 0; x < V; ++x) v[i + x] = -INFINITY;
+      } else {
+        const uint32_t ws[4] = {w[i / V].x, w[i / V].y, w[i / V].z, w[i / V].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if constexpr (V == 4) {
+            v[i + x] = __uint_as_float(ws[x]);
+          } else {
+            const float2 p = unpack_type<TYPE>(ws[x]);
+            v[i + 2 * x] = p.x, v[i + 2 * x + 1] = p.y;
+          }
+        }
       }
     }
   }
-}
+};
 // Counts of the sequence; the factor num_experts / (C T) that goes with them.
 template <int G, int PER, int V>
 __device__ __forceinline__ float load_counts(const BalanceArgs& a, const BalanceItem& it, int u, float (&c)[PER]) {
@@ -633,13 +649,16 @@ __global__ void __launch_bounds__(kRtThreads) balance_kernel(const __grid_consta
   const bool any = it.s >= 0 && it.t0 < it.t1;
   if (any) {
     float c[PER], sum = 0.0f;
+    TeamRow<TYPE, G, PER, V> next;
+    next.fetch(a.logits, (it.t0 + team) * a.ld, a.E, u, it.t0 + team < it.t1);
     const float factor = load_counts<G, PER, V>(a, it, u, c);
     double total = 0.0;
     int n = 0;
     for (int t = it.t0; t < it.t1; t += kTeams, ++n) {
       const int token = t + team;
       float v[PER], inner = 0.0f;
-      load_team<TYPE, G, PER, V>(a.logits, token * a.ld, a.E, u, token < it.t1, v);
+      next.widen(a.E, u, token < it.t1, v);
+      next.fetch(a.logits, (token + kTeams) * a.ld, a.E, u, token + kTeams < it.t1);
       const float inv = probabilities<G, PER>(v, a.score == MOE_SCORE_SOFTMAX, nullptr);
 #pragma unroll
       for (int i = 0; i < PER; ++i) inner = fmaf(v[i], c[i], inner);
@@ -653,14 +672,13 @@ __global__ void __launch_bounds__(kRtThreads) balance_kernel(const __grid_consta
     if (u == 0) parts[team] = total * factor;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    if (any) {
-      double sum = 0.0;
-      for (int i = 0; i < kTeams; ++i) sum += parts[i];
-      a.partial[blockIdx.x] = (float)sum;
+  if (threadIdx.x < 32) {
+    const double sum = warp_sum(any && lane < kTeams ? parts[lane] : 0.0);
+    if (lane == 0) {
+      if (any) a.partial[blockIdx.x] = (float)sum;
+      __threadfence();
+      last = slice_arrive_last(a.counter, gridDim.x);
     }
-    __threadfence();
-    last = slice_arrive_last(a.counter, gridDim.x);
   }
   __syncthreads();
   if (!last) return;
@@ -698,7 +716,11 @@ __global__ void __launch_bounds__(kRtThreads) balance_grad_kernel(const __grid_c
   if (it.t0 >= it.t1) return;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
   float c[PER], factor = 0.0f;
-  if (it.s >= 0) factor = load_counts<G, PER, V>(a, it, u, c) * a.dloss[it.s];
+  TeamRow<TYPE, G, PER, V> next;
+  if (it.s >= 0) {
+    next.fetch(a.logits, (it.t0 + team) * a.ld, a.E, u, it.t0 + team < it.t1);
+    factor = load_counts<G, PER, V>(a, it, u, c) * a.dloss[it.s];
+  }
   for (int t = it.t0; t < it.t1; t += kTeams) {
     const int token = t + team;
     const bool on = token < it.t1;
@@ -708,7 +730,8 @@ __global__ void __launch_bounds__(kRtThreads) balance_grad_kernel(const __grid_c
       for (int i = 0; i < PER; ++i) v[i] = 0.0f;
     } else {
       float rest[PER], inner = 0.0f;
-      load_team<TYPE, G, PER, V>(a.logits, token * a.ld, a.E, u, on, v);
+      next.widen(a.E, u, on, v);
+      next.fetch(a.logits, (token + kTeams) * a.ld, a.E, u, token + kTeams < it.t1);
       const float inv = probabilities<G, PER>(v, softmax, rest);
 #pragma unroll
       for (int i = 0; i < PER; ++i) inner = fmaf(v[i], c[i], inner);
@@ -821,12 +844,13 @@ static int check_workspace(const void* workspace, int64_t bytes) {
   return bytes < MOE_PRODUCTS_WORKSPACE_BYTES ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 
-// Tokens to a CTA: four CTAs to an SM, but a token to a team at least; as many parts as the workspace holds.
+// Tokens to a CTA: three CTAs to an SM, which run at one time, but a token to a team at least; as many parts as the
+// workspace holds.
 static int plan_balance(BalanceArgs& a, int64_t* grid) {
   const int sms = prod_sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
   const int64_t most = (MOE_PRODUCTS_WORKSPACE_BYTES - MOE_PRODUCTS_WORKSPACE_HEAD_BYTES) / 8 - kRtSequences;
-  int64_t chunk = ((int64_t)a.tokens + 4 * sms - 1) / (4 * sms);
+  int64_t chunk = ((int64_t)a.tokens + 3 * sms - 1) / (3 * sms);
   if (chunk < a.tokens / most + 1) chunk = a.tokens / most + 1;
   a.chunk = (int)((chunk + 31) / 32 * 32);
   if (a.chunk < 32) a.chunk = 32;

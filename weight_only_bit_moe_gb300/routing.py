@@ -37,7 +37,10 @@ def _logits(logits: torch.Tensor) -> Tuple[int, int, int, int]:
         raise ValueError(f"logits of {logits.dtype}, expected bfloat16, float16 or float32")
     if not 1 <= experts <= MAX_EXPERTS:
         raise ValueError(f"logits of {experts} experts, at most {MAX_EXPERTS}")
-    return code, tokens, experts, P._rows(logits, "logits", experts, tokens)
+    ld, step = logits.stride()
+    if step != 1 or ld < experts:
+        ld = P._rows(logits, "logits", experts, tokens)
+    return code, tokens, experts, ld
 
 
 def _dlogits(out: Optional[torch.Tensor], logits: torch.Tensor, stream) -> Tuple[torch.Tensor, int]:
@@ -51,7 +54,7 @@ def _dlogits(out: Optional[torch.Tensor], logits: torch.Tensor, stream) -> Tuple
 
 def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> int:
     """Address of a contiguous tensor of that type and shape."""
-    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} {list(shape)}, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -76,10 +79,14 @@ def topk_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: O
     bias_at = None if bias is None else _vector(bias, "bias", torch.float32, (experts,))
     if weights is None:
         weights = P._empty((tokens, top_k), torch.float32, logits, stream)
+        weights_at = weights.data_ptr()
+    else:
+        weights_at = _vector(weights, "weights", torch.float32, (tokens, top_k))
     if ids is None:
         ids = P._empty((tokens, top_k), torch.int32, logits, stream)
-    weights_at = _vector(weights, "weights", torch.float32, (tokens, top_k))
-    ids_at = _vector(ids, "ids", torch.int32, (tokens, top_k))
+        ids_at = ids.data_ptr()
+    else:
+        ids_at = _vector(ids, "ids", torch.int32, (tokens, top_k))
     if stream is not None:
         P._used_on(stream, logits, bias, weights, ids)
     rc = B.function("moe_route")(code, logits.data_ptr(), ld, bias_at, tokens, experts, top_k, how,
@@ -172,7 +179,9 @@ def expert_counts(ids: torch.Tensor, num_experts: int, offsets: Optional[torch.T
     shape = (num_experts,) if offsets is None else (S, num_experts)
     if out is None:
         out = P._empty(shape, torch.int32, ids, stream)
-    out_at = _vector(out, "out", torch.int32, shape)
+        out_at = out.data_ptr()
+    else:
+        out_at = _vector(out, "out", torch.int32, shape)
     if stream is not None:
         P._used_on(stream, ids, offsets, out)
     h = P._handle(dev, stream)
