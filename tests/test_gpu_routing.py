@@ -135,6 +135,10 @@ def test_extreme_logits(R, score):
             assert_bound(w, want, 2.0 ** -16 * want.abs() + 2.0 ** -126, "weights")
             d = R.topk_route_grad(torch.ones_like(w), logits, ids, score, renormalize)
             assert torch.isfinite(d).all()
+    ids = R.topk_route(logits, 2, score)[1]
+    check_balance(R, logits[2:], R.expert_counts(ids, 4), None, score)
+    loss = R.balance(logits, R.expert_counts(ids, 4), None, score)
+    assert torch.isfinite(loss) and torch.isfinite(R.balance_grad(torch.ones_like(loss), logits, R.expert_counts(ids, 4), None, score)).all()
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])

@@ -15,7 +15,7 @@ BUILD = os.path.join(HERE, "_build", platform.machine())
 LIB = os.path.join(HERE, "_build", f"libmoe_w4a16_{platform.machine()}.so")
 SOURCES = ["align.cu", "repack.cu", "gemm_int4.cu", "gemm_int4x.cu", "gemm_mxfp4.cu", "gemm_nvfp4.cu", "combine.cu",
            "requant.cu", "products.cu", "products_any.cu", "products_grouped.cu", "products_fp8.cu", "quant.cu",
-           "routing.cu", "adapters.cu", "adapters_any.cu", "adapters_few.cu",
+           "routing.cu", "routing_team.cu", "adapters.cu", "adapters_any.cu", "adapters_few.cu",
            "adapters_mid.cu", "adapters_out_fwd.cu", "adapters_out_dx.cu", "adapters_grad.cu",
            "api.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

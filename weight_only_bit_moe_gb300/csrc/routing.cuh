@@ -1,0 +1,342 @@
+// What the kernels of moe_routing.h share.
+#pragma once
+
+#include "../../include/moe_routing.h"
+#include "adapters.cuh"
+
+namespace moe {
+
+constexpr int kRtThreads = 256, kRtWarps = kRtThreads / 32;
+constexpr int kRtSequences = 1 << 20;
+// The counter of the last CTA of a loss, behind those of the products' tiles.
+constexpr int kRtCounter = kProdCounterBytes / 4 - 1;
+static_assert(kRtCounter >= kProdPartials, "a product's counter");
+
+struct RouteArgs {
+  const void* logits;
+  int64_t ld;
+  const float* bias;
+  int tokens, E, k, score, renorm;
+  float scale;
+  float* weights;
+  int32_t* ids;
+  const float* dw;       // gradient
+  int64_t dw_ld;
+  const int32_t* in_ids;
+  void* out;
+  int64_t out_ld;
+};
+
+// ---------------------------------------------------------------- values
+// Order of floats as unsigned numbers: -infinity is above 0, which stands for no value.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // (-0 counts as 0)
+  return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ float warp_max(float v) {
+  return key_value(__reduce_max_sync(0xffffffffu, order_key(v)));
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// sigmoid(l) / exp(min(top, 0)), top at least the largest l: in range where the sigmoids themselves are not.
+__device__ __forceinline__ float shifted_sigmoid(float l, float floor) {
+  return __fdividef(expf(fminf(l, 0.0f) - floor), 1.0f + expf(-fabsf(l)));
+}
+__device__ __forceinline__ float sigmoid(float l) {
+  const float u = expf(-fabsf(l));
+  return (l >= 0.0f ? 1.0f : u) / (1.0f + u);
+}
+// What is subtracted before exponentials: the largest value, or 0 for a token of -infinities.
+__device__ __forceinline__ float finite_or_0(float v) { return v == -INFINITY ? 0.0f : v; }
+
+// Four consecutive values.
+template <int TYPE>
+__device__ __forceinline__ void load_four(const void* base, int64_t at, float* v) {
+  if (TYPE == kFp32) {
+    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
+    const float2 f = unpack_type<TYPE>(u.x), g = unpack_type<TYPE>(u.y);
+    v[0] = f.x, v[1] = f.y, v[2] = g.x, v[3] = g.y;
+  }
+}
+template <int TYPE>
+__device__ __forceinline__ void store_four(void* base, int64_t at, const float* v) {
+  if (TYPE == kFp32)
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + at) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at) =
+        make_uint2(pack_type<TYPE>(v[0], v[1]), pack_type<TYPE>(v[2], v[3]));
+}
+// The lane's experts of a token, -infinity past the last.  V = 4: rows on a boundary of four elements, E a multiple
+// of four.
+template <int TYPE, int PER, int V>
+__device__ __forceinline__ void load_row(const void* base, int64_t row_at, int E, int lane, float (&v)[PER]) {
+#pragma unroll
+  for (int i = 0; i < PER; i += V) {
+    const int e = lane * PER + i;
+    if (e >= E) {
+#pragma unroll
+      for (int u = 0; u < V; ++u) v[i + u] = -INFINITY;
+    } else if constexpr (V == 1) {
+      v[i] = load_elem(base, row_at + e, TYPE);
+    } else {
+      load_four<TYPE>(base, row_at + e, v + i);
+    }
+  }
+}
+template <int TYPE, int PER, int V>
+__device__ __forceinline__ void store_row(void* base, int64_t row_at, int E, int lane, const float (&v)[PER]) {
+#pragma unroll
+  for (int i = 0; i < PER; i += V) {
+    const int e = lane * PER + i;
+    if (e >= E) continue;
+    if constexpr (V == 1) store_elem(base, row_at + e, TYPE, v[i]);
+    else store_four<TYPE>(base, row_at + e, v + i);
+  }
+}
+
+// Descending order of a lane's keys, by merging sorted halves (Batcher's odd-even merge).
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
+#pragma unroll
+  for (int lp = 0; (1 << lp) < N; ++lp)
+#pragma unroll
+    for (int lq = lp; lq >= 0; --lq)
+#pragma unroll
+      for (int x = 0; x < N; ++x) {
+        const int p = 1 << lp, q = 1 << lq, from = q % p;
+        if (x >= from && ((x - from) / q) % 2 == 0 && x + q < N && x / (2 * p) == (x + q) / (2 * p)) {
+          const uint32_t hi = max(k[x], k[x + q]);
+          k[x + q] = min(k[x], k[x + q]);
+          k[x] = hi;
+        }
+      }
+}
+
+// ---------------------------------------------------------------- teams
+// Teams: G lanes to a token, lane u of them the experts (G i + u) V .. + V - 1, i = 0, 1, ..
+template <int G>
+__device__ __forceinline__ float team_sum(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float team_max(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+// A team's row on its way: 16 bytes at a time (V = 8 or 4 elements), or single values; nothing past the last expert.
+template <int TYPE, int G, int PER, int V>
+struct TeamRow {
+  uint4 w[V == 1 ? 1 : PER / V];
+  float f[V == 1 ? PER : 1];
+  __device__ __forceinline__ void fetch(const void* base, int64_t row_at, int E, int u, bool on) {
+    const char* const row = static_cast<const char*>(base) + row_at * (TYPE == kFp32 ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < PER / V; ++i) {
+      const int e = (i * G + u) * V;
+      if constexpr (V == 1) f[i] = on && e < E ? load_elem(row, e, TYPE) : -INFINITY;
+      else if (on && e < E) w[i] = __ldg(reinterpret_cast<const uint4*>(row + 16 * (i * G + u)));
+    }
+  }
+  __device__ __forceinline__ void widen(int E, int u, bool on, float (&v)[PER]) const {
+#pragma unroll
+    for (int i = 0; i < PER; i += V) {
+      const bool in = on && (i / V * G + u) * V < E;
+      if constexpr (V == 1) {
+        v[i] = f[i];
+      } else if (!in) {
+#pragma unroll
+        for (int x = 0; x < V; ++x) v[i + x] = -INFINITY;
+      } else {
+        const uint32_t ws[4] = {w[i / V].x, w[i / V].y, w[i / V].z, w[i / V].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if constexpr (V == 4) {
+            v[i + x] = __uint_as_float(ws[x]);
+          } else {
+            const float2 p = unpack_type<TYPE>(ws[x]);
+            v[i + 2 * x] = p.x, v[i + 2 * x + 1] = p.y;
+          }
+        }
+      }
+    }
+  }
+};
+template <int TYPE, int G, int PER, int V>
+__device__ __forceinline__ void store_team(void* base, int64_t row_at, int E, int u, const float (&v)[PER]) {
+#pragma unroll
+  for (int i = 0; i < PER; i += V) {
+    const int e = (i / V * G + u) * V;
+    if (e >= E) continue;
+    if constexpr (V == 1) {
+      store_elem(base, row_at + e, TYPE, v[i]);
+    } else if constexpr (V == 4) {
+      store_four<TYPE>(base, row_at + e, v + i);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) w[x] = pack_type<TYPE>(v[i + 2 * x], v[i + 2 * x + 1]);
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + row_at + e) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+// 2^x.
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// p of a token in v's place, times z; returns 1 / z.  `rest` gets 1 - sigmoid.  exp(l - top) = 2^((l - top) log2 e): two
+// roundings of 2^-24 of the exponent more than the function, for a third of its instructions.
+template <int G, int PER>
+__device__ __forceinline__ float probabilities(float (&v)[PER], bool softmax, float* rest) {
+  constexpr float kLog2e = 1.44269504f;
+  float most = v[0];
+#pragma unroll
+  for (int i = 1; i < PER; ++i) most = fmaxf(most, v[i]);
+  const float shift = finite_or_0(team_max<G>(most));
+  float z = 0.0f;
+  if (softmax) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      v[i] = exp2_of((v[i] - shift) * kLog2e);
+      z += v[i];
+    }
+  } else {
+    const float s = fminf(shift, 0.0f);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const float u = exp2_of(-fabsf(v[i]) * kLog2e), inv = __fdividef(1.0f, 1.0f + u);
+      if (rest) rest[i] = (v[i] >= 0.0f ? u : 1.0f) * inv;
+      v[i] = exp2_of((fminf(v[i], 0.0f) - s) * kLog2e) * inv;
+      z += v[i];
+    }
+  }
+  z = team_sum<G>(z);
+  return z == 0.0f ? 0.0f : 1.0f / z;
+}
+
+// Kernels that give a token a team instead of a warp: up to kRtTeamK experts of up to kRtTeamExperts.
+constexpr int kRtTeamK = 8, kRtTeamExperts = 512;
+bool route_by_teams(int E, int top_k, bool bias);
+const void* route_team_instance(int type, int E, bool vec, bool bias, int* teams);
+const void* route_team_grad_instance(int type, int E, bool vec, int* teams);
+
+// The choice of a token, in 64 bits where 32 do not settle it, all lanes of a warp: lane j gets the j-th expert or -1.
+// Lane c < n brings the candidate `e` (all experts that can be chosen are among them), or with n = 0 every expert is
+// looked at.  shift, sum: the largest logit and the sum of the exponentials (softmax with a bias).
+// p + bias of an expert in 64 bits; without bias the logit.
+static __device__ __noinline__ double key_in_64(const RouteArgs& a, double l, int e, double top, double z) {
+  if (l == -INFINITY) return -INFINITY;
+  if (!a.bias) return l;
+  const double u = exp(a.score == MOE_SCORE_SOFTMAX ? l - top : -fabs(l));
+  const double p = a.score == MOE_SCORE_SOFTMAX ? u / z : (l >= 0.0 ? 1.0 : u) / (1.0 + u);
+  return p + (double)a.bias[e];
+}
+
+static __device__ __noinline__ int choose_in_64(const RouteArgs& a, int type, int64_t row_at, int lane, int e, int n, float shift,
+                                                float sum) {
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  const double logit = lane < n ? load_elem(a.logits, row_at + e, type) : 0.0;
+  int rank = 0, mine = -1;
+  if (n > 0) {  // all that 32 bits can tell first: most of what comes here the keys' upper bits alone could not
+    float v = (float)logit, margin = 0.0f;
+    if (a.bias && lane < n) {
+      v = (softmax ? expf(v - shift) / sum : sigmoid(v)) + a.bias[e];
+      margin = 2.0f * (softmax ? 7.6293945e-6f / sum : 9.5367432e-7f) + 4.7683716e-7f * fabsf(v);
+    }
+    bool near = false;
+#pragma unroll 1
+    for (int c = 0; c < n; ++c) {
+      const float other = __shfl_sync(0xffffffffu, v, c);
+      const int other_e = __shfl_sync(0xffffffffu, e, c);
+      rank += other > v || (other == v && other_e < e);
+      near |= c != lane && fabsf(other - v) <= margin;
+    }
+    if (!__any_sync(0xffffffffu, a.bias && lane < n && near && rank <= a.k)) {
+#pragma unroll 1
+      for (int c = 0; c < n; ++c) {
+        const int at = __shfl_sync(0xffffffffu, rank, c), other_e = __shfl_sync(0xffffffffu, e, c);
+        if (at == lane) mine = other_e;
+      }
+      return lane < a.k ? mine : -1;
+    }
+  }
+  double top = 0.0, z = 1.0;
+  if (a.bias && softmax) {
+    top = -INFINITY;
+#pragma unroll 1
+    for (int i = lane; i < a.E; i += 32) top = fmax(top, (double)load_elem(a.logits, row_at + i, type));
+    for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+    z = 0.0;
+#pragma unroll 1
+    for (int i = lane; i < a.E; i += 32) z += exp((double)load_elem(a.logits, row_at + i, type) - top);
+    z = warp_sum(z);
+  }
+  if (n > 0) {
+    const double key = lane < n ? key_in_64(a, logit, e, top, z) : 0.0;
+    rank = 0;
+#pragma unroll 1
+    for (int c = 0; c < n; ++c) {
+      const double other = __shfl_sync(0xffffffffu, key, c);
+      const int other_e = __shfl_sync(0xffffffffu, e, c);
+      rank += other > key || (other == key && other_e < e);
+    }
+#pragma unroll 1
+    for (int c = 0; c < n; ++c) {
+      const int at = __shfl_sync(0xffffffffu, rank, c), other_e = __shfl_sync(0xffffffffu, e, c);
+      if (at == lane) mine = other_e;
+    }
+    return lane < a.k ? mine : -1;
+  }
+  double key[kProdGroups / 32];
+  const int own = (a.E + 31) / 32;
+#pragma unroll 1
+  for (int i = 0; i < own; ++i) {
+    const int x = lane + 32 * i;
+    key[i] = x < a.E ? key_in_64(a, load_elem(a.logits, row_at + x, type), x, top, z) : -INFINITY;
+  }
+#pragma unroll 1
+  for (int j = 0; j < a.k; ++j) {
+    double best = -INFINITY;
+    int at = 1 << 30;
+#pragma unroll 1
+    for (int i = 0; i < own; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = lane + 32 * i;
+      }
+    for (int o = 16; o > 0; o >>= 1) {
+      const double other = __shfl_xor_sync(0xffffffffu, best, o);
+      const int other_at = __shfl_xor_sync(0xffffffffu, at, o);
+      if (other > best || (other == best && other_at < at)) {
+        best = other;
+        at = other_at;
+      }
+    }
+    if (best == -INFINITY) break;
+    if (lane == j) mine = at;
+#pragma unroll 1
+    for (int i = 0; i < own; ++i)
+      if (lane + 32 * i == at) key[i] = -INFINITY;
+  }
+  return mine;
+}
+
+}  // namespace moe

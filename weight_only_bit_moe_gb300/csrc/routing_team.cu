@@ -1,0 +1,388 @@
+// The experts of each token, up to eight of up to 512, and the gradient of their weights
+// by the logits: a team of G lanes to a token, 32 experts at most to a lane, eight tokens
+// to a warp where there are 128 experts.
+//
+// What bounds these is the number of instructions, so what is done once a lane serves as
+// many tokens as a warp has teams.  A key is a value's order in its upper 22 bits and the
+// expert, lowest best, in the lower ten, so minima and maxima move both.  Each lane sorts
+// its keys in blocks of eight and keeps the eight best of two sorted blocks (the larger
+// ones of one block against the other reversed, sorted again), as do the lanes of a team
+// among each other; the largest key dropped tells whether more than eight come into
+// question.  How keys decide, and what happens where they cannot: routing.cu.
+#include "routing.cuh"
+
+namespace moe {
+
+// The eight largest of two descending lists into `a`, descending; the largest other one into `rest`.
+__device__ __forceinline__ void keep_eight(uint32_t (&a)[8], const uint32_t (&b)[8], uint32_t& rest) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    rest = max(rest, min(a[i], b[7 - i]));
+    a[i] = max(a[i], b[7 - i]);
+  }
+#pragma unroll
+  for (int d = 4; d >= 1; d /= 2)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & d) == 0) {
+        const uint32_t hi = max(a[i], a[i + d]);
+        a[i + d] = min(a[i], a[i + d]);
+        a[i] = hi;
+      }
+}
+
+// Experts of a token whose value, less `largest`, may reach `reach`: all lanes, n of them dealt to lanes 0 .. n - 1
+// (n = 0: more than the lanes).  inv_z: softmax with a bias.
+__device__ __noinline__ int gather_candidates(const RouteArgs& a, int type, int64_t row_at, int lane, float shift, float inv_z,
+                                              float largest, float reach, int* count) {
+  // (few tokens come here, and what they wait for most is the code: it is kept small)
+  int mine = 0, n = 0;
+#pragma unroll 1
+  for (int e0 = 0; e0 < a.E; e0 += 32) {
+    const int e = e0 + lane;
+    float v = e < a.E ? load_elem(a.logits, row_at + e, type) : -INFINITY;
+    if (a.bias && v != -INFINITY) {
+      const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+      const float w = __expf(softmax ? v - shift : -fabsf(v));
+      v = (softmax ? w * inv_z : __fdividef(v >= 0.0f ? 1.0f : w, 1.0f + w)) + __ldg(a.bias + e);
+    }
+    uint32_t left = __ballot_sync(0xffffffffu, v != -INFINITY && v - largest >= reach);
+    while (left) {
+      if (lane == n) mine = e0 + __ffs(left) - 1;
+      left &= left - 1;
+      ++n;
+    }
+  }
+  *count = n <= 32 ? n : 0;
+  return mine;
+}
+
+template <int TYPE, int G, int PER, int V, bool BIAS>
+__global__ void __launch_bounds__(kRtThreads) route_team_kernel(const __grid_constant__ RouteArgs a) {
+  constexpr bool kExact = TYPE != kFp32 && !BIAS;
+  constexpr uint32_t kLow = G * PER - 1;  // as many bits as the experts need
+  constexpr int kSlots = G < 8 ? 8 / G : 1;  // of a lane
+  const int lane = threadIdx.x & 31, u = lane % G, team = lane / G;
+  const int64_t first_token = ((int64_t)blockIdx.x * kRtWarps + (threadIdx.x >> 5)) * (32 / G);
+  grid_dependents_launch();
+  grid_dependency_wait();
+  if (first_token >= a.tokens) return;
+  const int64_t token = first_token + team;
+  const bool on = token < a.tokens, softmax = a.score == MOE_SCORE_SOFTMAX;
+  const int64_t row_at = (on ? token : 0) * a.ld;
+  TeamRow<TYPE, G, PER, V> row;
+  row.fetch(a.logits, row_at, a.E, u, on);
+  float v[PER];
+  row.widen(a.E, u, on, v);
+  float most = v[0];  // (NaN passes on)
+#pragma unroll
+  for (int i = 1; i < PER; ++i) most = fmax_nan(most, v[i]);
+  bool bad = !(most < INFINITY);
+  const float shift = finite_or_0(team_max<G>(most));
+  constexpr float kLog2e = 1.44269504f;
+  float z = 1.0f;
+  if (softmax && (BIAS || !a.renorm)) {
+    z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) z += exp2_of((v[i] - shift) * kLog2e);
+    z = team_sum<G>(z);
+  }
+  float largest = shift;  // of what is chosen by
+  if (BIAS) {
+    const float inv = 1.0f / z;
+    most = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = (i / V * G + u) * V + i % V;
+      if (e < a.E) {
+        const float b = __ldg(a.bias + e);
+        bad |= !(b < INFINITY);
+        float p;
+        if (softmax) {
+          p = exp2_of((v[i] - shift) * kLog2e) * inv;
+        } else {
+          const float w = exp2_of(-fabsf(v[i]) * kLog2e);
+          p = __fdividef(v[i] >= 0.0f ? 1.0f : w, 1.0f + w);
+        }
+        if (v[i] != -INFINITY) v[i] = p + b;
+        most = fmaxf(most, v[i]);
+      }
+    }
+    largest = finite_or_0(team_max<G>(most));
+  }
+  // NaN or +infinity among the team's values
+  const bool lost = (__ballot_sync(0xffffffffu, bad) >> (team * G)) & (G == 32 ? 0xffffffffu : (1u << G) - 1u);
+
+  uint32_t best[8], rest = 0;
+#pragma unroll
+  for (int b = 0; b < PER / 8; ++b) {
+    uint32_t key[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int i = 8 * b + x;
+      const float y = kExact ? v[i] : v[i] - largest;
+      key[x] = v[i] == -INFINITY ? 0u : (order_key(y) & ~kLow) | (kLow - ((i / V * G + u) * V + i % V));
+    }
+    sort_keys(key);
+    if (b == 0) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) best[x] = key[x];
+    } else {
+      keep_eight(best, key, rest);
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < G; o *= 2) {
+    uint32_t other[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) other[x] = __shfl_xor_sync(0xffffffffu, best[x], o);
+    rest = max(rest, __shfl_xor_sync(0xffffffffu, rest, o));
+    keep_eight(best, other, rest);
+  }
+  int id[kSlots];
+  float picked[kSlots];
+#pragma unroll
+  for (int m = 0; m < kSlots; ++m) {
+    uint32_t key = 0;
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      if (x / G == m && x % G == u) key = best[x];
+    id[m] = key && u + m * G < a.k && !lost ? (int)(kLow - (key & kLow)) : -1;
+    // (what a 16-bit value leaves of its order's lower bits: zeros, or of a negative one ones)
+    if (kExact) picked[m] = id[m] >= 0 ? key_value(key >> 31 ? key & ~kLow : key | kLow) : -INFINITY;
+  }
+  if (!kExact) {
+    // Errors of p + bias: see route_kernel.
+    const float slack = !BIAS ? 0.0f : 2.0f * (softmax ? 7.6293945e-6f / z : 9.5367432e-7f) + 2.3841858e-7f * fabsf(largest);
+    bool close = false;
+    float reach = -INFINITY;
+    int n = 1;
+#pragma unroll
+    for (int x = 1; x <= 8; ++x) {
+      const uint32_t next = x < 8 ? best[x < 8 ? x : 0] : rest;
+      n += x < 8 && next != 0u;
+      if (x <= a.k && best[x - 1] != 0u) {
+        const float low = key_value(best[x - 1] & ~kLow), high = key_value(next | kLow);
+        const float margin = BIAS ? slack + 2.3841858e-7f * fabsf(high) : 0.0f;
+        if (next != 0u) close |= BIAS ? low - high <= margin : (best[x - 1] ^ next) <= kLow;
+        if (x == a.k) reach = low - (next != 0u ? margin : 0.0f);
+      }
+    }
+    if (rest != 0u && key_value(rest | kLow) >= reach) n = 0;  // more than these eight
+    const float lower = reach - slack - 4.7683716e-7f * fabsf(reach);  // (as far off as two ways to compute p can be)
+    uint32_t left = __ballot_sync(0xffffffffu, close && on && !lost && u == 0);
+    while (left) {
+      const int from = __ffs(left) - 1;
+      left &= left - 1;
+      int e = 0;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const uint32_t key = __shfl_sync(0xffffffffu, best[x], from);
+        if (lane == x) e = (int)(kLow - (key & kLow));
+      }
+      const int64_t at = (first_token + from / G) * a.ld;
+      int count = __shfl_sync(0xffffffffu, n, from);
+      const float its_shift = __shfl_sync(0xffffffffu, shift, from), its_z = __shfl_sync(0xffffffffu, z, from);
+      const float its_largest = __shfl_sync(0xffffffffu, largest, from), its_lower = __shfl_sync(0xffffffffu, lower, from);
+      if (count == 0) e = gather_candidates(a, TYPE, at, lane, its_shift, 1.0f / its_z, its_largest, its_lower, &count);
+      const int chosen = choose_in_64(a, TYPE, at, lane, e, count, its_shift, its_z);
+#pragma unroll
+      for (int m = 0; m < kSlots; ++m) {
+        const int mine = __shfl_sync(0xffffffffu, chosen, (u + m * G) & 31);
+        if (from / G == team) id[m] = u + m * G < a.k ? mine : -1;
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < kSlots; ++m) picked[m] = id[m] >= 0 ? load_elem(a.logits, row_at + id[m], TYPE) : -INFINITY;
+  }
+  float w[kSlots], sum = 0.0f, first = picked[0];
+#pragma unroll
+  for (int m = 1; m < kSlots; ++m) first = fmaxf(first, picked[m]);
+  first = finite_or_0(team_max<G>(first));
+#pragma unroll
+  for (int m = 0; m < kSlots; ++m) {
+    w[m] = 0.0f;
+    if (id[m] >= 0) {
+      if (softmax) w[m] = a.renorm ? expf(picked[m] - first) : expf(picked[m] - shift) / z;
+      else w[m] = a.renorm ? shifted_sigmoid(picked[m], fminf(first, 0.0f)) : sigmoid(picked[m]);
+    }
+    sum += w[m];
+  }
+  if (a.renorm) {
+    sum = team_sum<G>(sum);
+#pragma unroll
+    for (int m = 0; m < kSlots; ++m)
+      if (id[m] >= 0) w[m] = w[m] / sum;
+  }
+#pragma unroll
+  for (int m = 0; m < kSlots; ++m) {
+    const int j = u + m * G;
+    if (!on || j >= a.k) continue;
+    a.ids[token * a.k + j] = id[m];
+    a.weights[token * a.k + j] = lost ? __uint_as_float(0x7FC00000u) : id[m] >= 0 ? a.scale * w[m] : 0.0f;
+  }
+}
+
+// The formulas: routing.cu.  What goes to every expert and then what goes to the chosen ones meet in shared memory,
+// the slots' parts in their order.
+template <int TYPE, int G, int PER, int V>
+__global__ void __launch_bounds__(kRtThreads) route_team_grad_kernel(const __grid_constant__ RouteArgs a) {
+  constexpr int kSlots = G < 8 ? 8 / G : 1;
+  __shared__ __align__(16) float rows[kRtWarps][32 / G][G * PER];
+  const int lane = threadIdx.x & 31, u = lane % G, team = lane / G;
+  const int64_t first_token = ((int64_t)blockIdx.x * kRtWarps + (threadIdx.x >> 5)) * (32 / G);
+  grid_dependents_launch();
+  grid_dependency_wait();
+  if (first_token >= a.tokens) return;
+  const int64_t token = first_token + team;
+  const bool on = token < a.tokens, softmax = a.score == MOE_SCORE_SOFTMAX, whole = softmax && !a.renorm;
+  const int64_t row_at = (on ? token : 0) * a.ld;
+  float* const row = rows[threadIdx.x >> 5][team];
+  int id[kSlots];
+  float g[kSlots], l[kSlots], part[kSlots];
+#pragma unroll
+  for (int m = 0; m < kSlots; ++m) {
+    const int j = u + m * G;
+    id[m] = -1, g[m] = 0.0f;
+    if (on && j < a.k) {
+      id[m] = a.in_ids[token * a.k + j];
+      g[m] = a.dw[token * a.dw_ld + j];
+    }
+  }
+  float out[PER];
+  if (whole) {
+    TeamRow<TYPE, G, PER, V> next;
+    next.fetch(a.logits, row_at, a.E, u, on);
+    next.widen(a.E, u, on, out);
+  }
+#pragma unroll
+  for (int m = 0; m < kSlots; ++m) {
+    if (id[m] < 0 || id[m] >= a.E) id[m] = -1, g[m] = 0.0f;
+    l[m] = id[m] >= 0 ? load_elem(a.logits, row_at + id[m], TYPE) : -INFINITY;
+  }
+  if (whole) {
+    const float inv = probabilities<G, PER>(out, true, nullptr);
+    // p of a chosen expert as the others have it: its place among the exponentials
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+      if constexpr (V >= 4) {
+        *reinterpret_cast<float4*>(row + (i / V * G + u) * V + i % V) = make_float4(out[i], out[i + 1], out[i + 2], out[i + 3]);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) row[(i + x) * G + u] = out[i + x];
+      }
+    }
+    __syncwarp();
+    float mean = 0.0f;
+#pragma unroll
+    for (int m = 0; m < kSlots; ++m) {
+      part[m] = id[m] >= 0 ? g[m] * row[id[m]] * inv : 0.0f;
+      mean += part[m];
+      part[m] *= a.scale;
+    }
+    mean = team_sum<G>(mean);
+    bool some = false;
+#pragma unroll
+    for (int m = 0; m < kSlots; ++m) some |= id[m] >= 0;
+    const bool any = (__ballot_sync(0xffffffffu, some) >> (team * G)) & (G == 32 ? 0xffffffffu : (1u << G) - 1u);
+    const float add = -a.scale * mean * inv;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) out[i] = any ? out[i] * add : 0.0f;
+  } else {
+    float first = l[0], sum = 0.0f, mean = 0.0f, e[kSlots];
+#pragma unroll
+    for (int m = 1; m < kSlots; ++m) first = fmaxf(first, l[m]);
+    first = finite_or_0(team_max<G>(first));
+#pragma unroll
+    for (int m = 0; m < kSlots; ++m) {
+      e[m] = 0.0f;
+      if (id[m] >= 0) e[m] = !a.renorm ? sigmoid(l[m]) : softmax ? expf(l[m] - first) : shifted_sigmoid(l[m], fminf(first, 0.0f));
+      sum += e[m];
+    }
+    if (a.renorm) {
+      sum = team_sum<G>(sum);
+#pragma unroll
+      for (int m = 0; m < kSlots; ++m) {
+        e[m] = sum > 0.0f || sum != sum ? e[m] / sum : 0.0f;
+        mean += g[m] * e[m];
+      }
+      mean = team_sum<G>(mean);
+    }
+#pragma unroll
+    for (int m = 0; m < kSlots; ++m) {
+      part[m] = id[m] >= 0 ? a.scale * e[m] * (g[m] - mean) : 0.0f;
+      if (!softmax && id[m] >= 0) part[m] *= sigmoid(-l[m]);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) out[i] = 0.0f;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < PER; i += 4) {
+    if constexpr (V >= 4) {
+      *reinterpret_cast<float4*>(row + (i / V * G + u) * V + i % V) = make_float4(out[i], out[i + 1], out[i + 2], out[i + 3]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) row[(i + x) * G + u] = out[i + x];
+    }
+  }
+  for (int j = 0; j < a.k; ++j) {
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < kSlots; ++m)
+      if (u + m * G == j && id[m] >= 0) row[id[m]] += part[m];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < PER; i += 4) {
+    if constexpr (V >= 4) {
+      const float4 f = *reinterpret_cast<const float4*>(row + (i / V * G + u) * V + i % V);
+      out[i] = f.x, out[i + 1] = f.y, out[i + 2] = f.z, out[i + 3] = f.w;
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) out[i + x] = row[(i + x) * G + u];
+    }
+  }
+  if (on) store_team<TYPE, G, PER, V>(a.out, token * a.out_ld, a.E, u, out);
+}
+
+// ---------------------------------------------------------------- host
+// Teams of four lanes up to 128 experts, of eight up to 256 and sixteen up to 512; with a bias, up to 128 experts.
+template <int TYPE, int V>
+static const void* pick_team(int E, bool bias) {
+  if (E <= 64) return bias ? (const void*)route_team_kernel<TYPE, 4, 16, V, true> : (const void*)route_team_kernel<TYPE, 4, 16, V, false>;
+  if (E <= 128) return bias ? (const void*)route_team_kernel<TYPE, 4, 32, V, true> : (const void*)route_team_kernel<TYPE, 4, 32, V, false>;
+  if (E <= 256) return (const void*)route_team_kernel<TYPE, 8, 32, V, false>;
+  return (const void*)route_team_kernel<TYPE, 16, 32, V, false>;
+}
+template <int TYPE, int V>
+static const void* pick_team_grad(int E) {
+  if (E <= 64) return (const void*)route_team_grad_kernel<TYPE, 4, 16, V>;
+  if (E <= 128) return (const void*)route_team_grad_kernel<TYPE, 4, 32, V>;
+  if (E <= 256) return (const void*)route_team_grad_kernel<TYPE, 8, 32, V>;
+  return (const void*)route_team_grad_kernel<TYPE, 16, 32, V>;
+}
+static int teams_of(int E) { return E <= 128 ? 8 : E <= 256 ? 4 : 2; }
+
+// Against a warp to a token (us of GPU time, eight experts of a token; fp32, softmax): 65536 tokens over 64 experts 12.4
+// to 45.7, with a bias 27.5 to 69.6; 32768 over 128 12.7 to 25.5 and 26.0 to 40.7; 8191 over 256 10.0 to 10.8 and 29.7 to
+// 24.5 (so not with a bias there: fewer warps run at one time, and the slowest tokens are those compared in 64 bits);
+// in bf16 without a bias 65536 over 64 7.2 to 25.9, 8191 over 512 7.8 to 8.7.
+bool route_by_teams(int E, int top_k, bool bias) {
+  return top_k <= kRtTeamK && E <= (bias ? 128 : kRtTeamExperts);
+}
+// vec: rows on the grid of 16 bytes.  teams: tokens of a warp.
+const void* route_team_instance(int type, int E, bool vec, bool bias, int* teams) {
+  *teams = teams_of(E);
+  if (type == kBf16) return vec ? pick_team<kBf16, 8>(E, bias) : pick_team<kBf16, 1>(E, bias);
+  if (type == kFp16) return vec ? pick_team<kFp16, 8>(E, bias) : pick_team<kFp16, 1>(E, bias);
+  return vec ? pick_team<kFp32, 4>(E, bias) : pick_team<kFp32, 1>(E, bias);
+}
+const void* route_team_grad_instance(int type, int E, bool vec, int* teams) {
+  *teams = teams_of(E);
+  if (type == kBf16) return vec ? pick_team_grad<kBf16, 8>(E) : pick_team_grad<kBf16, 1>(E);
+  if (type == kFp16) return vec ? pick_team_grad<kFp16, 8>(E) : pick_team_grad<kFp16, 1>(E);
+  return vec ? pick_team_grad<kFp32, 4>(E) : pick_team_grad<kFp32, 1>(E);
+}
+
+}  // namespace moe
