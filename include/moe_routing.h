@@ -8,8 +8,8 @@
  * return values from moe_status.  Strides count elements; the experts of a token
  * and the slots of a token are contiguous.  Logits are MOE_BF16, MOE_FP16 or
  * MOE_FP32 (moe_products.h); everything is computed in 32 bits, or in 64 where
- * said.  1 <= num_experts <= 1024, 0 <= tokens (0 is a no-op where nothing but
- * token rows is written), tokens * num_experts < 2^40.
+ * said.  1 <= num_experts <= 1024, 0 <= tokens < 2^31 - 65536 (0 is a no-op where
+ * nothing but token rows is written), tokens * num_experts < 2^40.
  *
  * Workspace (where there is one): as in moe_products.h, and the same one serves.
  */

@@ -25,7 +25,7 @@ ROUTE = dict(dtype=2, logits=BUF, ld=64, bias=0, tokens=10, experts=64, top_k=4,
              weights=BUF, ids=BUF, stream=0)
 ROUTE_GRAD = dict(dtype=2, dweights=BUF, dw_ld=4, logits=BUF, ld=64, ids=BUF, tokens=10, experts=64, top_k=4, score=0,
                   renormalize=1, scale=1.0, out=BUF, out_ld=64, stream=0)
-SHARED = [dict(dtype=3), dict(dtype=-1), dict(ld=63), dict(tokens=-1), dict(experts=0), dict(experts=1025, ld=1025),
+SHARED = [dict(tokens=2 ** 31 - 65536), dict(dtype=3), dict(dtype=-1), dict(ld=63), dict(tokens=-1), dict(experts=0), dict(experts=1025, ld=1025),
           dict(top_k=0), dict(top_k=33), dict(top_k=5, experts=4), dict(score=2), dict(score=-1), dict(renormalize=2),
           dict(logits=0), dict(logits=BUF + 2), dict(ids=0), dict(ids=BUF + 2)]
 
@@ -55,7 +55,7 @@ COUNTS = dict(ids=BUF, ld=4, tokens=10, top_k=4, offsets=BUF, sequences=2, exper
 
 @pytest.mark.parametrize("bad", [
     dict(ids=0), dict(ids=BUF + 1), dict(ld=3), dict(tokens=-1), dict(top_k=0), dict(tokens=2 ** 30, top_k=4),
-    dict(offsets=0), dict(offsets=BUF + 1), dict(sequences=0), dict(sequences=(1 << 20) + 1), dict(experts=0),
+    dict(tokens=2 ** 31 - 65536, top_k=1), dict(offsets=0), dict(offsets=BUF + 1), dict(sequences=0), dict(sequences=(1 << 20) + 1), dict(experts=0),
     dict(experts=1025), dict(counts=0), dict(counts=BUF + 2), dict(workspace=0), dict(workspace=BUF + 8)], ids=str)
 def test_counts_refusals(lib, bad):
     assert call(lib, "moe_expert_counts", {**COUNTS, **workspace(lib)}, bad) == lib.MOE_ERR_INVALID

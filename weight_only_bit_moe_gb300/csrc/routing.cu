@@ -525,7 +525,7 @@ static bool in_vectors(const void* p, int64_t ld, int E, int type, int n) {
 
 static bool good_rows(const void* p, int64_t ld, int E, int type) { return p && ld >= E && on_elements(p, elem_bytes(type)); }
 static bool good_logits(int type, int tokens, int E) {
-  return type >= kBf16 && type <= kFp32 && tokens >= 0 && E >= 1 && E <= kProdGroups &&
+  return type >= kBf16 && type <= kFp32 && tokens >= 0 && tokens <= kRtTokens && E >= 1 && E <= kProdGroups &&
          (int64_t)tokens * E < (int64_t)1 << 40;
 }
 static bool good_score(int score) { return score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID; }
@@ -631,7 +631,7 @@ extern "C" int moe_route_grad(int dtype, const float* dweights, int64_t dweights
 extern "C" int moe_expert_counts(const int32_t* ids, int64_t ids_stride, int tokens, int top_k,
                                  const int32_t* offsets, int num_sequences, int num_experts, int32_t* counts,
                                  void* workspace, int64_t workspace_bytes, void* stream) {
-  if (tokens < 0 || top_k < 1 || (int64_t)tokens * top_k >= (int64_t)1 << 31 || ids_stride < top_k) return MOE_ERR_INVALID;
+  if (tokens < 0 || tokens > kRtTokens || top_k < 1 || (int64_t)tokens * top_k >= (int64_t)1 << 31 || ids_stride < top_k) return MOE_ERR_INVALID;
   if (num_experts < 1 || num_experts > kProdGroups || num_sequences < 1 || num_sequences > kRtSequences)
     return MOE_ERR_INVALID;
   if (!offsets && num_sequences != 1) return MOE_ERR_INVALID;

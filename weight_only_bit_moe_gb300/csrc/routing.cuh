@@ -8,6 +8,7 @@ namespace moe {
 
 constexpr int kRtThreads = 256, kRtWarps = kRtThreads / 32;
 constexpr int kRtSequences = 1 << 20;
+constexpr int kRtTokens = 0x7FFFFFFF - 65536;  // token numbers may run past the last one by a CTA's
 // The counter of the last CTA of a loss, behind those of the products' tiles.
 constexpr int kRtCounter = kProdCounterBytes / 4 - 1;
 static_assert(kRtCounter >= kProdPartials, "a product's counter");
