@@ -19,17 +19,25 @@
 
 namespace moe {
 
-constexpr int kDwThreads = 672, kDwLoaders = 256, kDwConverters = 256;  // warps 0-7, 12-19; 8-11 epilogue, 20 MMA
+constexpr int kDwLoaders = 256;  // warps 0-7; 8-11 epilogue, then converters and the MMA warp
 constexpr int kDwCols = 128;
 
-template <int VEC>  // float4 of a stage's mid to a converter: ceil(R / 16)
+template <int TYPE, int VEC>  // VEC: sixteens of ranks
 struct DwCfg {
   static constexpr int RB = (VEC + 3) / 4;  // blocks of 64 ranks
-  static constexpr int kAhead = VEC <= 8 ? 8 / VEC : 1;  // stages of mid on their way in registers
-  static constexpr int kStages = RB == 1 ? 6 : RB == 2 ? 4 : 2;
-  static constexpr int kLag = RB == 1 ? 4 : RB == 2 ? 3 : 1;
+  // threads (what a warp does beside converting counts too, but fp16 reads an item's mid twice)
+  static constexpr int kConverters = VEC <= 2 && TYPE == kBf16 ? 128 : 256;
+  static constexpr int kThreads = kDwLoaders + 128 + kConverters + 32, kMmaWarp = kThreads / 32 - 1;
+  static constexpr int kPerLine = kConverters / 64, kVec = VEC * 4 / kPerLine;  // threads to a position, float4 to a thread
+  static constexpr int kAhead = kVec <= 8 ? 8 / kVec : 1;  // stages of mid on their way in registers
+  // Up to 32 ranks the two parts lie side by side in the lines of one block: one MMA for both, into columns that are
+  // added at the end, and room for more stages.
+  static constexpr bool kJoin = VEC <= 2;
+  static constexpr int kLow = 16 * VEC;  // the low part's first column
+  static constexpr int kStages = kJoin ? 8 : RB == 1 ? 6 : RB == 2 ? 4 : 2;
+  static constexpr int kLag = kJoin ? 6 : RB == 1 ? 4 : RB == 2 ? 3 : 1;
   static constexpr int kMidBytes = RB * 8192;  // of one part
-  static constexpr int kStageBytes = 16384 + 2 * kMidBytes;
+  static constexpr int kStageBytes = 16384 + (kJoin ? 1 : 2) * kMidBytes;
   static constexpr int kAlloc = kStages * kStageBytes + 1024;
   static_assert(kLag < kStages, "a loader would wait for a stage that it has not signalled");
   static_assert(kAlloc + 2 * (kAdAdapters + 1) * 4 + 512 <= 227 * 1024, "shared memory over the per-CTA limit");
@@ -173,12 +181,12 @@ __device__ __forceinline__ void dw_put_any(const AdapterGradArgs& a, const Adapt
   }
 }
 
-template <int VEC>
-__global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_constant__ AdapterGradArgs a) {
-  using C = DwCfg<VEC>;
+template <int TYPE, int VEC>
+__global__ void __launch_bounds__(DwCfg<TYPE, VEC>::kThreads, 1) adapter_dw_kernel(const __grid_constant__ AdapterGradArgs a) {
+  using C = DwCfg<TYPE, VEC>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ int start[kAdAdapters + 1], part[kAdAdapters + 1];
-  __shared__ int warp_tot[2 * kDwThreads / 32];
+  __shared__ int warp_tot[2 * C::kThreads / 32];
   __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], drain_bar;
   __shared__ uint32_t misc[2];
   __shared__ float factor[2];      // of the accumulators (fp16)
@@ -186,21 +194,21 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&misc[1]);
   const uint32_t smem_s = (smem_u32(smem_raw) + 1023) & ~1023u;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const uint32_t ranks = (a.R + 15) / 16 * 16, columns = tmem_columns(2 * ranks);
+  const uint32_t ranks = C::kJoin ? 2 * C::kLow : (a.R + 15) / 16 * 16, columns = tmem_columns(2 * ranks);  // of the MMAs
   if (tid == 0) {
-    for (int i = 0; i < C::kStages; ++i) { mbar_init(&full[i], kDwLoaders + kDwConverters); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < C::kStages; ++i) { mbar_init(&full[i], kDwLoaders + C::kConverters); mbar_init(&empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
     mbar_init(&drain_bar, 1);
     misc[1] = 0;
     fence_mbar_init();
   }
-  if (warp == 20) {
+  if (warp == C::kMmaWarp) {
     tmem_alloc(&misc[0], columns);
     tmem_relinquish();
   }
   grid_dependents_launch();
   grid_dependency_wait();
-  const bool good = plan_dw<kDwThreads>(a, start, part, warp_tot);
+  const bool good = plan_dw<C::kThreads>(a, start, part, warp_tot);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -232,21 +240,31 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
           if (at < it.n) r[u] = a.order ? min((uint32_t)__ldg(a.order + it.pos + at), 0xFFFFFFFEu) : it.pos + at;
         }
       };
-      load_rows(0);
+      if (a.order) load_rows(0);
+      const uint8_t* line = in + (uint64_t)(uint32_t)(it.pos + line0) * ld;  // without an order: of a whole stage
       for (int i = 0; i < it.n; i += 64) {
         if (!mbar_wait(&empty[slot.i], slot.phase ^ 1, abort_flag, a.status)) {
           ok = false;
           break;
         }
         const uint32_t dst = smem_s + slot.i * C::kStageBytes + to;
+        if (!a.order && i + 64 <= it.n) {
 #pragma unroll
-        for (int u = 0; u < kLines; ++u) {
-          const bool have = r[u] < rows;
-          bad |= !have && r[u] != 0xFFFFFFFFu;
-          cp_async16(dst + u * 2048, in + (uint64_t)(have ? r[u] : 0u) * ld, have && column ? 16 : 0);
+          for (int u = 0; u < kLines; ++u) {
+            cp_async16(dst + u * 2048, line, column ? 16 : 0);
+            line += 16 * (uint64_t)ld;
+          }
+        } else {
+          if (!a.order) load_rows(i);
+#pragma unroll
+          for (int u = 0; u < kLines; ++u) {
+            const bool have = r[u] < rows;
+            bad |= !have && r[u] != 0xFFFFFFFFu;
+            cp_async16(dst + u * 2048, in + (uint64_t)(have ? r[u] : 0u) * ld, have && column ? 16 : 0);
+          }
+          if (a.order) load_rows(i + 64);
         }
         cp_async_commit();
-        load_rows(i + 64);
         slot.next();
         if (++filled > C::kLag) {
           cp_async_wait<C::kLag>();
@@ -264,7 +282,7 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
       mbar_arrive(&full[done.i]);
       done.next();
     }
-  } else if (warp >= 12 && warp < 20) {
+  } else if (warp >= 12 && warp < C::kMmaWarp) {
     // ------------------------------------------------------------ converters: mid to two 16-bit parts
     const int ct = tid - 12 * 32;
     const int quads = a.R / 4;  // float4 of a position
@@ -277,19 +295,19 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
       if (it.n == 0) continue;
       const float4* mid = reinterpret_cast<const float4*>(a.side[it.side].mid + (int64_t)it.pos * a.R);
       float inv = 1.0f;
-      if (a.type == kFp16) {
+      if (TYPE == kFp16) {
         float top = 0.0f;
         const int64_t all = (int64_t)it.n * quads;
 #pragma unroll 4
-        for (int64_t u = ct; u < all; u += kDwConverters) {
+        for (int64_t u = ct; u < all; u += C::kConverters) {
           const float4 v = __ldg(mid + u);
           top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
         }
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // (not negative)
         if (lane == 0) warp_top[warp - 12] = top;
-        named_bar_sync(1, kDwConverters);
+        named_bar_sync(1, C::kConverters);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) top = fmaxf(top, warp_top[u]);
+        for (int u = 0; u < C::kConverters / 32; ++u) top = fmaxf(top, warp_top[u]);
         float f = 1.0f;
         const int e = max((int)((__float_as_uint(top) >> 23) & 255) - 13, 1);
         if (top > 0.0f && top < INFINITY) f = __uint_as_float((uint32_t)e << 23);
@@ -298,19 +316,19 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
         if (!(ok = warp_wait(&acc_empty[acc.i], acc.phase ^ 1, abort_flag, a.status))) break;
         if (ct == 0) factor[acc.i] = f;
         acc.next();
-        named_bar_sync(1, kDwConverters);
+        named_bar_sync(1, C::kConverters);
       }
-      // four threads to a position, which take its float4 in turn; the loads run some stages ahead (one stage ahead, a
-      // stage took as long as memory answers: 205 us where this takes less than half)
-      const int line = ct >> 2, first = ct & 3;
+      // two or four threads to a position, which take its float4 in turn; the loads run some stages ahead
+      const int line = ct / C::kPerLine, first = ct % C::kPerLine;
       const float4* const from = mid + (int64_t)line * quads + first;
       const uint32_t to = smem_s + 16384 + line * 128 + (first & 1) * 8;
-      float4 v[C::kAhead][VEC];
-      auto load = [&](float4 (&x)[VEC], int i) {
+      float4 v[C::kAhead][C::kVec];
+      auto load = [&](float4 (&x)[C::kVec], int i) {
         const bool in = i + line < it.n;
 #pragma unroll
-        for (int u = 0; u < VEC; ++u)
-          x[u] = in && first + 4 * u < quads ? __ldg(from + (int64_t)i * quads + 4 * u) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int u = 0; u < C::kVec; ++u)
+          x[u] = in && first + C::kPerLine * u < quads ? __ldg(from + (int64_t)i * quads + C::kPerLine * u)
+                                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       };
 #pragma unroll
       for (int d = 0; d < C::kAhead; ++d) load(v[d], 64 * d);
@@ -325,20 +343,17 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
           }
           const uint32_t dst = to + slot.i * C::kStageBytes;
 #pragma unroll
-          for (int u = 0; u < VEC; ++u) {
+          for (int u = 0; u < C::kVec; ++u) {
             const float4 x = v[d][u];
             uint32_t h0, h1, l0, l1;
-            if (a.type == kBf16) {
-              split_type<kBf16>(x.x, x.y, h0, l0);
-              split_type<kBf16>(x.z, x.w, h1, l1);
-            } else {
-              split_type<kFp16>(x.x * inv, x.y * inv, h0, l0);
-              split_type<kFp16>(x.z * inv, x.w * inv, h1, l1);
-            }
-            const int c = 2 * u + (first >> 1);  // 16-byte column
+            const float f = TYPE == kFp16 ? inv : 1.0f;
+            split_type<TYPE>(x.x * f, x.y * f, h0, l0);
+            split_type<TYPE>(x.z * f, x.w * f, h1, l1);
+            const int c = C::kPerLine / 2 * u + (first >> 1);  // 16-byte column
             const uint32_t at = dst + (c >> 3) * 8192 + (((c & 7) ^ (line & 7)) << 4);
+            const uint32_t low = C::kJoin ? dst + (((c + 2 * VEC) ^ (line & 7)) << 4) : at + C::kMidBytes;
             asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(h0), "r"(h1) : "memory");
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + C::kMidBytes), "r"(l0), "r"(l1) : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(low), "r"(l0), "r"(l1) : "memory");
           }
           fence_async_proxy();
           mbar_arrive(&full[slot.i]);
@@ -347,9 +362,9 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
         }
       }
     }
-  } else if (warp == 20) {
+  } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMA
-    const uint32_t idesc = idesc_f16_f32(kDwCols, ranks, a.type == kBf16 ? 1u : 0u) | kIdescMajorA | kIdescMajorB;
+    const uint32_t idesc = idesc_f16_f32(kDwCols, ranks, TYPE == kBf16 ? 1u : 0u) | kIdescMajorA | kIdescMajorB;
     const uint64_t xd0 = smem_desc_sw128_mn(smem_s, 8192), hd0 = smem_desc_sw128_mn(smem_s + 16384, 8192),
                    ld0 = smem_desc_sw128_mn(smem_s + 16384 + C::kMidBytes, 8192);
     Ring<C::kStages> slot;
@@ -367,7 +382,7 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
         tc_fence_after();
         const uint32_t at = slot.i * (C::kStageBytes >> 4);
         umma1_f16_stage_elect<128, 128>(d, xd0 + at, hd0 + at, idesc, i > 0 ? 1u : 0u);
-        umma1_f16_stage_elect<128, 128>(d, xd0 + at, ld0 + at, idesc, 1u);
+        if (!C::kJoin) umma1_f16_stage_elect<128, 128>(d, xd0 + at, ld0 + at, idesc, 1u);
         umma_commit_elect(&empty[slot.i]);
         slot.next();
       }
@@ -391,7 +406,7 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
       tc_fence_after();
       const bool whole = it.slices == 1;
       float mul = whole && a.scale && some ? a.scale[it.l] : 1.0f;
-      if (a.type == kFp16 && some) mul *= *(volatile float*)&factor[acc.i];
+      if (TYPE == kFp16 && some) mul *= *(volatile float*)&factor[acc.i];
       const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc.i * ranks;
       const bool there = it.p0 + at < g.P;
       const int64_t first = it.l * g.out_l + (it.p0 + at) * g.out_p;
@@ -401,7 +416,15 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
         uint32_t v[16] = {};
         if (some) {
           tmem_ld16(src + j, v);
-          tmem_ld_wait();
+          if (C::kJoin) {
+            uint32_t low[16];
+            tmem_ld16(src + C::kLow + j, low);
+            tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < 16; ++u) v[u] = __float_as_uint(__uint_as_float(v[u]) + __uint_as_float(low[u]));
+          } else {
+            tmem_ld_wait();
+          }
         }
         if (there) {
           if (whole) dw_put_any(a, g, it.side, first + j * g.out_j, v, mul, a.R - j);
@@ -421,7 +444,7 @@ __global__ void __launch_bounds__(kDwThreads, 1) adapter_dw_kernel(const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 20) tmem_dealloc(tmem, columns);
+  if (warp == C::kMmaWarp) tmem_dealloc(tmem, columns);
 }
 
 // Adds the slices of the adapters that have several, four values to a thread.
@@ -464,12 +487,21 @@ __global__ void __launch_bounds__(kDsThreads) adapter_dw_sum_kernel(const __grid
 }
 
 // ---------------------------------------------------------------- host
-template <int VEC>
+template <int TYPE, int VEC>
 static cudaError_t launch_dw(const AdapterGradArgs& a, int sms, cudaStream_t st) {
   static std::atomic<bool> ready[64] = {};
-  const cudaError_t rc = allow_smem(adapter_dw_kernel<VEC>, DwCfg<VEC>::kAlloc, ready);
+  using C = DwCfg<TYPE, VEC>;
+  const cudaError_t rc = allow_smem(adapter_dw_kernel<TYPE, VEC>, C::kAlloc, ready);
   if (rc != cudaSuccess) return rc;
-  return launch_dependent(adapter_dw_kernel<VEC>, dim3(sms), dim3(kDwThreads), DwCfg<VEC>::kAlloc, st, a);
+  return launch_dependent(adapter_dw_kernel<TYPE, VEC>, dim3(sms), dim3(C::kThreads), C::kAlloc, st, a);
+}
+template <int TYPE>
+static cudaError_t launch_dw(const AdapterGradArgs& a, int sms, cudaStream_t st) {
+  if (a.R <= 16) return launch_dw<TYPE, 1>(a, sms, st);
+  if (a.R <= 32) return launch_dw<TYPE, 2>(a, sms, st);
+  if (a.R <= 64) return launch_dw<TYPE, 4>(a, sms, st);
+  if (a.R <= 128) return launch_dw<TYPE, 8>(a, sms, st);
+  return launch_dw<TYPE, 16>(a, sms, st);
 }
 
 // part_values: what the workspace holds of partial sums.
@@ -488,11 +520,7 @@ cudaError_t launch_adapter_grad_tc(AdapterGradArgs& a, int64_t part_values, cuda
   rows = (rows + 63) / 64 * 64;
   a.slice_rows = (int)(rows > a.rows ? a.rows : rows);
   if (a.slice_rows < 1) a.slice_rows = 1;
-  const cudaError_t rc = a.R <= 16    ? launch_dw<1>(a, sms, st)
-                         : a.R <= 32  ? launch_dw<2>(a, sms, st)
-                         : a.R <= 64  ? launch_dw<4>(a, sms, st)
-                         : a.R <= 128 ? launch_dw<8>(a, sms, st)
-                                      : launch_dw<16>(a, sms, st);
+  const cudaError_t rc = a.type == kBf16 ? launch_dw<kBf16>(a, sms, st) : launch_dw<kFp16>(a, sms, st);
   if (rc != cudaSuccess || a.slice_rows >= a.rows) return rc;
   return launch_dependent(adapter_dw_sum_kernel, dim3(sms * 4), dim3(256), 0, st, a);
 }
