@@ -181,6 +181,20 @@ __device__ __forceinline__ void dw_put_any(const AdapterGradArgs& a, const Adapt
   }
 }
 
+// A barrier of n threads that tells whether all of them bring true.
+__device__ __forceinline__ bool named_bar_and(int id, int n, bool p) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(n), "r"(p ? 1u : 0u)
+      : "memory");
+  return all != 0;
+}
+
 template <int TYPE, int VEC>
 __global__ void __launch_bounds__(DwCfg<TYPE, VEC>::kThreads, 1) adapter_dw_kernel(const __grid_constant__ AdapterGradArgs a) {
   using C = DwCfg<TYPE, VEC>;
@@ -290,7 +304,8 @@ __global__ void __launch_bounds__(DwCfg<TYPE, VEC>::kThreads, 1) adapter_dw_kern
     Ring<2> acc;
     bool ok = true;
     int l = 0;
-    for (int64_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
+    // (fp16: the warps meet for every item, so they also leave together)
+    for (int64_t w = blockIdx.x; w < items && (ok || TYPE == kFp16); w += gridDim.x) {
       const DwItem it = dw_item(a, start, part, w, l);
       if (it.n == 0) continue;
       const float4* mid = reinterpret_cast<const float4*>(a.side[it.side].mid + (int64_t)it.pos * a.R);
@@ -305,7 +320,7 @@ __global__ void __launch_bounds__(DwCfg<TYPE, VEC>::kThreads, 1) adapter_dw_kern
         }
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // (not negative)
         if (lane == 0) warp_top[warp - 12] = top;
-        named_bar_sync(1, C::kConverters);
+        if (!(ok = named_bar_and(1, C::kConverters, ok))) break;
 #pragma unroll
         for (int u = 0; u < C::kConverters / 32; ++u) top = fmaxf(top, warp_top[u]);
         float f = 1.0f;
@@ -313,10 +328,10 @@ __global__ void __launch_bounds__(DwCfg<TYPE, VEC>::kThreads, 1) adapter_dw_kern
         if (top > 0.0f && top < INFINITY) f = __uint_as_float((uint32_t)e << 23);
         inv = 1.0f / f;
         // the accumulator's last reader is done before its factor changes
-        if (!(ok = warp_wait(&acc_empty[acc.i], acc.phase ^ 1, abort_flag, a.status))) break;
-        if (ct == 0) factor[acc.i] = f;
+        ok = warp_wait(&acc_empty[acc.i], acc.phase ^ 1, abort_flag, a.status);
+        if (ct == 0 && ok) factor[acc.i] = f;
         acc.next();
-        named_bar_sync(1, C::kConverters);
+        if (!(ok = named_bar_and(1, C::kConverters, ok))) break;
       }
       // two or four threads to a position, which take its float4 in turn; the loads run some stages ahead
       const int line = ct / C::kPerLine, first = ct % C::kPerLine;

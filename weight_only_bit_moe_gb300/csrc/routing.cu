@@ -8,8 +8,8 @@
 
 namespace moe {
 
-// A key is a value's order in its upper 22 bits and the expert, lowest best, in the
-// lower ten: the largest of the lanes' heads, by one reduction of the warp, names the
+// A key is a value's order in its upper 22 bits or more and the expert, lowest best, in
+// the others: the largest of the lanes' heads, by one reduction of the warp, names the
 // next expert, and the lane that held it moves its list up.
 //
 // Logits of 16 bits fit the 22 and decide as they are.  Logits of fp32, and p + bias,
@@ -20,7 +20,7 @@ namespace moe {
 template <int TYPE, int PER, int V, bool BIAS>
 __global__ void __launch_bounds__(kRtThreads) route_kernel(const __grid_constant__ RouteArgs a) {
   constexpr bool kExact = TYPE != kFp32 && !BIAS;
-  constexpr uint32_t kLow = kProdGroups - 1;
+  constexpr uint32_t kLow = 32 * PER - 1;
   grid_dependents_launch();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const __grid_constant
   if (!kExact && close) {
     // (32 candidates and perhaps more: look at all)
     const int e = mine ? (int)(kLow - (mine & kLow)) : 0;
-    id = choose_in_64(a, TYPE, row_at, lane, e, n < 32 ? n : 0, shift, z);
+    id = !BIAS && n < 32 ? rank_logits(a.logits, TYPE, row_at, lane, e, n, a.k) : choose_in_64(a, TYPE, row_at, lane, e, n < 32 ? n : 0);
   }
   const float picked = id >= 0 ? load_elem(a.logits, row_at + id, TYPE) : -INFINITY;
   float w = 0.0f;
@@ -399,16 +399,13 @@ __global__ void __launch_bounds__(kRtThreads) balance_kernel(const __grid_consta
   __syncthreads();
   if (!last) return;
   // the last CTA adds the parts of each sequence in their order, 8 to 32 lanes to a sequence
-  bool bad = false;
-  if (a.offsets)
-    for (int s = threadIdx.x; s < a.S; s += kRtThreads) bad |= sequence_bad(a.offsets, s, a.tokens);
-  if (bad) atomicOr(a.status, kStatusRouting);
-  if (__syncthreads_or(bad)) return;  // (parts of overlapping sequences are not where they are looked for)
   const int first = a.offsets ? 1 : 0, lanes = a.S <= 8 ? 32 : a.S <= 16 ? 16 : 8;
   for (int s0 = 0; s0 < a.S; s0 += kRtThreads / lanes) {
     const int s = s0 + threadIdx.x / lanes, at = threadIdx.x % lanes;
     double sum = 0.0;
-    if (s < a.S) {
+    if (s < a.S && sequence_bad(a.offsets, s, a.tokens)) {
+      if (at == 0) atomicOr(a.status, kStatusRouting);
+    } else if (s < a.S) {
       const int r0 = balance_start(a, s + first), r1 = balance_start(a, s + first + 1);
       const int end = r0 < r1 ? (r1 - 1) / a.chunk + s + first : -1;
 #pragma unroll 4
@@ -589,7 +586,7 @@ extern "C" int moe_route(int dtype, const void* logits, int64_t logits_stride, c
   a.logits = logits, a.ld = logits_stride, a.bias = bias, a.tokens = tokens, a.E = num_experts, a.k = top_k;
   a.score = score, a.renorm = renormalize, a.scale = scale, a.weights = weights, a.ids = ids;
   int teams;
-  if (route_by_teams(num_experts, top_k, bias != nullptr)) {
+  if (route_by_teams(dtype, num_experts, top_k, bias != nullptr)) {
     const bool vec = in_vectors(logits, logits_stride, num_experts, dtype, 16 / elem_bytes(dtype));
     const void* kernel = route_team_instance(dtype, num_experts, vec, bias != nullptr, &teams);
     return launch_routing(kernel, (tokens - 1) / (kRtWarps * teams) + 1, a, stream);

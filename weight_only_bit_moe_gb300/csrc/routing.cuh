@@ -235,15 +235,32 @@ __device__ __forceinline__ float probabilities(float (&v)[PER], bool softmax, fl
 
 // Kernels that give a token a team instead of a warp: up to kRtTeamK experts of up to kRtTeamExperts.
 constexpr int kRtTeamK = 8, kRtTeamExperts = 512;
-bool route_by_teams(int E, int top_k, bool bias);
+bool route_by_teams(int type, int E, int top_k, bool bias);
 const void* route_team_instance(int type, int E, bool vec, bool bias, int* teams);
 const void* route_team_grad_instance(int type, int E, bool vec, int* teams);
 
-// The choice of a token, in 64 bits where 32 do not settle it, all lanes of a warp: lane j gets the j-th expert or -1.
-// Lane c < n brings the candidate `e` (all experts that can be chosen are among them), or with n = 0 every expert is
-// looked at.  shift, sum: the largest logit and the sum of the exponentials (softmax with a bias).
+// The order of a token's candidates by their logits as they are, all lanes of a warp: lane c < n brings the candidate
+// `e`, lane j gets the j-th expert or -1.
+static __device__ __noinline__ int rank_logits(const void* logits, int type, int64_t row_at, int lane, int e, int n, int k) {
+  const float v = lane < n ? load_elem(logits, row_at + e, type) : 0.0f;
+  int rank = 0, mine = -1;
+#pragma unroll 1
+  for (int c = 0; c < n; ++c) {
+    const float other = __shfl_sync(0xffffffffu, v, c);
+    const int other_e = __shfl_sync(0xffffffffu, e, c);
+    rank += other > v || (other == v && other_e < e);
+  }
+#pragma unroll 1
+  for (int c = 0; c < n; ++c) {
+    const int at = __shfl_sync(0xffffffffu, rank, c), other_e = __shfl_sync(0xffffffffu, e, c);
+    if (at == lane) mine = other_e;
+  }
+  return lane < k ? mine : -1;
+}
+// The choice of a token in 64 bits, all lanes of a warp: lane j gets the j-th expert or -1.  Lane c < n brings the
+// candidate `e` (all experts that can be chosen are among them), or with n = 0 every expert is looked at.
 // p + bias of an expert in 64 bits; without bias the logit.
-static __device__ __noinline__ double key_in_64(const RouteArgs& a, double l, int e, double top, double z) {
+static __device__ __forceinline__ double key_in_64(const RouteArgs& a, double l, int e, double top, double z) {
   if (l == -INFINITY) return -INFINITY;
   if (!a.bias) return l;
   const double u = exp(a.score == MOE_SCORE_SOFTMAX ? l - top : -fabs(l));
@@ -251,34 +268,10 @@ static __device__ __noinline__ double key_in_64(const RouteArgs& a, double l, in
   return p + (double)a.bias[e];
 }
 
-static __device__ __noinline__ int choose_in_64(const RouteArgs& a, int type, int64_t row_at, int lane, int e, int n, float shift,
-                                                float sum) {
+static __device__ __noinline__ int choose_in_64(const RouteArgs& a, int type, int64_t row_at, int lane, int e, int n) {
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-  const double logit = lane < n ? load_elem(a.logits, row_at + e, type) : 0.0;
+  const float logit = lane < n ? load_elem(a.logits, row_at + e, type) : 0.0f;
   int rank = 0, mine = -1;
-  if (n > 0) {  // all that 32 bits can tell first: most of what comes here the keys' upper bits alone could not
-    float v = (float)logit, margin = 0.0f;
-    if (a.bias && lane < n) {
-      v = (softmax ? expf(v - shift) / sum : sigmoid(v)) + a.bias[e];
-      margin = 2.0f * (softmax ? 7.6293945e-6f / sum : 9.5367432e-7f) + 4.7683716e-7f * fabsf(v);
-    }
-    bool near = false;
-#pragma unroll 1
-    for (int c = 0; c < n; ++c) {
-      const float other = __shfl_sync(0xffffffffu, v, c);
-      const int other_e = __shfl_sync(0xffffffffu, e, c);
-      rank += other > v || (other == v && other_e < e);
-      near |= c != lane && fabsf(other - v) <= margin;
-    }
-    if (!__any_sync(0xffffffffu, a.bias && lane < n && near && rank <= a.k)) {
-#pragma unroll 1
-      for (int c = 0; c < n; ++c) {
-        const int at = __shfl_sync(0xffffffffu, rank, c), other_e = __shfl_sync(0xffffffffu, e, c);
-        if (at == lane) mine = other_e;
-      }
-      return lane < a.k ? mine : -1;
-    }
-  }
   double top = 0.0, z = 1.0;
   if (a.bias && softmax) {
     top = -INFINITY;

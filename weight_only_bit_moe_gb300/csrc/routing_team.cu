@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kRtThreads) route_team_kernel(const __grid_con
       const float its_shift = __shfl_sync(0xffffffffu, shift, from), its_z = __shfl_sync(0xffffffffu, z, from);
       const float its_largest = __shfl_sync(0xffffffffu, largest, from), its_lower = __shfl_sync(0xffffffffu, lower, from);
       if (count == 0) e = gather_candidates(a, TYPE, at, lane, its_shift, 1.0f / its_z, its_largest, its_lower, &count);
-      const int chosen = choose_in_64(a, TYPE, at, lane, e, count, its_shift, its_z);
+      const int chosen = !BIAS && count > 0 ? rank_logits(a.logits, TYPE, at, lane, e, count, a.k) : choose_in_64(a, TYPE, at, lane, e, count);
 #pragma unroll
       for (int m = 0; m < kSlots; ++m) {
         const int mine = __shfl_sync(0xffffffffu, chosen, (u + m * G) & 31);
@@ -347,13 +347,25 @@ __global__ void __launch_bounds__(kRtThreads) route_team_grad_kernel(const __gri
 }
 
 // ---------------------------------------------------------------- host
-// Teams of four lanes up to 128 experts, of eight up to 256 and sixteen up to 512; with a bias, up to 128 experts.
+// Teams of four lanes up to 128 experts, of eight up to 256 and sixteen up to 512.
+//
+// Against a warp to a token (us of GPU time, eight experts of a token, softmax): in fp32 65536 tokens over 64 experts
+// 10.1 to 40.6, with a bias 21.9 to 60.5; 32768 over 128 10.4 to 20.9 and 22.9 to 35.1; 8191 over 256 7.7 to 7.6 and
+// (sigmoid) 16.3 to 13.7, over 512 11.9 to 10.3: there fewer warps run at one time, and the slowest tokens are those whose
+// keys lie too close.  16-bit logits without a bias have none of those: 65536 over 64 7.2 to 25.9, 8191 over 256 4.7
+// to 5.8, over 512 7.9 to 8.7.
+bool route_by_teams(int type, int E, int top_k, bool bias) {
+  return top_k <= kRtTeamK && E <= (bias || type == kFp32 ? 128 : kRtTeamExperts);
+}
+
 template <int TYPE, int V>
 static const void* pick_team(int E, bool bias) {
   if (E <= 64) return bias ? (const void*)route_team_kernel<TYPE, 4, 16, V, true> : (const void*)route_team_kernel<TYPE, 4, 16, V, false>;
-  if (E <= 128) return bias ? (const void*)route_team_kernel<TYPE, 4, 32, V, true> : (const void*)route_team_kernel<TYPE, 4, 32, V, false>;
-  if (E <= 256) return (const void*)route_team_kernel<TYPE, 8, 32, V, false>;
-  return (const void*)route_team_kernel<TYPE, 16, 32, V, false>;
+  if constexpr (TYPE != kFp32) {
+    if (E > 256) return (const void*)route_team_kernel<TYPE, 16, 32, V, false>;
+    if (E > 128) return (const void*)route_team_kernel<TYPE, 8, 32, V, false>;
+  }
+  return bias ? (const void*)route_team_kernel<TYPE, 4, 32, V, true> : (const void*)route_team_kernel<TYPE, 4, 32, V, false>;
 }
 template <int TYPE, int V>
 static const void* pick_team_grad(int E) {
@@ -364,13 +376,6 @@ static const void* pick_team_grad(int E) {
 }
 static int teams_of(int E) { return E <= 128 ? 8 : E <= 256 ? 4 : 2; }
 
-// Against a warp to a token (us of GPU time, eight experts of a token; fp32, softmax): 65536 tokens over 64 experts 12.4
-// to 45.7, with a bias 27.5 to 69.6; 32768 over 128 12.7 to 25.5 and 26.0 to 40.7; 8191 over 256 10.0 to 10.8 and 29.7 to
-// 24.5 (so not with a bias there: fewer warps run at one time, and the slowest tokens are those compared in 64 bits);
-// in bf16 without a bias 65536 over 64 7.2 to 25.9, 8191 over 512 7.8 to 8.7.
-bool route_by_teams(int E, int top_k, bool bias) {
-  return top_k <= kRtTeamK && E <= (bias ? 128 : kRtTeamExperts);
-}
 // vec: rows on the grid of 16 bytes.  teams: tokens of a warp.
 const void* route_team_instance(int type, int E, bool vec, bool bias, int* teams) {
   *teams = teams_of(E);
