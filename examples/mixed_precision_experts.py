@@ -6,6 +6,9 @@ serve()  a layer whose routed experts are 4-bit (MoELayer) beside a shared exper
 experts_fp8()  routed experts in FP8: the tokens are gathered in expert order on their
          way through the quantisation, the products are grouped by expert.
 tune()   routed experts in bf16 and their gradients: a few steps of gradient descent.
+tune_adapters()  frozen experts with a low-rank adapter each, behind a router that is trained
+         with them: the outputs, the balance loss and every gradient.
+serve_adapters()  one FP8 projection for requests that each bring an adapter, or none.
 
     python examples/mixed_precision_experts.py
 """
@@ -16,7 +19,9 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
+from weight_only_bit_moe_gb300 import adapters as A  # noqa: E402
 from weight_only_bit_moe_gb300 import products as P  # noqa: E402
+from weight_only_bit_moe_gb300 import routing as R  # noqa: E402
 from weight_only_bit_moe_gb300 import workloads as wk  # noqa: E402
 from weight_only_bit_moe_gb300.layer import MoELayer, batch_to_device  # noqa: E402
 
@@ -109,6 +114,59 @@ def tune(steps=8, tokens=192, experts=4, top_k=2, hidden=256, inter=128, rate=0.
     return losses
 
 
+def tune_adapters(tokens=160, experts=4, top_k=2, hidden=256, inter=128, rank=8, seed=0):
+    """One step's leaves (router, a, b), the objective's gradients by them and, from fp32, the same."""
+    g = torch.Generator("cuda").manual_seed(seed)
+
+    def normal(*shape, scale=1.0):
+        return torch.randn(*shape, generator=g, device="cuda") * scale
+
+    x = normal(tokens, hidden).to(torch.bfloat16)
+    w = normal(experts, inter, hidden, scale=hidden ** -0.5).to(torch.bfloat16)  # frozen
+    leaves = [normal(experts, hidden, scale=hidden ** -0.5), normal(experts, rank, hidden, scale=hidden ** -0.5).to(torch.bfloat16),
+              normal(experts, inter, rank, scale=rank ** -0.5).to(torch.bfloat16)]
+    scale = torch.full((experts,), 2.0, device="cuda")
+    router, a, b = (t.requires_grad_() for t in leaves)
+
+    logits = x.float() @ router.t()
+    weights, ids = R.route(logits, top_k)
+    balance = R.balance_loss(logits, R.expert_counts(ids, experts))
+    order, offsets = P.expert_order(ids, experts)
+    rows = x[(order // top_k).long()]
+    h = A.adapter_linear(rows, a, b, offsets, scale=scale, base=P.grouped_mm(rows, w, offsets))
+    objective = combine(h, order, weights).square().mean() + 0.01 * balance
+    grads = torch.autograd.grad(objective, (router, a, b))
+
+    router, a, b = (t.detach().float().requires_grad_() for t in leaves)
+    logits = x.float() @ router.t()
+    p = torch.softmax(logits, 1)
+    picked = torch.softmax(logits.gather(1, ids.long()), 1)
+    counts = torch.bincount(ids.flatten().long(), minlength=experts).float()
+    balance = experts * (counts / counts.sum() * p.mean(0)).sum()
+    full = torch.einsum("tk,enk->ten", x.float(), w.float())
+    full = full + 2.0 * torch.einsum("tk,erk,enr->ten", x.float(), a, b)
+    out = (full.gather(1, ids.long()[:, :, None].expand(-1, -1, inter)) * picked[:, :, None]).sum(1)
+    want = torch.autograd.grad(out.square().mean() + 0.01 * balance, (router, a, b))
+    return leaves, grads, want
+
+
+def serve_adapters(requests=24, adapters=6, hidden=512, out=384, rank=16, seed=0):
+    """Outputs of one FP8 projection with each request's adapter, and the same in fp32."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    x = torch.randn(requests, hidden, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(out, hidden, generator=g, device="cuda") * hidden ** -0.5
+    a = (torch.randn(adapters, rank, hidden, generator=g, device="cuda") * hidden ** -0.5).to(torch.bfloat16)
+    b = (torch.randn(adapters, out, rank, generator=g, device="cuda") * rank ** -0.5).to(torch.bfloat16)
+    who = torch.randint(-1, adapters, (requests, 1), generator=g, device="cuda")
+    order, offsets = P.expert_order(who, adapters)  # once for all projections of a step
+    y = P.gemm_fp8_block(*P.quant_fp8_block(x), *fp8_weights(w))
+    A.adapter_mm(x, a, b, offsets, order, base=y, out=y)
+    delta = torch.einsum("tk,lrk,lnr->tln", x.float(), a.float(), b.float())
+    delta = torch.cat([torch.zeros_like(delta[:, :1]), delta], 1)  # number -1: none
+    want = x.float() @ w.t() + delta[torch.arange(requests, device="cuda"), who[:, 0] + 1]
+    return y, want
+
+
 def relative(got, want):
     return float((got.float() - want).norm() / want.norm())
 
@@ -119,4 +177,7 @@ if __name__ == "__main__":
     out, want = experts_fp8()
     print(f"routed experts in FP8: relative error {relative(out, want):.4f}")
     print("tuning bf16 experts, loss by step: " + " ".join(f"{v:.4f}" for v in tune()))
+    _, grads, want = tune_adapters()
+    print("adapters and router, relative errors of the gradients: " + " ".join(f"{relative(g, w):.4f}" for g, w in zip(grads, want)))
+    print(f"adapters of many requests on an FP8 projection: relative error {relative(*serve_adapters()):.4f}")
     assert P.products_status() == 0

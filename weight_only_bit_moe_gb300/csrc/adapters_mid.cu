@@ -6,6 +6,12 @@
 // (forward: F = A, S = B; gradient by the rows: F = B^T, S = A^T, read where they lie.)
 // Both are streams: 2 P bytes a row in, then 2 Q in and out, against 2 R (P + 2 Q)
 // operations, R of 8 to 256.
+//
+// This one: 16384 rows of 7168 (one adapter, rank 16) take 43 us, 5.5 TB/s (floor 35);
+// 8191 rows of 4096 of 23 requests, rank 64, 23 us (floor 10): the plan of the tiles,
+// the pipeline's filling and the last tiles' sums cost about 8 us whatever the rows.
+// With the sum cut into slices of equal number instead of equal CTAs: 21 and, for 8188
+// rows of 32 experts of 2880, 19.4 instead of 16.
 #include "adapters.cuh"
 
 namespace moe {

@@ -4,6 +4,13 @@
 // Routing here: a warp owns a token, lane l the PER experts from l PER on; rows on the
 // vectors' grid are loaded four values at a time (V = 4).  (Up to eight experts of up to
 // 512: routing_team.cu.)  Balance: a team of G lanes owns a token.
+//
+// Bound by instructions and, below some thousand tokens, by latencies: 8191 tokens over
+// 256 experts in fp32 take 13.3 us of GPU time with sigmoid and bias (8.9 MB, floor 1.3;
+// 7.6 without a bias: the rest is waited for by the few tokens compared in 64 bits).
+// 65536 tokens over 128 experts in bf16, 17 sequences: counts 4.1, loss 13.9 (16.8 MB,
+// floor 2.5), of which the sums at the end, one latency after the other, are about 4;
+// gradient 8.8 (33.6 MB, floor 5.0).
 #include "routing.cuh"
 
 namespace moe {

@@ -9,6 +9,9 @@
 // ones of one block against the other reversed, sorted again), as do the lanes of a team
 // among each other; the largest key dropped tells whether more than eight come into
 // question.  How keys decide, and what happens where they cannot: routing.cu.
+//
+// 32768 tokens over 128 experts in bf16 take 8.5 us of GPU time (8.4 MB in, floor 1.6),
+// the gradient 7.4 (floor 2.8); a warp to a token took 12.8 and 10.3.
 #include "routing.cuh"
 
 namespace moe {
