@@ -22,8 +22,9 @@
  * at all are unspecified.
  *
  * Sizes.  num_adapters 1 .. 4096, rank 1 .. 256, 1 <= N, K <= 2^21, 0 <= rows <
- * 2^31 - 1024.  Any strides and alignment are computed; the fast kernels take
- * matrices whose base addresses and strides are multiples of 16 bytes.
+ * 2^31 - 1024.  Any sizes, strides and alignment are computed; the fast kernels take
+ * N, K and ranks that are multiples of 8 and matrices whose base addresses and strides
+ * are multiples of 16 bytes (ranks in between: a and b filled up with zeros).
  */
 #ifndef MOE_ADAPTERS_H
 #define MOE_ADAPTERS_H
@@ -48,8 +49,8 @@ extern "C" {
  *           b_stride_n >= rank
  *   scale   fp32 [num_adapters], or NULL for ones
  *   base    [rows, N] or NULL for zeros; may be out itself (same strides: then the
- *           rows without an adapter are not touched), else does not overlap it
- *   out     [rows, N], or NULL: then only mid is computed (b, base and scale are not
+ *           rows without an adapter are not touched)
+ *   out     [rows, N], overlapping no other operand; or NULL: then only mid is computed (b, base and scale are not
  *           read)
  *   mid     fp32 [rows, rank], contiguous: written at the positions of adapters (for
  *           moe_adapter_mm_dw), unspecified at the others.  NULL: kept in the

@@ -87,6 +87,20 @@ def test_parts_that_the_workspace_does_not_hold(A, dtype):
     check_all(A, make([500, 700], 256, 13000, 12808, dtype))  # gradients by whole adapters
 
 
+def test_no_rows(A):
+    for rank, n, k in ((16, 136, 264), (5, 33, 50)):
+        s = make([0, 0], rank, n, k, BF)
+        assert A.adapter_mm(s["x"], s["a"], s["b"], s["offsets"], base=s["base"]).shape == (0, n)
+        da, db = A.adapter_mm_dw(s["dy"], s["x"], *(torch.zeros(0, rank, device="cuda") for _ in range(2)), s["offsets"])
+        assert (da == 0).all() and (db == 0).all() and da.shape == (2, rank, k) and db.shape == (2, n, rank)
+
+
+@pytest.mark.parametrize("rank", [4, 12])
+@pytest.mark.parametrize("sizes", [[1, 0, 2, 61], [100, 180, 40]])
+def test_ranks_off_the_grid(A, rank, sizes):
+    check_all(A, make(sizes, rank, 264, 520, BF, before=1, after=2), torch.float32)
+
+
 def test_one_adapter_of_many_rows(A):
     check_all(A, make([70000], 16, 136, 264, BF, order=False))
     check_all(A, make([3, 30000, 5], 40, 264, 136, FP), torch.float32)

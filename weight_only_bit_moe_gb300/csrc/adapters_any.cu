@@ -1,7 +1,9 @@
-// The adapters of moe_adapters.h for any size, stride and alignment, in three plain
-// kernels: the first product (mid), the second (out) and the gradients.  64 x 64
-// values to a CTA, 4 x 4 fp32 sums to a thread, 16 terms at a time in shared memory,
-// single elements loaded: bound by these loads and the fp32 multiply-adds.
+// The adapters of moe_adapters.h for any size, stride and alignment, in plain kernels:
+// the first product (mid), the second (out) and the gradients.  64 x 64 values to a CTA,
+// 4 x 4 fp32 sums to a thread, 16 terms at a time in shared memory, single elements
+// loaded: bound by these loads and the fp32 multiply-adds.  Few rows, which would leave
+// most of the GPU without work so, have a warp to a value of mid and a thread to one of
+// out.
 #include "adapters.cuh"
 
 namespace moe {
@@ -126,6 +128,45 @@ __global__ void __launch_bounds__(kAaThreads) adapter_any_out_kernel(const __gri
   }
 }
 
+template <bool FWD>
+__global__ void __launch_bounds__(kAaThreads) adapter_any_few_mid_kernel(const __grid_constant__ AdapterArgs a) {
+  if (aa_broken(a.offsets, a.rows, a.L, a.status)) return;
+  const int i = blockIdx.x, j = blockIdx.y * (kAaThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int l = first_adapter(a.offsets, a.rows, a.L, i);
+  if (l >= a.L || j >= a.R) return;
+  int i0, i1;
+  adapter_rows(a.offsets, a.rows, l, i0, i1);
+  if (i < i0) return;
+  const int r = row_of(a.order, a.rows, i, a.status);
+  float sum = 0.0f;
+  if (r >= 0)
+#pragma unroll 4
+    for (int p = lane; p < a.P; p += 32)
+      sum = fmaf(load_elem(a.in, r * a.in_ld + p, a.type),
+                 load_elem(a.f, l * a.f_l + (FWD ? j * a.f_r + p : p * a.f_r + j), a.type), sum);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) a.mid[(int64_t)i * a.R + j] = sum;
+}
+
+template <bool FWD>
+__global__ void __launch_bounds__(kAaThreads) adapter_any_few_out_kernel(const __grid_constant__ AdapterArgs a) {
+  if (aa_broken(a.offsets, a.rows, a.L, a.status)) return;
+  const int i = blockIdx.x, q = blockIdx.y * kAaThreads + threadIdx.x;
+  const int l = first_adapter(a.offsets, a.rows, a.L, i);
+  if (l >= a.L || q >= a.Q) return;
+  int i0, i1;
+  adapter_rows(a.offsets, a.rows, l, i0, i1);
+  const int r = i < i0 ? -1 : row_of(a.order, a.rows, i, a.status);
+  if (r < 0) return;
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int j = 0; j < a.R; ++j)
+    sum = fmaf(a.mid[(int64_t)i * a.R + j], load_elem(a.s, l * a.s_l + (FWD ? q * a.s_r + j : j * a.s_r + q), a.type), sum);
+  const float base = a.base ? load_elem(a.base, r * a.base_ld + q, a.type) : 0.0f;
+  store_elem(a.out, r * a.out_ld + q, a.type, fmaf(a.scale ? a.scale[l] : 1.0f, sum, base));
+}
+
 // out = base for the rows without an adapter: positions before the first adapter's and
 // from the last one's end on.  A CTA per position, in turn.
 __global__ void __launch_bounds__(kAaThreads) adapter_rest_kernel(const __grid_constant__ AdapterArgs a) {
@@ -179,6 +220,18 @@ __global__ void __launch_bounds__(kAaThreads) adapter_any_grad_kernel(const __gr
 static unsigned aa_tiles(int n) { return (unsigned)((n + kAaTile - 1) / kAaTile); }
 
 cudaError_t launch_adapter_any(const AdapterArgs& a, bool fwd, cudaStream_t st) {
+  if (a.rows <= kAdFewRows) {
+    const dim3 mid(a.rows, (unsigned)((a.R + kAaThreads / 32 - 1) / (kAaThreads / 32)));
+    const dim3 out(a.rows, (unsigned)((a.Q + kAaThreads - 1) / kAaThreads));
+    if (fwd) {
+      adapter_any_few_mid_kernel<true><<<mid, kAaThreads, 0, st>>>(a);
+      if (a.out) adapter_any_few_out_kernel<true><<<out, kAaThreads, 0, st>>>(a);
+    } else {
+      adapter_any_few_mid_kernel<false><<<mid, kAaThreads, 0, st>>>(a);
+      if (a.out) adapter_any_few_out_kernel<false><<<out, kAaThreads, 0, st>>>(a);
+    }
+    return cudaPeekAtLastError();
+  }
   const dim3 mid(aa_tiles(a.rows), aa_tiles(a.R)), out(aa_tiles(a.rows), aa_tiles(a.Q));
   if (fwd) {
     adapter_any_mid_kernel<true><<<mid, kAaThreads, 0, st>>>(a);
