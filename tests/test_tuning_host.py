@@ -123,6 +123,43 @@ def test_adapter_gradient_refusals(lib, bad):
     assert call(lib, "moe_adapter_mm_dw", {**DW, **workspace(lib)}, bad) == lib.MOE_ERR_INVALID
 
 
+# ---------------------------------------------------------------- arguments in one array
+def entries(lib):
+    return (("moe_route", lib.route, ROUTE), ("moe_route_grad", lib.route_grad, ROUTE_GRAD),
+            ("moe_expert_counts", lib.expert_counts, {**COUNTS, **workspace(lib)}),
+            ("moe_balance_loss", lib.balance_loss, {**LOSS, **workspace(lib)}),
+            ("moe_balance_loss_grad", lib.balance_loss_grad, {**LOSS_GRAD, **workspace(lib)}),
+            ("moe_adapter_mm", lib.adapter_mm, {**MM, **workspace(lib)}),
+            ("moe_adapter_mm_dx", lib.adapter_mm_dx, {**MM, **workspace(lib)}),
+            ("moe_adapter_mm_dw", lib.adapter_mm_dw, {**DW, **workspace(lib)}))
+
+
+def test_packed_arguments_arrive_in_their_places(lib):
+    # Each argument made wrong on its own, so that nothing is launched: both ways give the entry's own answer.
+    for fn, packed, args in entries(lib):
+        for name in args:
+            if name in ("scale", "stream", "order", "bias") and fn.startswith("moe_route"):
+                continue
+            bad = dict(args, **{name: -1 if name not in ("stream", "accumulate", "renormalize") else 2})
+            if name == "stream":
+                bad["rows" if "rows" in bad else "tokens"] = -1
+            assert packed(*bad.values()) == call(lib, fn, bad, {}) in (lib.MOE_ERR_INVALID, lib.MOE_ERR_WORKSPACE), (fn, name)
+
+
+def test_packed_calls_refuse(lib):
+    import struct
+    moe_call = lib.load().moe_call
+    one = struct.pack("q", 0)
+    for entry in (-1, 8, 1 << 20):
+        assert moe_call(entry, one, 1) == lib.MOE_ERR_INVALID
+    for entry, (fn, _, args) in enumerate(entries(lib)):
+        n = len(args)
+        values = struct.pack(f"{n + 1}q", *[0] * (n + 1))
+        assert moe_call(entry, None, n) == lib.MOE_ERR_INVALID
+        for count in (-1, 0, n - 1, n + 1):
+            assert moe_call(entry, values, count) == lib.MOE_ERR_INVALID, (fn, count)
+
+
 def test_no_fallback_on_the_cpu(lib):
     from weight_only_bit_moe_gb300 import adapters as A
     from weight_only_bit_moe_gb300 import routing as R

@@ -25,11 +25,11 @@ from . import products as P
 # As in ``products``, the checks read each attribute of a tensor once: for a decode step they are most of a call's time.
 
 def _positions(offsets: torch.Tensor, order: Optional[torch.Tensor], scale: Optional[torch.Tensor], adapters: int,
-               rows: int) -> Tuple[Optional[int], Optional[int]]:
-    """Addresses of order and scale, which may be None."""
+               rows: int) -> Tuple[int, int]:
+    """Addresses of order and scale (0: None)."""
     if offsets.dtype is not torch.int32 or offsets.shape != (adapters + 1,) or not offsets.is_contiguous():
         P._check_offsets(offsets, adapters)
-    order_at = scale_at = None
+    order_at = scale_at = 0
     if order is not None:
         if order.dtype is not torch.int32 or order.shape != (rows,) or not order.is_contiguous():
             raise ValueError(f"order: expected contiguous int32 [{rows}], got {order.dtype} {tuple(order.shape)}")
@@ -86,8 +86,7 @@ def _by_row(fn: str, name: str, rows_in: torch.Tensor, a, b, offsets, order, sca
     if width != in_width or step != 1 or ld < width:
         ld = P._rows(rows_in, name, in_width, rows)
     order_at, scale_at = _positions(offsets, order, scale, L, rows)
-    base_at = out_at = mid_at = None
-    base_ld = out_ld = 0
+    base_at = out_at = mid_at = base_ld = out_ld = 0
     if base is not None:
         base_at, base_ld = base.data_ptr(), _ld(base, "base", dtype, out_width, rows)
     if out is not None:
@@ -103,9 +102,10 @@ def _by_row(fn: str, name: str, rows_in: torch.Tensor, a, b, offsets, order, sca
     if stream is not None:
         P._used_on(stream, rows_in, a, b, offsets, order, scale, base, out, mid)
     h = P._handle(dev, stream)
-    rc = B.function(fn)(code, rows_in.data_ptr(), ld, a.data_ptr(), a_l, a_r, b.data_ptr(), b_l, b_n,
-                        offsets.data_ptr(), order_at, scale_at, L, rows, N, K, R, base_at, base_ld, out_at, out_ld,
-                        mid_at, P._workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    rc = (B.adapter_mm if forward else B.adapter_mm_dx)(
+        code, rows_in.data_ptr(), ld, a.data_ptr(), a_l, a_r, b.data_ptr(), b_l, b_n, offsets.data_ptr(), order_at,
+        scale_at, L, rows, N, K, R, base_at, base_ld, out_at, out_ld, mid_at, P._workspace(dev, h, stream),
+        B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
     if rc:
         raise B.MoeError(fn, rc)
     return out
@@ -169,10 +169,10 @@ def adapter_mm_dw(dy: Optional[torch.Tensor], x: Optional[torch.Tensor], mid_x: 
         raise ValueError(f"adapter_mm_dw: {out_dtype} gradients, expected {dtype} or float32")
     if accumulate and (out_dtype is not torch.float32 or any(out[i] is None for i in sides)):
         raise ValueError("adapter_mm_dw: accumulate needs float32 out")
-    widths, lds, mid_at, grads, args = [1, 1], [0, 0], [None, None], [None, None], []
+    widths, lds, mid_at, grads, args = [1, 1], [0, 0], [0, 0], [None, None], []
     for i in range(2):
         if rows_in[i] is None:
-            args += [None, 0, 0]
+            args += [0, 0, 0]
             continue
         widths[i] = P._dims(rows_in[i], names[i], 2)[1]
         lds[i] = P._rows(rows_in[i], names[i], widths[i], rows)
@@ -187,8 +187,8 @@ def adapter_mm_dw(dy: Optional[torch.Tensor], x: Optional[torch.Tensor], mid_x: 
     if stream is not None:
         P._used_on(stream, *rows_in, *mids, offsets, order, scale, *grads)
     h = P._handle(dev, stream)
-    at = [None if t is None else t.data_ptr() for t in rows_in]
-    rc = B.function("moe_adapter_mm_dw")(
+    at = [0 if t is None else t.data_ptr() for t in rows_in]
+    rc = B.adapter_mm_dw(
         code, at[1], lds[1], at[0], lds[0], mid_at[1], mid_at[0], offsets.data_ptr(), order_at, scale_at, L, rows,
         widths[1], widths[0], R, code if out_dtype is dtype else B.MOE_FP32, 1 if accumulate else 0, *args,
         P._workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)

@@ -1,5 +1,5 @@
 """ctypes binding of the C ABI declared in include/ (moe_w4a16.h, moe_requant.h,
-moe_products.h, moe_routing.h, moe_adapters.h).
+moe_products.h, moe_routing.h, moe_adapters.h, moe_calls.h).
 
 Argument marshalling only: torch tensors are passed as their data pointers,
 streams as their CUDA handles; every step of the layer runs in the library's
@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import platform
+import struct
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -26,7 +27,7 @@ EXPORTED = ("moe_repack_size", "moe_repack_weights", "moe_repack_weights_ex", "m
             "moe_requant_launch_geometry", "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw",
             "moe_quant_fp8_block", "moe_gemm_fp8_block", "moe_capture_id", "moe_capture_mode", "moe_capture_watch",
             "moe_route", "moe_route_grad", "moe_expert_counts", "moe_balance_loss", "moe_balance_loss_grad",
-            "moe_adapter_mm", "moe_adapter_mm_dx", "moe_adapter_mm_dw")
+            "moe_adapter_mm", "moe_adapter_mm_dx", "moe_adapter_mm_dw", "moe_call")
 MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_MAX_TOP_K = 32
@@ -112,6 +113,7 @@ def load(path: str = ""):
                                             p, i64, p, i64, p, p, i64, p]),
                 "moe_adapter_mm_dw": (i32, [i32, p, i64, p, i64, p, p, p, p, p, i32, i32, i32, i32, i32, i32, i32, p,
                                             i64, i64, p, i64, i64, p, i64, p]),
+                "moe_call": (i32, [i32, ctypes.c_char_p, i32]),
                 "moe_capture_id": (i32, [p, ctypes.POINTER(ctypes.c_uint64)]),
                 "moe_capture_mode": (i32, [ctypes.POINTER(i32)]),
                 "moe_capture_watch": (i32, [p, ctypes.POINTER(ctypes.POINTER(ctypes.c_int32))]),
@@ -132,6 +134,27 @@ def function(name: str):
     if fn is None:
         fn = _functions[name] = getattr(load(), name)
     return fn
+
+
+def _packed(entry: int, args: str):
+    """A call of moe_call: the arguments of the entry's own signature, each as `args` has it (q: an integer or address,
+    0 for NULL; d: a float)."""
+    pack, count = struct.Struct(args).pack, len(args)
+
+    def call(*values) -> int:
+        return function("moe_call")(entry, pack(*values), count)
+
+    return call
+
+
+route = _packed(0, "qqqqqqqqqdqqq")
+route_grad = _packed(1, "qqqqqqqqqqqdqqq")
+expert_counts = _packed(2, "q" * 11)
+balance_loss = _packed(3, "q" * 13)
+balance_loss_grad = _packed(4, "q" * 15)
+adapter_mm = _packed(5, "q" * 25)
+adapter_mm_dx = _packed(6, "q" * 25)
+adapter_mm_dw = _packed(7, "q" * 26)
 
 
 def _p(t):

@@ -17,7 +17,7 @@ SOURCES = ["align.cu", "repack.cu", "gemm_int4.cu", "gemm_int4x.cu", "gemm_mxfp4
            "requant.cu", "products.cu", "products_any.cu", "products_grouped.cu", "products_fp8.cu", "quant.cu",
            "routing.cu", "routing_team.cu", "adapters.cu", "adapters_any.cu", "adapters_few.cu",
            "adapters_mid.cu", "adapters_out_fwd.cu", "adapters_out_dx.cu", "adapters_grad.cu",
-           "api.cu"]
+           "calls.cu", "api.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC"]

@@ -1,0 +1,49 @@
+// The entry of moe_calls.h.
+#include <string.h>
+
+#include <type_traits>
+#include <utility>
+
+#include "../../include/moe_calls.h"
+
+namespace moe {
+
+template <typename T>
+static T argument(int64_t v) {
+  if constexpr (std::is_pointer<T>::value) {
+    return reinterpret_cast<T>(static_cast<intptr_t>(v));
+  } else if constexpr (std::is_same<T, float>::value) {
+    double d;
+    memcpy(&d, &v, sizeof(d));
+    return static_cast<float>(d);
+  } else {
+    return static_cast<T>(v);
+  }
+}
+
+template <typename... Args, size_t... I>
+static int spread(int (*entry)(Args...), const int64_t* args, int count, std::index_sequence<I...>) {
+  if (count != (int)sizeof...(Args)) return MOE_ERR_INVALID;
+  return entry(argument<Args>(args[I])...);
+}
+template <typename... Args>
+static int spread(int (*entry)(Args...), const int64_t* args, int count) {
+  return spread(entry, args, count, std::index_sequence_for<Args...>{});
+}
+
+}  // namespace moe
+
+extern "C" int moe_call(int entry, const int64_t* args, int count) {
+  if (!args) return MOE_ERR_INVALID;
+  switch (entry) {
+    case MOE_ENTRY_ROUTE: return moe::spread(moe_route, args, count);
+    case MOE_ENTRY_ROUTE_GRAD: return moe::spread(moe_route_grad, args, count);
+    case MOE_ENTRY_EXPERT_COUNTS: return moe::spread(moe_expert_counts, args, count);
+    case MOE_ENTRY_BALANCE_LOSS: return moe::spread(moe_balance_loss, args, count);
+    case MOE_ENTRY_BALANCE_LOSS_GRAD: return moe::spread(moe_balance_loss_grad, args, count);
+    case MOE_ENTRY_ADAPTER_MM: return moe::spread(moe_adapter_mm, args, count);
+    case MOE_ENTRY_ADAPTER_MM_DX: return moe::spread(moe_adapter_mm_dx, args, count);
+    case MOE_ENTRY_ADAPTER_MM_DW: return moe::spread(moe_adapter_mm_dw, args, count);
+    default: return MOE_ERR_INVALID;
+  }
+}

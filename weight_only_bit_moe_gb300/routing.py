@@ -76,7 +76,7 @@ def topk_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: O
     how = _score(score)
     if not 1 <= top_k <= min(experts, B.MOE_MAX_TOP_K):
         raise ValueError(f"top_k {top_k} of {experts} experts, at most {B.MOE_MAX_TOP_K}")
-    bias_at = None if bias is None else _vector(bias, "bias", torch.float32, (experts,))
+    bias_at = 0 if bias is None else _vector(bias, "bias", torch.float32, (experts,))
     if weights is None:
         weights = P._empty((tokens, top_k), torch.float32, logits, stream)
         weights_at = weights.data_ptr()
@@ -89,8 +89,8 @@ def topk_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: O
         ids_at = _vector(ids, "ids", torch.int32, (tokens, top_k))
     if stream is not None:
         P._used_on(stream, logits, bias, weights, ids)
-    rc = B.function("moe_route")(code, logits.data_ptr(), ld, bias_at, tokens, experts, top_k, how,
-                                 1 if renormalize else 0, scale, weights_at, ids_at, P._handle(dev, stream))
+    rc = B.route(code, logits.data_ptr(), ld, bias_at, tokens, experts, top_k, how, 1 if renormalize else 0, scale,
+                 weights_at, ids_at, P._handle(dev, stream))
     if rc:
         raise B.MoeError("moe_route", rc)
     return weights, ids
@@ -117,9 +117,8 @@ def topk_route_grad(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Ten
     out, out_ld = _dlogits(out, logits, stream)
     if stream is not None:
         P._used_on(stream, dweights, logits, ids, out)
-    rc = B.function("moe_route_grad")(code, dweights.data_ptr(), dw_ld, logits.data_ptr(), ld, ids_at, tokens, experts,
-                                      top_k, how, 1 if renormalize else 0, scale, out.data_ptr(), out_ld,
-                                      P._handle(dev, stream))
+    rc = B.route_grad(code, dweights.data_ptr(), dw_ld, logits.data_ptr(), ld, ids_at, tokens, experts, top_k,
+                      how, 1 if renormalize else 0, scale, out.data_ptr(), out_ld, P._handle(dev, stream))
     if rc:
         raise B.MoeError("moe_route_grad", rc)
     return out
@@ -149,10 +148,10 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: Option
     return Route.apply(logits, top_k, score, bias, renormalize, scale)
 
 
-def _sequences(offsets: Optional[torch.Tensor]) -> Tuple[Optional[int], int]:
+def _sequences(offsets: Optional[torch.Tensor]) -> Tuple[int, int]:
     """Address of the offsets and number of sequences (None: one of all tokens)."""
     if offsets is None:
-        return None, 1
+        return 0, 1
     S = P._dims(offsets, "offsets", 1)[0] - 1
     if S < 1:
         raise ValueError("offsets: no sequence")
@@ -185,8 +184,8 @@ def expert_counts(ids: torch.Tensor, num_experts: int, offsets: Optional[torch.T
     if stream is not None:
         P._used_on(stream, ids, offsets, out)
     h = P._handle(dev, stream)
-    rc = B.function("moe_expert_counts")(ids.data_ptr(), ld, tokens, top_k, at, S, num_experts, out_at,
-                                         P._workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    rc = B.expert_counts(ids.data_ptr(), ld, tokens, top_k, at, S, num_experts, out_at,
+                         P._workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
     if rc:
         raise B.MoeError("moe_expert_counts", rc)
     return out
@@ -210,9 +209,8 @@ def balance(logits: torch.Tensor, counts: torch.Tensor, offsets: Optional[torch.
     if stream is not None:
         P._used_on(stream, logits, counts, offsets, loss)
     h = P._handle(dev, stream)
-    rc = B.function("moe_balance_loss")(code, logits.data_ptr(), ld, tokens, experts, counts_at, at, S, how,
-                                        loss.data_ptr(), P._workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES,
-                                        h)
+    rc = B.balance_loss(code, logits.data_ptr(), ld, tokens, experts, counts_at, at, S, how, loss.data_ptr(),
+                        P._workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
     if rc:
         raise B.MoeError("moe_balance_loss", rc)
     return loss
@@ -236,9 +234,8 @@ def balance_grad(dloss: torch.Tensor, logits: torch.Tensor, counts: torch.Tensor
     if stream is not None:
         P._used_on(stream, dloss, logits, counts, offsets, out)
     h = P._handle(dev, stream)
-    rc = B.function("moe_balance_loss_grad")(code, dloss_at, logits.data_ptr(), ld, tokens, experts, counts_at, at, S,
-                                             how, out.data_ptr(), out_ld, P._workspace(dev, h, stream),
-                                             B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
+    rc = B.balance_loss_grad(code, dloss_at, logits.data_ptr(), ld, tokens, experts, counts_at, at, S, how,
+                             out.data_ptr(), out_ld, P._workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
     if rc:
         raise B.MoeError("moe_balance_loss_grad", rc)
     return out
