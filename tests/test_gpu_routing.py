@@ -141,6 +141,21 @@ def test_extreme_logits(R, score):
     assert torch.isfinite(loss) and torch.isfinite(R.balance_grad(torch.ones_like(loss), logits, R.expert_counts(ids, 4), None, score)).all()
 
 
+@pytest.mark.parametrize("experts,top_k", [(16, 2), (40, 3), (40, 20), (300, 8), (1000, 32)])
+def test_distances_past_the_largest_number(R, experts, top_k):
+    """Experts so far below the largest that fp32 has no number for the distance still go by their own values."""
+    g = torch.Generator("cuda").manual_seed(experts)
+    far = -(1.0 + 2.3 * torch.rand(20, experts, generator=g, device="cuda")) * 1e38
+    far[:, 7] = 3.3e38
+    far[10:, 3] = 2e29
+    for score in ("softmax", "sigmoid"):
+        for logits, bias in ((far, None), (far, far[0] * 0.1), (far * 1e-38, far[0].contiguous()), (far, -far[1])):
+            w, ids = R.topk_route(logits, top_k, score, bias)
+            want, want_ids = ref_route(logits, top_k, score, bias, True, 1.0)
+            assert torch.equal(ids, want_ids)
+            assert_bound(w, want, 2.0 ** -16 * want.abs() + 2.0 ** -126, "weights")
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_nan_and_infinity_are_seen(R, score):
     logits = make_logits(6, 40)
@@ -391,6 +406,38 @@ def test_captured_and_on_another_stream(R):
         side.synchronize()
         for a, b in zip((w, ids, counts, loss, d), want_other):
             assert torch.equal(a, b)
+
+
+def test_captured_training_step(R):
+    """Route, balance loss and adapters with their gradients in one graph, no eager graph of them left."""
+    from weight_only_bit_moe_gb300 import adapters as A
+    g = torch.Generator("cuda").manual_seed(5)
+
+    def make(*shape):
+        return (torch.randn(*shape, generator=g, device="cuda") * 0.2).to(torch.bfloat16)
+
+    x, a, b = make(300, 64), make(2, 8, 64), make(2, 72, 8)
+    logits, offsets = make_logits(300, 32), offsets_of([200, 90])
+
+    def run():
+        leaves = [t.detach().requires_grad_() for t in (x, a, b, logits)]
+        y = A.adapter_linear(*leaves[:3], offsets)
+        weights, ids = R.route(leaves[3], 4)
+        loss = R.balance_loss(leaves[3], R.expert_counts(ids, 32, offsets), offsets)
+        total = y.float().square().sum() + (weights * weights).sum() + loss.sum()
+        return torch.autograd.grad(total, leaves)
+
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for t in (x, a, b):
+        t.copy_(make(*t.shape))
+    logits.copy_(make_logits(300, 32, seed=9))
+    graph.replay()
+    torch.cuda.synchronize()
+    for replayed, eager in zip(got, run()):
+        assert torch.equal(replayed, eager)
 
 
 def test_router_layer_adapters_together(R):

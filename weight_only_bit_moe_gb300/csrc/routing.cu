@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const __grid_constant
     for (int i = 0; i < PER; ++i) z += expf(v[i] - shift);
     z = warp_sum(z);
   }
-  float largest = shift;  // of what is chosen by
+  float largest = key_origin(shift);  // of what is chosen by
   if (BIAS) {
     most = -INFINITY;
 #pragma unroll
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const __grid_constant
         most = fmaxf(most, v[i]);
       }
     }
-    largest = finite_or_0(warp_max(most));
+    largest = key_origin(warp_max(most));
   }
   int32_t* ids = a.ids + token * a.k;
   float* weights = a.weights + token * a.k;

@@ -60,6 +60,8 @@ __device__ __forceinline__ float sigmoid(float l) {
 }
 // What is subtracted before exponentials: the largest value, or 0 for a token of -infinities.
 __device__ __forceinline__ float finite_or_0(float v) { return v == -INFINITY ? 0.0f : v; }
+// What keys are relative to: the largest value; 0 where there is none or a distance from it could overflow.
+__device__ __forceinline__ float key_origin(float v) { return fabsf(v) < 1e30f ? v : 0.0f; }
 
 // Four consecutive values.
 template <int TYPE>

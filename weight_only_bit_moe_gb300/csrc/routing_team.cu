@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kRtThreads) route_team_kernel(const __grid_con
     for (int i = 0; i < PER; ++i) z += exp2_of((v[i] - shift) * kLog2e);
     z = team_sum<G>(z);
   }
-  float largest = shift;  // of what is chosen by
+  float largest = key_origin(shift);  // of what is chosen by
   if (BIAS) {
     const float inv = 1.0f / z;
     most = -INFINITY;
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kRtThreads) route_team_kernel(const __grid_con
         most = fmaxf(most, v[i]);
       }
     }
-    largest = finite_or_0(team_max<G>(most));
+    largest = key_origin(team_max<G>(most));
   }
   // NaN or +infinity among the team's values
   const bool lost = (__ballot_sync(0xffffffffu, bad) >> (team * G)) & (G == 32 ? 0xffffffffu : (1u << G) - 1u);
