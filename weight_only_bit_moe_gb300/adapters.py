@@ -134,6 +134,27 @@ def adapter_mm_dx(dy: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets: t
     return _by_row("moe_adapter_mm_dx", "dy", dy, a, b, offsets, order, scale, base, out, mid, stream, False)
 
 
+def _rows_and_mid(t: torch.Tensor, name: str, mid: torch.Tensor, mid_name: str, rows: int,
+                  rank: int) -> Tuple[int, int, int, int]:
+    """(address, row stride, columns) of t, address of its mid."""
+    there, width = P._dims(t, name, 2)
+    ld, step = t.stride()
+    if there != rows or step != 1 or ld < width:
+        ld = P._rows(t, name, width, rows)
+    return t.data_ptr(), ld, width, _mid(mid, mid_name, rows, rank)
+
+
+def _gradient(out: Optional[torch.Tensor], shape: Tuple[int, int, int], dtype: torch.dtype, like: torch.Tensor,
+              stream) -> Tuple[torch.Tensor, int, int, int]:
+    """The gradient of a factor (new unless given), its address and strides."""
+    if out is None:
+        out = P._empty(shape, dtype, like, stream)
+        return out, out.data_ptr(), shape[1] * shape[2], shape[2]
+    if out.shape != shape or out.dtype is not dtype:
+        raise ValueError(f"out: {out.dtype} {tuple(out.shape)}, expected {dtype} {list(shape)}")
+    return (out, out.data_ptr(), *P._bank(out, "out", shape))
+
+
 def adapter_mm_dw(dy: Optional[torch.Tensor], x: Optional[torch.Tensor], mid_x: Optional[torch.Tensor],
                   mid_dy: Optional[torch.Tensor], offsets: torch.Tensor, order: Optional[torch.Tensor] = None,
                   scale: Optional[torch.Tensor] = None, out=(None, None), out_dtype: Optional[torch.dtype] = None,
@@ -142,59 +163,53 @@ def adapter_mm_dw(dy: Optional[torch.Tensor], x: Optional[torch.Tensor], mid_x: 
     adapter_mm_dx, in out_dtype (the operands' type or float32): da = scale[l] mid_dy^T x, db = scale[l] dy^T mid_x
     over the rows of each adapter.  Without x and mid_dy there is no da, without dy and mid_x no db (None in its
     place).  out: (da, db) to write, or with accumulate to add to (float32)."""
-    rows_in, mids = (x, dy), (mid_dy, mid_x)
-    names, mid_names = ("x", "dy"), ("mid_dy", "mid_x")
-    sides = [i for i in range(2) if rows_in[i] is not None]
-    if not sides or any((rows_in[i] is None) != (mids[i] is None) for i in range(2)):
+    if (x is None) is not (mid_dy is None) or (dy is None) is not (mid_x is None) or (x is None and dy is None):
         raise ValueError("adapter_mm_dw: x with mid_dy, dy with mid_x, or both pairs expected")
-    first = rows_in[sides[0]]
-    dev = P._device(first, *rows_in, *mids, offsets, order, scale, *out)
+    da, db = out
+    first, name, mid, mid_name = (dy, "dy", mid_x, "mid_x") if x is None else (x, "x", mid_dy, "mid_dy")
+    dev = P._device(first, x, dy, mid_dy, mid_x, offsets, order, scale, da, db)
     if dev != P._current_device():
         with torch.cuda.device(dev):
             return adapter_mm_dw(dy, x, mid_x, mid_dy, offsets, order, scale, out, out_dtype, accumulate, stream)
-    rows = P._dims(first, names[sides[0]], 2)[0]
-    R = P._dims(mids[sides[0]], mid_names[sides[0]], 2)[1]
+    rows = P._dims(first, name, 2)[0]
+    R = P._dims(mid, mid_name, 2)[1]
     L = P._dims(offsets, "offsets", 1)[0] - 1
     if not 1 <= R <= B.MOE_MAX_RANK or not 1 <= L <= B.MOE_MAX_ADAPTERS:
         raise ValueError(f"adapter_mm_dw: {L} adapters of rank {R}, at most {B.MOE_MAX_ADAPTERS} of {B.MOE_MAX_RANK}")
     order_at, scale_at = _positions(offsets, order, scale, L, rows)
     dtype = first.dtype
     code = P._HALF.get(dtype)
-    if code is None or any(rows_in[i].dtype is not dtype for i in sides):
-        raise P._types("adapter_mm_dw", *(rows_in[i] for i in sides))
-    given = [t for t in out if t is not None]
+    if code is None or (x is not None and dy is not None and dy.dtype is not dtype):
+        raise P._types("adapter_mm_dw", *(t for t in (x, dy) if t is not None))
     if out_dtype is None:
-        out_dtype = given[0].dtype if given else dtype
+        out_dtype = dtype if da is None and db is None else db.dtype if da is None else da.dtype
     if out_dtype is not dtype and out_dtype is not torch.float32:
         raise ValueError(f"adapter_mm_dw: {out_dtype} gradients, expected {dtype} or float32")
-    if accumulate and (out_dtype is not torch.float32 or any(out[i] is None for i in sides)):
+    missing = (x is not None and da is None) or (dy is not None and db is None)
+    if accumulate and (missing or out_dtype is not torch.float32):
         raise ValueError("adapter_mm_dw: accumulate needs float32 out")
-    widths, lds, mid_at, grads, args = [1, 1], [0, 0], [0, 0], [None, None], []
-    for i in range(2):
-        if rows_in[i] is None:
-            args += [0, 0, 0]
-            continue
-        widths[i] = P._dims(rows_in[i], names[i], 2)[1]
-        lds[i] = P._rows(rows_in[i], names[i], widths[i], rows)
-        mid_at[i] = _mid(mids[i], mid_names[i], rows, R)
-        shape = (L, R, widths[i]) if i == 0 else (L, widths[i], R)
-        grads[i] = out[i]
-        if grads[i] is None:
-            grads[i] = P._empty(shape, out_dtype, first, stream)
-        elif tuple(grads[i].shape) != shape or grads[i].dtype is not out_dtype:
-            raise ValueError(f"out: {grads[i].dtype} {tuple(grads[i].shape)}, expected {out_dtype} {list(shape)}")
-        args += [grads[i].data_ptr(), *P._bank(grads[i], "out", shape)]
+    x_at = x_ld = mid_dy_at = da_at = da_l = da_r = dy_at = dy_ld = mid_x_at = db_at = db_l = db_n = 0
+    N = K = 1
+    if x is None:
+        da = None
+    else:
+        x_at, x_ld, K, mid_dy_at = _rows_and_mid(x, "x", mid_dy, "mid_dy", rows, R)
+        da, da_at, da_l, da_r = _gradient(da, (L, R, K), out_dtype, x, stream)
+    if dy is None:
+        db = None
+    else:
+        dy_at, dy_ld, N, mid_x_at = _rows_and_mid(dy, "dy", mid_x, "mid_x", rows, R)
+        db, db_at, db_l, db_n = _gradient(db, (L, N, R), out_dtype, dy, stream)
     if stream is not None:
-        P._used_on(stream, *rows_in, *mids, offsets, order, scale, *grads)
+        P._used_on(stream, x, dy, mid_dy, mid_x, offsets, order, scale, da, db)
     h = P._handle(dev, stream)
-    at = [0 if t is None else t.data_ptr() for t in rows_in]
     rc = B.adapter_mm_dw(
-        code, at[1], lds[1], at[0], lds[0], mid_at[1], mid_at[0], offsets.data_ptr(), order_at, scale_at, L, rows,
-        widths[1], widths[0], R, code if out_dtype is dtype else B.MOE_FP32, 1 if accumulate else 0, *args,
+        code, dy_at, dy_ld, x_at, x_ld, mid_x_at, mid_dy_at, offsets.data_ptr(), order_at, scale_at, L, rows, N, K, R,
+        code if out_dtype is dtype else B.MOE_FP32, 1 if accumulate else 0, da_at, da_l, da_r, db_at, db_l, db_n,
         P._workspace(dev, h, stream), B.MOE_PRODUCTS_WORKSPACE_BYTES, h)
     if rc:
         raise B.MoeError("moe_adapter_mm_dw", rc)
-    return tuple(grads)
+    return da, db
 
 
 class AdapterLinear(torch.autograd.Function):
