@@ -54,6 +54,7 @@ struct AdapterGradArgs {
   int L, rows, R, type, out_type, accumulate;
   int slice_rows;            // positions of a slice
   float* part;               // partial tiles
+  float* tops;               // fp16: largest value of mid of each slice and side
   unsigned* status;
 };
 

@@ -5,9 +5,9 @@
 // the sum over positions in stages of 64; both operands lie with the sum outermost and
 // enter through MN-major descriptors.  mid is fp32 and enters as a high and a low
 // 16-bit part, two MMAs on one accumulator (fp16: divided by a power of two that
-// brings the item's largest value to 2^13 .. 2^14, so that values 2^-27 of it still
-// keep 11 bits).  Roles: eight warps gather rows with asynchronous copies, eight convert
-// mid, an MMA warp, four epilogue warps.
+// brings the slice's largest value to 2^13 .. 2^14, so that values 2^-27 of it still
+// keep 11 bits; a launch of its own finds it).  Roles: eight warps gather rows with
+// asynchronous copies, four or eight convert mid, an MMA warp, four epilogue warps.
 //
 // Items: an adapter's positions are cut into slices of a.slice_rows, times the tiles
 // of p of both sides in one launch.  An adapter of one slice is written at once; the
@@ -16,9 +16,9 @@
 //
 // 16384 rows of 4096 x 7168, rank 16: 65 us + 4 for the sum of slices (371 MB, floor 55; 210 before
 // its loaders shed instructions).  8188 rows of 32 experts of 2880 x 2880 (94 MB in, 12
-// out, floor 16): 37 in bf16 and 50 in fp16, which reads an item's mid once more for its
-// largest value; rank 64 45 and 68, rank 128 68 and 102: 1472 items of four or five
-// stages each, whose first and last stages do not overlap their neighbours'.
+// out, floor 16): 38 in bf16 and 45 in fp16; rank 64 45 and 56, rank 128 68 and 81: 1472
+// items of four or five stages each, whose first and last stages do not overlap their
+// neighbours'.
 #include <type_traits>
 
 #include "adapters.cuh"
@@ -31,8 +31,7 @@ constexpr int kDwCols = 128;
 template <int TYPE, int VEC>  // VEC: sixteens of ranks
 struct DwCfg {
   static constexpr int RB = (VEC + 3) / 4;  // blocks of 64 ranks
-  // threads (what a warp does beside converting counts too, but fp16 reads an item's mid twice)
-  static constexpr int kConverters = VEC <= 2 && TYPE == kBf16 ? 128 : 256;
+  static constexpr int kConverters = VEC <= 2 ? 128 : 256;  // threads (what a warp does beside converting counts too)
   static constexpr int kThreads = kDwLoaders + 128 + kConverters + 32, kMmaWarp = kThreads / 32 - 1;
   static constexpr int kPerLine = kConverters / 64, kVec = VEC * 4 / kPerLine;  // threads to a position, float4 to a thread
   static constexpr int kAhead = kVec <= 8 ? 8 / kVec : 1;  // stages of mid on their way in registers
@@ -52,6 +51,7 @@ struct DwCfg {
 struct DwItem {
   int l, side, p0;
   int pos, n;       // positions
+  int slice;        // among all adapters' slices
   int slices;       // of the adapter
   int64_t part;     // partial tile, for adapters of several slices
 };
@@ -113,6 +113,7 @@ __device__ __forceinline__ DwItem dw_item(const AdapterGradArgs& a, const int* s
   const int slice = (int)(w / tiles), tile = (int)(w - (int64_t)slice * tiles);
   while (start[l + 1] <= slice) ++l;
   it.l = l;
+  it.slice = slice;
   it.side = tile >= a.side[0].tiles;
   it.p0 = (tile - (it.side ? a.side[0].tiles : 0)) * kDwCols;
   int i0, i1;
@@ -187,18 +188,51 @@ __device__ __forceinline__ void dw_put_any(const AdapterGradArgs& a, const Adapt
   }
 }
 
-// A barrier of n threads that tells whether all of them bring true.
-__device__ __forceinline__ bool named_bar_and(int id, int n, bool p) {
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "bar.red.and.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(all)
-      : "r"(id), "r"(n), "r"(p ? 1u : 0u)
-      : "memory");
-  return all != 0;
+// fp16: the largest value of mid in each slice, of both sides; the gradient's kernel divides by its power of two.  Found
+// there by each item for itself, so once more for every tile of columns, 8188 rows of 32 experts of 2880 x 2880 took 39 us
+// for rank 16, 50, 68 and 102 for 32, 64 and 128; with this launch, about 4 us, they take 40, 45, 56 and 81.
+constexpr int kDtThreads = 256;
+__global__ void __launch_bounds__(kDtThreads) adapter_dw_top_kernel(const __grid_constant__ AdapterGradArgs a) {
+  __shared__ int start[kAdAdapters + 1], part[kAdAdapters + 1];
+  __shared__ int warp_tot[2 * kDtThreads / 32];
+  __shared__ float warp_top[kDtThreads / 32];
+  const int tid = threadIdx.x;
+  grid_dependents_launch();
+  grid_dependency_wait();
+  if (!plan_dw<kDtThreads>(a, start, part, warp_tot)) return;
+  int l = 0;
+  for (int w = blockIdx.x; w < 2 * start[a.L]; w += gridDim.x) {
+    const int slice = w >> 1;
+    const AdapterGradSide& g = a.side[w & 1];
+    if (!g.out) continue;
+    while (start[l + 1] <= slice) ++l;
+    int i0, i1;
+    adapter_rows(a.offsets, a.rows, l, i0, i1);
+    const int pos = i0 + (slice - start[l]) * a.slice_rows;
+    const int64_t all = (int64_t)min(a.slice_rows, i1 - pos) * (a.R / 4);
+    const float4* const mid = reinterpret_cast<const float4*>(g.mid + (int64_t)pos * a.R);
+    float top = 0.0f;
+#pragma unroll 8
+    for (int64_t u = tid; u < all; u += kDtThreads) {
+      const float4 v = __ldg(mid + u);
+      top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+    }
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // (not negative)
+    if ((tid & 31) == 0) warp_top[tid >> 5] = top;
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+      for (int u = 1; u < kDtThreads / 32; ++u) top = fmaxf(top, warp_top[u]);
+      a.tops[w] = top;
+    }
+    __syncthreads();
+  }
+}
+// The power of two that brings the item's largest value to 2^13 .. 2^14.
+__device__ __forceinline__ float dw_factor(const AdapterGradArgs& a, const DwItem& it) {
+  const float top = __ldcg(a.tops + 2 * it.slice + it.side);
+  const int e = max((int)((__float_as_uint(top) >> 23) & 255) - 13, 1);
+  return top > 0.0f && top < INFINITY ? __uint_as_float((uint32_t)e << 23) : 1.0f;
 }
 
 template <int TYPE, int VEC>
@@ -209,8 +243,6 @@ __global__ void __launch_bounds__(DwCfg<TYPE, VEC>::kThreads, 1) adapter_dw_kern
   __shared__ int warp_tot[2 * C::kThreads / 32];
   __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], drain_bar;
   __shared__ uint32_t misc[2];
-  __shared__ float factor[2];      // of the accumulators (fp16)
-  __shared__ float warp_top[8];
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&misc[1]);
   const uint32_t smem_s = (smem_u32(smem_raw) + 1023) & ~1023u;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -307,38 +339,13 @@ __global__ void __launch_bounds__(DwCfg<TYPE, VEC>::kThreads, 1) adapter_dw_kern
     const int ct = tid - 12 * 32;
     const int quads = a.R / 4;  // float4 of a position
     Ring<C::kStages> slot;
-    Ring<2> acc;
     bool ok = true;
     int l = 0;
-    // (fp16: the warps meet for every item, so they also leave together)
-    for (int64_t w = blockIdx.x; w < items && (ok || TYPE == kFp16); w += gridDim.x) {
+    for (int64_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
       const DwItem it = dw_item(a, start, part, w, l);
       if (it.n == 0) continue;
       const float4* mid = reinterpret_cast<const float4*>(a.side[it.side].mid + (int64_t)it.pos * a.R);
-      float inv = 1.0f;
-      if (TYPE == kFp16) {
-        float top = 0.0f;
-        const int64_t all = (int64_t)it.n * quads;
-#pragma unroll 4
-        for (int64_t u = ct; u < all; u += C::kConverters) {
-          const float4 v = __ldg(mid + u);
-          top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-        }
-        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // (not negative)
-        if (lane == 0) warp_top[warp - 12] = top;
-        if (!(ok = named_bar_and(1, C::kConverters, ok))) break;
-#pragma unroll
-        for (int u = 0; u < C::kConverters / 32; ++u) top = fmaxf(top, warp_top[u]);
-        float f = 1.0f;
-        const int e = max((int)((__float_as_uint(top) >> 23) & 255) - 13, 1);
-        if (top > 0.0f && top < INFINITY) f = __uint_as_float((uint32_t)e << 23);
-        inv = 1.0f / f;
-        // the accumulator's last reader is done before its factor changes
-        ok = warp_wait(&acc_empty[acc.i], acc.phase ^ 1, abort_flag, a.status);
-        if (ct == 0 && ok) factor[acc.i] = f;
-        acc.next();
-        if (!(ok = named_bar_and(1, C::kConverters, ok))) break;
-      }
+      const float inv = TYPE == kFp16 ? 1.0f / dw_factor(a, it) : 1.0f;
       // two or four threads to a position, which take its float4 in turn; the loads run some stages ahead
       const int line = ct / C::kPerLine, first = ct % C::kPerLine;
       const float4* const from = mid + (int64_t)line * quads + first;
@@ -427,7 +434,7 @@ __global__ void __launch_bounds__(DwCfg<TYPE, VEC>::kThreads, 1) adapter_dw_kern
       tc_fence_after();
       const bool whole = it.slices == 1;
       float mul = whole && a.scale && some ? a.scale[it.l] : 1.0f;
-      if (TYPE == kFp16 && some) mul *= *(volatile float*)&factor[acc.i];
+      if (TYPE == kFp16 && some) mul *= dw_factor(a, it);
       const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc.i * ranks;
       const bool there = it.p0 + at < g.P;
       const int64_t first = it.l * g.out_l + (it.p0 + at) * g.out_p;
@@ -525,7 +532,7 @@ static cudaError_t launch_dw(const AdapterGradArgs& a, int sms, cudaStream_t st)
   return launch_dw<TYPE, 16>(a, sms, st);
 }
 
-// part_values: what the workspace holds of partial sums.
+// part_values: what the workspace holds behind a.part: partial sums, and at its end the slices' largest values.
 cudaError_t launch_adapter_grad_tc(AdapterGradArgs& a, int64_t part_values, cudaStream_t st) {
   const int sms = prod_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
@@ -533,7 +540,10 @@ cudaError_t launch_adapter_grad_tc(AdapterGradArgs& a, int64_t part_values, cuda
   const int64_t tiles = a.side[0].tiles + a.side[1].tiles;
   // Six items to a CTA, of 256 rows at least, if one adapter had all rows; n rows in slices make fewer than
   // 2 n / slice of them where there is more than one, all of which the workspace has to hold.
-  const int64_t items = (int64_t)sms * 6, room = part_values / (tiles * a.R * kDwCols);
+  // (an adapter has a slice more than its share of all rows at most)
+  const int64_t items = (int64_t)sms * 6, top_values = 2 * (kAdAdapters + items + 1);
+  a.tops = a.part + part_values - top_values;
+  const int64_t room = (part_values - top_values) / (tiles * a.R * kDwCols);
   int64_t rows = (a.rows * tiles + items - 1) / items;
   if (rows < 256) rows = 256;
   if (room < 2) rows = a.rows;
@@ -541,6 +551,10 @@ cudaError_t launch_adapter_grad_tc(AdapterGradArgs& a, int64_t part_values, cuda
   rows = (rows + 63) / 64 * 64;
   a.slice_rows = (int)(rows > a.rows ? a.rows : rows);
   if (a.slice_rows < 1) a.slice_rows = 1;
+  if (a.type == kFp16) {
+    const cudaError_t rc = launch_dependent(adapter_dw_top_kernel, dim3(sms * 2), dim3(kDtThreads), 0, st, a);
+    if (rc != cudaSuccess) return rc;
+  }
   const cudaError_t rc = a.type == kBf16 ? launch_dw<kBf16>(a, sms, st) : launch_dw<kFp16>(a, sms, st);
   if (rc != cudaSuccess || a.slice_rows >= a.rows) return rc;
   return launch_dependent(adapter_dw_sum_kernel, dim3(sms * 4), dim3(256), 0, st, a);
