@@ -166,3 +166,47 @@ def test_a_million_tokens(R, lengths):
     assert torch.equal(ids, want)
     offsets = None if lengths is None else offsets_of(lengths)
     check_balance(R, logits, R.expert_counts(ids, 8, offsets), offsets, "softmax")
+
+
+FIRST = """
+import torch
+from weight_only_bit_moe_gb300 import adapters as A, routing as R, products as P
+g = torch.Generator("cuda").manual_seed(0)
+sets = []
+for dt in (torch.bfloat16, torch.float16):
+    for rows in (12, 700):
+        for n, k, r in ((50, 44, 5), (72, 64, 8)):
+            make = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dt)
+            off = torch.tensor([0, rows // 2, rows - 3], dtype=torch.int32, device="cuda")
+            sets.append((make(rows, k), make(rows, n), make(2, r, k), make(2, n, r), off))
+l, off = torch.randn(700, 64, generator=g, device="cuda"), sets[-1][4]
+bias, dloss = torch.zeros(64, device="cuda"), torch.ones(2, device="cuda")
+def run():
+    out = []
+    for x, dy, a, b, o in sets:
+        mids = [torch.zeros(x.shape[0], a.shape[1], device="cuda") for _ in range(2)]
+        out += [A.adapter_mm(x, a, b, o, mid=mids[0]), A.adapter_mm_dx(dy, a, b, o, mid=mids[1])]
+        out += A.adapter_mm_dw(dy, x, *mids, o)
+    for top_k in (4, 9):
+        w, ids = R.topk_route(l, top_k, "sigmoid", bias)
+        out += [w, ids, R.topk_route_grad(w, l, ids, "sigmoid")]
+    c = R.expert_counts(ids, 64, off)
+    return out + [c, R.balance(l, c, off), R.balance_grad(dloss, l, c, off)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(u, v) for u, v in zip(got, run())) and P.products_status() == 0
+"""
+
+
+def test_first_calls_are_captured(A):
+    """A process whose first calls of all these kernels are those of a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
