@@ -217,7 +217,7 @@ class AdapterLinear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, a, b, offsets, order, scale, base):
-        mid = x.new_empty((x.shape[0], a.shape[1]), dtype=torch.float32)
+        mid = P._empty((x.shape[0], a.shape[1]), torch.float32, x, None)
         out = adapter_mm(x, a, b, offsets, order, scale, base=base, mid=mid)
         ctx.save_for_backward(x, a, b, offsets, order, scale, mid)
         return out
