@@ -237,11 +237,12 @@ __global__ void __launch_bounds__(kOuThreads, OutCfg<KS>::kCtas) adapter_out_ker
             }
         }
       };
-      float top[2] = {0.0f, 0.0f};  // fp16: the largest of a row, by reading it once more
+      float top[2] = {0.0f, 0.0f};  // fp16: the largest of a row, by reading it once more where it has more ranks than v
+      constexpr bool kOnce = TYPE == kFp16 && KS <= kBlock;
       if (TYPE == kFp16) {
 #pragma unroll 1
         for (int k0 = 0; k0 < steps; k0 += kBlock) {
-          load_mid(k0, false);
+          load_mid(k0, kOnce);
 #pragma unroll
           for (int k = 0; k < kBlock; ++k)
 #pragma unroll
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kOuThreads, OutCfg<KS>::kCtas) adapter_out_ker
 #pragma unroll
       for (int k0 = 0; k0 < KS; k0 += kBlock) {
         if (k0 >= steps) break;
-        load_mid(k0, true);
+        if (!kOnce) load_mid(k0, true);
 #pragma unroll
         for (int k = 0; k < kBlock; ++k) {
           uint32_t hi[4], lo[4];
